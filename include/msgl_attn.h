@@ -76,6 +76,8 @@ typedef enum msgl_status {
 #define MSGL_DEVERR_POSITION 0x8u    /* positions[t] != prefix_len + i for chunk row i */
 #define MSGL_DEVERR_TIMEOUT 0x10u    /* a bounded in-kernel wait gave up */
 #define MSGL_DEVERR_APPEND_SLOT 0x20u /* decode_append: new_loc[b] is not the slot of key seq_lens[b]-1 */
+#define MSGL_DEVERR_GROUP 0x40u      /* group_start / shared_lens do not describe a group (decode_shared) */
+#define MSGL_DEVERR_NO_PAGES 0x80u   /* step_tables: the free pages do not reach this far */
 
 /*
  * The unified KV pool of one layer.  k_pool and v_pool are device bf16
@@ -293,6 +295,125 @@ MSGL_API msgl_status msgl_attn_decode_noalloc(const msgl_kv_pool *pool, const ms
                                      const void *q, int32_t num_q_heads, const int32_t *seq_lens,
                                      int32_t num_reqs, int32_t max_seq_len, float scale, void *o,
                                      float *lse, uint32_t *status, msgl_stream_t stream);
+
+/*
+ * Block tables and slot maps of one step, built on the GPU from the request
+ * lengths, so that admitting and extending requests costs no host loop over
+ * tokens and no table upload: every request's pages come from one allocator
+ * ("不懂SGLang？从miniSGLang开始", §1.2 item 3; "Mini-SGLang 实战指南", §6.2),
+ * and the page table and positions locate each token ("不懂SGLang？从miniSGLang
+ * 开始", §1.3 item 3).  Request b holds cached_lens[b] tokens and gets
+ * new_lens[b] more.  With P(x) = ceil(x / page_size), s_b = cached + new,
+ * need_b = P(s_b) - P(cached_b), off_b = sum of need_i and cu_b = sum of new_i
+ * over i < b:
+ *   page p of request b = req_table[row_b][p]                for p < P(cached_b),
+ *                         free_pages[off_b + p - P(cached_b)] up to P(s_b)
+ *   out->page_ids[b][p]                = page p, p < P(s_b) (later entries are left as they were)
+ *   req_table[row_b][p]                = page p, P(cached_b) <= p < P(s_b)
+ *   out->seq_lens[b] = s_b,  out->cu_ext[b] = cu_b (and cu_ext[num_reqs] = the sum)
+ *   out->positions[cu_b + i] = cached_b + i
+ *   out->out_loc[cu_b + i]   = the slot of that position: page id * page_size + offset
+ *   out->pages_taken[0]      = sum of need_b: how many of free_pages are now in use
+ * These are the arguments of msgl_store_kv, msgl_attn_extend (prefix_lens =
+ * cached_lens, ext_lens = new_lens) and msgl_attn_decode (new_lens = 1).
+ *
+ *   req_table    device int32 [num_rows, table_stride]: the page ids of every running
+ *                request, table_width valid columns (in and out)
+ *   req_rows     device int32 [num_reqs] or NULL (row_b = b): distinct rows; a row named
+ *                twice ends with either one's new pages
+ *   cached_lens  device int32 [num_reqs];  new_lens device int32 [num_reqs] or NULL (1 each)
+ *   free_pages   device int32 [num_free]: page ids in the order they are handed out
+ *   out          total_tokens entries of positions and out_loc; when the step has fewer tokens
+ *                (a captured step padded to a bucket) the entries behind them are
+ *                positions = 0, out_loc = -1, so that a store skips them
+ * No output may overlap an input but req_table.  A request is refused when its
+ * length is negative or needs more columns than either table has, or its row is
+ * outside the table (MSGL_DEVERR_LENGTH), when its tokens pass total_tokens
+ * (MSGL_DEVERR_LENGTH), or when free_pages does not reach its last new page
+ * (MSGL_DEVERR_NO_PAGES; its place in the order is kept, so every later request
+ * that needs a page is refused too, and pages_taken counts up to the last one
+ * served).  A refused request gets seq_lens = 0 (the attention calls then
+ * write its row as zero), out_loc = -1 and positions = 0 for its tokens, and its table
+ * rows are left as they were.  A token on a page whose id is outside
+ * [0, num_slots / page_size) gets out_loc = -1 and MSGL_DEVERR_PAGE_RANGE.
+ * num_slots may not pass 2^31 (out_loc is int32).  The launch shape depends on
+ * host scalars only.
+ */
+typedef struct msgl_step_out {
+    int32_t *page_ids;             /* device int32 [num_reqs, stride] */
+    int32_t stride, width;         /* row pitch and valid columns of page_ids */
+    int32_t *seq_lens;             /* device int32 [num_reqs] */
+    int32_t *cu_ext;               /* device int32 [num_reqs + 1] */
+    int32_t *positions;            /* device int32 [total_tokens] */
+    int32_t *out_loc;              /* device int32 [total_tokens] */
+    int32_t *pages_taken;          /* device int32 [1] */
+    int32_t total_tokens;
+} msgl_step_out;
+
+MSGL_API msgl_status msgl_step_tables(int64_t num_slots, int32_t page_size, int32_t *req_table, int32_t num_rows,
+                                      int32_t table_stride, int32_t table_width, const int32_t *req_rows,
+                                      const int32_t *cached_lens, const int32_t *new_lens, int32_t num_reqs,
+                                      const int32_t *free_pages, int32_t num_free, const msgl_step_out *out,
+                                      uint32_t *status, msgl_stream_t stream);
+
+/*
+ * Groups of neighbouring requests whose page tables begin with the same pages:
+ * the input of msgl_attn_decode_shared.  A radix-cache hit gives requests the
+ * same prefix pages ("Mini-SGLang 实战指南", §6.5 "Radix Cache"), so the tables
+ * tell which requests share without the tree.  With d_b the number of leading
+ * columns on which rows b-1 and b agree (within both requests' pages) and
+ * m_b = min(d_b * page_size, seq_lens[b-1], seq_lens[b]):
+ *   b joins the group of b-1 when m_b >= min_shared
+ *   group_start[b] = the first row of b's group
+ *   shared_lens[b] = min of m over the group's joined rows (0 for a group of one)
+ * One level of sharing: a batch sorted by prefix gets the most out of it, and
+ * min_shared (at least 1) chooses between few groups with a short prefix in
+ * common and more groups with longer ones.
+ *
+ *   seq_lens     device int32 [num_reqs]; a request whose length is outside
+ *                [1, max_seq_len] (MSGL_DEVERR_LENGTH) or passes the table's width
+ *                (MSGL_DEVERR_PAGE_RANGE) is a group of one
+ *   group_start, shared_lens   device int32 [num_reqs] (output)
+ */
+MSGL_API msgl_status msgl_shared_prefixes(const msgl_page_table *pages, const int32_t *seq_lens, int32_t num_reqs,
+                                          int32_t page_size, int32_t max_seq_len, int32_t min_shared,
+                                          int32_t *group_start, int32_t *shared_lens, uint32_t *status,
+                                          msgl_stream_t stream);
+
+/*
+ * Decode for a batch in which groups of requests share a prefix: the result of
+ * msgl_attn_decode, with the keys that a group shares read once for all of its
+ * requests (a shared system prompt or document held once in the pool by the
+ * radix cache: "Mini-SGLang 实战指南", §6.5 "Radix Cache", §6.3).
+ * Requests group_start[b] .. are neighbours in the batch.  Row b attends keys
+ * 0..shared_lens[b]-1 at the slots of row group_start[b]'s page table, and keys
+ * shared_lens[b]..seq_lens[b]-1 at the slots of its own.  A group's query rows
+ * go through the tensor cores together against its shared keys; every row's
+ * own keys take the decode's path; the two are joined by their log-sum-exp.
+ *
+ *   group_start  device int32 [num_reqs]: the first row of b's group, so
+ *                group_start[b] is b or group_start[b-1]
+ *   shared_lens  device int32 [num_reqs]: 0 <= shared_lens[b] <= seq_lens[b],
+ *                the same for all rows of a group (of a group of one it is
+ *                not used: all keys are its own)
+ *   workspace    device scratch of at least msgl_decode_shared_workspace_size()
+ *                bytes, 256-byte aligned, fully rewritten by every call; two calls
+ *                (or captured graphs) that may overlap need one each
+ * Every other argument, the outputs and the status bits are those of
+ * msgl_attn_decode.  A row whose group entries break these rules sets
+ * MSGL_DEVERR_GROUP and is written as o = 0, lse = -inf; a bad page among the
+ * shared keys does that to every row of the group (MSGL_DEVERR_PAGE_RANGE).
+ * The launch shapes depend on host scalars only.
+ */
+MSGL_API size_t msgl_decode_shared_workspace_size(int32_t num_reqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                                  int32_t head_dim, int32_t max_seq_len);
+
+MSGL_API msgl_status msgl_attn_decode_shared(const msgl_kv_pool *pool, const msgl_page_table *pages, const void *q,
+                                             int32_t num_q_heads, const int32_t *group_start,
+                                             const int32_t *shared_lens, const int32_t *seq_lens,
+                                             int32_t num_reqs, int32_t max_seq_len, float scale, void *o,
+                                             float *lse, void *workspace, size_t workspace_bytes,
+                                             uint32_t *status, msgl_stream_t stream);
 
 /*
  * Synchronises `stream`, reads the device status word into *flags (may be

@@ -59,6 +59,13 @@ msgl_status check_pool(const msgl_kv_pool *pool, msgl::PoolView &view) {
     return MSGL_OK;
 }
 
+msgl_status check_page_size(int32_t page_size, int32_t &log2_ps) {
+    log2_ps = log2_exact(page_size);
+    if (log2_ps < 0 || page_size > 256)
+        return fail(MSGL_ERR_UNSUPPORTED, "page_size %d is not a power of two in [1, 256]", page_size);
+    return MSGL_OK;
+}
+
 msgl_status check_pages(const msgl_page_table *pages, int32_t num_reqs, msgl::PageView &view) {
     if (!pages) return fail(MSGL_ERR_INVALID_ARG, "page table is NULL");
     if (num_reqs > 0 && !pages->page_ids) return fail(MSGL_ERR_INVALID_ARG, "page_ids is NULL");
@@ -342,6 +349,122 @@ msgl_status msgl_attn_mixed(const msgl_kv_pool *pool, const msgl_extend_batch *e
         e = msgl::launch_extend(ea, st);
     }
     return e == cudaSuccess ? MSGL_OK : cuda_fail(e, "mixed step launch");
+}
+
+msgl_status msgl_step_tables(int64_t num_slots, int32_t page_size, int32_t *req_table, int32_t num_rows,
+                             int32_t table_stride, int32_t table_width, const int32_t *req_rows,
+                             const int32_t *cached_lens, const int32_t *new_lens, int32_t num_reqs,
+                             const int32_t *free_pages, int32_t num_free, const msgl_step_out *out,
+                             uint32_t *status, msgl_stream_t stream) {
+    g_last_error[0] = 0;
+    if (!out) return fail(MSGL_ERR_INVALID_ARG, "out is NULL");
+    msgl::StepTablesArgs a{};
+    msgl_status s = check_page_size(page_size, a.log2_ps);
+    if (s) return s;
+    if (num_slots < 0 || num_slots % page_size != 0)
+        return fail(MSGL_ERR_INVALID_ARG, "num_slots must be a non-negative multiple of page_size");
+    if (num_slots > (int64_t)INT32_MAX + 1)
+        return fail(MSGL_ERR_UNSUPPORTED, "out_loc is int32: num_slots may not pass 2^31");
+    if (num_reqs < 0 || num_free < 0 || num_rows < 0 || out->total_tokens < 0)
+        return fail(MSGL_ERR_INVALID_ARG, "negative size");
+    if (num_reqs == INT32_MAX) return fail(MSGL_ERR_UNSUPPORTED, "num_reqs + 1 passes int32");
+    if (table_width < 0 || table_stride < table_width)
+        return fail(MSGL_ERR_INVALID_ARG, "req_table needs 0 <= table_width <= table_stride");
+    if (out->width < 0 || out->stride < out->width)
+        return fail(MSGL_ERR_INVALID_ARG, "out needs 0 <= width <= stride");
+    if (!out->cu_ext || !out->pages_taken)
+        return fail(MSGL_ERR_INVALID_ARG, "out->cu_ext and out->pages_taken must be non-NULL");
+    if (out->total_tokens > 0 && (!out->positions || !out->out_loc))
+        return fail(MSGL_ERR_INVALID_ARG, "out->positions and out->out_loc must be non-NULL");
+    if (num_reqs > 0 && (!cached_lens || !out->seq_lens))
+        return fail(MSGL_ERR_INVALID_ARG, "cached_lens and out->seq_lens must be non-NULL");
+    a.max_pages = table_width < out->width ? table_width : out->width;
+    if (num_reqs > 0 && num_rows > 0 && a.max_pages > 0 && (!req_table || !out->page_ids))
+        return fail(MSGL_ERR_INVALID_ARG, "req_table and out->page_ids must be non-NULL");
+    if (num_free > 0 && !free_pages) return fail(MSGL_ERR_INVALID_ARG, "free_pages is NULL");
+    if (out->total_tokens > msgl::kMaxStepItems || a.max_pages > msgl::kMaxStepItems)
+        return fail(MSGL_ERR_UNSUPPORTED, "more than %lld tokens or columns", (long long)msgl::kMaxStepItems);
+    a.req_table = req_table;
+    a.req_rows = req_rows;
+    a.cached_lens = cached_lens;
+    a.new_lens = new_lens;
+    a.free_pages = free_pages;
+    a.num_rows = num_rows;
+    a.table_stride = table_stride;
+    a.num_reqs = num_reqs;
+    a.num_free = num_free;
+    a.num_pages = (int32_t)(num_slots / page_size < INT32_MAX ? num_slots / page_size : INT32_MAX);
+    a.page_ids = out->page_ids;
+    a.seq_lens = out->seq_lens;
+    a.cu_ext = out->cu_ext;
+    a.positions = out->positions;
+    a.out_loc = out->out_loc;
+    a.pages_taken = out->pages_taken;
+    a.stride = out->stride;
+    a.total_tokens = out->total_tokens;
+    a.status = status;
+    cudaError_t e = msgl::launch_step_tables(a, (cudaStream_t)stream);
+    return e == cudaSuccess ? MSGL_OK : cuda_fail(e, "step_tables launch");
+}
+
+msgl_status msgl_shared_prefixes(const msgl_page_table *pages, const int32_t *seq_lens, int32_t num_reqs,
+                                 int32_t page_size, int32_t max_seq_len, int32_t min_shared,
+                                 int32_t *group_start, int32_t *shared_lens, uint32_t *status,
+                                 msgl_stream_t stream) {
+    g_last_error[0] = 0;
+    msgl::SharedPrefixesArgs a{};
+    msgl_status s = check_page_size(page_size, a.log2_ps);
+    if (s) return s;
+    if (num_reqs < 0) return fail(MSGL_ERR_INVALID_ARG, "num_reqs < 0");
+    if (num_reqs == 0) return MSGL_OK;
+    if ((s = check_pages(pages, num_reqs, a.pages))) return s;
+    if (max_seq_len <= 0) return fail(MSGL_ERR_INVALID_ARG, "max_seq_len must be > 0");
+    if (min_shared <= 0) return fail(MSGL_ERR_INVALID_ARG, "min_shared must be > 0");
+    if (!seq_lens || !group_start || !shared_lens)
+        return fail(MSGL_ERR_INVALID_ARG, "seq_lens, group_start and shared_lens must be non-NULL");
+    a.seq_lens = seq_lens;
+    a.num_reqs = num_reqs;
+    a.max_seq_len = max_seq_len;
+    a.min_shared = min_shared;
+    a.group_start = group_start;
+    a.shared_lens = shared_lens;
+    a.status = status;
+    cudaError_t e = msgl::launch_shared_prefixes(a, (cudaStream_t)stream);
+    return e == cudaSuccess ? MSGL_OK : cuda_fail(e, "shared_prefixes launch");
+}
+
+size_t msgl_decode_shared_workspace_size(int32_t num_reqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                         int32_t head_dim, int32_t max_seq_len) {
+    if (num_reqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim != msgl::kHeadDim || max_seq_len <= 0)
+        return 0;
+    return msgl::decode_shared_workspace_bytes(num_reqs, num_q_heads, num_kv_heads);
+}
+
+msgl_status msgl_attn_decode_shared(const msgl_kv_pool *pool, const msgl_page_table *pages, const void *q,
+                                    int32_t num_q_heads, const int32_t *group_start, const int32_t *shared_lens,
+                                    const int32_t *seq_lens, int32_t num_reqs, int32_t max_seq_len, float scale,
+                                    void *o, float *lse, void *workspace, size_t workspace_bytes,
+                                    uint32_t *status, msgl_stream_t stream) {
+    g_last_error[0] = 0;
+    // the workspace it needs includes a decode's, so the decode's check passes when this one does
+    if (num_reqs > 0 && pool && pool->num_kv_heads > 0 && num_q_heads > 0) {
+        if (!group_start || !shared_lens)
+            return fail(MSGL_ERR_INVALID_ARG, "group_start and shared_lens must be non-NULL");
+        const size_t need = msgl::decode_shared_workspace_bytes(num_reqs, num_q_heads, pool->num_kv_heads);
+        if (!workspace || workspace_bytes < need)
+            return fail(MSGL_ERR_WORKSPACE, "decode_shared needs %zu workspace bytes, got %zu", need,
+                        workspace ? workspace_bytes : (size_t)0);
+    }
+    msgl::DecodeSharedArgs a;
+    msgl::DecodePlan plan{};
+    msgl_status s = prepare_decode(pool, pages, q, num_q_heads, nullptr, nullptr, nullptr, seq_lens, num_reqs,
+                                   max_seq_len, scale, o, lse, workspace, workspace_bytes, status, a.dec, plan);
+    if (s || num_reqs == 0) return s;
+    a.group_start = group_start;
+    a.shared_lens = shared_lens;
+    a.workspace = workspace;
+    cudaError_t e = msgl::launch_decode_shared(a, (cudaStream_t)stream);
+    return e == cudaSuccess ? MSGL_OK : cuda_fail(e, "decode_shared launch");
 }
 
 msgl_status msgl_read_status(const uint32_t *status, uint32_t *flags, msgl_stream_t stream) {

@@ -67,6 +67,39 @@ struct ExtendArgs {
 };
 cudaError_t launch_extend(const ExtendArgs &a, cudaStream_t stream);
 
+// ------------------------------------------------- step tables, prefix groups
+constexpr int64_t kMaxStepItems = 65535ll * 2048;   // tokens of a step, columns of a table (grid.y)
+
+struct StepTablesArgs {
+    int32_t *req_table;
+    const int32_t *req_rows, *cached_lens, *new_lens, *free_pages;
+    int32_t num_rows, table_stride, num_reqs, num_free, num_pages, log2_ps;
+    int32_t max_pages;    // columns that both tables have
+    int32_t *page_ids, *seq_lens, *cu_ext, *positions, *out_loc, *pages_taken;
+    int32_t stride, total_tokens;
+    uint32_t *status;
+};
+cudaError_t launch_step_tables(const StepTablesArgs &a, cudaStream_t stream);
+
+struct SharedPrefixesArgs {
+    PageView pages;
+    const int32_t *seq_lens;
+    int32_t num_reqs, log2_ps, max_seq_len, min_shared;
+    int32_t *group_start, *shared_lens;
+    uint32_t *status;
+};
+cudaError_t launch_shared_prefixes(const SharedPrefixesArgs &a, cudaStream_t stream);
+
+// -------------------------------------------------------- shared-prefix decode
+size_t decode_shared_workspace_bytes(int32_t num_reqs, int32_t hq, int32_t hkv);
+
+struct DecodeSharedArgs {
+    DecodeArgs dec;                 // o, lse, the batch; part_o / part_lse: see the launcher
+    const int32_t *group_start, *shared_lens;
+    void *workspace;
+};
+cudaError_t launch_decode_shared(const DecodeSharedArgs &a, cudaStream_t stream);
+
 // cuTensorMapEncodeTiled from the driver (NULL if unavailable); looked up once.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 

@@ -1,0 +1,126 @@
+// Groups of neighbouring requests whose page tables begin with the same pages.
+//
+// "Mini-SGLang 实战指南", §6.5 "Radix Cache": requests with a common prefix are
+// given the same pages.  m_b is the length that rows b-1 and b have in common;
+// row b joins the group of b-1 when m_b reaches min_shared, and a group shares
+// the least m of its joined rows (the common prefix of a run of rows is the
+// least of its neighbours' common prefixes).
+//
+// Two kernels: one block per row compares it with the row before (2048 columns
+// a round, done at the first round with a difference), and one block then
+// finds each group's start and least m by scans over the rows.  m travels in
+// shared_lens, which the second kernel overwrites, so the call needs no scratch.
+#include <limits.h>
+
+#include "kernels.h"
+
+namespace msgl {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPerThread = 8;
+
+__device__ __forceinline__ bool row_ok(const SharedPrefixesArgs &a, int s) {
+    return s >= 1 && s <= a.max_seq_len && ((s - 1) >> a.log2_ps) < a.pages.width;
+}
+
+__global__ void __launch_bounds__(kThreads) row_match_kernel(const SharedPrefixesArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int b = blockIdx.x;
+    const int s1 = __ldg(a.seq_lens + b), s0 = b > 0 ? __ldg(a.seq_lens + b - 1) : 0;
+    if (threadIdx.x == 0) {
+        if (s1 < 1 || s1 > a.max_seq_len) report(a.status, MSGL_DEVERR_LENGTH);
+        else if (!row_ok(a, s1)) report(a.status, MSGL_DEVERR_PAGE_RANGE);
+    }
+    int m = 0;
+    if (b > 0 && row_ok(a, s0) && row_ok(a, s1)) {
+        const int both = min(s0, s1);
+        const int n = ((both - 1) >> a.log2_ps) + 1;
+        const int32_t *x = a.pages.ids + (long long)(b - 1) * a.pages.stride, *y = x + a.pages.stride;
+        __shared__ int first;
+        if (threadIdx.x == 0) first = n;
+        __syncthreads();
+        for (int c0 = 0; c0 < n; c0 += kThreads * kPerThread) {
+            int far = INT_MAX;
+#pragma unroll
+            for (int u = kPerThread - 1; u >= 0; --u) {
+                const int p = c0 + u * kThreads + (int)threadIdx.x;
+                if (p < n && __ldg(x + p) != __ldg(y + p)) far = p;
+            }
+            if (__syncthreads_or(far != INT_MAX)) {
+                if (far != INT_MAX) atomicMin(&first, far);
+                __syncthreads();
+                break;
+            }
+        }
+        m = (int)min((long long)first << a.log2_ps, (long long)both);
+    }
+    if (threadIdx.x == 0) a.shared_lens[b] = m;
+}
+
+// One block.  Rows are taken 1024 at a time; a row's group starts at the last row
+// that did not join (an inclusive max scan), and its least m is gathered by
+// atomicMin on the start row's entry, which holds no m of its own.
+constexpr int kScanThreads = 1024;
+
+__global__ void __launch_bounds__(kScanThreads) row_groups_kernel(const SharedPrefixesArgs a) {
+    __shared__ int warp_max[32];
+    __shared__ int carry;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) carry = 0;
+    __syncthreads();
+    for (int c0 = 0; c0 < a.num_reqs; c0 += kScanThreads) {
+        const int b = c0 + threadIdx.x;
+        const int m = b < a.num_reqs ? __ldcg(a.shared_lens + b) : 0;
+        const bool joined = b > 0 && m >= a.min_shared;
+        int start = b < a.num_reqs && !joined ? b : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, start, o);
+            if (lane >= o) start = max(start, u);
+        }
+        if (lane == 31) warp_max[warp] = start;
+        __syncthreads();
+        int before = carry;
+        for (int w = 0; w < warp; ++w) before = max(before, warp_max[w]);
+        start = max(start, before);
+        if (b < a.num_reqs) {
+            a.group_start[b] = start;
+            if (!joined) a.shared_lens[b] = INT_MAX;   // no m of its own: gathers the group's
+        }
+        __syncthreads();
+        if (threadIdx.x == kScanThreads - 1) carry = start;
+        if (b < a.num_reqs && joined) atomicMin(a.shared_lens + start, m);
+        __syncthreads();
+    }
+    // (read past L1: the atomics above worked in L2)
+    for (int b = threadIdx.x; b < a.num_reqs; b += kScanThreads) {
+        const int start = a.group_start[b];
+        if (start != b) a.shared_lens[b] = __ldcg(a.shared_lens + start);
+    }
+    __syncthreads();
+    for (int b = threadIdx.x; b < a.num_reqs; b += kScanThreads)
+        if (__ldcg(a.shared_lens + b) == INT_MAX) a.shared_lens[b] = 0;
+}
+
+}  // namespace
+
+cudaError_t launch_shared_prefixes(const SharedPrefixesArgs &a, cudaStream_t stream) {
+    row_match_kernel<<<a.num_reqs, kThreads, 0, stream>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(kScanThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, row_groups_kernel, a);
+}
+
+}  // namespace msgl

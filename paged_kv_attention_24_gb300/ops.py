@@ -9,10 +9,11 @@ raises immediately.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -28,6 +29,8 @@ DEVERR_LENGTH = 0x4
 DEVERR_POSITION = 0x8
 DEVERR_TIMEOUT = 0x10
 DEVERR_APPEND_SLOT = 0x20
+DEVERR_GROUP = 0x40
+DEVERR_NO_PAGES = 0x80
 
 
 class MsglError(RuntimeError):
@@ -61,6 +64,13 @@ class _DecodeBatch(ctypes.Structure):
                 ("o", ctypes.c_void_p), ("lse", ctypes.c_void_p)]
 
 
+class _StepOut(ctypes.Structure):
+    _fields_ = [("page_ids", ctypes.c_void_p), ("stride", ctypes.c_int32), ("width", ctypes.c_int32),
+                ("seq_lens", ctypes.c_void_p), ("cu_ext", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("out_loc", ctypes.c_void_p), ("pages_taken", ctypes.c_void_p),
+                ("total_tokens", ctypes.c_int32)]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -80,6 +90,11 @@ SIGNATURES = {
     "msgl_attn_decode_noalloc": ([PP, PT, P, I32, P, I32, I32, F32, P, P, P, P], ctypes.c_int),
     "msgl_attn_mixed": ([PP, ctypes.POINTER(_ExtendBatch), ctypes.POINTER(_DecodeBatch), I32, F32, P, SZ, P, P],
                         ctypes.c_int),
+    "msgl_step_tables": ([I64, I32, P, I32, I32, I32, P, P, P, I32, P, I32, ctypes.POINTER(_StepOut), P, P],
+                         ctypes.c_int),
+    "msgl_shared_prefixes": ([PT, P, I32, I32, I32, I32, P, P, P, P], ctypes.c_int),
+    "msgl_decode_shared_workspace_size": ([I32, I32, I32, I32, I32], SZ),
+    "msgl_attn_decode_shared": ([PP, PT, P, I32, P, P, P, I32, I32, F32, P, P, P, SZ, P, P], ctypes.c_int),
     "msgl_selftest_wait_timeout": ([P, I64, P], ctypes.c_int),
     "msgl_read_status": ([P, ctypes.POINTER(ctypes.c_uint32), P], ctypes.c_int),
     "msgl_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -354,6 +369,176 @@ def attn_decode_noalloc(pool: KVPool, q: torch.Tensor, page_table: torch.Tensor,
         ctypes.byref(pc), ctypes.byref(pt), _ptr(q), hq, _ptr(seq_lens), B, int(max_seq_len),
         float(scale), _ptr(out), _ptr(lse), _ptr(status), _stream(stream))
     _check(rc, "msgl_attn_decode_noalloc")
+    return out, lse
+
+
+# ------------------------------------------------- step tables and shared prefixes
+
+class StepTables(NamedTuple):
+    """The outputs of :func:`step_tables` (all int32): keep one and pass it as ``out`` to reuse its buffers."""
+    page_table: torch.Tensor   # [B, width] page ids; entries past a request's last page are left as they were
+    seq_lens: torch.Tensor     # [B]      cached + new tokens
+    cu_ext: torch.Tensor       # [B + 1]  prefix sums of the new tokens
+    positions: torch.Tensor    # [T]      absolute position of each new token
+    out_loc: torch.Tensor      # [T]      pool slot of each new token (-1: none)
+    pages_taken: torch.Tensor  # [1]      how many of the free pages are now in use
+
+
+_INT32 = torch.int32
+
+
+def _i32_on(device, **tensors):
+    """Every tensor is a contiguous int32 tensor on ``device``."""
+    for name, t in tensors.items():
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dtype is not _INT32:
+            raise ValueError(f"{name} must be {_INT32}, got {t.dtype}")
+        if t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _on(device: torch.device):
+    """Makes ``device`` current for a launch (a no-op context when it already is)."""
+    if device.type != "cuda":
+        raise ValueError("the tensors must be CUDA tensors")
+    return torch.cuda.device(device) if device.index != torch.cuda.current_device() else _HERE
+
+
+_HERE = contextlib.nullcontext()
+
+
+def step_tables(req_table: torch.Tensor, cached_lens: torch.Tensor, new_lens: Optional[torch.Tensor],
+                free_pages: torch.Tensor, num_slots: int, page_size: int, total_tokens: Optional[int] = None,
+                width: Optional[int] = None, req_rows: Optional[torch.Tensor] = None,
+                out: Optional[StepTables] = None, status: Optional[torch.Tensor] = None, stream=None) -> StepTables:
+    """Block tables and slot maps of one step from its request lengths (msgl_step_tables).
+
+    ``req_table`` int32 [rows, W] holds the page ids of every running request and gets
+    this step's new pages, taken from the front of ``free_pages``; request b is row
+    ``req_rows[b]`` (b when None), has ``cached_lens[b]`` tokens and gets ``new_lens[b]``
+    more (one each when None).  ``total_tokens`` and ``width`` size the outputs when
+    ``out`` is not given (W columns by default).
+    """
+    dev = cached_lens.device if isinstance(cached_lens, torch.Tensor) else None
+    B = int(cached_lens.shape[0])
+    if out is None:
+        if total_tokens is None:
+            raise ValueError("step_tables needs total_tokens or out")
+        def i32(*shape):
+            return torch.empty(*shape, dtype=_INT32, device=dev)
+        out = StepTables(torch.full((B, req_table.shape[1] if width is None else int(width)), -1, dtype=_INT32,
+                                    device=dev),
+                         i32(B), i32(B + 1), i32(int(total_tokens)), i32(int(total_tokens)), i32(1))
+    page_table, seq_lens, cu_ext, positions, out_loc, pages_taken = out
+    _i32_on(dev, req_table=req_table, cached_lens=cached_lens, free_pages=free_pages, page_table=page_table,
+            seq_lens=seq_lens, cu_ext=cu_ext, positions=positions, out_loc=out_loc, pages_taken=pages_taken)
+    if new_lens is not None:
+        _i32_on(dev, new_lens=new_lens)
+        if new_lens.shape != cached_lens.shape:
+            raise ValueError("new_lens must have one entry per request")
+    if req_rows is not None:
+        _i32_on(dev, req_rows=req_rows)
+        if req_rows.shape != cached_lens.shape:
+            raise ValueError("req_rows must have one entry per request")
+    rows, W = req_table.shape
+    T = positions.shape[0]
+    if (page_table.dim() != 2 or page_table.shape[0] != B or seq_lens.shape[0] != B or cu_ext.shape[0] != B + 1
+            or out_loc.shape[0] != T or pages_taken.numel() != 1):
+        raise ValueError("out must hold [B, width], [B], [B + 1], [T], [T] and [1] entries")
+    if total_tokens is not None and total_tokens != T:
+        raise ValueError("total_tokens must match out")
+    if width is not None and width != page_table.shape[1]:
+        raise ValueError("width must match out")
+    with _on(dev):
+        w = page_table.shape[1]
+        c = _StepOut(page_table.data_ptr(), w, w, seq_lens.data_ptr(), cu_ext.data_ptr(), positions.data_ptr(),
+                     out_loc.data_ptr(), pages_taken.data_ptr(), T)
+        rc = load().msgl_step_tables(
+            num_slots, page_size, req_table.data_ptr(), rows, W, W,
+            None if req_rows is None else req_rows.data_ptr(), cached_lens.data_ptr(),
+            None if new_lens is None else new_lens.data_ptr(), B, free_pages.data_ptr(), free_pages.shape[0],
+            ctypes.byref(c), _ptr(status), _stream(stream))
+    _check(rc, "msgl_step_tables")
+    return out
+
+
+def shared_prefixes(page_table: torch.Tensor, seq_lens: torch.Tensor, page_size: int, max_seq_len: int,
+                    min_shared: int, group_start: Optional[torch.Tensor] = None,
+                    shared_lens: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
+    """Groups of neighbouring requests over the same leading pages (msgl_shared_prefixes).
+
+    Returns (group_start int32 [B], shared_lens int32 [B]), the group arguments of
+    :func:`attn_decode_shared`.
+    """
+    dev = seq_lens.device if isinstance(seq_lens, torch.Tensor) else None
+    B = int(seq_lens.shape[0])
+    group_start = torch.empty_like(seq_lens) if group_start is None else group_start
+    shared_lens = torch.empty_like(seq_lens) if shared_lens is None else shared_lens
+    _i32_on(dev, page_table=page_table, seq_lens=seq_lens, group_start=group_start, shared_lens=shared_lens)
+    if page_table.dim() != 2 or page_table.shape[0] != B or group_start.shape[0] != B or shared_lens.shape[0] != B:
+        raise ValueError("page_table must be [B, width]; seq_lens, group_start and shared_lens [B]")
+    with _on(dev):
+        w = page_table.shape[1]
+        pt = _Pages(page_table.data_ptr(), w, w)
+        rc = load().msgl_shared_prefixes(ctypes.byref(pt), seq_lens.data_ptr(), B, page_size, max_seq_len, min_shared,
+                                         group_start.data_ptr(), shared_lens.data_ptr(), _ptr(status),
+                                         _stream(stream))
+    _check(rc, "msgl_shared_prefixes")
+    return group_start, shared_lens
+
+
+def decode_shared_workspace_size(num_reqs: int, hq: int, hkv: int, max_seq_len: int, head_dim: int = 128) -> int:
+    return int(load().msgl_decode_shared_workspace_size(num_reqs, hq, hkv, head_dim, max_seq_len))
+
+
+def attn_decode_shared(pool: KVPool, q: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
+                       group_start: torch.Tensor, shared_lens: torch.Tensor, max_seq_len: int, scale: float,
+                       out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
+    """:func:`attn_decode` with the keys that a group of requests shares read once for all of them.
+
+    ``group_start[b]`` is the first row of b's group (neighbouring rows) and
+    ``shared_lens[b]`` the leading keys the group has in common, read through the first
+    row's pages (:func:`shared_prefixes` finds both).  Returns (o bf16 [B,Hq,D], lse fp32 [B,Hq]).
+    """
+    _need(q, "q", torch.bfloat16)
+    dev = q.device
+    B, hq, d = q.shape
+    _i32_on(dev, page_table=page_table, seq_lens=seq_lens, group_start=group_start, shared_lens=shared_lens)
+    if (page_table.dim() != 2 or page_table.shape[0] != B or seq_lens.shape[0] != B or group_start.shape[0] != B
+            or shared_lens.shape[0] != B):
+        raise ValueError("page_table must be [B, width]; seq_lens, group_start and shared_lens [B]")
+    if pool.k.device != dev or pool.v.device != dev:
+        raise ValueError("the pool and q must be on the same device")
+    fresh = []                      # allocated here for the current stream
+    if out is None:
+        out = torch.empty_like(q)
+        fresh.append(out)
+    if lse is None:
+        lse = torch.empty(B, hq, dtype=torch.float32, device=dev)
+        fresh.append(lse)
+    _need(out, "out", torch.bfloat16)
+    _need(lse, "lse", torch.float32)
+    if out.shape != q.shape or lse.shape != q.shape[:2]:
+        raise ValueError("out must be [B, Hq, D] and lse [B, Hq]")
+    with _on(dev):
+        if workspace is None:
+            workspace = _workspace(decode_shared_workspace_size(B, hq, pool.num_kv_heads, max_seq_len, d), dev)
+            if workspace is not None:
+                fresh.append(workspace)
+        if stream is not None:
+            for t in fresh:
+                t.record_stream(stream)
+        pc, w = pool.c(), page_table.shape[1]
+        pt = _Pages(page_table.data_ptr(), w, w)
+        rc = load().msgl_attn_decode_shared(
+            ctypes.byref(pc), ctypes.byref(pt), q.data_ptr(), hq, group_start.data_ptr(), shared_lens.data_ptr(),
+            seq_lens.data_ptr(), B, max_seq_len, scale, out.data_ptr(), lse.data_ptr(), _ptr(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream))
+    _check(rc, "msgl_attn_decode_shared")
     return out, lse
 
 
