@@ -401,8 +401,9 @@ MSGL_API msgl_status msgl_shared_prefixes(const msgl_page_table *pages, const in
  *                (or captured graphs) that may overlap need one each
  * Every other argument, the outputs and the status bits are those of
  * msgl_attn_decode.  A row whose group entries break these rules sets
- * MSGL_DEVERR_GROUP and is written as o = 0, lse = -inf; a bad page among the
- * shared keys does that to every row of the group (MSGL_DEVERR_PAGE_RANGE).
+ * MSGL_DEVERR_GROUP and is written as o = 0, lse = -inf, and so may be the rows
+ * of its group behind it; a bad page among the shared keys does that to every
+ * row of the group (MSGL_DEVERR_PAGE_RANGE).
  * The launch shapes depend on host scalars only.
  */
 MSGL_API size_t msgl_decode_shared_workspace_size(int32_t num_reqs, int32_t num_q_heads, int32_t num_kv_heads,

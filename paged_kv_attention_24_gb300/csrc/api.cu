@@ -460,8 +460,8 @@ msgl_status msgl_attn_decode_shared(const msgl_kv_pool *pool, const msgl_page_ta
     msgl_status s = prepare_decode(pool, pages, q, num_q_heads, nullptr, nullptr, nullptr, seq_lens, num_reqs,
                                    max_seq_len, scale, o, lse, workspace, workspace_bytes, status, a.dec, plan);
     if (s || num_reqs == 0) return s;
-    a.group_start = group_start;
-    a.shared_lens = shared_lens;
+    a.dec.group_start = group_start;
+    a.dec.shared_lens = shared_lens;
     a.workspace = workspace;
     cudaError_t e = msgl::launch_decode_shared(a, (cudaStream_t)stream);
     return e == cudaSuccess ? MSGL_OK : cuda_fail(e, "decode_shared launch");

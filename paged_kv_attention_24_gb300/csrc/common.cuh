@@ -44,6 +44,31 @@ __device__ __forceinline__ void report(uint32_t *status, uint32_t bits) {
     if (status) atomicOr(status, bits);
 }
 
+__device__ __forceinline__ int seq_valid(const int32_t *seq_lens, int b, int max_seq) {
+    const int s = __ldg(seq_lens + b);
+    return (s >= 1 && s <= max_seq) ? s : 0;
+}
+
+// Keys per CTA range: an equal share, but at least two tiles, so that a small
+// batch does not scatter into hundreds of tiny partials for the merge to fold.
+constexpr long long kMinKeysPerCta = 32;
+__host__ __device__ __forceinline__ long long keys_per_cta(long long total, long long ctas) {
+    const long long share = (total + ctas - 1) / ctas;
+    return share > kMinKeysPerCta ? share : kMinKeysPerCta;
+}
+
+// Shared-prefix decode: the keys of request b that only it attends, and the first of them.  A
+// request with a neighbour in its group starts behind the shared keys; entries that break the
+// group rules give no keys (the merge reports them).
+__device__ __forceinline__ int own_keys_shared(const int32_t *seq_lens, const int32_t *group_start,
+                                               const int32_t *shared_lens, int num_reqs, int max_seq, int b,
+                                               int &first) {
+    const int s = seq_valid(seq_lens, b, max_seq);
+    const bool grouped = __ldg(group_start + b) != b || (b + 1 < num_reqs && __ldg(group_start + b + 1) == b);
+    first = grouped ? __ldg(shared_lens + b) : 0;
+    return first >= 0 && first <= s ? s - first : 0;
+}
+
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 

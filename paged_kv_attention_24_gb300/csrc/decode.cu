@@ -78,12 +78,8 @@ struct DecodeKernelArgs {
     // written to the pool at new_loc[b]
     const __nv_bfloat16 *k_new, *v_new;
     const int32_t *new_loc;
+    const int32_t *group_start, *shared_lens;   // kShared
 };
-
-__device__ __forceinline__ int seq_valid(const int32_t *seq_lens, int b, int max_seq) {
-    const int s = __ldg(seq_lens + b);
-    return (s >= 1 && s <= max_seq) ? s : 0;
-}
 
 __device__ __forceinline__ long long warp_incl_scan(long long v, int lane) {
 #pragma unroll
@@ -94,12 +90,16 @@ __device__ __forceinline__ long long warp_incl_scan(long long v, int lane) {
     return v;
 }
 
-// Keys per CTA range: an equal share, but at least two tiles, so that a small
-// batch does not scatter into hundreds of tiny partials for the merge to fold.
-constexpr long long kMinKeysPerCta = 2 * kTileKeys;
-__host__ __device__ __forceinline__ long long keys_per_cta(long long total, long long ctas) {
-    const long long share = (total + ctas - 1) / ctas;
-    return share > kMinKeysPerCta ? share : kMinKeysPerCta;
+// Keys of request b that this call's ranges cover, and the first of them: all of a valid
+// request's, or (kShared) those behind the prefix its group shares.
+template <bool kShared>
+__device__ __forceinline__ int own_keys(const DecodeKernelArgs &a, int b, int &first) {
+    if constexpr (kShared) {
+        return own_keys_shared(a.seq_lens, a.group_start, a.shared_lens, a.num_reqs, a.max_seq_len, b, first);
+    } else {
+        first = 0;
+        return seq_valid(a.seq_lens, b, a.max_seq_len);
+    }
 }
 
 // Bytes of one stage: K and V of 16 keys for hg heads.  Box stages hold four swizzled
@@ -115,7 +115,7 @@ size_t decode_smem_bytes(int hg, int stages, bool box) {
            16;
 }
 
-template <bool kBox>
+template <bool kBox, bool kShared>
 __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
     decode_split_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                         const DecodeKernelArgs a) {
@@ -154,7 +154,8 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
         const int B = a.num_reqs;
         long long total = 0;
         for (int c = 0; c < B; c += 32) {
-            const int s = (c + lane < B) ? seq_valid(a.seq_lens, c + lane, a.max_seq_len) : 0;
+            int f;
+            const int s = (c + lane < B) ? own_keys<kShared>(a, c + lane, f) : 0;
             total += s;
         }
 #pragma unroll
@@ -164,6 +165,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
         const long long r0 = per * blockIdx.x;
         const long long r1 = min(total, r0 + per);
         int it = 0;
+        int first_key;
         uint32_t patch_uses = 0;
         bool patch_pending = false;
         bool aborted = false;
@@ -183,7 +185,8 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
             long long base = 0, start_b = 0;
             int b = -1;
             for (int c = 0; c < B && b < 0; c += 32) {
-                const int s = (c + lane < B) ? seq_valid(a.seq_lens, c + lane, a.max_seq_len) : 0;
+                int f;
+                const int s = (c + lane < B) ? own_keys<kShared>(a, c + lane, f) : 0;
                 const long long incl = warp_incl_scan(s, lane);
                 const long long tot = __shfl_sync(0xffffffffu, incl, 31);
                 if (r0 < base + tot) {
@@ -196,11 +199,11 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
             }
             long long pos = r0;
             while (b >= 0 && b < B && pos < r1 && !aborted) {
-                const int sb = seq_valid(a.seq_lens, b, a.max_seq_len);
+                const int sb = own_keys<kShared>(a, b, first_key);
                 const long long end_b = start_b + sb;
                 if (end_b > pos) {
-                    const int lo = (int)(pos - start_b);
-                    const int hi = (int)(min(r1, end_b) - start_b);
+                    const int lo = (int)(pos - start_b) + first_key;
+                    const int hi = (int)(min(r1, end_b) - start_b) + first_key;
                     // page id of key `key` of request b (-1 when the page index is past the
                     // table's width, which then reads as a bad page)
                     auto load_pid = [&](int key) -> int {
@@ -756,6 +759,8 @@ DecodePlan plan_decode(int32_t num_reqs, int32_t hq, int32_t hkv, int32_t max_se
     return p;
 }
 
+int decode_split_ctas(int32_t hq, int32_t hkv) { return decode_launch_shape(hkv, decode_slices(hq / hkv), false).ctas; }
+
 cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, cudaStream_t stream, DecodePhase phase) {
     if (a.num_reqs == 0) return cudaSuccess;
     const int hkv = a.pool.hkv;
@@ -789,11 +794,11 @@ cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, cudaStrea
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(decode_split_kernel<false>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(decode_split_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     kSmemBudget);
+        cudaError_t e = cudaSuccess;
+        for (auto kernel : {decode_split_kernel<false, false>, decode_split_kernel<true, false>,
+                            decode_split_kernel<false, true>, decode_split_kernel<true, true>})
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
@@ -816,14 +821,15 @@ cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, cudaStrea
     k.k_new = a.k_new;
     k.v_new = a.v_new;
     k.new_loc = a.new_loc;
+    k.group_start = a.group_start;
+    k.shared_lens = a.shared_lens;
     (void)plan;
     if (L.smem > (size_t)kSmemBudget) return cudaErrorInvalidValue;
     if (phase != DecodePhase::kMerge) {
         dim3 grid(L.ctas, hkv / L.hg);
-        if (box)
-            decode_split_kernel<true><<<grid, 32 * (L.hg * slices + 1), L.smem, stream>>>(km, vm, k);
-        else
-            decode_split_kernel<false><<<grid, 32 * (L.hg * slices + 1), L.smem, stream>>>(km, vm, k);
+        auto kernel = a.group_start ? (box ? decode_split_kernel<true, true> : decode_split_kernel<false, true>)
+                                    : (box ? decode_split_kernel<true, false> : decode_split_kernel<false, false>);
+        kernel<<<grid, 32 * (L.hg * slices + 1), L.smem, stream>>>(km, vm, k);
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess || phase == DecodePhase::kSplit) return e;
     }

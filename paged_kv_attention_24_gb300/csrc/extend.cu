@@ -645,29 +645,26 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     return fn;
 }
 
-size_t extend_workspace_bytes(int32_t, int32_t, int32_t, int32_t, int32_t) { return 0; }
-
-cudaError_t launch_extend(const ExtendArgs &a, cudaStream_t stream) {
-    if (a.num_reqs == 0 || a.total_tokens == 0 || a.max_ext_len == 0) return cudaSuccess;
-    const int hkv = a.pool.hkv;
-    const int G = a.hq / hkv;
-    const int R = kRows / G;
-    const int q_box_rows = R < a.total_tokens ? R : a.total_tokens;
+cudaError_t encode_attn_maps(const PoolView &pool, const __nv_bfloat16 *q, int32_t hq, int32_t tokens, int32_t rows,
+                             AttnMaps &m) {
+    const int hkv = pool.hkv;
+    const int G = hq / hkv;
+    m.q_box_rows = rows < tokens ? rows : tokens;
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return cudaErrorNotSupported;
-
-    CUtensorMap qm, km, vm;
+    memset(&m.kt, 0, sizeof m.kt);
+    memset(&m.vt, 0, sizeof m.vt);
     {
-        cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)a.hq, (cuuint64_t)a.total_tokens};
-        cuuint64_t strides[2] = {(cuuint64_t)kHeadDim * 2, (cuuint64_t)a.hq * kHeadDim * 2};
-        cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)q_box_rows};
+        cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)hq, (cuuint64_t)tokens};
+        cuuint64_t strides[2] = {(cuuint64_t)kHeadDim * 2, (cuuint64_t)hq * kHeadDim * 2};
+        cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)m.q_box_rows};
         cuuint32_t es[3] = {1, 1, 1};
-        if (enc(&qm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, (void *)a.q, dims, strides, box, es,
+        if (enc(&m.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, (void *)q, dims, strides, box, es,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
     }
-    const long long pool_rows = a.pool.num_slots * hkv;
+    const long long pool_rows = pool.num_slots * hkv;
     if (pool_rows >= INT_MAX) return cudaErrorInvalidValue;
     // 2D view {128 dims, slots x heads} for four-row gathers
     for (int which = 0; which < 2; ++which) {
@@ -675,25 +672,25 @@ cudaError_t launch_extend(const ExtendArgs &a, cudaStream_t stream) {
         cuuint64_t strides[1] = {(cuuint64_t)kHeadDim * 2};
         cuuint32_t box[2] = {64, 1};
         cuuint32_t es[2] = {1, 1};
-        if (enc(which ? &vm : &km, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                (void *)(which ? a.pool.v : a.pool.k), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+        if (enc(which ? &m.v : &m.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                (void *)(which ? pool.v : pool.k), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
     }
     // tiled 3D view {128 dims, Hkv heads, slots}: one box = box_rows slots of one head
-    CUtensorMap ktm, vtm;
-    memset(&ktm, 0, sizeof ktm);
-    memset(&vtm, 0, sizeof vtm);
-    const int page = 1 << a.pool.log2_ps;
+    const int page = 1 << pool.log2_ps;
     const int box_rows = page >= 16 ? (page < kKeys ? page : kKeys) : 0;
     const int v_blocks = box_rows > 0;
+    m.box_rows = box_rows;
+    m.v_blocks = v_blocks;
+    m.oob_row = (int)pool_rows;
     if (box_rows > 0) {
-        cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)hkv, (cuuint64_t)a.pool.num_slots};
+        cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)hkv, (cuuint64_t)pool.num_slots};
         cuuint64_t strides[2] = {(cuuint64_t)kHeadDim * 2, (cuuint64_t)hkv * kHeadDim * 2};
         cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
         cuuint32_t es[3] = {1, 1, 1};
-        if (enc(&ktm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, (void *)a.pool.k, dims, strides, box, es,
+        if (enc(&m.kt, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, (void *)pool.k, dims, strides, box, es,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
@@ -702,21 +699,34 @@ cudaError_t launch_extend(const ExtendArgs &a, cudaStream_t stream) {
             // 16 slots}: one box brings one or two blocks in V's layout.  The view aliases slots
             // across its 3rd and 5th dimensions, so its bounds do not guard the pool: the
             // kernel uses a box only for a page whose slots are all valid.
-            cuuint64_t vdims[5] = {64, (cuuint64_t)hkv, (cuuint64_t)a.pool.num_slots, 2, (cuuint64_t)(kKeys / 16)};
+            cuuint64_t vdims[5] = {64, (cuuint64_t)hkv, (cuuint64_t)pool.num_slots, 2, (cuuint64_t)(kKeys / 16)};
             cuuint64_t vstrides[4] = {(cuuint64_t)kHeadDim * 2, (cuuint64_t)hkv * kHeadDim * 2, 128,
                                       (cuuint64_t)16 * hkv * kHeadDim * 2};
             cuuint32_t vbox[5] = {64, 1, 16, 2, (cuuint32_t)(box_rows > 32 ? 2 : box_rows / 16)};
             cuuint32_t ves[5] = {1, 1, 1, 1, 1};
-            if (enc(&vtm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, (void *)a.pool.v, vdims, vstrides, vbox, ves,
+            if (enc(&m.vt, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, (void *)pool.v, vdims, vstrides, vbox, ves,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
                 return cudaErrorInvalidValue;
-        } else if (enc(&vtm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, (void *)a.pool.v, dims, strides, box, es,
+        } else if (enc(&m.vt, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, (void *)pool.v, dims, strides, box, es,
                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) {
             return cudaErrorInvalidValue;
         }
     }
+    return cudaSuccess;
+}
+
+size_t extend_workspace_bytes(int32_t, int32_t, int32_t, int32_t, int32_t) { return 0; }
+
+cudaError_t launch_extend(const ExtendArgs &a, cudaStream_t stream) {
+    if (a.num_reqs == 0 || a.total_tokens == 0 || a.max_ext_len == 0) return cudaSuccess;
+    const int hkv = a.pool.hkv;
+    const int G = a.hq / hkv;
+    const int R = kRows / G;
+    AttnMaps m;
+    cudaError_t me = encode_attn_maps(a.pool, a.q, a.hq, a.total_tokens, R, m);
+    if (me != cudaSuccess) return me;
     static bool attr_set[64];
     int dev = 0;
     cudaGetDevice(&dev);
@@ -736,13 +746,13 @@ cudaError_t launch_extend(const ExtendArgs &a, cudaStream_t stream) {
     k.hq = a.hq;
     k.group = G;
     k.rows_per_tile = R;
-    k.q_box_rows = q_box_rows;
+    k.q_box_rows = m.q_box_rows;
     k.total_tokens = a.total_tokens;
     k.num_reqs = a.num_reqs;
     k.nblk = (a.max_ext_len + 2 * R - 1) / (2 * R);
-    k.oob_row = (int)pool_rows;
-    k.box_rows = box_rows;
-    k.v_blocks = v_blocks;
+    k.oob_row = m.oob_row;
+    k.box_rows = m.box_rows;
+    k.v_blocks = m.v_blocks;
     k.scale_log2 = a.scale * kLog2e;
     k.o = a.o;
     k.lse = a.lse;
@@ -751,7 +761,7 @@ cudaError_t launch_extend(const ExtendArgs &a, cudaStream_t stream) {
     const long long grid = (long long)k.nblk * hkv * a.num_reqs;
     if (grid >= INT_MAX) return cudaErrorInvalidValue;
     if (!a.pdl) {
-        extend_tc_kernel<<<(unsigned)grid, kThreads, kSmemBytes, stream>>>(qm, km, vm, ktm, vtm, k);
+        extend_tc_kernel<<<(unsigned)grid, kThreads, kSmemBytes, stream>>>(m.q, m.k, m.v, m.kt, m.vt, k);
         return cudaGetLastError();
     }
     cudaLaunchConfig_t cfg = {};
@@ -764,7 +774,7 @@ cudaError_t launch_extend(const ExtendArgs &a, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, extend_tc_kernel, qm, km, vm, ktm, vtm, k);
+    return cudaLaunchKernelEx(&cfg, extend_tc_kernel, m.q, m.k, m.v, m.kt, m.vt, k);
 }
 
 }  // namespace msgl

@@ -38,10 +38,14 @@ struct DecodeArgs {
     uint32_t *status;
     const __nv_bfloat16 *k_new = nullptr, *v_new = nullptr;   // append mode (see msgl_attn_decode_append)
     const int32_t *new_loc = nullptr;
+    // shared mode (kSplit only): row b's keys begin behind those its group shares
+    const int32_t *group_start = nullptr, *shared_lens = nullptr;
 };
 // Which kernels of a decode call to launch: the split (partials per key range), the
 // merge (LSE fold of the partials, launched with programmatic dependent launch), or both.
 enum class DecodePhase { kSplit, kMerge, kBoth };
+// Key ranges (CTAs) of the split kernel for hq / hkv heads.
+int decode_split_ctas(int32_t hq, int32_t hkv);
 cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, cudaStream_t stream,
                           DecodePhase phase = DecodePhase::kBoth);
 
@@ -94,11 +98,23 @@ cudaError_t launch_shared_prefixes(const SharedPrefixesArgs &a, cudaStream_t str
 size_t decode_shared_workspace_bytes(int32_t num_reqs, int32_t hq, int32_t hkv);
 
 struct DecodeSharedArgs {
-    DecodeArgs dec;                 // o, lse, the batch; part_o / part_lse: see the launcher
-    const int32_t *group_start, *shared_lens;
+    DecodeArgs dec;     // group_start and shared_lens among them
     void *workspace;
 };
 cudaError_t launch_decode_shared(const DecodeSharedArgs &a, cudaStream_t stream);
+
+// The tensor maps of an attention kernel with GQA-packed 128-row Q tiles of `rows` tokens and
+// 128-key K/V tiles: q[tokens, hq, 128], four-row gathers from the pools, and (page_size >= 16)
+// boxes of whole page runs.
+struct AttnMaps {
+    CUtensorMap q, k, v, kt, vt;
+    int32_t q_box_rows;   // tokens of one Q box
+    int32_t box_rows;     // slots of one K/V box (0: gathers or 16-byte copies only)
+    int32_t v_blocks;     // V boxes land in blocks of 16 keys
+    int32_t oob_row;      // a gather row past the pool (reads as zeros)
+};
+cudaError_t encode_attn_maps(const PoolView &pool, const __nv_bfloat16 *q, int32_t hq, int32_t tokens, int32_t rows,
+                             AttnMaps &m);
 
 // cuTensorMapEncodeTiled from the driver (NULL if unavailable); looked up once.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
