@@ -9,8 +9,8 @@ raises immediately.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 import threading
 from typing import NamedTuple, Optional
@@ -387,27 +387,42 @@ class StepTables(NamedTuple):
 _INT32 = torch.int32
 
 
-def _i32_on(device, **tensors):
-    """Every tensor is a contiguous int32 tensor on ``device``."""
+def _i32_on(index: int, **tensors):
+    """Raises for the first tensor that is not a contiguous int32 tensor on cuda:``index``."""
     for name, t in tensors.items():
         if not isinstance(t, torch.Tensor):
             raise ValueError(f"{name} must be a CUDA tensor")
         if t.dtype is not _INT32:
             raise ValueError(f"{name} must be {_INT32}, got {t.dtype}")
-        if t.device != device:
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
+        if index < 0 or t.get_device() != index:
+            raise ValueError(f"{name} must be on the same CUDA device as the other tensors, got {t.device}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
 
 
-def _on(device: torch.device):
-    """Makes ``device`` current for a launch (a no-op context when it already is)."""
-    if device.type != "cuda":
-        raise ValueError("the tensors must be CUDA tensors")
-    return torch.cuda.device(device) if device.index != torch.cuda.current_device() else _HERE
+def _all_i32_on(index: int, tensors) -> bool:
+    """:func:`_i32_on` without the names: these calls are short, and so are their checks."""
+    if index < 0:
+        return False
+    for t in tensors:
+        if not isinstance(t, torch.Tensor) or t.dtype is not _INT32 or t.get_device() != index \
+                or not t.is_contiguous():
+            return False
+    return True
 
 
-_HERE = contextlib.nullcontext()
+def _launch(index: int, stream, fn, *args) -> int:
+    """fn(*args, stream) with cuda:``index`` current; the stream is that device's current one by default."""
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return _launch(index, stream, fn, *args)
+    return fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
+
+
+def _device_index(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
 
 
 def step_tables(req_table: torch.Tensor, cached_lens: torch.Tensor, new_lens: Optional[torch.Tensor],
@@ -422,46 +437,51 @@ def step_tables(req_table: torch.Tensor, cached_lens: torch.Tensor, new_lens: Op
     more (one each when None).  ``total_tokens`` and ``width`` size the outputs when
     ``out`` is not given (W columns by default).
     """
-    dev = cached_lens.device if isinstance(cached_lens, torch.Tensor) else None
-    B = int(cached_lens.shape[0])
+    dev = _device_index(cached_lens, "cached_lens")
+    B = cached_lens.shape[0]
     if out is None:
         if total_tokens is None:
             raise ValueError("step_tables needs total_tokens or out")
+
         def i32(*shape):
-            return torch.empty(*shape, dtype=_INT32, device=dev)
-        out = StepTables(torch.full((B, req_table.shape[1] if width is None else int(width)), -1, dtype=_INT32,
-                                    device=dev),
-                         i32(B), i32(B + 1), i32(int(total_tokens)), i32(int(total_tokens)), i32(1))
+            return torch.empty(*shape, dtype=_INT32, device=cached_lens.device)
+        out = StepTables(i32(B, req_table.shape[1] if width is None else int(width)).fill_(-1), i32(B), i32(B + 1),
+                         i32(int(total_tokens)), i32(int(total_tokens)), i32(1))
     page_table, seq_lens, cu_ext, positions, out_loc, pages_taken = out
-    _i32_on(dev, req_table=req_table, cached_lens=cached_lens, free_pages=free_pages, page_table=page_table,
-            seq_lens=seq_lens, cu_ext=cu_ext, positions=positions, out_loc=out_loc, pages_taken=pages_taken)
+    if not _all_i32_on(dev, (req_table, cached_lens, free_pages, page_table, seq_lens, cu_ext, positions, out_loc,
+                             pages_taken)):
+        _i32_on(dev, req_table=req_table, cached_lens=cached_lens, free_pages=free_pages, page_table=page_table,
+                seq_lens=seq_lens, cu_ext=cu_ext, positions=positions, out_loc=out_loc, pages_taken=pages_taken)
+    new_ptr = rows_ptr = None
     if new_lens is not None:
         _i32_on(dev, new_lens=new_lens)
         if new_lens.shape != cached_lens.shape:
             raise ValueError("new_lens must have one entry per request")
+        new_ptr = new_lens.data_ptr()
     if req_rows is not None:
         _i32_on(dev, req_rows=req_rows)
         if req_rows.shape != cached_lens.shape:
             raise ValueError("req_rows must have one entry per request")
+        rows_ptr = req_rows.data_ptr()
+    if req_table.dim() != 2 or page_table.dim() != 2:
+        raise ValueError("req_table and out.page_table must have two dimensions")
     rows, W = req_table.shape
     T = positions.shape[0]
-    if (page_table.dim() != 2 or page_table.shape[0] != B or seq_lens.shape[0] != B or cu_ext.shape[0] != B + 1
-            or out_loc.shape[0] != T or pages_taken.numel() != 1):
+    n, w = page_table.shape
+    if (n != B or seq_lens.shape[0] != B or cu_ext.shape[0] != B + 1 or out_loc.shape[0] != T
+            or pages_taken.numel() != 1):
         raise ValueError("out must hold [B, width], [B], [B + 1], [T], [T] and [1] entries")
     if total_tokens is not None and total_tokens != T:
         raise ValueError("total_tokens must match out")
-    if width is not None and width != page_table.shape[1]:
+    if width is not None and width != w:
         raise ValueError("width must match out")
-    with _on(dev):
-        w = page_table.shape[1]
-        c = _StepOut(page_table.data_ptr(), w, w, seq_lens.data_ptr(), cu_ext.data_ptr(), positions.data_ptr(),
-                     out_loc.data_ptr(), pages_taken.data_ptr(), T)
-        rc = load().msgl_step_tables(
-            num_slots, page_size, req_table.data_ptr(), rows, W, W,
-            None if req_rows is None else req_rows.data_ptr(), cached_lens.data_ptr(),
-            None if new_lens is None else new_lens.data_ptr(), B, free_pages.data_ptr(), free_pages.shape[0],
-            ctypes.byref(c), _ptr(status), _stream(stream))
-    _check(rc, "msgl_step_tables")
+    c = _StepOut(page_table.data_ptr(), w, w, seq_lens.data_ptr(), cu_ext.data_ptr(), positions.data_ptr(),
+                 out_loc.data_ptr(), pages_taken.data_ptr(), T)
+    rc = _launch(dev, stream, load().msgl_step_tables, int(num_slots), int(page_size), req_table.data_ptr(), rows, W, W,
+                 rows_ptr, cached_lens.data_ptr(), new_ptr, B, free_pages.data_ptr(), free_pages.shape[0],
+                 ctypes.byref(c), None if status is None else status.data_ptr())
+    if rc:
+        _check(rc, "msgl_step_tables")
     return out
 
 
@@ -473,23 +493,25 @@ def shared_prefixes(page_table: torch.Tensor, seq_lens: torch.Tensor, page_size:
     Returns (group_start int32 [B], shared_lens int32 [B]), the group arguments of
     :func:`attn_decode_shared`.
     """
-    dev = seq_lens.device if isinstance(seq_lens, torch.Tensor) else None
-    B = int(seq_lens.shape[0])
+    dev = _device_index(seq_lens, "seq_lens")
+    B = seq_lens.shape[0]
     group_start = torch.empty_like(seq_lens) if group_start is None else group_start
     shared_lens = torch.empty_like(seq_lens) if shared_lens is None else shared_lens
-    _i32_on(dev, page_table=page_table, seq_lens=seq_lens, group_start=group_start, shared_lens=shared_lens)
+    if not _all_i32_on(dev, (page_table, seq_lens, group_start, shared_lens)):
+        _i32_on(dev, page_table=page_table, seq_lens=seq_lens, group_start=group_start, shared_lens=shared_lens)
     if page_table.dim() != 2 or page_table.shape[0] != B or group_start.shape[0] != B or shared_lens.shape[0] != B:
         raise ValueError("page_table must be [B, width]; seq_lens, group_start and shared_lens [B]")
-    with _on(dev):
-        w = page_table.shape[1]
-        pt = _Pages(page_table.data_ptr(), w, w)
-        rc = load().msgl_shared_prefixes(ctypes.byref(pt), seq_lens.data_ptr(), B, page_size, max_seq_len, min_shared,
-                                         group_start.data_ptr(), shared_lens.data_ptr(), _ptr(status),
-                                         _stream(stream))
-    _check(rc, "msgl_shared_prefixes")
+    w = page_table.shape[1]
+    pt = _Pages(page_table.data_ptr(), w, w)
+    rc = _launch(dev, stream, load().msgl_shared_prefixes, ctypes.byref(pt), seq_lens.data_ptr(), B, int(page_size),
+                 int(max_seq_len), int(min_shared), group_start.data_ptr(), shared_lens.data_ptr(),
+                 None if status is None else status.data_ptr())
+    if rc:
+        _check(rc, "msgl_shared_prefixes")
     return group_start, shared_lens
 
 
+@functools.lru_cache(maxsize=256)
 def decode_shared_workspace_size(num_reqs: int, hq: int, hkv: int, max_seq_len: int, head_dim: int = 128) -> int:
     return int(load().msgl_decode_shared_workspace_size(num_reqs, hq, hkv, head_dim, max_seq_len))
 
@@ -505,40 +527,49 @@ def attn_decode_shared(pool: KVPool, q: torch.Tensor, page_table: torch.Tensor, 
     row's pages (:func:`shared_prefixes` finds both).  Returns (o bf16 [B,Hq,D], lse fp32 [B,Hq]).
     """
     _need(q, "q", torch.bfloat16)
-    dev = q.device
+    dev = q.get_device()
     B, hq, d = q.shape
-    _i32_on(dev, page_table=page_table, seq_lens=seq_lens, group_start=group_start, shared_lens=shared_lens)
+    if not _all_i32_on(dev, (page_table, seq_lens, group_start, shared_lens)):
+        _i32_on(dev, page_table=page_table, seq_lens=seq_lens, group_start=group_start, shared_lens=shared_lens)
     if (page_table.dim() != 2 or page_table.shape[0] != B or seq_lens.shape[0] != B or group_start.shape[0] != B
             or shared_lens.shape[0] != B):
         raise ValueError("page_table must be [B, width]; seq_lens, group_start and shared_lens [B]")
-    if pool.k.device != dev or pool.v.device != dev:
+    if pool.k.get_device() != dev or pool.v.get_device() != dev:
         raise ValueError("the pool and q must be on the same device")
-    fresh = []                      # allocated here for the current stream
+    fresh = []                      # allocated here, for the current stream
     if out is None:
         out = torch.empty_like(q)
         fresh.append(out)
+    else:
+        _need(out, "out", torch.bfloat16)
     if lse is None:
-        lse = torch.empty(B, hq, dtype=torch.float32, device=dev)
+        lse = torch.empty(B, hq, dtype=torch.float32, device=q.device)
         fresh.append(lse)
-    _need(out, "out", torch.bfloat16)
-    _need(lse, "lse", torch.float32)
-    if out.shape != q.shape or lse.shape != q.shape[:2]:
-        raise ValueError("out must be [B, Hq, D] and lse [B, Hq]")
-    with _on(dev):
-        if workspace is None:
-            workspace = _workspace(decode_shared_workspace_size(B, hq, pool.num_kv_heads, max_seq_len, d), dev)
-            if workspace is not None:
-                fresh.append(workspace)
-        if stream is not None:
-            for t in fresh:
-                t.record_stream(stream)
-        pc, w = pool.c(), page_table.shape[1]
-        pt = _Pages(page_table.data_ptr(), w, w)
-        rc = load().msgl_attn_decode_shared(
-            ctypes.byref(pc), ctypes.byref(pt), q.data_ptr(), hq, group_start.data_ptr(), shared_lens.data_ptr(),
-            seq_lens.data_ptr(), B, max_seq_len, scale, out.data_ptr(), lse.data_ptr(), _ptr(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream))
-    _check(rc, "msgl_attn_decode_shared")
+    else:
+        _need(lse, "lse", torch.float32)
+    if out.shape != q.shape or lse.shape != q.shape[:2] or out.get_device() != dev or lse.get_device() != dev:
+        raise ValueError("out must be [B, Hq, D] and lse [B, Hq], on q's device")
+    ws_bytes = 0
+    if workspace is None:
+        ws_bytes = decode_shared_workspace_size(B, hq, pool.num_kv_heads, int(max_seq_len), d)
+        if ws_bytes:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+            fresh.append(workspace)
+    else:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous and on q's device")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    if stream is not None:
+        for t in fresh:
+            t.record_stream(stream)
+    pc, w = pool.c(), page_table.shape[1]
+    pt = _Pages(page_table.data_ptr(), w, w)
+    rc = _launch(dev, stream, load().msgl_attn_decode_shared, ctypes.byref(pc), ctypes.byref(pt), q.data_ptr(), hq,
+                 group_start.data_ptr(), shared_lens.data_ptr(), seq_lens.data_ptr(), B, int(max_seq_len), float(scale),
+                 out.data_ptr(), lse.data_ptr(), None if workspace is None else workspace.data_ptr(), ws_bytes,
+                 None if status is None else status.data_ptr())
+    if rc:
+        _check(rc, "msgl_attn_decode_shared")
     return out, lse
 
 
