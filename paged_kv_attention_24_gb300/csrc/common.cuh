@@ -69,6 +69,60 @@ __device__ __forceinline__ int own_keys_shared(const int32_t *seq_lens, const in
     return first >= 0 && first <= s ? s - first : 0;
 }
 
+// The rows of a shared-prefix decode.  A group's rows are cut into pairs of Q tiles of pair_rows / 2
+// rows each (the tiles of its tensor-core kernel; pair_rows = 2 * floor(128 / G)).
+struct GroupRows {
+    const int32_t *seq_lens, *group_start, *shared_lens;
+    int32_t num_reqs, max_seq_len, pair_rows;
+};
+
+constexpr int kPrefixTileKeys = 128;
+
+// 128-key tiles of shared keys of the pair that starts at row b; 0 when none does.  Whatever the
+// group arrays hold, the entries used (group_start[b], shared_lens[b]) are in range.
+__device__ __forceinline__ int pair_tiles(const GroupRows &r, int b) {
+    const int lead = __ldg(r.group_start + b), s = __ldg(r.shared_lens + b);
+    const int next = b + 1 < r.num_reqs ? __ldg(r.group_start + b + 1) : -1;
+    const bool starts = lead >= 0 && lead <= b && (b - lead) % r.pair_rows == 0 && (lead != b || next == b);
+    return starts && s > 0 && s <= r.max_seq_len ? (s + kPrefixTileKeys - 1) / kPrefixTileKeys : 0;
+}
+
+// The status bits of row b: its length, the rules of group_start and shared_lens, and that the
+// pair it belongs to can be worked on.  start: its first own key; pair: its pair's first row (-1:
+// no shared keys).
+__device__ __forceinline__ uint32_t group_row_errors(const GroupRows &r, int b, int &seq, int &start, int &pair) {
+    seq = __ldg(r.seq_lens + b);
+    start = 0;
+    pair = -1;
+    if (seq < 1 || seq > r.max_seq_len) return MSGL_DEVERR_LENGTH;
+    const int lead = __ldg(r.group_start + b);
+    if (lead == b && !(b + 1 < r.num_reqs && __ldg(r.group_start + b + 1) == b)) return 0;   // alone
+    const int s = __ldg(r.shared_lens + b);
+    if (lead < 0 || lead > b || s < 0 || s > seq) return MSGL_DEVERR_GROUP;
+    if (lead != b && (__ldg(r.group_start + b - 1) != lead || __ldg(r.group_start + lead) != lead ||
+                      __ldg(r.shared_lens + lead) != s))
+        return MSGL_DEVERR_GROUP;
+    start = s;
+    if (s == 0) return 0;
+    const int half = r.pair_rows / 2;
+    pair = lead + (b - lead) / r.pair_rows * r.pair_rows;
+    if (__ldg(r.group_start + pair) != lead || __ldg(r.shared_lens + pair) != s || pair_tiles(r, pair) == 0)
+        return MSGL_DEVERR_GROUP;
+    if (b - pair >= half && __ldg(r.group_start + pair + half) != lead) return MSGL_DEVERR_GROUP;
+    return 0;
+}
+
+// All keys of row b where the shared ones are read through its group's first row; 0 when its
+// entries are out of range.  from: the first key that is read through its own.
+__device__ __forceinline__ int through_keys(const GroupRows &r, int b, int *from = nullptr) {
+    int split;
+    const int own = own_keys_shared(r.seq_lens, r.group_start, r.shared_lens, r.num_reqs, r.max_seq_len, b, split);
+    const int lead = __ldg(r.group_start + b);
+    if (from) *from = split;
+    const int s = seq_valid(r.seq_lens, b, r.max_seq_len);
+    return lead >= 0 && lead <= b && split >= 0 && own + split == s ? s : 0;
+}
+
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 

@@ -78,7 +78,7 @@ struct DecodeKernelArgs {
     // written to the pool at new_loc[b]
     const __nv_bfloat16 *k_new, *v_new;
     const int32_t *new_loc;
-    const int32_t *group_start, *shared_lens;   // kShared
+    const int32_t *group_start, *shared_lens;   // kOwn, kThrough
 };
 
 __device__ __forceinline__ long long warp_incl_scan(long long v, int lane) {
@@ -90,14 +90,24 @@ __device__ __forceinline__ long long warp_incl_scan(long long v, int lane) {
     return v;
 }
 
-// Keys of request b that this call's ranges cover, and the first of them: all of a valid
-// request's, or (kShared) those behind the prefix its group shares.
-template <bool kShared>
-__device__ __forceinline__ int own_keys(const DecodeKernelArgs &a, int b, int &first) {
-    if constexpr (kShared) {
+// Which keys of a request the ranges cover, and through which page table.
+//   kPlain    all of them, through its own
+//   kOwn      those behind the prefix its group shares, through its own
+//   kThrough  all of them, the shared ones through its group's first request's
+enum KeyMode { kPlain, kOwn, kThrough };
+
+// Request b's keys in the ranges (0: not a valid request), the first of them, and (kThrough)
+// where those of its own page table begin.
+template <KeyMode kMode>
+__device__ __forceinline__ int range_keys(const DecodeKernelArgs &a, int b, int &first, int &split) {
+    first = split = 0;
+    if constexpr (kMode == kOwn) {
         return own_keys_shared(a.seq_lens, a.group_start, a.shared_lens, a.num_reqs, a.max_seq_len, b, first);
+    } else if constexpr (kMode == kThrough) {
+        // (rows whose entries break the group rules are written by the merge; here they only
+        // have to stay in range)
+        return through_keys(GroupRows{a.seq_lens, a.group_start, a.shared_lens, a.num_reqs, a.max_seq_len, 0}, b, &split);
     } else {
-        first = 0;
         return seq_valid(a.seq_lens, b, a.max_seq_len);
     }
 }
@@ -115,7 +125,7 @@ size_t decode_smem_bytes(int hg, int stages, bool box) {
            16;
 }
 
-template <bool kBox, bool kShared>
+template <bool kBox, KeyMode kMode>
 __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
     decode_split_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                         const DecodeKernelArgs a) {
@@ -154,8 +164,8 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
         const int B = a.num_reqs;
         long long total = 0;
         for (int c = 0; c < B; c += 32) {
-            int f;
-            const int s = (c + lane < B) ? own_keys<kShared>(a, c + lane, f) : 0;
+            int f, o;
+            const int s = (c + lane < B) ? range_keys<kMode>(a, c + lane, f, o) : 0;
             total += s;
         }
 #pragma unroll
@@ -165,7 +175,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
         const long long r0 = per * blockIdx.x;
         const long long r1 = min(total, r0 + per);
         int it = 0;
-        int first_key;
+        int first_key, own_from;
         uint32_t patch_uses = 0;
         bool patch_pending = false;
         bool aborted = false;
@@ -185,8 +195,8 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
             long long base = 0, start_b = 0;
             int b = -1;
             for (int c = 0; c < B && b < 0; c += 32) {
-                int f;
-                const int s = (c + lane < B) ? own_keys<kShared>(a, c + lane, f) : 0;
+                int f, o;
+                const int s = (c + lane < B) ? range_keys<kMode>(a, c + lane, f, o) : 0;
                 const long long incl = warp_incl_scan(s, lane);
                 const long long tot = __shfl_sync(0xffffffffu, incl, 31);
                 if (r0 < base + tot) {
@@ -199,30 +209,37 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
             }
             long long pos = r0;
             while (b >= 0 && b < B && pos < r1 && !aborted) {
-                const int sb = own_keys<kShared>(a, b, first_key);
+                const int sb = range_keys<kMode>(a, b, first_key, own_from);
                 const long long end_b = start_b + sb;
                 if (end_b > pos) {
                     const int lo = (int)(pos - start_b) + first_key;
                     const int hi = (int)(min(r1, end_b) - start_b) + first_key;
                     // page id of key `key` of request b (-1 when the page index is past the
                     // table's width, which then reads as a bad page)
+                    const int shared_row = kMode == kThrough ? __ldg(a.group_start + b) : b;
                     auto load_pid = [&](int key) -> int {
                         const int pidx = key >> a.pool.log2_ps;
-                        return pidx < a.pages.width ? __ldg(a.pages.ids + (int64_t)b * a.pages.stride + pidx) : -1;
+                        const int row = kMode == kThrough && key < own_from ? shared_row : b;
+                        return pidx < a.pages.width ? __ldg(a.pages.ids + (int64_t)row * a.pages.stride + pidx) : -1;
                     };
                     if constexpr (kBox) {
+                        // kThrough: the keys below own_from and those from there on may sit on different
+                        // pages of the same 16 keys, so they are tiled apart
+                        const int mid = kMode == kThrough ? min(max(own_from, lo), hi) : hi;
+                        for (int part = mid > lo ? 0 : 1; part < (mid < hi ? 2 : 1) && !aborted; ++part) {
+                        const int plo = part ? mid : lo, phi = part ? hi : mid;
                         // 16-key tiles aligned to 16 keys (each inside one page); keys outside
                         // [lo, hi) are loaded with the tile and masked.  Lane 0 does the work,
                         // with the next tile's page id looked up one tile ahead.
-                        const int tlo = lo & ~(kTileKeys - 1);
-                        int pid_cur = lane == 0 ? load_pid(tlo) : -1;
-                        for (int t0 = tlo; t0 < hi; t0 += kTileKeys) {
+                        const int tlo = plo & ~(kTileKeys - 1);
+                        int pid_cur = lane == 0 ? load_pid(max(tlo, plo)) : -1;
+                        for (int t0 = tlo; t0 < phi; t0 += kTileKeys) {
                             const int stage = it % S, round = it / S;
                             const int t1 = t0 + kTileKeys;
-                            const int pid_next = (lane == 0 && t1 < hi) ? load_pid(t1) : -1;
+                            const int pid_next = (lane == 0 && t1 < phi) ? load_pid(t1) : -1;
                             if (*abort_flag || !stage_wait_empty(stage, round)) { aborted = true; break; }
                             if (lane == 0) {
-                                const int klo = max(lo, t0) - t0, khi = min(hi, t1) - t0;
+                                const int klo = max(plo, t0) - t0, khi = min(phi, t1) - t0;
                                 const uint32_t keys = ((1u << khi) - 1u) & ~((1u << klo) - 1u);
                                 const bool ok = pid_cur >= 0 && pid_cur < a.pool.num_pages;
                                 const uint32_t full_bar = ptx::smem_u32(full + stage);
@@ -230,7 +247,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
                                 md.b = b;
                                 md.slot = b + (int)blockIdx.x;
                                 md.n = khi - klo;
-                                md.flags = (t0 == tlo ? kFirst : 0) | (t1 >= hi ? kLast : 0) | (ok ? 0 : kBad);
+                                md.flags = (t0 == tlo && plo == lo ? kFirst : 0) | (t1 >= phi && phi == hi ? kLast : 0) | (ok ? 0 : kBad);
                                 md.mask = ok ? keys : 0u;
                                 if (!ok) report(a.status, MSGL_DEVERR_PAGE_RANGE);
                                 // append mode: the tile holding the current token lands on the
@@ -300,6 +317,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
                             pid_cur = pid_next;
                             __syncwarp();
                             ++it;
+                        }
                         }
                         pos = min(r1, end_b);
                         start_b = end_b;
@@ -396,6 +414,12 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
             for (int k = first; k < it; ++k)
                 ptx::mbar_wait(ptx::smem_u32(full + (k % S)), (k / S) & 1, 200000000LL);
             if (patch_pending) ptx::mbar_wait(ptx::smem_u32(patch), patch_uses & 1, 200000000LL);
+        }
+        // kOwn runs behind the shared-prefix kernel by programmatic dependent launch: the last CTA
+        // ends after that kernel has, so what comes behind this grid sees both kernels' partials.
+        if constexpr (kMode == kOwn) {
+            if (lane == 0 && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1)
+                asm volatile("griddepcontrol.wait;" ::: "memory");
         }
     } else if (warp < n_consumers) {
         // ----------------------------------------------------------- consumers
@@ -579,19 +603,27 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
 // partials at a time so their loads overlap.
 constexpr int kMergeMaxParts = kMaxDecodeCtas + 1;
 
+template <bool kThrough>
 __global__ void __launch_bounds__(256) decode_merge_kernel(
-    const int32_t *__restrict__ seq_lens, int32_t num_reqs, int32_t max_seq_len, int32_t hq,
-    int32_t num_ctas, const float *__restrict__ part_o, const float *__restrict__ part_lse,
+    const GroupRows rows, int32_t hq, int32_t num_ctas, const float *__restrict__ part_o, const float *__restrict__ part_lse,
     __nv_bfloat16 *__restrict__ o, float *__restrict__ lse, uint32_t *status) {
     __shared__ long long s_start, s_total;
     __shared__ float s_w[8][kMergeMaxParts];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = blockIdx.y;
+    // a request's keys in the split's ranges; the split's count of them, rule for rule
+    auto keys_of = [&](int i) -> int {
+        if constexpr (kThrough) {
+            return through_keys(rows, i);
+        } else {
+            return seq_valid(rows.seq_lens, i, rows.max_seq_len);
+        }
+    };
     if (warp == 0) {
         long long total = 0, before = 0;
-        for (int c = 0; c < num_reqs; c += 32) {
+        for (int c = 0; c < rows.num_reqs; c += 32) {
             const int idx = c + lane;
-            const int s = idx < num_reqs ? seq_valid(seq_lens, idx, max_seq_len) : 0;
+            const int s = idx < rows.num_reqs ? keys_of(idx) : 0;
             total += s;
             if (idx < b) before += s;
         }
@@ -605,11 +637,16 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(
     __syncthreads();
     const int h = blockIdx.x * 8 + warp;
     if (h >= hq) return;
-    const int sb = seq_valid(seq_lens, b, max_seq_len);
+    const int sb = keys_of(b);
     const long long row = (long long)b * hq + h;
     __nv_bfloat16 *orow = o + row * kHeadDim + lane * 4;
-    if (sb == 0) {
-        if (blockIdx.x == 0 && warp == 0 && lane == 0) report(status, MSGL_DEVERR_LENGTH);
+    uint32_t err = sb == 0 ? MSGL_DEVERR_LENGTH : 0;
+    if constexpr (kThrough) {
+        int seq, start, pair;
+        err = group_row_errors(rows, b, seq, start, pair);
+    }
+    if (err) {
+        if (blockIdx.x == 0 && warp == 0 && lane == 0) report(status, err);
         *reinterpret_cast<uint2 *>(orow) = make_uint2(0u, 0u);
         if (lane == 0) lse[row] = -INFINITY;
         return;
@@ -795,8 +832,9 @@ cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, cudaStrea
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64 || !attr_set[dev]) {
         cudaError_t e = cudaSuccess;
-        for (auto kernel : {decode_split_kernel<false, false>, decode_split_kernel<true, false>,
-                            decode_split_kernel<false, true>, decode_split_kernel<true, true>})
+        for (auto kernel : {decode_split_kernel<false, kPlain>, decode_split_kernel<true, kPlain>,
+                            decode_split_kernel<false, kOwn>, decode_split_kernel<true, kOwn>,
+                            decode_split_kernel<false, kThrough>, decode_split_kernel<true, kThrough>})
             if (e == cudaSuccess)
                 e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget);
         if (e != cudaSuccess) return e;
@@ -827,9 +865,25 @@ cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, cudaStrea
     if (L.smem > (size_t)kSmemBudget) return cudaErrorInvalidValue;
     if (phase != DecodePhase::kMerge) {
         dim3 grid(L.ctas, hkv / L.hg);
-        auto kernel = a.group_start ? (box ? decode_split_kernel<true, true> : decode_split_kernel<false, true>)
-                                    : (box ? decode_split_kernel<true, false> : decode_split_kernel<false, false>);
-        kernel<<<grid, 32 * (L.hg * slices + 1), L.smem, stream>>>(km, vm, k);
+        auto kernel = !a.group_start ? (box ? decode_split_kernel<true, kPlain> : decode_split_kernel<false, kPlain>)
+                      : a.own_only   ? (box ? decode_split_kernel<true, kOwn> : decode_split_kernel<false, kOwn>)
+                                     : (box ? decode_split_kernel<true, kThrough> : decode_split_kernel<false, kThrough>);
+        const int threads = 32 * (L.hg * slices + 1);
+        if (a.own_only) {
+            // behind the shared-prefix kernel: SMs that it leaves free start at once
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = grid;
+            cfg.blockDim = dim3(threads);
+            cfg.dynamicSmemBytes = L.smem;
+            cfg.stream = stream;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[0].val.programmaticStreamSerializationAllowed = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            return cudaLaunchKernelEx(&cfg, kernel, km, vm, k);
+        }
+        kernel<<<grid, threads, L.smem, stream>>>(km, vm, k);
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess || phase == DecodePhase::kSplit) return e;
     }
@@ -845,9 +899,9 @@ cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, cudaStrea
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode_merge_kernel, a.seq_lens, a.num_reqs, a.max_seq_len, a.hq,
-                              L.ctas, (const float *)a.part_o, (const float *)a.part_lse, a.o, a.lse,
-                              a.status);
+    const GroupRows rows{a.seq_lens, a.group_start, a.shared_lens, a.num_reqs, a.max_seq_len, a.group_rows};
+    return cudaLaunchKernelEx(&cfg, a.group_start ? decode_merge_kernel<true> : decode_merge_kernel<false>, rows, a.hq,
+                              L.ctas, (const float *)a.part_o, (const float *)a.part_lse, a.o, a.lse, a.status);
 }
 
 }  // namespace msgl

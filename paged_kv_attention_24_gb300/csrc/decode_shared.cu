@@ -16,9 +16,10 @@
 //   (and from L2 after the first) instead of once per request.
 // * The merge joins all pieces of a row.
 //
-// The prefix kernel is launched behind the split with programmatic dependent
-// launch: its CTAs take each SM as the split's range there ends, and its last
-// CTA outwaits the split, so that the merge behind it finds both done.
+// The split kernel is launched behind the prefix kernel with programmatic
+// dependent launch: its CTAs take each SM as the prefix kernel's share there
+// ends (at once where there is none), and its last CTA outwaits the prefix
+// kernel, so that the merge behind it finds both done.
 #include <cuda.h>
 #include <limits.h>
 #include <math.h>
@@ -37,24 +38,9 @@ namespace {
 // CTA c takes units [c * per, (c + 1) * per).
 
 constexpr int kRows = 128;                 // rows per Q tile (MMA M)
-constexpr int kKeys = 128;                 // keys per K/V tile
+constexpr int kKeys = kPrefixTileKeys;     // keys per K/V tile
 constexpr int kMaxPrefixCtas = 160;        // bound on the grid, sizes the workspace
 constexpr int kMinUnits = 2;               // K/V tiles per CTA at least: fewer pieces to join
-
-struct Rows {
-    const int32_t *seq_lens, *group_start, *shared_lens;
-    int32_t num_reqs, max_seq_len;
-    int32_t pair_rows;                     // 2R
-};
-
-// K/V tiles of the pair that starts at row b; 0 when none does.  Whatever the group arrays
-// hold, the entries used (group_start[b], shared_lens[b]) are in range.
-__device__ __forceinline__ int pair_tiles(const Rows &r, int b) {
-    const int lead = __ldg(r.group_start + b), s = __ldg(r.shared_lens + b);
-    const int next = b + 1 < r.num_reqs ? __ldg(r.group_start + b + 1) : -1;
-    const bool starts = lead >= 0 && lead <= b && (b - lead) % r.pair_rows == 0 && (lead != b || next == b);
-    return starts && s > 0 && s <= r.max_seq_len ? (s + kKeys - 1) / kKeys : 0;
-}
 
 __host__ __device__ __forceinline__ long long units_per_cta(long long units, long long ctas) {
     const long long share = (units + ctas - 1) / ctas;
@@ -64,7 +50,7 @@ __host__ __device__ __forceinline__ long long units_per_cta(long long units, lon
 // ------------------------------------------------------------- prefix kernel
 constexpr int kStages = 2;                 // K tiles in flight
 constexpr int kVStages = 3;                // V tiles in flight (V is needed later than K)
-constexpr int kThreads = 512;              // 16 warps: 8 that load and issue, 8 of softmax
+constexpr int kThreads = 384;              // 12 warps: 4 that load and issue, 8 of softmax
 constexpr uint32_t kHalf = 16384;          // 128 rows x 128 bytes (64 bf16)
 constexpr uint32_t kTile = 2 * kHalf;      // 128 x 128 bf16
 constexpr uint32_t kVBlock = 4096, kVHalf = 2048;   // V in blocks of 16 keys (see extend.cu)
@@ -105,7 +91,7 @@ struct RowPlan {
 struct PrefixArgs {
     PoolView pool;
     PageView pages;
-    Rows rows;
+    GroupRows rows;
     int32_t hq, group, rows_per_tile, q_box_rows, oob_row, box_rows, v_blocks, split_ctas;
     float scale_log2;
     float *o, *lse;            // [num_reqs, hq, 128], [num_reqs, hq]: pieces that begin at the first key
@@ -123,29 +109,7 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, vol
     return false;
 }
 
-// The rules of group_start and shared_lens for row b, and that its pair was worked on.
-__device__ __forceinline__ uint32_t row_errors(const Rows &r, int rows_per_tile, int b, int &seq, int &start, int &pair) {
-    seq = __ldg(r.seq_lens + b);
-    start = 0;
-    pair = -1;
-    if (seq < 1 || seq > r.max_seq_len) return MSGL_DEVERR_LENGTH;
-    const int lead = __ldg(r.group_start + b);
-    if (lead == b && !(b + 1 < r.num_reqs && __ldg(r.group_start + b + 1) == b)) return 0;   // alone
-    const int s = __ldg(r.shared_lens + b);
-    if (lead < 0 || lead > b || s < 0 || s > seq) return MSGL_DEVERR_GROUP;
-    if (lead != b && (__ldg(r.group_start + b - 1) != lead || __ldg(r.group_start + lead) != lead ||
-                      __ldg(r.shared_lens + lead) != s))
-        return MSGL_DEVERR_GROUP;
-    start = s;
-    if (s == 0) return 0;
-    pair = lead + (b - lead) / r.pair_rows * r.pair_rows;
-    if (__ldg(r.group_start + pair) != lead || __ldg(r.shared_lens + pair) != s || pair_tiles(r, pair) == 0)
-        return MSGL_DEVERR_GROUP;
-    if (b - pair >= rows_per_tile && __ldg(r.group_start + pair + rows_per_tile) != lead) return MSGL_DEVERR_GROUP;
-    return 0;
-}
-
-// Exclusive prefix sum of v over the block; total gets the sum.  scratch: 16 entries.  (A
+// Exclusive prefix sum of v over the block; total gets the sum.  scratch: 12 entries.  (A
 // named barrier, because the two halves of the block run it from different places.)
 __device__ __forceinline__ void block_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
 
@@ -178,11 +142,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const __grid_constant__ CUtensorMap vt_map, const PrefixArgs a) {
     extern __shared__ uint8_t smem_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // The grid may start before the split kernel in front of it has finished.  The last CTA
-    // waits for that kernel, so this grid does not complete before it: what runs next sees
-    // the partials of both.
+    // the split kernel may take the SMs that this grid leaves free
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const bool last_cta = blockIdx.x == gridDim.x - 1;
-    if (last_cta && threadIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 
     const uint32_t raw = ptx::smem_u32(smem_raw);
     const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -200,13 +162,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long *scratch = reinterpret_cast<long long *>(smem + kOffX);   // of the block's scans, between windows
 
     // ---- this CTA's units: thread i counts rows [i * k, (i + 1) * k)
-    const Rows &rows = a.rows;
+    const GroupRows &rows = a.rows;
     const int hkv = a.pool.hkv;
     const int R = a.rows_per_tile, G = a.group;
     const int per_thread = (rows.num_reqs + kThreads - 1) / kThreads;
     const int b0 = min(rows.num_reqs, (int)threadIdx.x * per_thread);
     const int b1 = min(rows.num_reqs, b0 + per_thread);
-    int tiles0 = 0;   // of row b0, the only one in a batch of up to 512
+    int tiles0 = 0;   // of row b0, the only one in a batch of up to 384
     long long mine = 0;
     for (int b = b0; b < b1; ++b) {
         const int t = pair_tiles(rows, b);
@@ -241,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int n = own_keys_shared(rows.seq_lens, rows.group_start, rows.shared_lens, rows.num_reqs,
                                           rows.max_seq_len, b, first);
             RowPlan p;
-            p.err = (int32_t)row_errors(rows, R, b, seq, start, pair);
+            p.err = (int32_t)group_row_errors(rows, b, seq, start, pair);
             p.start = start;
             p.in_pair = pair >= 0 ? b - pair : -1;
             const long long c0 = own / split_per;
@@ -352,9 +314,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     long long w0 = u0;
 
-    // Registers: 256 x 80 + 256 x 176 = 512 x 128, what the block was launched with.
-    if (warp < 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    // Registers: 128 x 104 + 256 x 200 = 384 x 168, what the block was launched with.
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         // MMA issuer: stages and parities of the next K, V and P to use
         uint32_t ks = 0, kpar = 0, vs = 0, vpar = 0, ppar0 = 0, ppar1 = 0;
         while (w0 < u1) {
@@ -365,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const Seg p = segs[e];
                 const int g = p.g2 >> 1, n = p.n;
                 const bool two = p.g2 & 1;
-                if (warp == 6) {
+                if (warp == 2) {
                     // ---------------------------------------------------- Q loader
                     if (seg > 0)
                         ok = __all_sync(0xffffffffu, wait_or_abort(bar(kQEmpty), (seg & 1) ^ 1, abort_flag, a.status));
@@ -377,7 +339,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 ptx::tma_load_3d(sbase + kOffQ + t * kTile + h * kHalf, &q_map, 64 * h, g * G,
                                                  p.row + t * R, bar(kQFull));
                     }
-                } else if (warp == 0 || warp == 3 || (lsu && (warp == 2 || warp == 4 || warp == 5))) {
+                }
+                if (warp == 0 || warp == 3 || (lsu && warp == 2 && ok)) {
                     // ---------------------------------------------------- K/V loaders
                     const bool is_v = warp >= 3;
                     // Pool rows of tile j's keys, four consecutive keys per lane.  A key past the
@@ -408,23 +371,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     int64_t slot0;
                     if (lsu) {
                         // 16-byte cp.async copies into the SWIZZLE_128B K-major layout (see extend.cu).
-                        // One warp per stage: warps 0 and 2 copy K, warps 3 to 5 V, tile gi (counted
-                        // over the segments) by the warp of stage gi mod stages.
+                        // Warps 0 and 2 copy the K tiles of one stage each, warp 3 the V tiles; a
+                        // tile is handed over when the warp's next one has been issued, so that the
+                        // copies of two overlap.
                         const __nv_bfloat16 *pool = is_v ? a.pool.v : a.pool.k;
-                        const uint32_t step = is_v ? kVStages : kStages;
-                        const uint32_t st = is_v ? warp - 3 : warp >> 1;
-                        const int first = (int)((st + step - tile0 % step) % step);
-                        const uint32_t empty = bar((is_v ? kVEmpty : kKEmpty) + st);
-                        const uint32_t dst = sbase + (is_v ? kOffV : kOffK) + st * kTile;
+                        const int step = is_v ? 1 : 2;
+                        const int first = is_v ? 0 : (int)((tile0 ^ (warp == 2 ? 1u : 0u)) & 1u);
                         const int hi = lane >> 4, c = lane & 15;
                         const uint32_t col_off = (uint32_t)(c >> 3) * kHalf;
-                        int next[4] = {0, 0, 0, 0};
                         if (first < n) key_rows(first, kr, all_ok, slot0);
-                        for (int j = first; j < n && ok; j += (int)step) {
-                            const uint32_t round = (tile0 + j) / step;
-                            ok = __all_sync(0xffffffffu, !*abort_flag && wait_or_abort(empty, (round & 1) ^ 1,
-                                                                                       abort_flag, a.status));
+                        for (int j = first; j < n && ok; j += step) {
+                            const uint32_t gi = tile0 + j;
+                            const uint32_t st = is_v ? gi % kVStages : gi % kStages;
+                            const uint32_t round = is_v ? gi / kVStages : gi / kStages;
+                            ok = __all_sync(0xffffffffu, !*abort_flag &&
+                                                             wait_or_abort(bar((is_v ? kVEmpty : kKEmpty) + st),
+                                                                           (round & 1) ^ 1, abort_flag, a.status));
                             if (!ok) break;
+                            const uint32_t dst = sbase + (is_v ? kOffV : kOffK) + st * kTile;
 #pragma unroll 16
                             for (int i = 0; i < 64; ++i) {
                                 const int r0 = __shfl_sync(0xffffffffu, (i & 1) ? kr[2] : kr[0], i >> 1);
@@ -437,13 +401,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     pool + (valid ? (int64_t)row * kHeadDim + c * 8 : 0), valid ? 16u : 0u);
                             }
                             ptx::cp_async_commit();
-                            if (j + (int)step < n) key_rows(j + (int)step, next, all_ok, slot0);
-                            ptx::cp_async_wait_all();
-                            ptx::fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0) ptx::mbar_arrive(bar((is_v ? kVFull : kKFull) + st));
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) kr[x] = next[x];
+                            if (j + step < n) key_rows(j + step, kr, all_ok, slot0);
+                            if (is_v && j > 0) {
+                                // all but the newest copies have landed: hand over the tile before
+                                asm volatile("cp.async.wait_group 1;" ::: "memory");
+                                ptx::fence_proxy_async_smem();
+                                __syncwarp();
+                                if (lane == 0) ptx::mbar_arrive(bar(kVFull + (gi + kVStages - 1) % kVStages));
+                            }
+                            if (!is_v || j == n - 1) {
+                                ptx::cp_async_wait_all();
+                                ptx::fence_proxy_async_smem();
+                                __syncwarp();
+                                if (lane == 0) ptx::mbar_arrive(bar((is_v ? kVFull : kKFull) + st));
+                            }
                         }
                     } else {
                         // TMA: a page that is a contiguous run of pool rows and holds shared keys only
@@ -610,9 +581,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (*abort_flag) w0 = u1;   // (set before the barrier by the role that gave up: all agree)
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         // -------------------------------------------------------------- softmax
-        const int t = (warp - 8) >> 2;                 // stream of this warpgroup
+        const int t = (warp - 4) >> 2;                 // stream of this warpgroup
         const int quad = warp & 3;
         const int r = quad * 32 + lane;                // TMEM lane = tile row
         const int tok_l = r / G, jh = r - tok_l * G;
@@ -950,6 +921,8 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Merge
     if (lane == 0) a.lse[row] = none ? -INFINITY : M + logf(L);
 }
 
+constexpr long long kThroughBytes = 64ll << 20;
+
 // Where each part of the workspace begins.
 struct Layout {
     size_t pre_o, pre_lse, cont_o, cont_lse, plan, total;
@@ -975,8 +948,15 @@ size_t decode_shared_workspace_bytes(int32_t num_reqs, int32_t hq, int32_t hkv) 
 }
 
 cudaError_t launch_decode_shared(const DecodeSharedArgs &a, cudaStream_t stream) {
-    const DecodeArgs &d = a.dec;
+    DecodeArgs d = a.dec;
     const int hkv = d.pool.hkv, G = d.hq / hkv, R = kRows / G;
+    const DecodePlan plan = plan_decode(d.num_reqs, d.hq, hkv, d.max_seq_len);
+    d.group_rows = 2 * R;
+    // Small batches: with at most kThroughBytes of K/V behind the page tables, reading a shared key
+    // once for each request costs less than the kernel that reads it once for all.
+    if (d.num_reqs == 1 || (long long)d.num_reqs * d.max_seq_len * hkv * kHeadDim * 4 <= kThroughBytes)
+        return launch_decode(d, plan, stream);
+    d.own_only = true;
     const Layout l = layout_of(d.num_reqs, d.hq, hkv);
     char *ws = static_cast<char *>(a.workspace);
     AttnMaps m;
@@ -990,13 +970,11 @@ cudaError_t launch_decode_shared(const DecodeSharedArgs &a, cudaStream_t stream)
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
-    e = launch_decode(d, plan_decode(d.num_reqs, d.hq, hkv, d.max_seq_len), stream, DecodePhase::kSplit);
-    if (e != cudaSuccess) return e;
 
     PrefixArgs p{};
     p.pool = d.pool;
     p.pages = d.pages;
-    p.rows = Rows{d.seq_lens, d.group_start, d.shared_lens, d.num_reqs, d.max_seq_len, 2 * R};
+    p.rows = GroupRows{d.seq_lens, d.group_start, d.shared_lens, d.num_reqs, d.max_seq_len, 2 * R};
     p.hq = d.hq;
     p.group = G;
     p.rows_per_tile = R;
@@ -1014,17 +992,10 @@ cudaError_t launch_decode_shared(const DecodeSharedArgs &a, cudaStream_t stream)
     p.split_ctas = decode_split_ctas(d.hq, hkv);
     p.status = d.status;
     const int ctas = sm_count() < kMaxPrefixCtas ? sm_count() : kMaxPrefixCtas;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cfg.stream = stream;
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
-    e = cudaLaunchKernelEx(&cfg, prefix_tc_kernel, m.q, m.k, m.v, m.kt, m.vt, p);
+    prefix_tc_kernel<<<ctas, kThreads, kSmemBytes, stream>>>(m.q, m.k, m.v, m.kt, m.vt, p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    e = launch_decode(d, plan, stream, DecodePhase::kSplit);
     if (e != cudaSuccess) return e;
 
     MergeArgs g{};
@@ -1042,6 +1013,13 @@ cudaError_t launch_decode_shared(const DecodeSharedArgs &a, cudaStream_t stream)
     g.o = d.o;
     g.lse = d.lse;
     g.status = d.status;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.stream = stream;
     cfg.gridDim = dim3((d.hq + kMergeThreads / 32 - 1) / (kMergeThreads / 32), d.num_reqs);
     cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = 0;

@@ -38,8 +38,12 @@ struct DecodeArgs {
     uint32_t *status;
     const __nv_bfloat16 *k_new = nullptr, *v_new = nullptr;   // append mode (see msgl_attn_decode_append)
     const int32_t *new_loc = nullptr;
-    // shared mode (kSplit only): row b's keys begin behind those its group shares
+    // groups over shared prefixes (see msgl_attn_decode_shared): shared keys are read through
+    // the group's first row, or (own_only, split phase) left to another kernel, which the split
+    // is then launched behind
     const int32_t *group_start = nullptr, *shared_lens = nullptr;
+    int32_t group_rows = 0;   // rows of a pair of Q tiles
+    bool own_only = false;
 };
 // Which kernels of a decode call to launch: the split (partials per key range), the
 // merge (LSE fold of the partials, launched with programmatic dependent launch), or both.

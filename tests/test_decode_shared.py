@@ -3,7 +3,14 @@
 The tolerances are those of every other parity test (tests/parity.py): P is
 rounded to bf16 before the PV product (2^-8 of |v| under the softmax) and o
 once at the end; a joined prefix adds fp32 arithmetic only.
+
+A call whose bound on the keys (requests x max_seq_len) is small reads shared
+keys once a request instead of running the kernel that reads them once for
+all; max_seq_len is only a bound, so a large one takes any batch to the other
+side, and every case here runs on both.
 """
+import dataclasses
+
 import pytest
 import torch
 
@@ -20,15 +27,22 @@ def run(g, **kw):
                                   g.scale, **kw)
 
 
+FAR = 1 << 22
+
+
+def bounded(w, far):
+    return dataclasses.replace(w, max_seq=FAR) if far else w
+
+
 def check(w, what=""):
-    g = w.cuda()
-    status = ops.new_status()
-    o, lse = run(g, status=status)
-    assert ops.read_status(status) == 0
     ref_o, ref_l, a = w.reference()
-    assert_o_close(o, ref_o, what, abs_ref=a)
-    assert_lse_close(lse, ref_l, what)
-    return g, o, lse
+    for far in (False, True):
+        g = bounded(w, far).cuda()
+        status = ops.new_status()
+        o, lse = run(g, status=status)
+        assert ops.read_status(status) == 0
+        assert_o_close(o, ref_o, f"{what} {far}", abs_ref=a)
+        assert_lse_close(lse, ref_l, f"{what} {far}")
 
 
 def rising(n, lo, step):
@@ -79,13 +93,15 @@ def test_many_groups_split_over_the_grid():
     check(shared_batch.make(16, 8, 16, groups, seed=7))
 
 
-def test_prefix_is_read_through_the_first_row():
+@pytest.mark.parametrize("ps", [1, 16])
+@pytest.mark.parametrize("far", [False, True])
+def test_prefix_is_read_through_the_first_row(far, ps):
     """The rows behind a group's first may hold anything in the shared columns."""
-    w = shared_batch.make(40, 8, 16, [(320, [1, 50, 3]), (160, [20, 7])], seed=8)
+    w = shared_batch.make(40, 8, ps, [(320, [1, 50, 3]), (160, [20, 7])], seed=8)
     ref_o, ref_l, a = w.reference()
     for b in (1, 2, 4):
-        w.table[b, :int(w.shared[b]) // 16] = -1
-    o, lse = run(w.cuda())
+        w.table[b, :int(w.shared[b]) // ps] = -1
+    o, lse = run(bounded(w, far).cuda())
     assert_o_close(o, ref_o, abs_ref=a)
     assert_lse_close(lse, ref_l)
 
@@ -103,16 +119,18 @@ def test_large_scores_and_scales():
     check(w)
 
 
-def test_repeats_are_bit_identical():
+@pytest.mark.parametrize("far", [False, True])
+def test_repeats_are_bit_identical(far):
     w = shared_batch.make(64, 8, 64, [(1600, rising(20, 1, 13)), (640, [5, 6])], seed=11)
-    g = w.cuda()
+    g = bounded(w, far).cuda()
     a, b = run(g), run(g)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
-def test_dirty_workspace_and_outputs():
+@pytest.mark.parametrize("far", [False, True])
+def test_dirty_workspace_and_outputs(far):
     w = shared_batch.make(40, 8, 16, [(600, [1, 90, 3]), (0, [7])], seed=12)
-    g = w.cuda()
+    g = bounded(w, far).cuda()
     clean = run(g)
     n = ops.decode_shared_workspace_size(4, 40, 8, g.max_seq)
     ws = torch.full((n // 4,), float("nan"), device="cuda").view(torch.uint8)
@@ -121,13 +139,13 @@ def test_dirty_workspace_and_outputs():
     assert torch.equal(out, clean[0]) and torch.equal(lse, clean[1])
 
 
-def test_rows_in_error_leave_the_others_alone():
+@pytest.mark.parametrize("far", [False, True])
+def test_rows_in_error_leave_the_others_alone(far):
     w = shared_batch.make(16, 8, 16, [(160, [1, 40, 9]), (0, [20]), (320, [3, 4, 5, 6])], seed=13)
-    g = w.cuda()
+    g = bounded(w, far).cuda()
     good = run(g)
 
     def expect(bits, rows, maybe=(), **changed):
-        import dataclasses
         status = ops.new_status()
         o, lse = run(dataclasses.replace(g, **changed), status=status)
         assert ops.read_status(status) == bits
@@ -160,9 +178,10 @@ def test_rows_in_error_leave_the_others_alone():
     expect(ops.DEVERR_GROUP, {3}, first=edit(g.first, (3, 7)))
 
 
-def test_narrow_table_is_a_page_error():
+@pytest.mark.parametrize("far", [False, True])
+def test_narrow_table_is_a_page_error(far):
     w = shared_batch.make(16, 8, 16, [(160, [1, 40]), (0, [20])], seed=14)
-    g = w.cuda()
+    g = bounded(w, far).cuda()
     g.table = g.table[:, :9].contiguous()      # the prefix needs 10
     status = ops.new_status()
     o, lse = run(g, status=status)
@@ -170,9 +189,10 @@ def test_narrow_table_is_a_page_error():
     assert torch.all(o[:2] == 0) and torch.isfinite(lse[2]).all()
 
 
-def test_nan_query_rows_stay_their_own():
+@pytest.mark.parametrize("far", [False, True])
+def test_nan_query_rows_stay_their_own(far):
     w = shared_batch.make(64, 8, 64, [(500, rising(18, 1, 3))], seed=15)
-    g = w.cuda()
+    g = bounded(w, far).cuda()
     good = run(g)
     g.q[3] = float("nan")
     g.q[9, 5] = float("inf")
@@ -181,12 +201,13 @@ def test_nan_query_rows_stay_their_own():
     assert torch.equal(o[keep], good[0][keep]) and torch.equal(lse[keep], good[1][keep])
 
 
-def test_captured_replays_with_new_lengths_and_groups():
+@pytest.mark.parametrize("far", [False, True])
+def test_captured_replays_with_new_lengths_and_groups(far):
     """One captured call serves steps with other groups and lengths."""
     a = shared_batch.make(40, 8, 16, [(320, [1, 50, 3, 9]), (160, [20, 7])], seed=16, width=64)
     b = shared_batch.make(40, 8, 16, [(0, [100]), (600, [1, 2]), (48, [30, 31, 32])], seed=17, width=64)
     slots = max(a.k.shape[0], b.k.shape[0])
-    max_seq = max(a.max_seq, b.max_seq)
+    max_seq = FAR if far else max(a.max_seq, b.max_seq)
     k = torch.zeros(slots, 8, 128, dtype=torch.bfloat16, device="cuda")
     v = torch.zeros_like(k)
     live = a.cuda()
@@ -218,10 +239,11 @@ def test_captured_replays_with_new_lengths_and_groups():
         assert_lse_close(lse, ref_l)
 
 
-def test_on_another_stream():
+@pytest.mark.parametrize("far", [False, True])
+def test_on_another_stream(far):
     w = shared_batch.make(16, 8, 1, [(900, rising(8, 1, 11))], seed=18)
     ref_o, ref_l, a = w.reference()
-    g = w.cuda()
+    g = bounded(w, far).cuda()
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     o, lse = run(g, stream=s)
