@@ -40,7 +40,7 @@ namespace {
 constexpr int kRows = 128;                 // rows per Q tile (MMA M)
 constexpr int kKeys = kPrefixTileKeys;     // keys per K/V tile
 constexpr int kMaxPrefixCtas = 160;        // bound on the grid, sizes the workspace
-constexpr int kMinUnits = 2;               // K/V tiles per CTA at least: fewer pieces to join
+constexpr int kMinUnits = 4;               // K/V tiles per CTA at least: fewer pieces to join
 
 __host__ __device__ __forceinline__ long long units_per_cta(long long units, long long ctas) {
     const long long share = (units + ctas - 1) / ctas;
@@ -50,7 +50,8 @@ __host__ __device__ __forceinline__ long long units_per_cta(long long units, lon
 // ------------------------------------------------------------- prefix kernel
 constexpr int kStages = 2;                 // K tiles in flight
 constexpr int kVStages = 3;                // V tiles in flight (V is needed later than K)
-constexpr int kThreads = 384;              // 12 warps: 4 that load and issue, 8 of softmax
+constexpr int kLoadWarps = 4;              // they load and issue; 8 softmax warps behind them
+constexpr int kThreads = 32 * (kLoadWarps + 8);
 constexpr uint32_t kHalf = 16384;          // 128 rows x 128 bytes (64 bf16)
 constexpr uint32_t kTile = 2 * kHalf;      // 128 x 128 bf16
 constexpr uint32_t kVBlock = 4096, kVHalf = 2048;   // V in blocks of 16 keys (see extend.cu)
@@ -109,10 +110,8 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, vol
     return false;
 }
 
-// Exclusive prefix sum of v over the block; total gets the sum.  scratch: 12 entries.  (A
-// named barrier, because the two halves of the block run it from different places.)
-__device__ __forceinline__ void block_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
-
+// Exclusive prefix sum of v over the block; total gets the sum.  scratch: an entry per warp, not
+// used again before the block's next barrier.
 __device__ __forceinline__ long long block_excl_scan(long long v, long long *scratch, long long &total) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     long long x = v;
@@ -122,7 +121,7 @@ __device__ __forceinline__ long long block_excl_scan(long long v, long long *scr
         if (lane >= o) x += u;
     }
     if (lane == 31) scratch[warp] = x;
-    block_sync();
+    __syncthreads();
     // lane w of every warp takes warp w's sum
     const long long mine = lane < kThreads / 32 ? scratch[lane] : 0;
     long long before = lane < warp ? mine : 0;
@@ -132,9 +131,73 @@ __device__ __forceinline__ long long block_excl_scan(long long v, long long *scr
         before += __shfl_xor_sync(0xffffffffu, before, o);
         total += __shfl_xor_sync(0xffffffffu, total, o);
     }
-    block_sync();
     return before + x - v;
 }
+
+// The two halves of the block run to this one from different places.
+__device__ __forceinline__ void block_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+
+// A warp's walk over a CTA's units, segment by segment.
+struct Walk {
+    int32_t row, tiles;       // the current pair's first row and key tiles
+    int32_t off;              // next unit, counted from the pair's first
+    long long left;           // units to go
+
+    // The first pair at or behind row r; tiles = 0 when there is none.
+    __device__ __forceinline__ void find(const GroupRows &rows, int r) {
+        const int lane = threadIdx.x & 31;
+        tiles = 0;
+        for (; r < rows.num_reqs; r += 32) {
+            const int t = r + lane < rows.num_reqs ? pair_tiles(rows, r + lane) : 0;
+            const unsigned m = __ballot_sync(0xffffffffu, t > 0);
+            if (m) {
+                row = r + __ffs(m) - 1;
+                tiles = __shfl_sync(0xffffffffu, t, __ffs(m) - 1);
+                return;
+            }
+        }
+    }
+    // Stands on unit `at + skip`, where `at` units lie before row r.
+    __device__ __forceinline__ void start(const GroupRows &rows, int hkv, int r, long long skip, long long units) {
+        left = units;
+        for (find(rows, r); tiles > 0; find(rows, row + 1)) {
+            const long long here = (long long)tiles * hkv;
+            if (skip < here) break;
+            skip -= here;
+        }
+        off = (int)skip;
+    }
+    __device__ __forceinline__ bool next(const GroupRows &rows, int hkv, Seg &s) {
+        if (left <= 0) return false;
+        if (off == tiles * hkv) {
+            find(rows, row + 1);
+            off = 0;
+        }
+        if (tiles == 0) return false;   // (the lengths changed under the call)
+        s.row = row;
+        s.lead = __ldg(rows.group_start + row);
+        s.shared = __ldg(rows.shared_lens + row);
+        const int second = row + rows.pair_rows / 2;
+        const int two = second < rows.num_reqs && __ldg(rows.group_start + second) == s.lead;
+        const int g = off / tiles;
+        s.g2 = 2 * g + two;
+        s.t0 = off - g * tiles;
+        s.n = (int)min((long long)(tiles - s.t0), left);
+        off += s.n;
+        left -= s.n;
+        return true;
+    }
+    // The next segments, as many as fit.
+    __device__ __forceinline__ int fill(const GroupRows &rows, int hkv, Seg *segs) {
+        int n = 0;
+        Seg s;
+        while (n < kMaxSegs && next(rows, hkv, s)) {
+            if ((threadIdx.x & 31) == 0) segs[n] = s;
+            ++n;
+        }
+        return n;
+    }
+};
 
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
@@ -154,73 +217,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + kOffBar + 8 * kNumBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffBar + 8 * kNumBars + 4);
     volatile int *num_segs = reinterpret_cast<volatile int *>(smem + kOffBar + 8 * kNumBars + 8);
-    volatile long long *window_end = reinterpret_cast<volatile long long *>(smem + kOffBar + 8 * kNumBars + 16);
-    volatile int *bad_seg = reinterpret_cast<volatile int *>(smem + kOffBar + 8 * kNumBars + 24);   // [kBadRing]
-    static_assert(8 * kNumBars + 24 + 4 * kBadRing <= 256, "barrier block");
+    volatile int *more_segs = reinterpret_cast<volatile int *>(smem + kOffBar + 8 * kNumBars + 12);
+    volatile int *bad_seg = reinterpret_cast<volatile int *>(smem + kOffBar + 8 * kNumBars + 16);   // [kBadRing]
+    Walk *saved_walk = reinterpret_cast<Walk *>(smem + kOffBar + 8 * kNumBars + 16 + 4 * kBadRing);
+    static_assert(8 * kNumBars + 16 + 4 * kBadRing + sizeof(Walk) <= 256, "barrier block");
     Seg *segs = reinterpret_cast<Seg *>(smem + kOffSegs);
     float2 *xchg = reinterpret_cast<float2 *>(smem + kOffX);            // (m, l) of stream 1's rows
-    long long *scratch = reinterpret_cast<long long *>(smem + kOffX);   // of the block's scans, between windows
+    long long *scratch = reinterpret_cast<long long *>(smem + kOffX);   // of the block's scans
 
-    // ---- this CTA's units: thread i counts rows [i * k, (i + 1) * k)
     const GroupRows &rows = a.rows;
     const int hkv = a.pool.hkv;
     const int R = a.rows_per_tile, G = a.group;
+
+    // ---- this CTA's units: thread i counts rows [i * k, (i + 1) * k)
     const int per_thread = (rows.num_reqs + kThreads - 1) / kThreads;
     const int b0 = min(rows.num_reqs, (int)threadIdx.x * per_thread);
     const int b1 = min(rows.num_reqs, b0 + per_thread);
-    int tiles0 = 0;   // of row b0, the only one in a batch of up to 384
     long long mine = 0;
-    for (int b = b0; b < b1; ++b) {
-        const int t = pair_tiles(rows, b);
-        if (b == b0) tiles0 = t;
-        mine += t;
-    }
-    auto tiles_of = [&](int b) -> int { return b == b0 ? tiles0 : pair_tiles(rows, b); };
-    long long units;
-    const long long before = block_excl_scan(mine, scratch, units) * hkv;
-    units *= hkv;
-    const long long per = units_per_cta(units, gridDim.x);
-    const long long u0 = per * blockIdx.x, u1 = min(units, u0 + per);
+    for (int b = b0; b < b1; ++b) mine += pair_tiles(rows, b);
 
-    if (last_cta) {
-        // the rows' places among the pieces, for the merge
-        long long own = 0, own_all;
-        int first;
-        for (int b = b0; b < b1; ++b)
-            own += own_keys_shared(rows.seq_lens, rows.group_start, rows.shared_lens, rows.num_reqs, rows.max_seq_len,
-                                   b, first);
-        own = block_excl_scan(own, scratch, own_all);
-        const long long split_per = keys_per_cta(own_all, a.split_ctas);
-        long long unit = before;
-        for (int b = b0; b < b1; ++b) {
-            a.plan[b].unit = unit;
-            unit += (long long)tiles_of(b) * hkv;
-        }
-        __threadfence_block();
-        block_sync();
-        for (int b = b0; b < b1; ++b) {
-            int seq, start, pair;
-            const int n = own_keys_shared(rows.seq_lens, rows.group_start, rows.shared_lens, rows.num_reqs,
-                                          rows.max_seq_len, b, first);
-            RowPlan p;
-            p.err = (int32_t)group_row_errors(rows, b, seq, start, pair);
-            p.start = start;
-            p.in_pair = pair >= 0 ? b - pair : -1;
-            const long long c0 = own / split_per;
-            p.own_slot = b + c0;
-            p.own_pieces = n > 0 ? (int)((own + n - 1) / split_per - c0) + 1 : 0;
-            a.plan[b].err = p.err;
-            a.plan[b].start = p.start;
-            a.plan[b].in_pair = p.in_pair;
-            a.plan[b].own_pieces = p.own_pieces;
-            a.plan[b].own_slot = p.own_slot;
-            a.plan[b].unit_of_pair = pair >= 0 ? __ldcg(&a.plan[pair].unit) : 0;
-            own += n;
-        }
-        if (threadIdx.x == 0) *a.per_cta = per;
-    }
-    if (u0 >= u1) return;
-
+    // (while those loads are on their way)
     if (threadIdx.x == 0) {
         ptx::mbar_init(bar(kQFull), 1);
         ptx::mbar_init(bar(kQEmpty), 1);
@@ -259,51 +275,65 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         ptx::fence_proxy_async_smem();
     }
-    ptx::tc_fence_before();
 
-    // ---- windows: the next segments of this CTA's units from w0 on, at most kMaxSegs at a time.
-    // Returns their count and moves w0 behind them.
-    auto next_window = [&](long long &w0) -> int {
-        long long at = before, n_all;
-        int n = 0;
+    long long units;
+    const long long before = block_excl_scan(mine, scratch, units) * hkv;
+    units *= hkv;
+    const long long per = units_per_cta(units, gridDim.x);
+    const long long u0 = per * blockIdx.x, u1 = min(units, u0 + per);
+    // the warp whose rows hold the first unit lays out the first segments
+    const unsigned owner = __ballot_sync(0xffffffffu, u0 < u1 && before <= u0 && u0 < before + mine * hkv);
+    if (owner) {
+        const int l = __ffs(owner) - 1;
+        Walk walk;
+        walk.start(rows, hkv, __shfl_sync(0xffffffffu, b0, l), __shfl_sync(0xffffffffu, u0 - before, l), u1 - u0);
+        const int n = walk.fill(rows, hkv, segs);
+        if (lane == 0) {
+            *num_segs = n;
+            *more_segs = walk.left > 0 && n > 0;
+            *saved_walk = walk;
+        }
+    }
+
+    if (last_cta) {
+        // the rows' places among the pieces, for the merge
+        long long own = 0, own_all;
+        int first;
+        for (int b = b0; b < b1; ++b)
+            own += own_keys_shared(rows.seq_lens, rows.group_start, rows.shared_lens, rows.num_reqs, rows.max_seq_len,
+                                   b, first);
+        own = block_excl_scan(own, scratch + kThreads / 32, own_all);
+        const long long split_per = keys_per_cta(own_all, a.split_ctas);
+        long long unit = before;
         for (int b = b0; b < b1; ++b) {
-            const int tiles = tiles_of(b);
-            const long long here = (long long)tiles * hkv;
-            if (here > 0 && at + here > w0 && at < u1) {
-                const int lo = (int)(max(w0, at) - at), hi = (int)(min(u1, at + here) - at);
-                n += (hi - 1) / tiles - lo / tiles + 1;
-            }
-            at += here;
+            a.plan[b].unit = unit;
+            unit += (long long)pair_tiles(rows, b) * hkv;
         }
-        long long idx = block_excl_scan(n, scratch, n_all);
-        at = before;
-        for (int b = b0; b < b1 && n > 0 && idx < kMaxSegs; ++b) {
-            const int tiles = tiles_of(b);
-            const long long here = (long long)tiles * hkv;
-            if (here > 0 && at + here > w0 && at < u1) {
-                const int lo = (int)(max(w0, at) - at), hi = (int)(min(u1, at + here) - at);
-                Seg s;
-                s.row = b;
-                s.lead = __ldg(rows.group_start + b);
-                s.shared = __ldg(rows.shared_lens + b);
-                const int two = b + R < rows.num_reqs && __ldg(rows.group_start + b + R) == s.lead;
-                for (int g = lo / tiles; g <= (hi - 1) / tiles && idx < kMaxSegs; ++g) {
-                    s.g2 = 2 * g + two;
-                    s.t0 = max(lo - g * tiles, 0);
-                    s.n = min(hi - g * tiles, tiles) - s.t0;
-                    segs[idx] = s;
-                    if (idx == kMaxSegs - 1 || idx == n_all - 1) *window_end = at + (long long)g * tiles + s.t0 + s.n;
-                    ++idx;
-                }
-            }
-            at += here;
+        __threadfence_block();
+        __syncthreads();
+        for (int b = b0; b < b1; ++b) {
+            int seq, start, pair;
+            const int n = own_keys_shared(rows.seq_lens, rows.group_start, rows.shared_lens, rows.num_reqs,
+                                          rows.max_seq_len, b, first);
+            const long long c0 = own / split_per;
+            a.plan[b].err = (int32_t)group_row_errors(rows, b, seq, start, pair);
+            a.plan[b].start = start;
+            a.plan[b].in_pair = pair >= 0 ? b - pair : -1;
+            a.plan[b].own_pieces = n > 0 ? (int)((own + n - 1) / split_per - c0) + 1 : 0;
+            a.plan[b].own_slot = b + c0;
+            a.plan[b].unit_of_pair = pair >= 0 ? __ldcg(&a.plan[pair].unit) : 0;
+            own += n;
         }
-        if (threadIdx.x == 0) *num_segs = (int)min(n_all, (long long)kMaxSegs);
-        block_sync();
-        const int count = *num_segs;
-        w0 = count > 0 ? *window_end : u1;
-        return count;
-    };
+        if (threadIdx.x == 0) *a.per_cta = per;
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    if (u0 >= u1) {
+        if (warp == 2) ptx::tc_dealloc(tmem, 512);
+        return;
+    }
 
     // Every role counts segments and K/V tiles the same way.  A segment with rows in both Q
     // tiles runs them as two streams over the same key tiles; one with rows in the first only
@@ -312,17 +342,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool lsu = a.box_rows == 0;
     uint32_t seg = 0, tile0 = 0;
     bool ok = true;
-    long long w0 = u0;
+    // When a list of segments is used up, warp 0 lays out the next; both halves of the block meet
+    // before it and after.  False at the end, or when a role gave up (all agree: its flag was set
+    // before the barrier).
+    auto next_segs = [&]() -> bool {
+        if (!*more_segs) return false;
+        block_sync();
+        if (*abort_flag) return false;
+        if (warp == 0) {
+            Walk walk = *saved_walk;
+            const int n = walk.fill(rows, hkv, segs);
+            __syncwarp();
+            if (lane == 0) {
+                *num_segs = n;
+                *more_segs = walk.left > 0 && n > 0;
+                *saved_walk = walk;
+            }
+        }
+        block_sync();
+        return true;
+    };
 
-    // Registers: 128 x 104 + 256 x 200 = 384 x 168, what the block was launched with.
-    if (warp < 4) {
+    // (registers: 128 x 104 + 256 x 200 = 384 x 168, what the block was launched with)
+    if (warp < kLoadWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         // MMA issuer: stages and parities of the next K, V and P to use
         uint32_t ks = 0, kpar = 0, vs = 0, vpar = 0, ppar0 = 0, ppar1 = 0;
-        while (w0 < u1) {
-            const int count = next_window(w0);
-            ptx::tc_fence_after();
-            const uint32_t tmem = *tmem_slot;
+        do {
+            const int count = *num_segs;
             for (int e = 0; e < count && ok; ++e) {
                 const Seg p = segs[e];
                 const int g = p.g2 >> 1, n = p.n;
@@ -577,23 +624,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tile0 += n;
                 ++seg;
             }
-            block_sync();
-            if (*abort_flag) w0 = u1;   // (set before the barrier by the role that gave up: all agree)
-        }
+        } while (next_segs());
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         // -------------------------------------------------------------- softmax
-        const int t = (warp - 4) >> 2;                 // stream of this warpgroup
+        const int t = (warp - kLoadWarps) >> 2;                 // stream of this warpgroup
         const int quad = warp & 3;
         const int r = quad * 32 + lane;                // TMEM lane = tile row
         const int tok_l = r / G, jh = r - tok_l * G;
         uint32_t spar = 0, opar = 0, xpar = 0;         // parities of the next S, O and exchange
-        while (w0 < u1) {
-            const int count = next_window(w0);
-            ptx::tc_fence_after();
-            const uint32_t lane_base = *tmem_slot + ((uint32_t)(quad * 32) << 16);
-            const uint32_t tS = lane_base + 128 * t;
-            const uint32_t tO = lane_base + 256 + 128 * t;
+        const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
+        const uint32_t tS = lane_base + 128 * t;
+        const uint32_t tO = lane_base + 256 + 128 * t;
+        do {
+            const int count = *num_segs;
             for (int e = 0; e < count && ok; ++e) {
                 const bool two = segs[e].g2 & 1;
                 const int n = segs[e].n, step = two ? 1 : 2;
@@ -774,9 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tile0 += n;
                 ++seg;
             }
-            block_sync();
-            if (*abort_flag) w0 = u1;   // (set before the barrier by the role that gave up: all agree)
-        }
+        } while (next_segs());
     }
 
     if (warp == 1 && lane == 0) {
@@ -794,7 +836,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (warp == 2) {
         ptx::tc_fence_after();
-        ptx::tc_dealloc(*tmem_slot, 512);
+        ptx::tc_dealloc(tmem, 512);
     }
 }
 
