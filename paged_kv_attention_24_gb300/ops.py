@@ -454,13 +454,13 @@ def step_tables(req_table: torch.Tensor, cached_lens: torch.Tensor, new_lens: Op
                 seq_lens=seq_lens, cu_ext=cu_ext, positions=positions, out_loc=out_loc, pages_taken=pages_taken)
     new_ptr = rows_ptr = None
     if new_lens is not None:
-        _i32_on(dev, new_lens=new_lens)
-        if new_lens.shape != cached_lens.shape:
+        if not _all_i32_on(dev, (new_lens,)) or new_lens.numel() != B:
+            _i32_on(dev, new_lens=new_lens)
             raise ValueError("new_lens must have one entry per request")
         new_ptr = new_lens.data_ptr()
     if req_rows is not None:
-        _i32_on(dev, req_rows=req_rows)
-        if req_rows.shape != cached_lens.shape:
+        if not _all_i32_on(dev, (req_rows,)) or req_rows.numel() != B:
+            _i32_on(dev, req_rows=req_rows)
             raise ValueError("req_rows must have one entry per request")
         rows_ptr = req_rows.data_ptr()
     if req_table.dim() != 2 or page_table.dim() != 2:
@@ -477,7 +477,7 @@ def step_tables(req_table: torch.Tensor, cached_lens: torch.Tensor, new_lens: Op
         raise ValueError("width must match out")
     c = _StepOut(page_table.data_ptr(), w, w, seq_lens.data_ptr(), cu_ext.data_ptr(), positions.data_ptr(),
                  out_loc.data_ptr(), pages_taken.data_ptr(), T)
-    rc = _launch(dev, stream, load().msgl_step_tables, int(num_slots), int(page_size), req_table.data_ptr(), rows, W, W,
+    rc = _launch(dev, stream, (_lib or load()).msgl_step_tables, int(num_slots), int(page_size), req_table.data_ptr(), rows, W, W,
                  rows_ptr, cached_lens.data_ptr(), new_ptr, B, free_pages.data_ptr(), free_pages.shape[0],
                  ctypes.byref(c), None if status is None else status.data_ptr())
     if rc:
@@ -503,7 +503,7 @@ def shared_prefixes(page_table: torch.Tensor, seq_lens: torch.Tensor, page_size:
         raise ValueError("page_table must be [B, width]; seq_lens, group_start and shared_lens [B]")
     w = page_table.shape[1]
     pt = _Pages(page_table.data_ptr(), w, w)
-    rc = _launch(dev, stream, load().msgl_shared_prefixes, ctypes.byref(pt), seq_lens.data_ptr(), B, int(page_size),
+    rc = _launch(dev, stream, (_lib or load()).msgl_shared_prefixes, ctypes.byref(pt), seq_lens.data_ptr(), B, int(page_size),
                  int(max_seq_len), int(min_shared), group_start.data_ptr(), shared_lens.data_ptr(),
                  None if status is None else status.data_ptr())
     if rc:
@@ -536,38 +536,52 @@ def attn_decode_shared(pool: KVPool, q: torch.Tensor, page_table: torch.Tensor, 
         raise ValueError("page_table must be [B, width]; seq_lens, group_start and shared_lens [B]")
     if pool.k.get_device() != dev or pool.v.get_device() != dev:
         raise ValueError("the pool and q must be on the same device")
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return attn_decode_shared(pool, q, page_table, seq_lens, group_start, shared_lens, max_seq_len, scale,
+                                      out, lse, workspace, status, stream)
+    raw_stream = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     fresh = []                      # allocated here, for the current stream
     if out is None:
         out = torch.empty_like(q)
         fresh.append(out)
     else:
         _need(out, "out", torch.bfloat16)
+        if out.shape != q.shape or out.get_device() != dev:
+            raise ValueError("out must be [B, Hq, D], on q's device")
     if lse is None:
-        lse = torch.empty(B, hq, dtype=torch.float32, device=q.device)
+        lse = torch.empty((B, hq), dtype=torch.float32, device=q.device)
         fresh.append(lse)
     else:
         _need(lse, "lse", torch.float32)
-    if out.shape != q.shape or lse.shape != q.shape[:2] or out.get_device() != dev or lse.get_device() != dev:
-        raise ValueError("out must be [B, Hq, D] and lse [B, Hq], on q's device")
-    ws_bytes = 0
-    if workspace is None:
-        ws_bytes = decode_shared_workspace_size(B, hq, pool.num_kv_heads, int(max_seq_len), d)
-        if ws_bytes:
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-            fresh.append(workspace)
-    else:
-        if workspace.get_device() != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous and on q's device")
-        ws_bytes = workspace.numel() * workspace.element_size()
+        if lse.shape != q.shape[:2] or lse.get_device() != dev:
+            raise ValueError("lse must be [B, Hq], on q's device")
     if stream is not None:
         for t in fresh:
             t.record_stream(stream)
-    pc, w = pool.c(), page_table.shape[1]
-    pt = _Pages(page_table.data_ptr(), w, w)
-    rc = _launch(dev, stream, load().msgl_attn_decode_shared, ctypes.byref(pc), ctypes.byref(pt), q.data_ptr(), hq,
-                 group_start.data_ptr(), shared_lens.data_ptr(), seq_lens.data_ptr(), B, int(max_seq_len), float(scale),
-                 out.data_ptr(), lse.data_ptr(), None if workspace is None else workspace.data_ptr(), ws_bytes,
-                 None if status is None else status.data_ptr())
+    scratch = None
+    if workspace is None:
+        # Straight from the caching allocator, in the stream's order, and back to it below (what
+        # torch.cuda.caching_allocator_alloc does): a tensor that nobody sees would cost as much
+        # host time as the launches.
+        ws_ptr = None
+        ws_bytes = decode_shared_workspace_size(B, hq, pool.num_kv_heads, int(max_seq_len), d)
+        if ws_bytes:
+            ws_ptr = scratch = torch._C._cuda_cudaCachingAllocator_raw_alloc(ws_bytes, raw_stream)
+    else:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous and on q's device")
+        ws_bytes, ws_ptr = workspace.numel() * workspace.element_size(), workspace.data_ptr()
+    try:
+        pc, w = pool.c(), page_table.shape[1]
+        pt = _Pages(page_table.data_ptr(), w, w)
+        rc = (_lib or load()).msgl_attn_decode_shared(
+            ctypes.byref(pc), ctypes.byref(pt), q.data_ptr(), hq, group_start.data_ptr(), shared_lens.data_ptr(),
+            seq_lens.data_ptr(), B, int(max_seq_len), float(scale), out.data_ptr(), lse.data_ptr(), ws_ptr, ws_bytes,
+            None if status is None else status.data_ptr(), raw_stream)
+    finally:
+        if scratch is not None:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(scratch)
     if rc:
         _check(rc, "msgl_attn_decode_shared")
     return out, lse
