@@ -1,8 +1,10 @@
-"""Compile libmsgl_attn.so in-tree with nvcc for sm_103a.
+"""Compile libmsgl_attn.so in-tree with nvcc for sm_103a, and its native Python binding.
 
 One translation unit per .cu file, compiled in parallel, then linked into
-``paged_kv_attention_24_gb300/_build/libmsgl_attn.so``.  The build is
-skipped when the library is newer than every source and header.
+``paged_kv_attention_24_gb300/_build/libmsgl_attn.so``.  The binding
+(``csrc/python/binding.cpp``, against the installed torch's headers) becomes
+``_build/_msgl_binding.so`` beside it.  The build is skipped when both are newer
+than every source and header.
 """
 from __future__ import annotations
 
@@ -17,6 +19,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libmsgl_attn.so")
+BINDING_SRC = os.path.join(CSRC, "python", "binding.cpp")
+BINDING = os.path.join(BUILD, "_msgl_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                      "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr",
@@ -36,13 +40,13 @@ def sources() -> list[str]:
 
 def _deps() -> list[str]:
     return (sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-            + glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)])
+            + glob.glob(os.path.join(ROOT, "include", "*.h")) + [BINDING_SRC, os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
@@ -64,14 +68,42 @@ def build(verbose: bool = False, force: bool = False, extra_flags: list[str] | N
             print(r.stdout + r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(sources()), os.cpu_count() or 1))) as ex:
+    def compile_binding() -> str:
+        import sysconfig
+
+        import torch
+        t = os.path.dirname(os.path.abspath(torch.__file__))
+        cuda = os.path.dirname(os.path.dirname(os.path.realpath(cc)))
+        obj = os.path.join(BUILD, "binding.o")
+        cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden", "-c", BINDING_SRC, "-o", obj,
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(t, "include"),
+               "-isystem", os.path.join(t, "include", "torch", "csrc", "api", "include"),
+               "-isystem", os.path.join(cuda, "include")]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+        return obj
+
+    with cf.ThreadPoolExecutor(max_workers=max(2, min(len(sources()) + 1, os.cpu_count() or 1))) as ex:
+        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, sources()))
+        binding_obj = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [cc] + ARCH + ["-shared", "-o", tmp] + objs + ["-lcuda"]
+    cmd = [cc] + ARCH + ["-shared", "-Xlinker", "-soname=libmsgl_attn.so", "-o", tmp] + objs + ["-lcuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    import torch
+    torch_lib = os.path.join(os.path.dirname(os.path.abspath(torch.__file__)), "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, binding_obj, LIB, "-L", torch_lib, "-ltorch_python", "-ltorch", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
     return LIB
 
 

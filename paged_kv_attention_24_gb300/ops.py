@@ -5,12 +5,14 @@ scalars, calls the C ABI declared in ``include/msgl_attn.h`` with the
 current CUDA stream, and turns a non-OK status into :class:`MsglError`.
 All compute happens in the library's CUDA kernels; there is no CPU or
 PyTorch fallback, and calling anything here without the built library
-raises immediately.
+raises immediately.  The step tables, the prefix groups and the
+shared-prefix decode, whose kernels are short, marshal their arguments in
+a native extension over the same C ABI (``csrc/python/binding.cpp``).
 """
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.util
 import os
 import threading
 from typing import NamedTuple, Optional
@@ -19,6 +21,7 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_build", "libmsgl_attn.so")
+BINDING_PATH = os.path.join(_PKG, "_build", "_msgl_binding.so")
 
 MSGL_OK = 0
 STATUS_NAMES = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "CUDA", 4: "OUT_OF_RANGE",
@@ -384,45 +387,25 @@ class StepTables(NamedTuple):
     pages_taken: torch.Tensor  # [1]      how many of the free pages are now in use
 
 
-_INT32 = torch.int32
+_native = None
 
 
-def _i32_on(index: int, **tensors):
-    """Raises for the first tensor that is not a contiguous int32 tensor on cuda:``index``."""
-    for name, t in tensors.items():
-        if not isinstance(t, torch.Tensor):
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if t.dtype is not _INT32:
-            raise ValueError(f"{name} must be {_INT32}, got {t.dtype}")
-        if index < 0 or t.get_device() != index:
-            raise ValueError(f"{name} must be on the same CUDA device as the other tensors, got {t.device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+def _binding():
+    """The native binding of the calls below (csrc/python/binding.cpp); raises if it has not been built."""
+    global _native
+    load()
+    if not os.path.exists(BINDING_PATH):
+        raise RuntimeError(f"the native binding is not built ({BINDING_PATH} missing); run "
+                           "`python -c 'import __graft_entry__ as g; g.build()'`")
+    spec = importlib.util.spec_from_file_location("_msgl_binding", BINDING_PATH)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    _native = module
+    return module
 
 
-def _all_i32_on(index: int, tensors) -> bool:
-    """:func:`_i32_on` without the names: these calls are short, and so are their checks."""
-    if index < 0:
-        return False
-    for t in tensors:
-        if not isinstance(t, torch.Tensor) or t.dtype is not _INT32 or t.get_device() != index \
-                or not t.is_contiguous():
-            return False
-    return True
-
-
-def _launch(index: int, stream, fn, *args) -> int:
-    """fn(*args, stream) with cuda:``index`` current; the stream is that device's current one by default."""
-    if index != torch._C._cuda_getDevice():
-        with torch.cuda.device(index):
-            return _launch(index, stream, fn, *args)
-    return fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
-
-
-def _device_index(t, name: str) -> int:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return t.get_device()
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def step_tables(req_table: torch.Tensor, cached_lens: torch.Tensor, new_lens: Optional[torch.Tensor],
@@ -437,50 +420,29 @@ def step_tables(req_table: torch.Tensor, cached_lens: torch.Tensor, new_lens: Op
     more (one each when None).  ``total_tokens`` and ``width`` size the outputs when
     ``out`` is not given (W columns by default).
     """
-    dev = _device_index(cached_lens, "cached_lens")
-    B = cached_lens.shape[0]
     if out is None:
         if total_tokens is None:
             raise ValueError("step_tables needs total_tokens or out")
+        B, T, dev = cached_lens.shape[0], int(total_tokens), cached_lens.device
 
         def i32(*shape):
-            return torch.empty(*shape, dtype=_INT32, device=cached_lens.device)
+            return torch.empty(*shape, dtype=torch.int32, device=dev)
         out = StepTables(i32(B, req_table.shape[1] if width is None else int(width)).fill_(-1), i32(B), i32(B + 1),
-                         i32(int(total_tokens)), i32(int(total_tokens)), i32(1))
+                         i32(T), i32(T), i32(1))
+        if stream is not None:
+            for t in out:
+                t.record_stream(stream)
+            stream.wait_stream(torch.cuda.current_stream(dev))   # behind the fill
+    else:
+        if total_tokens is not None and total_tokens != out[3].shape[0]:
+            raise ValueError("total_tokens must match out")
+        if width is not None and width != out[0].shape[1]:
+            raise ValueError("width must match out")
     page_table, seq_lens, cu_ext, positions, out_loc, pages_taken = out
-    if not _all_i32_on(dev, (req_table, cached_lens, free_pages, page_table, seq_lens, cu_ext, positions, out_loc,
-                             pages_taken)):
-        _i32_on(dev, req_table=req_table, cached_lens=cached_lens, free_pages=free_pages, page_table=page_table,
-                seq_lens=seq_lens, cu_ext=cu_ext, positions=positions, out_loc=out_loc, pages_taken=pages_taken)
-    new_ptr = rows_ptr = None
-    if new_lens is not None:
-        if not _all_i32_on(dev, (new_lens,)) or new_lens.numel() != B:
-            _i32_on(dev, new_lens=new_lens)
-            raise ValueError("new_lens must have one entry per request")
-        new_ptr = new_lens.data_ptr()
-    if req_rows is not None:
-        if not _all_i32_on(dev, (req_rows,)) or req_rows.numel() != B:
-            _i32_on(dev, req_rows=req_rows)
-            raise ValueError("req_rows must have one entry per request")
-        rows_ptr = req_rows.data_ptr()
-    if req_table.dim() != 2 or page_table.dim() != 2:
-        raise ValueError("req_table and out.page_table must have two dimensions")
-    rows, W = req_table.shape
-    T = positions.shape[0]
-    n, w = page_table.shape
-    if (n != B or seq_lens.shape[0] != B or cu_ext.shape[0] != B + 1 or out_loc.shape[0] != T
-            or pages_taken.numel() != 1):
-        raise ValueError("out must hold [B, width], [B], [B + 1], [T], [T] and [1] entries")
-    if total_tokens is not None and total_tokens != T:
-        raise ValueError("total_tokens must match out")
-    if width is not None and width != w:
-        raise ValueError("width must match out")
-    c = _StepOut(page_table.data_ptr(), w, w, seq_lens.data_ptr(), cu_ext.data_ptr(), positions.data_ptr(),
-                 out_loc.data_ptr(), pages_taken.data_ptr(), T)
-    rc = _launch(dev, stream, (_lib or load()).msgl_step_tables, int(num_slots), int(page_size), req_table.data_ptr(), rows, W, W,
-                 rows_ptr, cached_lens.data_ptr(), new_ptr, B, free_pages.data_ptr(), free_pages.shape[0],
-                 ctypes.byref(c), None if status is None else status.data_ptr())
-    if rc:
+    rc = (_native or _binding()).step_tables(req_table, cached_lens, new_lens, free_pages, num_slots, page_size,
+                                             req_rows, page_table, seq_lens, cu_ext, positions, out_loc, pages_taken,
+                                             status, _handle(stream))
+    if rc is not None:
         _check(rc, "msgl_step_tables")
     return out
 
@@ -493,25 +455,13 @@ def shared_prefixes(page_table: torch.Tensor, seq_lens: torch.Tensor, page_size:
     Returns (group_start int32 [B], shared_lens int32 [B]), the group arguments of
     :func:`attn_decode_shared`.
     """
-    dev = _device_index(seq_lens, "seq_lens")
-    B = seq_lens.shape[0]
-    group_start = torch.empty_like(seq_lens) if group_start is None else group_start
-    shared_lens = torch.empty_like(seq_lens) if shared_lens is None else shared_lens
-    if not _all_i32_on(dev, (page_table, seq_lens, group_start, shared_lens)):
-        _i32_on(dev, page_table=page_table, seq_lens=seq_lens, group_start=group_start, shared_lens=shared_lens)
-    if page_table.dim() != 2 or page_table.shape[0] != B or group_start.shape[0] != B or shared_lens.shape[0] != B:
-        raise ValueError("page_table must be [B, width]; seq_lens, group_start and shared_lens [B]")
-    w = page_table.shape[1]
-    pt = _Pages(page_table.data_ptr(), w, w)
-    rc = _launch(dev, stream, (_lib or load()).msgl_shared_prefixes, ctypes.byref(pt), seq_lens.data_ptr(), B, int(page_size),
-                 int(max_seq_len), int(min_shared), group_start.data_ptr(), shared_lens.data_ptr(),
-                 None if status is None else status.data_ptr())
-    if rc:
-        _check(rc, "msgl_shared_prefixes")
-    return group_start, shared_lens
+    r = (_native or _binding()).shared_prefixes(page_table, seq_lens, page_size, max_seq_len, min_shared, group_start,
+                                                shared_lens, status, _handle(stream))
+    if type(r) is int:
+        _check(r, "msgl_shared_prefixes")
+    return r
 
 
-@functools.lru_cache(maxsize=256)
 def decode_shared_workspace_size(num_reqs: int, hq: int, hkv: int, max_seq_len: int, head_dim: int = 128) -> int:
     return int(load().msgl_decode_shared_workspace_size(num_reqs, hq, hkv, head_dim, max_seq_len))
 
@@ -526,65 +476,12 @@ def attn_decode_shared(pool: KVPool, q: torch.Tensor, page_table: torch.Tensor, 
     ``shared_lens[b]`` the leading keys the group has in common, read through the first
     row's pages (:func:`shared_prefixes` finds both).  Returns (o bf16 [B,Hq,D], lse fp32 [B,Hq]).
     """
-    _need(q, "q", torch.bfloat16)
-    dev = q.get_device()
-    B, hq, d = q.shape
-    if not _all_i32_on(dev, (page_table, seq_lens, group_start, shared_lens)):
-        _i32_on(dev, page_table=page_table, seq_lens=seq_lens, group_start=group_start, shared_lens=shared_lens)
-    if (page_table.dim() != 2 or page_table.shape[0] != B or seq_lens.shape[0] != B or group_start.shape[0] != B
-            or shared_lens.shape[0] != B):
-        raise ValueError("page_table must be [B, width]; seq_lens, group_start and shared_lens [B]")
-    if pool.k.get_device() != dev or pool.v.get_device() != dev:
-        raise ValueError("the pool and q must be on the same device")
-    if dev != torch._C._cuda_getDevice():
-        with torch.cuda.device(dev):
-            return attn_decode_shared(pool, q, page_table, seq_lens, group_start, shared_lens, max_seq_len, scale,
-                                      out, lse, workspace, status, stream)
-    raw_stream = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    fresh = []                      # allocated here, for the current stream
-    if out is None:
-        out = torch.empty_like(q)
-        fresh.append(out)
-    else:
-        _need(out, "out", torch.bfloat16)
-        if out.shape != q.shape or out.get_device() != dev:
-            raise ValueError("out must be [B, Hq, D], on q's device")
-    if lse is None:
-        lse = torch.empty((B, hq), dtype=torch.float32, device=q.device)
-        fresh.append(lse)
-    else:
-        _need(lse, "lse", torch.float32)
-        if lse.shape != q.shape[:2] or lse.get_device() != dev:
-            raise ValueError("lse must be [B, Hq], on q's device")
-    if stream is not None:
-        for t in fresh:
-            t.record_stream(stream)
-    scratch = None
-    if workspace is None:
-        # Straight from the caching allocator, in the stream's order, and back to it below (what
-        # torch.cuda.caching_allocator_alloc does): a tensor that nobody sees would cost as much
-        # host time as the launches.
-        ws_ptr = None
-        ws_bytes = decode_shared_workspace_size(B, hq, pool.num_kv_heads, int(max_seq_len), d)
-        if ws_bytes:
-            ws_ptr = scratch = torch._C._cuda_cudaCachingAllocator_raw_alloc(ws_bytes, raw_stream)
-    else:
-        if workspace.get_device() != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous and on q's device")
-        ws_bytes, ws_ptr = workspace.numel() * workspace.element_size(), workspace.data_ptr()
-    try:
-        pc, w = pool.c(), page_table.shape[1]
-        pt = _Pages(page_table.data_ptr(), w, w)
-        rc = (_lib or load()).msgl_attn_decode_shared(
-            ctypes.byref(pc), ctypes.byref(pt), q.data_ptr(), hq, group_start.data_ptr(), shared_lens.data_ptr(),
-            seq_lens.data_ptr(), B, int(max_seq_len), float(scale), out.data_ptr(), lse.data_ptr(), ws_ptr, ws_bytes,
-            None if status is None else status.data_ptr(), raw_stream)
-    finally:
-        if scratch is not None:
-            torch._C._cuda_cudaCachingAllocator_raw_delete(scratch)
-    if rc:
-        _check(rc, "msgl_attn_decode_shared")
-    return out, lse
+    r = (_native or _binding()).attn_decode_shared(pool.k, pool.v, pool.page_size, q, page_table, seq_lens, group_start,
+                                                   shared_lens, max_seq_len, scale, out, lse, workspace, status,
+                                                   _handle(stream))
+    if type(r) is int:
+        _check(r, "msgl_attn_decode_shared")
+    return r
 
 
 def selftest_wait_timeout(status: torch.Tensor, budget_cycles: int = 10_000_000, stream=None) -> None:
