@@ -99,7 +99,7 @@ def build(verbose: bool = False, force: bool = False, extra_flags: list[str] | N
     torch_lib = os.path.join(os.path.dirname(os.path.abspath(torch.__file__)), "lib")
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = ["g++", "-shared", "-o", tmp, binding_obj, LIB, "-L", torch_lib, "-ltorch_python", "-ltorch", "-ltorch_cpu",
-           "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"]
+           "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")

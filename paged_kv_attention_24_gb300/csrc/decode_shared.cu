@@ -964,6 +964,7 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Merge
 }
 
 constexpr long long kThroughBytes = 64ll << 20;
+constexpr int kShortKeys = 512;
 
 // Where each part of the workspace begins.
 struct Layout {
@@ -997,7 +998,8 @@ cudaError_t launch_decode_shared(const DecodeSharedArgs &a, cudaStream_t stream)
     // Small batches: with at most kThroughBytes of K/V behind the page tables, reading a shared key
     // once for each request costs less than the kernel that reads it once for all.
     if (d.num_reqs == 1 || (long long)d.num_reqs * d.max_seq_len * hkv * kHeadDim * 4 <= kThroughBytes)
-        return launch_decode(d, plan, stream);
+        return d.max_seq_len <= kShortKeys && d.num_reqs <= 65535 ? launch_decode_short(d, stream)
+                                                                  : launch_decode(d, plan, stream);
     d.own_only = true;
     const Layout l = layout_of(d.num_reqs, d.hq, hkv);
     char *ws = static_cast<char *>(a.workspace);

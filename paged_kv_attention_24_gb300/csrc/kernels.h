@@ -105,6 +105,9 @@ struct DecodeSharedArgs {
     DecodeArgs dec;     // group_start and shared_lens among them
     void *workspace;
 };
+// One launch for short requests (decode_short.cu); the groups' shared keys are read through the
+// first row.
+cudaError_t launch_decode_short(const DecodeArgs &a, cudaStream_t stream);
 cudaError_t launch_decode_shared(const DecodeSharedArgs &a, cudaStream_t stream);
 
 // The tensor maps of an attention kernel with GQA-packed 128-row Q tiles of `rows` tokens and

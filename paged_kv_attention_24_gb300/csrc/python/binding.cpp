@@ -8,8 +8,7 @@
 // call's non-zero status, which the Python side turns into MsglError.
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
-#include <ATen/ops/empty_like.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -74,6 +73,10 @@ c10::cuda::CUDAStream stream_of(PyObject *o, int dev) {
     return c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(p), dev);
 }
 
+at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, int dev) {
+    return at::detail::empty_cuda(sizes, type, c10::Device(c10::kCUDA, (c10::DeviceIndex)dev), c10::nullopt);
+}
+
 msgl_stream_t raw(const c10::cuda::CUDAStream &s) { return reinterpret_cast<msgl_stream_t>(s.stream()); }
 
 PyObject *done(msgl_status rc) {
@@ -122,11 +125,11 @@ PyObject *step_tables(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const at::Tensor &loc = checked(a[11], "out_loc", at::kInt, dev);
         const at::Tensor &taken = checked(a[12], "pages_taken", at::kInt, dev);
         const int32_t B = size32(cached.numel(), "cached_lens");
-        const int32_t *fresh = nullptr, *rows = nullptr;
+        const int32_t *added = nullptr, *rows = nullptr;
         if (a[2] != Py_None) {
             const at::Tensor &t = checked(a[2], "new_lens", at::kInt, dev);
             if (t.numel() != B) refuse("%s must have one entry per request", "new_lens");
-            fresh = i32(t);
+            added = i32(t);
         }
         if (a[6] != Py_None) {
             const at::Tensor &t = checked(a[6], "req_rows", at::kInt, dev);
@@ -152,7 +155,7 @@ PyObject *step_tables(PyObject *, PyObject *const *a, Py_ssize_t n) {
         uint32_t *status = status_ptr(a[13]);
         c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
         return done(msgl_step_tables(slots, ps, i32(table), size32(table.size(0), "req_table"), W, W, rows, i32(cached),
-                                     fresh, B, i32(free_pages), size32(free_pages.numel(), "free_pages"), &out, status,
+                                     added, B, i32(free_pages), size32(free_pages.numel(), "free_pages"), &out, status,
                                      raw(stream_of(a[14], dev))));
     });
 }
@@ -169,8 +172,8 @@ PyObject *shared_prefixes(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int32_t ps = integer32(a[2], "page_size"), max_seq = integer32(a[3], "max_seq_len"),
                       min_shared = integer32(a[4], "min_shared");
         c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
-        const at::Tensor first = a[5] == Py_None ? at::empty_like(seq) : checked(a[5], "group_start", at::kInt, dev);
-        const at::Tensor shared = a[6] == Py_None ? at::empty_like(seq) : checked(a[6], "shared_lens", at::kInt, dev);
+        const at::Tensor first = a[5] == Py_None ? fresh(seq.sizes(), at::kInt, dev) : checked(a[5], "group_start", at::kInt, dev);
+        const at::Tensor shared = a[6] == Py_None ? fresh(seq.sizes(), at::kInt, dev) : checked(a[6], "shared_lens", at::kInt, dev);
         if (pages.dim() != 2 || pages.size(0) != B || first.numel() != B || shared.numel() != B)
             refuse("%s must be [B, width]; seq_lens, group_start and shared_lens [B]", "page_table");
         uint32_t *status = status_ptr(a[7]);
@@ -230,8 +233,8 @@ PyObject *attn_decode_shared(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
         c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
         const c10::cuda::CUDAStream stream = stream_of(a[14], dev);
-        const at::Tensor out = a[10] == Py_None ? at::empty_like(q) : checked(a[10], "out", at::kBFloat16, dev);
-        const at::Tensor lse = a[11] == Py_None ? at::empty({q.size(0), q.size(1)}, q.options().dtype(at::kFloat))
+        const at::Tensor out = a[10] == Py_None ? fresh(q.sizes(), at::kBFloat16, dev) : checked(a[10], "out", at::kBFloat16, dev);
+        const at::Tensor lse = a[11] == Py_None ? fresh({q.size(0), q.size(1)}, at::kFloat, dev)
                                                 : checked(a[11], "lse", at::kFloat, dev);
         if (out.sizes() != q.sizes()) refuse("%s must be [B, Hq, D]", "out");
         if (lse.dim() != 2 || lse.size(0) != B || lse.size(1) != hq) refuse("%s must be [B, Hq]", "lse");

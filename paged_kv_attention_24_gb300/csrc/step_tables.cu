@@ -66,11 +66,17 @@ __device__ __forceinline__ void block_sum2(long long &x, long long &y) {
 __global__ void __launch_bounds__(kThreads) step_tables_kernel(const StepTablesArgs a) {
     const int b = blockIdx.x;
     const int at0 = blockIdx.y * kChunk + threadIdx.x;   // this thread's first column and token
+    Request r{};
+    if (b < a.num_reqs) {
+        // a chunk behind the request's last column and token has nothing to do
+        r = request_at(a, b);
+        if (blockIdx.y > 0 && blockIdx.y * kChunk >= max(r.old_pages + r.need, r.tokens)) return;
+    }
     long long cu = 0, off = 0;   // tokens and new pages of the requests before b
     for (int i = threadIdx.x; i < b; i += kThreads) {
-        const Request r = request_at(a, i);
-        cu += r.tokens;
-        off += r.need;
+        const Request x = request_at(a, i);
+        cu += x.tokens;
+        off += x.need;
     }
     block_sum2(cu, off);
     if (b == a.num_reqs) {
@@ -83,10 +89,10 @@ __global__ void __launch_bounds__(kThreads) step_tables_kernel(const StepTablesA
                 long long c = 0, o = 0;
                 taken = 0;
                 for (int i = 0; i < b; ++i) {
-                    const Request r = request_at(a, i);
-                    c += r.tokens;
-                    o += r.need;
-                    if (r.need > 0 && c <= a.total_tokens && o <= a.num_free) taken = o;
+                    const Request x = request_at(a, i);
+                    c += x.tokens;
+                    o += x.need;
+                    if (x.need > 0 && c <= a.total_tokens && o <= a.num_free) taken = o;
                 }
             }
             a.pages_taken[0] = (int)taken;
@@ -101,7 +107,6 @@ __global__ void __launch_bounds__(kThreads) step_tables_kernel(const StepTablesA
         }
         return;
     }
-    const Request r = request_at(a, b);
     const bool fits = cu + r.tokens <= a.total_tokens;
     const bool paged = r.need == 0 || off + r.need <= a.num_free;
     const bool served = r.ok && fits && paged;

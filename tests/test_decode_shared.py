@@ -6,8 +6,9 @@ once at the end; a joined prefix adds fp32 arithmetic only.
 
 A call whose bound on the keys (requests x max_seq_len) is small reads shared
 keys once a request instead of running the kernel that reads them once for
-all; max_seq_len is only a bound, so a large one takes any batch to the other
-side, and every case here runs on both.
+all, and one of short requests does so in a single launch; max_seq_len is only
+a bound, so a larger one takes any batch to the other variants, and every case
+here runs on all three.
 """
 import dataclasses
 
@@ -27,16 +28,16 @@ def run(g, **kw):
                                   g.scale, **kw)
 
 
-FAR = 1 << 22
+BOUNDS = {"own": 0, "over-short": 1000, "far": 1 << 22}
 
 
 def bounded(w, far):
-    return dataclasses.replace(w, max_seq=FAR) if far else w
+    return dataclasses.replace(w, max_seq=max(w.max_seq, BOUNDS[far]))
 
 
 def check(w, what=""):
     ref_o, ref_l, a = w.reference()
-    for far in (False, True):
+    for far in BOUNDS:
         g = bounded(w, far).cuda()
         status = ops.new_status()
         o, lse = run(g, status=status)
@@ -94,7 +95,7 @@ def test_many_groups_split_over_the_grid():
 
 
 @pytest.mark.parametrize("ps", [1, 16])
-@pytest.mark.parametrize("far", [False, True])
+@pytest.mark.parametrize("far", list(BOUNDS))
 def test_prefix_is_read_through_the_first_row(far, ps):
     """The rows behind a group's first may hold anything in the shared columns."""
     w = shared_batch.make(40, 8, ps, [(320, [1, 50, 3]), (160, [20, 7])], seed=8)
@@ -119,7 +120,7 @@ def test_large_scores_and_scales():
     check(w)
 
 
-@pytest.mark.parametrize("far", [False, True])
+@pytest.mark.parametrize("far", list(BOUNDS))
 def test_repeats_are_bit_identical(far):
     w = shared_batch.make(64, 8, 64, [(1600, rising(20, 1, 13)), (640, [5, 6])], seed=11)
     g = bounded(w, far).cuda()
@@ -127,7 +128,7 @@ def test_repeats_are_bit_identical(far):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
-@pytest.mark.parametrize("far", [False, True])
+@pytest.mark.parametrize("far", list(BOUNDS))
 def test_dirty_workspace_and_outputs(far):
     w = shared_batch.make(40, 8, 16, [(600, [1, 90, 3]), (0, [7])], seed=12)
     g = bounded(w, far).cuda()
@@ -139,7 +140,7 @@ def test_dirty_workspace_and_outputs(far):
     assert torch.equal(out, clean[0]) and torch.equal(lse, clean[1])
 
 
-@pytest.mark.parametrize("far", [False, True])
+@pytest.mark.parametrize("far", list(BOUNDS))
 def test_rows_in_error_leave_the_others_alone(far):
     w = shared_batch.make(16, 8, 16, [(160, [1, 40, 9]), (0, [20]), (320, [3, 4, 5, 6])], seed=13)
     g = bounded(w, far).cuda()
@@ -178,7 +179,7 @@ def test_rows_in_error_leave_the_others_alone(far):
     expect(ops.DEVERR_GROUP, {3}, first=edit(g.first, (3, 7)))
 
 
-@pytest.mark.parametrize("far", [False, True])
+@pytest.mark.parametrize("far", list(BOUNDS))
 def test_narrow_table_is_a_page_error(far):
     w = shared_batch.make(16, 8, 16, [(160, [1, 40]), (0, [20])], seed=14)
     g = bounded(w, far).cuda()
@@ -189,7 +190,7 @@ def test_narrow_table_is_a_page_error(far):
     assert torch.all(o[:2] == 0) and torch.isfinite(lse[2]).all()
 
 
-@pytest.mark.parametrize("far", [False, True])
+@pytest.mark.parametrize("far", list(BOUNDS))
 def test_nan_query_rows_stay_their_own(far):
     w = shared_batch.make(64, 8, 64, [(500, rising(18, 1, 3))], seed=15)
     g = bounded(w, far).cuda()
@@ -201,13 +202,13 @@ def test_nan_query_rows_stay_their_own(far):
     assert torch.equal(o[keep], good[0][keep]) and torch.equal(lse[keep], good[1][keep])
 
 
-@pytest.mark.parametrize("far", [False, True])
+@pytest.mark.parametrize("far", list(BOUNDS))
 def test_captured_replays_with_new_lengths_and_groups(far):
     """One captured call serves steps with other groups and lengths."""
     a = shared_batch.make(40, 8, 16, [(320, [1, 50, 3, 9]), (160, [20, 7])], seed=16, width=64)
     b = shared_batch.make(40, 8, 16, [(0, [100]), (600, [1, 2]), (48, [30, 31, 32])], seed=17, width=64)
     slots = max(a.k.shape[0], b.k.shape[0])
-    max_seq = FAR if far else max(a.max_seq, b.max_seq)
+    max_seq = max(a.max_seq, b.max_seq, BOUNDS[far])
     k = torch.zeros(slots, 8, 128, dtype=torch.bfloat16, device="cuda")
     v = torch.zeros_like(k)
     live = a.cuda()
@@ -239,7 +240,25 @@ def test_captured_replays_with_new_lengths_and_groups(far):
         assert_lse_close(lse, ref_l)
 
 
-@pytest.mark.parametrize("far", [False, True])
+@pytest.mark.parametrize("far", list(BOUNDS))
+def test_captured_with_its_own_scratch(far):
+    """A capture without a workspace takes its scratch from the graph's memory."""
+    w = bounded(shared_batch.make(40, 8, 16, [(320, [1, 50, 3, 9]), (160, [20, 7])], seed=20), far)
+    ref_o, ref_l, abs_ref = w.reference()
+    g = w.cuda()
+    run(g)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = run(g)
+    for _ in range(3):
+        o.fill_(float("nan")), lse.fill_(float("nan"))
+        graph.replay()
+        run(g)
+        assert_o_close(o, ref_o, abs_ref=abs_ref)
+        assert_lse_close(lse, ref_l)
+
+
+@pytest.mark.parametrize("far", list(BOUNDS))
 def test_on_another_stream(far):
     w = shared_batch.make(16, 8, 1, [(900, rising(8, 1, 11))], seed=18)
     ref_o, ref_l, a = w.reference()
