@@ -385,17 +385,22 @@ MSGL_API msgl_status msgl_shared_prefixes(const msgl_page_table *pages, const in
  * msgl_attn_decode, with the keys that a group shares read once for all of its
  * requests (a shared system prompt or document held once in the pool by the
  * radix cache: "Mini-SGLang 实战指南", §6.5 "Radix Cache", §6.3).
- * Requests group_start[b] .. are neighbours in the batch.  Row b attends keys
+ * The requests of a group are neighbours in the batch.  Row b attends keys
  * 0..shared_lens[b]-1 at the slots of row group_start[b]'s page table, and keys
- * shared_lens[b]..seq_lens[b]-1 at the slots of its own.  A group's query rows
- * go through the tensor cores together against its shared keys; every row's
- * own keys take the decode's path; the two are joined by their log-sum-exp.
+ * shared_lens[b]..seq_lens[b]-1 at the slots of its own.  Where it pays, a
+ * group's query rows go through the tensor cores together against its shared
+ * keys, every row's own keys take the decode's path, and the two are joined by
+ * their log-sum-exp; elsewhere the decode's path reads a shared key once for
+ * each request, out of L2 after the first.
  *
  *   group_start  device int32 [num_reqs]: the first row of b's group, so
  *                group_start[b] is b or group_start[b-1]
  *   shared_lens  device int32 [num_reqs]: 0 <= shared_lens[b] <= seq_lens[b],
  *                the same for all rows of a group (of a group of one it is
  *                not used: all keys are its own)
+ *   sharing      MSGL_SHARE_AUTO: by the batch's lengths and groups, found on the
+ *                device; MSGL_SHARE_ALWAYS / MSGL_SHARE_NEVER: one or the other, for
+ *                results that do not depend on what else is in the batch
  *   workspace    device scratch of at least msgl_decode_shared_workspace_size()
  *                bytes, 256-byte aligned, fully rewritten by every call; two calls
  *                (or captured graphs) that may overlap need one each
@@ -406,15 +411,19 @@ MSGL_API msgl_status msgl_shared_prefixes(const msgl_page_table *pages, const in
  * row of the group (MSGL_DEVERR_PAGE_RANGE).
  * The launch shapes depend on host scalars only.
  */
+#define MSGL_SHARE_AUTO 0
+#define MSGL_SHARE_ALWAYS 1
+#define MSGL_SHARE_NEVER 2
+
 MSGL_API size_t msgl_decode_shared_workspace_size(int32_t num_reqs, int32_t num_q_heads, int32_t num_kv_heads,
                                                   int32_t head_dim, int32_t max_seq_len);
 
 MSGL_API msgl_status msgl_attn_decode_shared(const msgl_kv_pool *pool, const msgl_page_table *pages, const void *q,
                                              int32_t num_q_heads, const int32_t *group_start,
                                              const int32_t *shared_lens, const int32_t *seq_lens,
-                                             int32_t num_reqs, int32_t max_seq_len, float scale, void *o,
-                                             float *lse, void *workspace, size_t workspace_bytes,
-                                             uint32_t *status, msgl_stream_t stream);
+                                             int32_t num_reqs, int32_t max_seq_len, int32_t sharing,
+                                             float scale, void *o, float *lse, void *workspace,
+                                             size_t workspace_bytes, uint32_t *status, msgl_stream_t stream);
 
 /*
  * Synchronises `stream`, reads the device status word into *flags (may be

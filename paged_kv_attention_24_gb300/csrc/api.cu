@@ -442,10 +442,12 @@ size_t msgl_decode_shared_workspace_size(int32_t num_reqs, int32_t num_q_heads, 
 
 msgl_status msgl_attn_decode_shared(const msgl_kv_pool *pool, const msgl_page_table *pages, const void *q,
                                     int32_t num_q_heads, const int32_t *group_start, const int32_t *shared_lens,
-                                    const int32_t *seq_lens, int32_t num_reqs, int32_t max_seq_len, float scale,
-                                    void *o, float *lse, void *workspace, size_t workspace_bytes,
+                                    const int32_t *seq_lens, int32_t num_reqs, int32_t max_seq_len, int32_t sharing,
+                                    float scale, void *o, float *lse, void *workspace, size_t workspace_bytes,
                                     uint32_t *status, msgl_stream_t stream) {
     g_last_error[0] = 0;
+    if (sharing < MSGL_SHARE_AUTO || sharing > MSGL_SHARE_NEVER)
+        return fail(MSGL_ERR_INVALID_ARG, "sharing %d is not one of MSGL_SHARE_*", sharing);
     // the workspace it needs includes a decode's, so the decode's check passes when this one does
     if (num_reqs > 0 && pool && pool->num_kv_heads > 0 && num_q_heads > 0) {
         if (!group_start || !shared_lens)
@@ -462,6 +464,7 @@ msgl_status msgl_attn_decode_shared(const msgl_kv_pool *pool, const msgl_page_ta
     if (s || num_reqs == 0) return s;
     a.dec.group_start = group_start;
     a.dec.shared_lens = shared_lens;
+    a.sharing = sharing;
     a.workspace = workspace;
     cudaError_t e = msgl::launch_decode_shared(a, (cudaStream_t)stream);
     return e == cudaSuccess ? MSGL_OK : cuda_fail(e, "decode_shared launch");

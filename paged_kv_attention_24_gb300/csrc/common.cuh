@@ -123,6 +123,87 @@ __device__ __forceinline__ int through_keys(const GroupRows &r, int b, int *from
     return lead >= 0 && lead <= b && split >= 0 && own + split == s ? s : 0;
 }
 
+// What a batch asks for.
+struct BatchSums {
+    long long all, own;      // keys attended, and those of them that are not shared
+    long long shared;        // shared keys, each group's once
+    long long tiles;         // key tiles of all pairs, and (kPairShift) the pairs
+};
+constexpr int kPairShift = 44;
+constexpr long long kTilesMask = (1ll << kPairShift) - 1;
+
+__device__ __forceinline__ void add_row(const GroupRows &r, int i, BatchSums &s) {
+    int from;
+    s.own += own_keys_shared(r.seq_lens, r.group_start, r.shared_lens, r.num_reqs, r.max_seq_len, i, from);
+    s.all += through_keys(r, i);
+    const int t = pair_tiles(r, i);
+    if (t > 0) {
+        s.tiles += t + (1ll << kPairShift);
+        if (__ldg(r.group_start + i) == i) s.shared += __ldg(r.shared_lens + i);
+    }
+}
+
+// Whether the kernel that reads shared keys once for their group pays (whole nanoseconds, so that
+// every kernel of a call comes to the same answer).  Without it the split kernel reads them once a
+// request, which after the first comes out of L2: the call takes what HBM needs for the keys in the
+// pool or what L2 needs for all that are attended.  With it, HBM's time for the requests' own
+// keys, a fixed part (start, first tile, pieces, join) and the tiles.  Measured: 6.4 TB/s from
+// HBM, 10.5 TB/s from L2, 14 us, 1.5 us a tile and SM.
+__device__ __forceinline__ bool prefix_pays(const BatchSums &s, int hkv, int sms) {
+    const long long key = (long long)hkv * kHeadDim * 4;   // bytes
+    const long long through = max((s.own + s.shared) * key / 6400, s.all * key / 10500);
+    const long long prefix = s.own * key / 6400 + 14000 + (s.tiles & kTilesMask) * hkv * 1500 / sms;
+    return prefix < through;
+}
+
+// A batch as one block sees it: thread i has rows [b0, b1) = [i * k, (i + 1) * k).  `before` counts
+// the keys (all and own) and tiles of the rows before b0.  scratch: 4 entries per warp, not used
+// again before the block's next barrier.
+struct BatchScan {
+    int b0, b1;
+    BatchSums before, mine, total;
+};
+
+template <int kMaxWarps>
+__device__ __forceinline__ void scan_batch(const GroupRows &r, long long (*scratch)[4], BatchScan &s) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, threads = blockDim.x;
+    const int k = (r.num_reqs + threads - 1) / threads;
+    s.b0 = min(r.num_reqs, (int)threadIdx.x * k);
+    s.b1 = min(r.num_reqs, s.b0 + k);
+    s.mine = BatchSums{0, 0, 0, 0};
+    for (int b = s.b0; b < s.b1; ++b) add_row(r, b, s.mine);
+    long long x[4] = {s.mine.all, s.mine.own, s.mine.tiles, s.mine.shared};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(0xffffffffu, x[i], o);
+            if (lane >= o) x[i] += u;
+        }
+    if (lane == 31)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) scratch[warp][i] = x[i];
+    __syncthreads();
+    long long before[4], total[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        before[i] = x[i];
+        total[i] = 0;
+    }
+    const int warps = threads >> 5;
+#pragma unroll
+    for (int w = 0; w < kMaxWarps; ++w)
+        if (w < warps)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const long long y = scratch[w][i];
+                total[i] += y;
+                if (w < warp) before[i] += y;
+            }
+    s.before = BatchSums{before[0] - s.mine.all, before[1] - s.mine.own, 0, before[2] - s.mine.tiles};
+    s.total = BatchSums{total[0], total[1], total[3], total[2]};
+}
+
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 

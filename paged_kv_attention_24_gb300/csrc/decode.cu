@@ -78,7 +78,9 @@ struct DecodeKernelArgs {
     // written to the pool at new_loc[b]
     const __nv_bfloat16 *k_new, *v_new;
     const int32_t *new_loc;
-    const int32_t *group_start, *shared_lens;   // kOwn, kThrough
+    const int32_t *group_start, *shared_lens;   // kGrouped
+    int32_t pair_rows, prefix_ctas;             // prefix_ctas = 0: no shared-prefix kernel in this call
+    bool prefix_always;
 };
 
 __device__ __forceinline__ long long warp_incl_scan(long long v, int lane) {
@@ -92,21 +94,29 @@ __device__ __forceinline__ long long warp_incl_scan(long long v, int lane) {
 
 // Which keys of a request the ranges cover, and through which page table.
 //   kPlain    all of them, through its own
-//   kOwn      those behind the prefix its group shares, through its own
-//   kThrough  all of them, the shared ones through its group's first request's
-enum KeyMode { kPlain, kOwn, kThrough };
+//   kGrouped  all of them, or those behind the prefix that its group shares (where the
+//             shared-prefix kernel takes that: prefix_pays); shared keys through the group's
+//             first request's table
+enum KeyMode { kPlain, kGrouped };
 
-// Request b's keys in the ranges (0: not a valid request), the first of them, and (kThrough)
-// where those of its own page table begin.
+__device__ __forceinline__ GroupRows group_rows_of(const DecodeKernelArgs &a) {
+    return GroupRows{a.seq_lens, a.group_start, a.shared_lens, a.num_reqs, a.max_seq_len, a.pair_rows};
+}
+
+// Request b's keys in the ranges (0: not a valid request), the first of them, and where those of its
+// own page table begin.
 template <KeyMode kMode>
-__device__ __forceinline__ int range_keys(const DecodeKernelArgs &a, int b, int &first, int &split) {
-    first = split = 0;
-    if constexpr (kMode == kOwn) {
-        return own_keys_shared(a.seq_lens, a.group_start, a.shared_lens, a.num_reqs, a.max_seq_len, b, first);
-    } else if constexpr (kMode == kThrough) {
-        // (rows whose entries break the group rules are written by the merge; here they only
-        // have to stay in range)
-        return through_keys(GroupRows{a.seq_lens, a.group_start, a.shared_lens, a.num_reqs, a.max_seq_len, 0}, b, &split);
+__device__ __forceinline__ int range_keys(const DecodeKernelArgs &a, int b, bool own_only, int &first, int &own_from) {
+    first = own_from = 0;
+    if constexpr (kMode == kGrouped) {
+        // (rows whose entries break the group rules are written by the merge; here they only have to
+        // stay in range)
+        if (own_only) {
+            const int n = own_keys_shared(a.seq_lens, a.group_start, a.shared_lens, a.num_reqs, a.max_seq_len, b, first);
+            own_from = first;
+            return n;
+        }
+        return through_keys(group_rows_of(a), b, &own_from);
     } else {
         return seq_valid(a.seq_lens, b, a.max_seq_len);
     }
@@ -158,18 +168,39 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
     }
     __syncthreads();
 
+    // kGrouped: the block counts the batch, and the thread whose rows hold the range's first key
+    // says where that is
+    __shared__ long long s_scan[kMaxHeadGroup + 1][4], s_base;
+    __shared__ int s_row;
+    long long total = 0;
+    bool own_only = false;
+    if constexpr (kMode == kGrouped) {
+        BatchScan batch;
+        scan_batch<kMaxHeadGroup + 1>(group_rows_of(a), s_scan, batch);
+        own_only = a.prefix_ctas > 0 && (a.prefix_always || prefix_pays(batch.total, a.pool.hkv, a.prefix_ctas));
+        total = own_only ? batch.total.own : batch.total.all;
+        const long long at = own_only ? batch.before.own : batch.before.all;
+        const long long n = own_only ? batch.mine.own : batch.mine.all;
+        const long long r0 = keys_per_cta(total, gridDim.x) * blockIdx.x;
+        if (r0 < total && at <= r0 && r0 < at + n) {
+            s_row = batch.b0;
+            s_base = at;
+        }
+        __syncthreads();
+    }
+
     const int n_consumers = hg * a.slices;
     if (warp == n_consumers) {
         // ------------------------------------------------------------ producer
         const int B = a.num_reqs;
-        long long total = 0;
-        for (int c = 0; c < B; c += 32) {
-            int f, o;
-            const int s = (c + lane < B) ? range_keys<kMode>(a, c + lane, f, o) : 0;
-            total += s;
-        }
+        if constexpr (kMode == kPlain) {
+            for (int c = 0; c < B; c += 32) {
+                const int s = (c + lane < B) ? seq_valid(a.seq_lens, c + lane, a.max_seq_len) : 0;
+                total += s;
+            }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+            for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        }
         const long long P = gridDim.x;
         const long long per = keys_per_cta(total, P);
         const long long r0 = per * blockIdx.x;
@@ -193,10 +224,14 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
         if (r0 < r1) {
             // locate the request holding key r0
             long long base = 0, start_b = 0;
-            int b = -1;
-            for (int c = 0; c < B && b < 0; c += 32) {
+            int b = -1, c0 = 0;
+            if constexpr (kMode == kGrouped) {
+                c0 = s_row;
+                base = s_base;
+            }
+            for (int c = c0; c < B && b < 0; c += 32) {
                 int f, o;
-                const int s = (c + lane < B) ? range_keys<kMode>(a, c + lane, f, o) : 0;
+                const int s = (c + lane < B) ? range_keys<kMode>(a, c + lane, own_only, f, o) : 0;
                 const long long incl = warp_incl_scan(s, lane);
                 const long long tot = __shfl_sync(0xffffffffu, incl, 31);
                 if (r0 < base + tot) {
@@ -209,23 +244,23 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
             }
             long long pos = r0;
             while (b >= 0 && b < B && pos < r1 && !aborted) {
-                const int sb = range_keys<kMode>(a, b, first_key, own_from);
+                const int sb = range_keys<kMode>(a, b, own_only, first_key, own_from);
                 const long long end_b = start_b + sb;
                 if (end_b > pos) {
                     const int lo = (int)(pos - start_b) + first_key;
                     const int hi = (int)(min(r1, end_b) - start_b) + first_key;
                     // page id of key `key` of request b (-1 when the page index is past the
                     // table's width, which then reads as a bad page)
-                    const int shared_row = kMode == kThrough ? __ldg(a.group_start + b) : b;
+                    const int shared_row = kMode == kGrouped ? __ldg(a.group_start + b) : b;
                     auto load_pid = [&](int key) -> int {
                         const int pidx = key >> a.pool.log2_ps;
-                        const int row = kMode == kThrough && key < own_from ? shared_row : b;
+                        const int row = kMode == kGrouped && key < own_from ? shared_row : b;
                         return pidx < a.pages.width ? __ldg(a.pages.ids + (int64_t)row * a.pages.stride + pidx) : -1;
                     };
                     if constexpr (kBox) {
-                        // kThrough: the keys below own_from and those from there on may sit on different
+                        // kGrouped: the keys below own_from and those from there on may sit on different
                         // pages of the same 16 keys, so they are tiled apart
-                        const int mid = kMode == kThrough ? min(max(own_from, lo), hi) : hi;
+                        const int mid = kMode == kGrouped ? min(max(own_from, lo), hi) : hi;
                         for (int part = mid > lo ? 0 : 1; part < (mid < hi ? 2 : 1) && !aborted; ++part) {
                         const int plo = part ? mid : lo, phi = part ? hi : mid;
                         // 16-key tiles aligned to 16 keys (each inside one page); keys outside
@@ -415,10 +450,10 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
                 ptx::mbar_wait(ptx::smem_u32(full + (k % S)), (k / S) & 1, 200000000LL);
             if (patch_pending) ptx::mbar_wait(ptx::smem_u32(patch), patch_uses & 1, 200000000LL);
         }
-        // kOwn runs behind the shared-prefix kernel by programmatic dependent launch: the last CTA
-        // ends after that kernel has, so what comes behind this grid sees both kernels' partials.
-        if constexpr (kMode == kOwn) {
-            if (lane == 0 && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1)
+        // Behind the shared-prefix kernel by programmatic dependent launch: the last CTA ends after
+        // that kernel has, so what comes behind this grid sees both kernels' partials.
+        if constexpr (kMode == kGrouped) {
+            if (a.prefix_ctas > 0 && lane == 0 && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1)
                 asm volatile("griddepcontrol.wait;" ::: "memory");
         }
     } else if (warp < n_consumers) {
@@ -833,8 +868,7 @@ cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, cudaStrea
     if (dev < 0 || dev >= 64 || !attr_set[dev]) {
         cudaError_t e = cudaSuccess;
         for (auto kernel : {decode_split_kernel<false, kPlain>, decode_split_kernel<true, kPlain>,
-                            decode_split_kernel<false, kOwn>, decode_split_kernel<true, kOwn>,
-                            decode_split_kernel<false, kThrough>, decode_split_kernel<true, kThrough>})
+                            decode_split_kernel<false, kGrouped>, decode_split_kernel<true, kGrouped>})
             if (e == cudaSuccess)
                 e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget);
         if (e != cudaSuccess) return e;
@@ -861,15 +895,18 @@ cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, cudaStrea
     k.new_loc = a.new_loc;
     k.group_start = a.group_start;
     k.shared_lens = a.shared_lens;
+    k.pair_rows = a.pair_rows;
+    k.prefix_ctas = a.prefix_ctas;
+    k.prefix_always = a.prefix_always;
     (void)plan;
     if (L.smem > (size_t)kSmemBudget) return cudaErrorInvalidValue;
     if (phase != DecodePhase::kMerge) {
         dim3 grid(L.ctas, hkv / L.hg);
-        auto kernel = !a.group_start ? (box ? decode_split_kernel<true, kPlain> : decode_split_kernel<false, kPlain>)
-                      : a.own_only   ? (box ? decode_split_kernel<true, kOwn> : decode_split_kernel<false, kOwn>)
-                                     : (box ? decode_split_kernel<true, kThrough> : decode_split_kernel<false, kThrough>);
+        auto kernel = a.group_start
+                          ? (box ? decode_split_kernel<true, kGrouped> : decode_split_kernel<false, kGrouped>)
+                          : (box ? decode_split_kernel<true, kPlain> : decode_split_kernel<false, kPlain>);
         const int threads = 32 * (L.hg * slices + 1);
-        if (a.own_only) {
+        if (a.prefix_ctas > 0) {
             // behind the shared-prefix kernel: SMs that it leaves free start at once
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = grid;
@@ -899,7 +936,7 @@ cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, cudaStrea
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const GroupRows rows{a.seq_lens, a.group_start, a.shared_lens, a.num_reqs, a.max_seq_len, a.group_rows};
+    const GroupRows rows{a.seq_lens, a.group_start, a.shared_lens, a.num_reqs, a.max_seq_len, a.pair_rows};
     return cudaLaunchKernelEx(&cfg, a.group_start ? decode_merge_kernel<true> : decode_merge_kernel<false>, rows, a.hq,
                               L.ctas, (const float *)a.part_o, (const float *)a.part_lse, a.o, a.lse, a.status);
 }

@@ -40,11 +40,13 @@ namespace {
 constexpr int kRows = 128;                 // rows per Q tile (MMA M)
 constexpr int kKeys = kPrefixTileKeys;     // keys per K/V tile
 constexpr int kMaxPrefixCtas = 160;        // bound on the grid, sizes the workspace
-constexpr int kMinUnits = 4;               // K/V tiles per CTA at least: fewer pieces to join
+constexpr int kMinUnits = 4;               // K/V tiles per CTA at least, where the pairs have as many
 
-__host__ __device__ __forceinline__ long long units_per_cta(long long units, long long ctas) {
+// An equal share each, but (a small batch) not less than kMinUnits, so that there are few pieces to
+// join, nor than an average item's units, because a CTA gains nothing from beginning a second.
+__device__ __forceinline__ long long units_per_cta(long long units, long long items, long long ctas) {
     const long long share = (units + ctas - 1) / ctas;
-    return share > kMinUnits ? share : kMinUnits;
+    return max(share, min((long long)kMinUnits, (units + items - 1) / max(items, 1ll)));
 }
 
 // ------------------------------------------------------------- prefix kernel
@@ -83,7 +85,7 @@ constexpr int kQFull = 0, kQEmpty = 1, kKFull = 2, kKEmpty = 4, kVFull = 6, kVEm
 struct RowPlan {
     int32_t err, start;                    // status bits; first own key
     int32_t in_pair;                       // row within its pair of Q tiles, -1: no shared keys
-    int32_t own_pieces;
+    int32_t own_pieces;                    // pieces of the split kernel's
     int64_t own_slot;                      // its first piece's row of the split's partials
     int64_t unit;                          // units before the row
     int64_t unit_of_pair;                  // units before its pair
@@ -94,6 +96,7 @@ struct PrefixArgs {
     PageView pages;
     GroupRows rows;
     int32_t hq, group, rows_per_tile, q_box_rows, oob_row, box_rows, v_blocks, split_ctas;
+    bool always;               // MSGL_SHARE_ALWAYS
     float scale_log2;
     float *o, *lse;            // [num_reqs, hq, 128], [num_reqs, hq]: pieces that begin at the first key
     float *cont_o, *cont_lse;  // [CTA, 2, 128, 128], [CTA, 2, 128]: a CTA's piece that begins later
@@ -108,30 +111,6 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, vol
     report(status, MSGL_DEVERR_TIMEOUT);
     *abort_flag = 1;
     return false;
-}
-
-// Exclusive prefix sum of v over the block; total gets the sum.  scratch: an entry per warp, not
-// used again before the block's next barrier.
-__device__ __forceinline__ long long block_excl_scan(long long v, long long *scratch, long long &total) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    long long x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += u;
-    }
-    if (lane == 31) scratch[warp] = x;
-    __syncthreads();
-    // lane w of every warp takes warp w's sum
-    const long long mine = lane < kThreads / 32 ? scratch[lane] : 0;
-    long long before = lane < warp ? mine : 0;
-    total = mine;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        before += __shfl_xor_sync(0xffffffffu, before, o);
-        total += __shfl_xor_sync(0xffffffffu, total, o);
-    }
-    return before + x - v;
 }
 
 // The two halves of the block run to this one from different places.
@@ -223,20 +202,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     static_assert(8 * kNumBars + 16 + 4 * kBadRing + sizeof(Walk) <= 256, "barrier block");
     Seg *segs = reinterpret_cast<Seg *>(smem + kOffSegs);
     float2 *xchg = reinterpret_cast<float2 *>(smem + kOffX);            // (m, l) of stream 1's rows
-    long long *scratch = reinterpret_cast<long long *>(smem + kOffX);   // of the block's scans
+    long long(*scratch)[4] = reinterpret_cast<long long(*)[4]>(smem + kOffX);   // of the block's scan
 
     const GroupRows &rows = a.rows;
     const int hkv = a.pool.hkv;
     const int R = a.rows_per_tile, G = a.group;
 
-    // ---- this CTA's units: thread i counts rows [i * k, (i + 1) * k)
-    const int per_thread = (rows.num_reqs + kThreads - 1) / kThreads;
-    const int b0 = min(rows.num_reqs, (int)threadIdx.x * per_thread);
-    const int b1 = min(rows.num_reqs, b0 + per_thread);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += pair_tiles(rows, b);
-
-    // (while those loads are on their way)
     if (threadIdx.x == 0) {
         ptx::mbar_init(bar(kQFull), 1);
         ptx::mbar_init(bar(kQEmpty), 1);
@@ -276,17 +247,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::fence_proxy_async_smem();
     }
 
-    long long units;
-    const long long before = block_excl_scan(mine, scratch, units) * hkv;
-    units *= hkv;
-    const long long per = units_per_cta(units, gridDim.x);
+    // ---- this CTA's units; none when the split kernel takes the shared keys too
+    BatchScan batch;
+    scan_batch<kThreads / 32>(rows, scratch, batch);
+    const bool pays = a.always || prefix_pays(batch.total, hkv, gridDim.x);
+    const long long before = (batch.before.tiles & kTilesMask) * hkv, mine = (batch.mine.tiles & kTilesMask) * hkv;
+    const long long units = pays ? (batch.total.tiles & kTilesMask) * hkv : 0;
+    const long long per = units_per_cta(units, (batch.total.tiles >> kPairShift) * hkv, gridDim.x);
     const long long u0 = per * blockIdx.x, u1 = min(units, u0 + per);
     // the warp whose rows hold the first unit lays out the first segments
-    const unsigned owner = __ballot_sync(0xffffffffu, u0 < u1 && before <= u0 && u0 < before + mine * hkv);
+    const unsigned owner = __ballot_sync(0xffffffffu, u0 < u1 && before <= u0 && u0 < before + mine);
     if (owner) {
         const int l = __ffs(owner) - 1;
         Walk walk;
-        walk.start(rows, hkv, __shfl_sync(0xffffffffu, b0, l), __shfl_sync(0xffffffffu, u0 - before, l), u1 - u0);
+        walk.start(rows, hkv, __shfl_sync(0xffffffffu, batch.b0, l), __shfl_sync(0xffffffffu, u0 - before, l), u1 - u0);
         const int n = walk.fill(rows, hkv, segs);
         if (lane == 0) {
             *num_segs = n;
@@ -297,32 +271,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (last_cta) {
         // the rows' places among the pieces, for the merge
-        long long own = 0, own_all;
-        int first;
-        for (int b = b0; b < b1; ++b)
-            own += own_keys_shared(rows.seq_lens, rows.group_start, rows.shared_lens, rows.num_reqs, rows.max_seq_len,
-                                   b, first);
-        own = block_excl_scan(own, scratch + kThreads / 32, own_all);
-        const long long split_per = keys_per_cta(own_all, a.split_ctas);
-        long long unit = before;
-        for (int b = b0; b < b1; ++b) {
+        const long long split_per = keys_per_cta(pays ? batch.total.own : batch.total.all, a.split_ctas);
+        long long at = pays ? batch.before.own : batch.before.all, unit = before;
+        for (int b = batch.b0; b < batch.b1; ++b) {
             a.plan[b].unit = unit;
             unit += (long long)pair_tiles(rows, b) * hkv;
         }
         __threadfence_block();
         __syncthreads();
-        for (int b = b0; b < b1; ++b) {
-            int seq, start, pair;
-            const int n = own_keys_shared(rows.seq_lens, rows.group_start, rows.shared_lens, rows.num_reqs,
-                                          rows.max_seq_len, b, first);
-            const long long c0 = own / split_per;
+        for (int b = batch.b0; b < batch.b1; ++b) {
+            int seq, start, pair, first;
+            const int n = pays ? own_keys_shared(rows.seq_lens, rows.group_start, rows.shared_lens, rows.num_reqs,
+                                                 rows.max_seq_len, b, first)
+                               : through_keys(rows, b);
+            const long long c0 = at / split_per;
             a.plan[b].err = (int32_t)group_row_errors(rows, b, seq, start, pair);
+            if (!pays) pair = -1;
             a.plan[b].start = start;
             a.plan[b].in_pair = pair >= 0 ? b - pair : -1;
-            a.plan[b].own_pieces = n > 0 ? (int)((own + n - 1) / split_per - c0) + 1 : 0;
+            a.plan[b].own_pieces = n > 0 ? (int)((at + n - 1) / split_per - c0) + 1 : 0;
             a.plan[b].own_slot = b + c0;
             a.plan[b].unit_of_pair = pair >= 0 ? __ldcg(&a.plan[pair].unit) : 0;
-            own += n;
+            at += n;
         }
         if (threadIdx.x == 0) *a.per_cta = per;
     }
@@ -963,8 +933,20 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Merge
     if (lane == 0) a.lse[row] = none ? -INFINITY : M + logf(L);
 }
 
-constexpr long long kThroughBytes = 64ll << 20;
-constexpr int kShortKeys = 512;
+constexpr long long kThroughBytes = 140ll << 20;
+
+// Where the one-launch kernel of short requests is taken.  Up to 128 keys its blocks are small
+// enough to keep several on an SM, and it was never behind the split and merge (32 keys, 256
+// requests: 13.4 against 22.7 us).  Longer ones have an SM to themselves, or nearly: ahead as long as
+// there are at most two a SM (512 keys: 8 requests 8.2 against 12.4 us, 32 requests 12.7 against 16.0,
+// 64 requests 23 against 20; 1024 keys: 16 requests 13.1 against 16.7, 32 requests 21.2 against
+// 20.5), and the split's many CTAs win on the longest.
+bool takes_short(const DecodeArgs &d) {
+    if (d.num_reqs > 65535) return false;
+    const long long blocks = (long long)d.num_reqs * d.pool.hkv * ((d.hq / d.pool.hkv + 7) / 8);
+    if (d.max_seq_len <= 128) return true;
+    return blocks <= (d.max_seq_len <= 512 ? 2 : d.max_seq_len <= 1024 ? 1 : 0) * (long long)sm_count();
+}
 
 // Where each part of the workspace begins.
 struct Layout {
@@ -994,13 +976,15 @@ cudaError_t launch_decode_shared(const DecodeSharedArgs &a, cudaStream_t stream)
     DecodeArgs d = a.dec;
     const int hkv = d.pool.hkv, G = d.hq / hkv, R = kRows / G;
     const DecodePlan plan = plan_decode(d.num_reqs, d.hq, hkv, d.max_seq_len);
-    d.group_rows = 2 * R;
-    // Small batches: with at most kThroughBytes of K/V behind the page tables, reading a shared key
-    // once for each request costs less than the kernel that reads it once for all.
-    if (d.num_reqs == 1 || (long long)d.num_reqs * d.max_seq_len * hkv * kHeadDim * 4 <= kThroughBytes)
-        return d.max_seq_len <= kShortKeys && d.num_reqs <= 65535 ? launch_decode_short(d, stream)
-                                                                  : launch_decode(d, plan, stream);
-    d.own_only = true;
+    d.pair_rows = 2 * R;
+    // Small batches: with at most kThroughBytes of K/V to attend, prefix_pays() cannot say yes, so its
+    // kernel is left out.
+    const bool small =
+        d.num_reqs == 1 || (long long)d.num_reqs * d.max_seq_len * hkv * kHeadDim * 4 <= kThroughBytes;
+    if (a.sharing == MSGL_SHARE_NEVER || (a.sharing == MSGL_SHARE_AUTO && small))
+        return takes_short(d) ? launch_decode_short(d, stream) : launch_decode(d, plan, stream);
+    d.prefix_always = a.sharing == MSGL_SHARE_ALWAYS;
+    d.prefix_ctas = sm_count() < kMaxPrefixCtas ? sm_count() : kMaxPrefixCtas;
     const Layout l = layout_of(d.num_reqs, d.hq, hkv);
     char *ws = static_cast<char *>(a.workspace);
     AttnMaps m;
@@ -1026,6 +1010,7 @@ cudaError_t launch_decode_shared(const DecodeSharedArgs &a, cudaStream_t stream)
     p.oob_row = m.oob_row;
     p.box_rows = m.box_rows;
     p.v_blocks = m.v_blocks;
+    p.always = d.prefix_always;
     p.scale_log2 = d.scale * kLog2e;
     p.o = reinterpret_cast<float *>(ws + l.pre_o);
     p.lse = reinterpret_cast<float *>(ws + l.pre_lse);
@@ -1035,7 +1020,7 @@ cudaError_t launch_decode_shared(const DecodeSharedArgs &a, cudaStream_t stream)
     p.plan = reinterpret_cast<RowPlan *>(ws + l.plan + 256);
     p.split_ctas = decode_split_ctas(d.hq, hkv);
     p.status = d.status;
-    const int ctas = sm_count() < kMaxPrefixCtas ? sm_count() : kMaxPrefixCtas;
+    const int ctas = d.prefix_ctas;
     prefix_tc_kernel<<<ctas, kThreads, kSmemBytes, stream>>>(m.q, m.k, m.v, m.kt, m.vt, p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;

@@ -38,12 +38,13 @@ struct DecodeArgs {
     uint32_t *status;
     const __nv_bfloat16 *k_new = nullptr, *v_new = nullptr;   // append mode (see msgl_attn_decode_append)
     const int32_t *new_loc = nullptr;
-    // groups over shared prefixes (see msgl_attn_decode_shared): shared keys are read through
-    // the group's first row, or (own_only, split phase) left to another kernel, which the split
-    // is then launched behind
+    // groups over shared prefixes (see msgl_attn_decode_shared): shared keys are read through the
+    // group's first row, or, where that pays, left to the shared-prefix kernel of prefix_ctas
+    // CTAs behind which the split is then launched (split phase only)
     const int32_t *group_start = nullptr, *shared_lens = nullptr;
-    int32_t group_rows = 0;   // rows of a pair of Q tiles
-    bool own_only = false;
+    int32_t pair_rows = 0;      // rows of a pair of its Q tiles
+    int32_t prefix_ctas = 0;
+    bool prefix_always = false;
 };
 // Which kernels of a decode call to launch: the split (partials per key range), the
 // merge (LSE fold of the partials, launched with programmatic dependent launch), or both.
@@ -103,6 +104,7 @@ size_t decode_shared_workspace_bytes(int32_t num_reqs, int32_t hq, int32_t hkv);
 
 struct DecodeSharedArgs {
     DecodeArgs dec;     // group_start and shared_lens among them
+    int32_t sharing;    // MSGL_SHARE_*
     void *workspace;
 };
 // One launch for short requests (decode_short.cu); the groups' shared keys are read through the

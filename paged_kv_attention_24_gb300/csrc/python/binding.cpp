@@ -198,9 +198,9 @@ PyObject *shared_prefixes(PyObject *, PyObject *const *a, Py_ssize_t n) {
 }
 
 // (k_pool, v_pool, page_size, q, page_table, seq_lens, group_start, shared_lens, max_seq_len, scale, out | None,
-//  lse | None, workspace | None, status | None, stream | None) -> (out, lse) or the status
+//  lse | None, workspace | None, status | None, stream | None, sharing) -> (out, lse) or the status
 PyObject *attn_decode_shared(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (!arity(n, 15)) return nullptr;
+    if (!arity(n, 16)) return nullptr;
     return guarded([&]() -> PyObject * {
         int dev = -1;
         const at::Tensor &q = checked(a[3], "q", at::kBFloat16, dev);
@@ -216,7 +216,8 @@ PyObject *attn_decode_shared(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (q.size(2) != k.size(2)) refuse("%s and the pool must have the same head_dim", "q");
         if (pages.dim() != 2 || pages.size(0) != B || seq.numel() != B || first.numel() != B || shared.numel() != B)
             refuse("%s must be [B, width]; seq_lens, group_start and shared_lens [B]", "page_table");
-        const int32_t ps = integer32(a[2], "page_size"), max_seq = integer32(a[8], "max_seq_len");
+        const int32_t ps = integer32(a[2], "page_size"), max_seq = integer32(a[8], "max_seq_len"),
+                      sharing = integer32(a[15], "sharing");
         const double scale = PyFloat_AsDouble(a[9]);
         if (scale == -1.0 && PyErr_Occurred()) throw Refused{};
         uint32_t *status = status_ptr(a[13]);
@@ -264,7 +265,7 @@ PyObject *attn_decode_shared(PyObject *, PyObject *const *a, Py_ssize_t n) {
                 ws = scratch.p = c10::cuda::CUDACachingAllocator::raw_alloc_with_stream(ws_bytes, stream.stream());
         }
         const msgl_status rc =
-            msgl_attn_decode_shared(&pool, &pt, q.data_ptr(), hq, i32(first), i32(shared), i32(seq), B, max_seq,
+            msgl_attn_decode_shared(&pool, &pt, q.data_ptr(), hq, i32(first), i32(shared), i32(seq), B, max_seq, sharing,
                                     (float)scale, out.data_ptr(), static_cast<float *>(lse.data_ptr()), ws, ws_bytes,
                                     status, raw(stream));
         if (rc != MSGL_OK) return done(rc);

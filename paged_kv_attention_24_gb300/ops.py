@@ -97,7 +97,7 @@ SIGNATURES = {
                          ctypes.c_int),
     "msgl_shared_prefixes": ([PT, P, I32, I32, I32, I32, P, P, P, P], ctypes.c_int),
     "msgl_decode_shared_workspace_size": ([I32, I32, I32, I32, I32], SZ),
-    "msgl_attn_decode_shared": ([PP, PT, P, I32, P, P, P, I32, I32, F32, P, P, P, SZ, P, P], ctypes.c_int),
+    "msgl_attn_decode_shared": ([PP, PT, P, I32, P, P, P, I32, I32, I32, F32, P, P, P, SZ, P, P], ctypes.c_int),
     "msgl_selftest_wait_timeout": ([P, I64, P], ctypes.c_int),
     "msgl_read_status": ([P, ctypes.POINTER(ctypes.c_uint32), P], ctypes.c_int),
     "msgl_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -466,19 +466,26 @@ def decode_shared_workspace_size(num_reqs: int, hq: int, hkv: int, max_seq_len: 
     return int(load().msgl_decode_shared_workspace_size(num_reqs, hq, hkv, head_dim, max_seq_len))
 
 
+SHARING = {"auto": 0, "always": 1, "never": 2}
+
+
 def attn_decode_shared(pool: KVPool, q: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
                        group_start: torch.Tensor, shared_lens: torch.Tensor, max_seq_len: int, scale: float,
                        out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
-                       workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
+                       workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None,
+                       sharing: str = "auto"):
     """:func:`attn_decode` with the keys that a group of requests shares read once for all of them.
 
     ``group_start[b]`` is the first row of b's group (neighbouring rows) and
     ``shared_lens[b]`` the leading keys the group has in common, read through the first
-    row's pages (:func:`shared_prefixes` finds both).  Returns (o bf16 [B,Hq,D], lse fp32 [B,Hq]).
+    row's pages (:func:`shared_prefixes` finds both).  ``sharing`` = "always" or "never"
+    settles whether a group's rows go through its shared keys together, which "auto"
+    does where the batch's lengths and groups make it pay.  Returns (o bf16 [B,Hq,D],
+    lse fp32 [B,Hq]).
     """
     r = (_native or _binding()).attn_decode_shared(pool.k, pool.v, pool.page_size, q, page_table, seq_lens, group_start,
                                                    shared_lens, max_seq_len, scale, out, lse, workspace, status,
-                                                   _handle(stream))
+                                                   _handle(stream), SHARING[sharing])
     if type(r) is int:
         _check(r, "msgl_attn_decode_shared")
     return r

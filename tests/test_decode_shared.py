@@ -4,11 +4,10 @@ The tolerances are those of every other parity test (tests/parity.py): P is
 rounded to bf16 before the PV product (2^-8 of |v| under the softmax) and o
 once at the end; a joined prefix adds fp32 arithmetic only.
 
-A call whose bound on the keys (requests x max_seq_len) is small reads shared
-keys once a request instead of running the kernel that reads them once for
-all, and one of short requests does so in a single launch; max_seq_len is only
-a bound, so a larger one takes any batch to the other variants, and every case
-here runs on all three.
+Every case runs in each of the call's variants: the group's rows together
+against its shared keys ("always"), shared keys read once a request by the
+split kernel, or, for short requests, in a single launch ("never"; max_seq_len
+is only a bound, and a larger one takes a short batch to the split kernel).
 """
 import dataclasses
 
@@ -28,22 +27,23 @@ def run(g, **kw):
                                   g.scale, **kw)
 
 
-BOUNDS = {"own": 0, "over-short": 1000, "far": 1 << 22}
+VARIANTS = {"always": ("always", 0), "short": ("never", 0), "split": ("never", 2000)}
 
 
-def bounded(w, far):
-    return dataclasses.replace(w, max_seq=max(w.max_seq, BOUNDS[far]))
+def varied(w, variant):
+    """The batch with the variant's bound, and the keyword that asks for the variant."""
+    return dataclasses.replace(w, max_seq=max(w.max_seq, VARIANTS[variant][1])), dict(sharing=VARIANTS[variant][0])
 
 
 def check(w, what=""):
     ref_o, ref_l, a = w.reference()
-    for far in BOUNDS:
-        g = bounded(w, far).cuda()
+    for variant in VARIANTS:
+        g, kw = varied(w, variant)
         status = ops.new_status()
-        o, lse = run(g, status=status)
+        o, lse = run(g.cuda(), status=status, **kw)
         assert ops.read_status(status) == 0
-        assert_o_close(o, ref_o, f"{what} {far}", abs_ref=a)
-        assert_lse_close(lse, ref_l, f"{what} {far}")
+        assert_o_close(o, ref_o, f"{what} {variant}", abs_ref=a)
+        assert_lse_close(lse, ref_l, f"{what} {variant}")
 
 
 def rising(n, lo, step):
@@ -95,14 +95,15 @@ def test_many_groups_split_over_the_grid():
 
 
 @pytest.mark.parametrize("ps", [1, 16])
-@pytest.mark.parametrize("far", list(BOUNDS))
-def test_prefix_is_read_through_the_first_row(far, ps):
+@pytest.mark.parametrize("variant", list(VARIANTS))
+def test_prefix_is_read_through_the_first_row(variant, ps):
     """The rows behind a group's first may hold anything in the shared columns."""
     w = shared_batch.make(40, 8, ps, [(320, [1, 50, 3]), (160, [20, 7])], seed=8)
     ref_o, ref_l, a = w.reference()
     for b in (1, 2, 4):
         w.table[b, :int(w.shared[b]) // ps] = -1
-    o, lse = run(bounded(w, far).cuda())
+    w, kw = varied(w, variant)
+    o, lse = run(w.cuda(), **kw)
     assert_o_close(o, ref_o, abs_ref=a)
     assert_lse_close(lse, ref_l)
 
@@ -120,35 +121,38 @@ def test_large_scores_and_scales():
     check(w)
 
 
-@pytest.mark.parametrize("far", list(BOUNDS))
-def test_repeats_are_bit_identical(far):
+@pytest.mark.parametrize("variant", list(VARIANTS))
+def test_repeats_are_bit_identical(variant):
     w = shared_batch.make(64, 8, 64, [(1600, rising(20, 1, 13)), (640, [5, 6])], seed=11)
-    g = bounded(w, far).cuda()
-    a, b = run(g), run(g)
+    w, kw = varied(w, variant)
+    g = w.cuda()
+    a, b = run(g, **kw), run(g, **kw)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
-@pytest.mark.parametrize("far", list(BOUNDS))
-def test_dirty_workspace_and_outputs(far):
+@pytest.mark.parametrize("variant", list(VARIANTS))
+def test_dirty_workspace_and_outputs(variant):
     w = shared_batch.make(40, 8, 16, [(600, [1, 90, 3]), (0, [7])], seed=12)
-    g = bounded(w, far).cuda()
-    clean = run(g)
+    w, kw = varied(w, variant)
+    g = w.cuda()
+    clean = run(g, **kw)
     n = ops.decode_shared_workspace_size(4, 40, 8, g.max_seq)
     ws = torch.full((n // 4,), float("nan"), device="cuda").view(torch.uint8)
     out, lse = torch.full_like(g.q, float("nan")), torch.full((4, 40), float("nan"), device="cuda")
-    run(g, workspace=ws, out=out, lse=lse)
+    run(g, workspace=ws, out=out, lse=lse, **kw)
     assert torch.equal(out, clean[0]) and torch.equal(lse, clean[1])
 
 
-@pytest.mark.parametrize("far", list(BOUNDS))
-def test_rows_in_error_leave_the_others_alone(far):
+@pytest.mark.parametrize("variant", list(VARIANTS))
+def test_rows_in_error_leave_the_others_alone(variant):
     w = shared_batch.make(16, 8, 16, [(160, [1, 40, 9]), (0, [20]), (320, [3, 4, 5, 6])], seed=13)
-    g = bounded(w, far).cuda()
-    good = run(g)
+    w, kw = varied(w, variant)
+    g = w.cuda()
+    good = run(g, **kw)
 
     def expect(bits, rows, maybe=(), **changed):
         status = ops.new_status()
-        o, lse = run(dataclasses.replace(g, **changed), status=status)
+        o, lse = run(dataclasses.replace(g, **changed), status=status, **kw)
         assert ops.read_status(status) == bits
         for b in range(8):
             if b in rows or (b in maybe and torch.all(lse[b] == float("-inf"))):
@@ -179,36 +183,38 @@ def test_rows_in_error_leave_the_others_alone(far):
     expect(ops.DEVERR_GROUP, {3}, first=edit(g.first, (3, 7)))
 
 
-@pytest.mark.parametrize("far", list(BOUNDS))
-def test_narrow_table_is_a_page_error(far):
+@pytest.mark.parametrize("variant", list(VARIANTS))
+def test_narrow_table_is_a_page_error(variant):
     w = shared_batch.make(16, 8, 16, [(160, [1, 40]), (0, [20])], seed=14)
-    g = bounded(w, far).cuda()
+    w, kw = varied(w, variant)
+    g = w.cuda()
     g.table = g.table[:, :9].contiguous()      # the prefix needs 10
     status = ops.new_status()
-    o, lse = run(g, status=status)
+    o, lse = run(g, status=status, **kw)
     assert ops.read_status(status) == ops.DEVERR_PAGE_RANGE
     assert torch.all(o[:2] == 0) and torch.isfinite(lse[2]).all()
 
 
-@pytest.mark.parametrize("far", list(BOUNDS))
-def test_nan_query_rows_stay_their_own(far):
+@pytest.mark.parametrize("variant", list(VARIANTS))
+def test_nan_query_rows_stay_their_own(variant):
     w = shared_batch.make(64, 8, 64, [(500, rising(18, 1, 3))], seed=15)
-    g = bounded(w, far).cuda()
-    good = run(g)
+    w, kw = varied(w, variant)
+    g = w.cuda()
+    good = run(g, **kw)
     g.q[3] = float("nan")
     g.q[9, 5] = float("inf")
-    o, lse = run(g)
+    o, lse = run(g, **kw)
     keep = [b for b in range(18) if b not in (3, 9)]
     assert torch.equal(o[keep], good[0][keep]) and torch.equal(lse[keep], good[1][keep])
 
 
-@pytest.mark.parametrize("far", list(BOUNDS))
-def test_captured_replays_with_new_lengths_and_groups(far):
+@pytest.mark.parametrize("variant", list(VARIANTS))
+def test_captured_replays_with_new_lengths_and_groups(variant):
     """One captured call serves steps with other groups and lengths."""
     a = shared_batch.make(40, 8, 16, [(320, [1, 50, 3, 9]), (160, [20, 7])], seed=16, width=64)
     b = shared_batch.make(40, 8, 16, [(0, [100]), (600, [1, 2]), (48, [30, 31, 32])], seed=17, width=64)
     slots = max(a.k.shape[0], b.k.shape[0])
-    max_seq = max(a.max_seq, b.max_seq, BOUNDS[far])
+    max_seq = max(a.max_seq, b.max_seq, VARIANTS[variant][1])
     k = torch.zeros(slots, 8, 128, dtype=torch.bfloat16, device="cuda")
     v = torch.zeros_like(k)
     live = a.cuda()
@@ -218,7 +224,8 @@ def test_captured_replays_with_new_lengths_and_groups(far):
 
     def call():
         ops.attn_decode_shared(ops.KVPool(k, v, 16), live.q, live.table, live.seq, live.first, live.shared, max_seq,
-                               a.scale, out=out, lse=lse, workspace=ws, status=status)
+                               a.scale, out=out, lse=lse, workspace=ws, status=status,
+                               sharing=VARIANTS[variant][0])
 
     k[:a.k.shape[0]], v[:a.k.shape[0]] = live.k, live.v
     side = torch.cuda.Stream()
@@ -240,33 +247,50 @@ def test_captured_replays_with_new_lengths_and_groups(far):
         assert_lse_close(lse, ref_l)
 
 
-@pytest.mark.parametrize("far", list(BOUNDS))
-def test_captured_with_its_own_scratch(far):
+@pytest.mark.parametrize("variant", list(VARIANTS))
+def test_captured_with_its_own_scratch(variant):
     """A capture without a workspace takes its scratch from the graph's memory."""
-    w = bounded(shared_batch.make(40, 8, 16, [(320, [1, 50, 3, 9]), (160, [20, 7])], seed=20), far)
+    w, kw = varied(shared_batch.make(40, 8, 16, [(320, [1, 50, 3, 9]), (160, [20, 7])], seed=20), variant)
     ref_o, ref_l, abs_ref = w.reference()
     g = w.cuda()
-    run(g)
+    run(g, **kw)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        o, lse = run(g)
+        o, lse = run(g, **kw)
     for _ in range(3):
         o.fill_(float("nan")), lse.fill_(float("nan"))
         graph.replay()
-        run(g)
+        run(g, **kw)
         assert_o_close(o, ref_o, abs_ref=abs_ref)
         assert_lse_close(lse, ref_l)
 
 
-@pytest.mark.parametrize("far", list(BOUNDS))
-def test_on_another_stream(far):
+@pytest.mark.parametrize("variant", list(VARIANTS))
+def test_on_another_stream(variant):
     w = shared_batch.make(16, 8, 1, [(900, rising(8, 1, 11))], seed=18)
     ref_o, ref_l, a = w.reference()
-    g = bounded(w, far).cuda()
+    w, kw = varied(w, variant)
+    g = w.cuda()
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
-    o, lse = run(g, stream=s)
+    o, lse = run(g, stream=s, **kw)
     s.synchronize()
+    assert_o_close(o, ref_o, abs_ref=a)
+    assert_lse_close(lse, ref_l)
+
+
+@pytest.mark.parametrize("ps", [1, 64])
+@pytest.mark.parametrize("own", [3, 500])
+def test_auto_takes_either_way(ps, own):
+    """Batches large enough for the choice to be made on the device, from their lengths: with little of
+    their own the shared keys are worth a pass of their own, with much they are not."""
+    w = shared_batch.make(16, 8, ps, [(1200, [own + i % 7 for i in range(40)]), (0, [own]),
+                                      (900, [own + i % 5 for i in range(30)])], seed=21)
+    ref_o, ref_l, a = w.reference()
+    g = w.cuda()
+    status = ops.new_status()
+    o, lse = run(g, status=status)
+    assert ops.read_status(status) == 0
     assert_o_close(o, ref_o, abs_ref=a)
     assert_lse_close(lse, ref_l)
 
@@ -287,3 +311,5 @@ def test_binding_refusals():
     with pytest.raises(ops.MsglError) as e:
         ops.attn_decode_shared(pool, *args, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     assert e.value.status == 6
+    with pytest.raises(KeyError):
+        ops.attn_decode_shared(pool, *args, sharing="maybe")
