@@ -143,17 +143,52 @@ __device__ __forceinline__ void add_row(const GroupRows &r, int i, BatchSums &s)
     }
 }
 
-// Whether the kernel that reads shared keys once for their group pays (whole nanoseconds, so that
-// every kernel of a call comes to the same answer).  Without it the split kernel reads them once a
-// request, which after the first comes out of L2: the call takes what HBM needs for the keys in the
-// pool or what L2 needs for all that are attended.  With it, HBM's time for the requests' own
-// keys, a fixed part (start, first tile, pieces, join) and the tiles.  Measured: 6.4 TB/s from
-// HBM, 10.5 TB/s from L2, 14 us, 1.5 us a tile and SM.
-__device__ __forceinline__ bool prefix_pays(const BatchSums &s, int hkv, int sms) {
-    const long long key = (long long)hkv * kHeadDim * 4;   // bytes
-    const long long through = max((s.own + s.shared) * key / 6400, s.all * key / 10500);
-    const long long prefix = s.own * key / 6400 + 14000 + (s.tiles & kTilesMask) * hkv * 1500 / sms;
-    return prefix < through;
+// What a call's kernels know of each other's cost (whole nanoseconds, so that all of them come to
+// the same answer).  Measured: HBM gives 6.4 TB/s; a split CTA starts within 5 us, takes a 16-key tile
+// of its heads in tile_ns (0.93 us for page boxes, the per-key copies' 39 GB/s an SM below page size
+// 16) out of L2 or HBM, and 0.6 us more for every request it begins; a prefix CTA takes 8 us to its
+// first scores and out of its last piece, 1.55 us for a key tile (2.35 us while the other SMs
+// saturate HBM) and 2.5 us for every item it begins.
+struct ShareModel {
+    int32_t sms;               // CTAs of the prefix grid, one an SM
+    int32_t gx, ngr;           // the split's grid: key ranges, groups of kv heads
+    int32_t tile_ns;
+    int32_t always;            // MSGL_SHARE_ALWAYS
+};
+
+// The SMs' shares: `prefix` of them take the groups' shared keys, the others the requests' own
+// (`split` key ranges for each group of heads).  prefix = 0: the split takes all keys, the shared
+// ones once a request.
+struct Share {
+    int32_t prefix, split;
+};
+
+// Sharing reads less but has two kernels to feed, so each gets SMs of its own: the split is bound
+// by HBM with two thirds of them, and the prefix kernel's fixed cost is paid by the others only.
+// Every lane prices some of the partitions; the cheapest one is taken, the one with fewer prefix
+// CTAs (fewer pieces to join) among equals.
+__device__ __forceinline__ Share share_plan(const BatchSums &s, const ShareModel &m, int hkv, int num_reqs) {
+    const long long units = (s.tiles & kTilesMask) * hkv, items = (s.tiles >> kPairShift) * hkv;
+    if (m.sms == 0 || units == 0) return Share{0, m.gx};
+    auto ns = [](long long x) -> uint32_t { return (uint32_t)min(x, 1ll << 30); };
+    const uint32_t hbm = ns((s.own + s.shared) * (hkv * kHeadDim * 4) / 6400);
+    // (a request's own keys end in a tile that is half empty on average)
+    const uint32_t own = ns((s.own / 16 + num_reqs / 2) * m.tile_ns + num_reqs * 600ll);
+    const uint32_t all = ns((s.all / 16 + num_reqs / 2) * m.tile_ns + num_reqs * 600ll);
+    const uint32_t pre = ns(units * 1550 + items * 2500), crowded = ns(units * 800);
+    uint32_t best = 0xffffffffu;   // time in units of 128 ns, then the prefix CTAs
+    for (int p = 1 + (threadIdx.x & 31); p <= m.sms - m.ngr; p += 32) {
+        const uint32_t k = min((m.sms - p) / m.ngr, m.gx);
+        const uint32_t t = max(8000 + (pre + crowded / 100 * min(m.sms - p, 100)) / p, 5000 + max(hbm, own / k));
+        best = min(best, (min(t, (1u << 30) - 1) >> 7) << 8 | p);
+    }
+    best = __reduce_min_sync(0xffffffffu, best);
+    const uint32_t through = 5000 + max(hbm, all / m.gx);
+    // (3 us for the pieces that sharing adds to the join)
+    if (best == 0xffffffffu || (!m.always && through <= (best >> 8 << 7) + 3000))
+        return m.always ? Share{m.sms, m.gx} : Share{0, m.gx};
+    const int p = best & 255;
+    return Share{p, min((m.sms - p) / m.ngr, m.gx)};
 }
 
 // A batch as one block sees it: thread i has rows [b0, b1) = [i * k, (i + 1) * k).  `before` counts

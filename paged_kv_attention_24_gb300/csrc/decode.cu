@@ -79,8 +79,8 @@ struct DecodeKernelArgs {
     const __nv_bfloat16 *k_new, *v_new;
     const int32_t *new_loc;
     const int32_t *group_start, *shared_lens;   // kGrouped
-    int32_t pair_rows, prefix_ctas;             // prefix_ctas = 0: no shared-prefix kernel in this call
-    bool prefix_always;
+    int32_t pair_rows;
+    ShareModel share;                           // sms = 0: no shared-prefix kernel in this call
 };
 
 __device__ __forceinline__ long long warp_incl_scan(long long v, int lane) {
@@ -174,14 +174,17 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
     __shared__ int s_row;
     long long total = 0;
     bool own_only = false;
+    int ranges = gridDim.x;   // the batch's keys are cut into
     if constexpr (kMode == kGrouped) {
         BatchScan batch;
         scan_batch<kMaxHeadGroup + 1>(group_rows_of(a), s_scan, batch);
-        own_only = a.prefix_ctas > 0 && (a.prefix_always || prefix_pays(batch.total, a.pool.hkv, a.prefix_ctas));
+        const Share share = share_plan(batch.total, a.share, a.pool.hkv, a.num_reqs);
+        own_only = share.prefix > 0;
+        ranges = share.split;
         total = own_only ? batch.total.own : batch.total.all;
         const long long at = own_only ? batch.before.own : batch.before.all;
         const long long n = own_only ? batch.mine.own : batch.mine.all;
-        const long long r0 = keys_per_cta(total, gridDim.x) * blockIdx.x;
+        const long long r0 = keys_per_cta(total, ranges) * blockIdx.x;
         if (r0 < total && at <= r0 && r0 < at + n) {
             s_row = batch.b0;
             s_base = at;
@@ -201,7 +204,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
         }
-        const long long P = gridDim.x;
+        const long long P = ranges;
         const long long per = keys_per_cta(total, P);
         const long long r0 = per * blockIdx.x;
         const long long r1 = min(total, r0 + per);
@@ -453,7 +456,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
         // Behind the shared-prefix kernel by programmatic dependent launch: the last CTA ends after
         // that kernel has, so what comes behind this grid sees both kernels' partials.
         if constexpr (kMode == kGrouped) {
-            if (a.prefix_ctas > 0 && lane == 0 && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1)
+            if (a.share.sms > 0 && lane == 0 && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1)
                 asm volatile("griddepcontrol.wait;" ::: "memory");
         }
     } else if (warp < n_consumers) {
@@ -831,7 +834,15 @@ DecodePlan plan_decode(int32_t num_reqs, int32_t hq, int32_t hkv, int32_t max_se
     return p;
 }
 
-int decode_split_ctas(int32_t hq, int32_t hkv) { return decode_launch_shape(hkv, decode_slices(hq / hkv), false).ctas; }
+ShareModel decode_split_model(int32_t hq, const PoolView &pool) {
+    const bool box = (1 << pool.log2_ps) >= kTileKeys;
+    const Launch l = decode_launch_shape(pool.hkv, decode_slices(hq / pool.hkv), box);
+    ShareModel m{};
+    m.gx = l.ctas;
+    m.ngr = pool.hkv / l.hg;
+    m.tile_ns = box || l.hg < 5 ? 930 : 210 * l.hg;
+    return m;
+}
 
 cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, cudaStream_t stream, DecodePhase phase) {
     if (a.num_reqs == 0) return cudaSuccess;
@@ -896,8 +907,8 @@ cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, cudaStrea
     k.group_start = a.group_start;
     k.shared_lens = a.shared_lens;
     k.pair_rows = a.pair_rows;
-    k.prefix_ctas = a.prefix_ctas;
-    k.prefix_always = a.prefix_always;
+    k.share = a.share;
+    if (k.share.sms == 0) k.share.gx = L.ctas;
     (void)plan;
     if (L.smem > (size_t)kSmemBudget) return cudaErrorInvalidValue;
     if (phase != DecodePhase::kMerge) {
@@ -906,7 +917,7 @@ cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, cudaStrea
                           ? (box ? decode_split_kernel<true, kGrouped> : decode_split_kernel<false, kGrouped>)
                           : (box ? decode_split_kernel<true, kPlain> : decode_split_kernel<false, kPlain>);
         const int threads = 32 * (L.hg * slices + 1);
-        if (a.prefix_ctas > 0) {
+        if (a.share.sms > 0) {
             // behind the shared-prefix kernel: SMs that it leaves free start at once
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = grid;

@@ -35,19 +35,11 @@ namespace {
 // A group's rows are cut into pairs of Q tiles: a tile packs R = 128 / G rows x the G q
 // heads of a kv head, a pair 2R rows.  A unit of work is one 128-key tile for one pair and
 // kv head; units are numbered pair by pair (in row order), head by head, tile by tile, and
-// CTA c takes units [c * per, (c + 1) * per).
+// CTA c takes units [c * per, (c + 1) * per).  share_plan() says how many CTAs have any.
 
 constexpr int kRows = 128;                 // rows per Q tile (MMA M)
 constexpr int kKeys = kPrefixTileKeys;     // keys per K/V tile
 constexpr int kMaxPrefixCtas = 160;        // bound on the grid, sizes the workspace
-constexpr int kMinUnits = 4;               // K/V tiles per CTA at least, where the pairs have as many
-
-// An equal share each, but (a small batch) not less than kMinUnits, so that there are few pieces to
-// join, nor than an average item's units, because a CTA gains nothing from beginning a second.
-__device__ __forceinline__ long long units_per_cta(long long units, long long items, long long ctas) {
-    const long long share = (units + ctas - 1) / ctas;
-    return max(share, min((long long)kMinUnits, (units + items - 1) / max(items, 1ll)));
-}
 
 // ------------------------------------------------------------- prefix kernel
 constexpr int kStages = 2;                 // K tiles in flight
@@ -95,8 +87,8 @@ struct PrefixArgs {
     PoolView pool;
     PageView pages;
     GroupRows rows;
-    int32_t hq, group, rows_per_tile, q_box_rows, oob_row, box_rows, v_blocks, split_ctas;
-    bool always;               // MSGL_SHARE_ALWAYS
+    int32_t hq, group, rows_per_tile, q_box_rows, oob_row, box_rows, v_blocks;
+    ShareModel share;
     float scale_log2;
     float *o, *lse;            // [num_reqs, hq, 128], [num_reqs, hq]: pieces that begin at the first key
     float *cont_o, *cont_lse;  // [CTA, 2, 128, 128], [CTA, 2, 128]: a CTA's piece that begins later
@@ -250,10 +242,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- this CTA's units; none when the split kernel takes the shared keys too
     BatchScan batch;
     scan_batch<kThreads / 32>(rows, scratch, batch);
-    const bool pays = a.always || prefix_pays(batch.total, hkv, gridDim.x);
+    const Share share = share_plan(batch.total, a.share, hkv, rows.num_reqs);
+    const bool pays = share.prefix > 0;
     const long long before = (batch.before.tiles & kTilesMask) * hkv, mine = (batch.mine.tiles & kTilesMask) * hkv;
     const long long units = pays ? (batch.total.tiles & kTilesMask) * hkv : 0;
-    const long long per = units_per_cta(units, (batch.total.tiles >> kPairShift) * hkv, gridDim.x);
+    const long long per = pays ? (units + share.prefix - 1) / share.prefix : 1;
     const long long u0 = per * blockIdx.x, u1 = min(units, u0 + per);
     // the warp whose rows hold the first unit lays out the first segments
     const unsigned owner = __ballot_sync(0xffffffffu, u0 < u1 && before <= u0 && u0 < before + mine);
@@ -271,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (last_cta) {
         // the rows' places among the pieces, for the merge
-        const long long split_per = keys_per_cta(pays ? batch.total.own : batch.total.all, a.split_ctas);
+        const long long split_per = keys_per_cta(pays ? batch.total.own : batch.total.all, share.split);
         long long at = pays ? batch.before.own : batch.before.all, unit = before;
         for (int b = batch.b0; b < batch.b1; ++b) {
             a.plan[b].unit = unit;
@@ -977,14 +970,15 @@ cudaError_t launch_decode_shared(const DecodeSharedArgs &a, cudaStream_t stream)
     const int hkv = d.pool.hkv, G = d.hq / hkv, R = kRows / G;
     const DecodePlan plan = plan_decode(d.num_reqs, d.hq, hkv, d.max_seq_len);
     d.pair_rows = 2 * R;
-    // Small batches: with at most kThroughBytes of K/V to attend, prefix_pays() cannot say yes, so its
-    // kernel is left out.
+    // Small batches: with at most kThroughBytes of K/V to attend, sharing cannot win back what its
+    // kernel costs, which is left out.
     const bool small =
         d.num_reqs == 1 || (long long)d.num_reqs * d.max_seq_len * hkv * kHeadDim * 4 <= kThroughBytes;
     if (a.sharing == MSGL_SHARE_NEVER || (a.sharing == MSGL_SHARE_AUTO && small))
         return takes_short(d) ? launch_decode_short(d, stream) : launch_decode(d, plan, stream);
-    d.prefix_always = a.sharing == MSGL_SHARE_ALWAYS;
-    d.prefix_ctas = sm_count() < kMaxPrefixCtas ? sm_count() : kMaxPrefixCtas;
+    d.share = decode_split_model(d.hq, d.pool);
+    d.share.sms = sm_count() < kMaxPrefixCtas ? sm_count() : kMaxPrefixCtas;
+    d.share.always = a.sharing == MSGL_SHARE_ALWAYS;
     const Layout l = layout_of(d.num_reqs, d.hq, hkv);
     char *ws = static_cast<char *>(a.workspace);
     AttnMaps m;
@@ -1010,7 +1004,7 @@ cudaError_t launch_decode_shared(const DecodeSharedArgs &a, cudaStream_t stream)
     p.oob_row = m.oob_row;
     p.box_rows = m.box_rows;
     p.v_blocks = m.v_blocks;
-    p.always = d.prefix_always;
+    p.share = d.share;
     p.scale_log2 = d.scale * kLog2e;
     p.o = reinterpret_cast<float *>(ws + l.pre_o);
     p.lse = reinterpret_cast<float *>(ws + l.pre_lse);
@@ -1018,9 +1012,8 @@ cudaError_t launch_decode_shared(const DecodeSharedArgs &a, cudaStream_t stream)
     p.cont_lse = reinterpret_cast<float *>(ws + l.cont_lse);
     p.per_cta = reinterpret_cast<int64_t *>(ws + l.plan);
     p.plan = reinterpret_cast<RowPlan *>(ws + l.plan + 256);
-    p.split_ctas = decode_split_ctas(d.hq, hkv);
     p.status = d.status;
-    const int ctas = d.prefix_ctas;
+    const int ctas = d.share.sms;
     prefix_tc_kernel<<<ctas, kThreads, kSmemBytes, stream>>>(m.q, m.k, m.v, m.kt, m.vt, p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;

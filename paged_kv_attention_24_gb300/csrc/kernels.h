@@ -39,18 +39,17 @@ struct DecodeArgs {
     const __nv_bfloat16 *k_new = nullptr, *v_new = nullptr;   // append mode (see msgl_attn_decode_append)
     const int32_t *new_loc = nullptr;
     // groups over shared prefixes (see msgl_attn_decode_shared): shared keys are read through the
-    // group's first row, or, where that pays, left to the shared-prefix kernel of prefix_ctas
-    // CTAs behind which the split is then launched (split phase only)
+    // group's first row, or, where that pays, left to the shared-prefix kernel behind which the
+    // split is then launched (split phase only, share.sms > 0)
     const int32_t *group_start = nullptr, *shared_lens = nullptr;
     int32_t pair_rows = 0;      // rows of a pair of its Q tiles
-    int32_t prefix_ctas = 0;
-    bool prefix_always = false;
+    ShareModel share{};
 };
 // Which kernels of a decode call to launch: the split (partials per key range), the
 // merge (LSE fold of the partials, launched with programmatic dependent launch), or both.
 enum class DecodePhase { kSplit, kMerge, kBoth };
-// Key ranges (CTAs) of the split kernel for hq / hkv heads.
-int decode_split_ctas(int32_t hq, int32_t hkv);
+// The split kernel's grid and speed for these heads and pages (sms and always are not set).
+ShareModel decode_split_model(int32_t hq, const PoolView &pool);
 cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, cudaStream_t stream,
                           DecodePhase phase = DecodePhase::kBoth);
 
