@@ -153,7 +153,10 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(patch + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g0 = blockIdx.y * hg;   // first kv head of this CTA
+    // which key range, of which group of kv heads (kGrouped: the groups of a range are neighbours in
+    // the grid, because CTAs past the last range in use would keep the others waiting)
+    const int range = kMode == kGrouped ? blockIdx.y : blockIdx.x;
+    const int g0 = (kMode == kGrouped ? blockIdx.x : blockIdx.y) * hg;   // first kv head of this CTA
     // let the merge kernel launch now; it waits for this grid before reading partials
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -174,7 +177,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
     __shared__ int s_row;
     long long total = 0;
     bool own_only = false;
-    int ranges = gridDim.x;   // the batch's keys are cut into
+    int ranges = gridDim.x;   // that the batch's keys are cut into
     if constexpr (kMode == kGrouped) {
         BatchScan batch;
         scan_batch<kMaxHeadGroup + 1>(group_rows_of(a), s_scan, batch);
@@ -184,7 +187,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
         total = own_only ? batch.total.own : batch.total.all;
         const long long at = own_only ? batch.before.own : batch.before.all;
         const long long n = own_only ? batch.mine.own : batch.mine.all;
-        const long long r0 = keys_per_cta(total, ranges) * blockIdx.x;
+        const long long r0 = keys_per_cta(total, ranges) * range;
         if (r0 < total && at <= r0 && r0 < at + n) {
             s_row = batch.b0;
             s_base = at;
@@ -206,7 +209,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
         }
         const long long P = ranges;
         const long long per = keys_per_cta(total, P);
-        const long long r0 = per * blockIdx.x;
+        const long long r0 = per * range;
         const long long r1 = min(total, r0 + per);
         int it = 0;
         int first_key, own_from;
@@ -245,9 +248,34 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
                 }
                 base += tot;
             }
+            // kGrouped: a batch of short requests would wait for each one's numbers and first page id
+            // in turn, so the lanes look up those of 32 requests at once
+            int info_b = INT_MIN / 2, info_n = 0, info_first = 0, info_from = 0, info_pid = -1;
             long long pos = r0;
             while (b >= 0 && b < B && pos < r1 && !aborted) {
-                const int sb = range_keys<kMode>(a, b, own_only, first_key, own_from);
+                int sb, first_pid = -1;
+                if constexpr (kMode == kGrouped) {
+                    if (b >= info_b + 32) {
+                        info_b = b;
+                        const int row = b + lane;
+                        info_n = info_first = info_from = 0;
+                        info_pid = -1;
+                        if (row < B) info_n = range_keys<kMode>(a, row, own_only, info_first, info_from);
+                        if (kBox && info_n > 0) {
+                            const int pidx = info_first >> a.pool.log2_ps;
+                            const int from = info_first < info_from ? __ldg(a.group_start + row) : row;
+                            if (pidx < a.pages.width)
+                                info_pid = __ldg(a.pages.ids + (int64_t)from * a.pages.stride + pidx);
+                        }
+                    }
+                    const int l = b - info_b;
+                    sb = __shfl_sync(0xffffffffu, info_n, l);
+                    first_key = __shfl_sync(0xffffffffu, info_first, l);
+                    own_from = __shfl_sync(0xffffffffu, info_from, l);
+                    first_pid = __shfl_sync(0xffffffffu, info_pid, l);
+                } else {
+                    sb = range_keys<kMode>(a, b, own_only, first_key, own_from);
+                }
                 const long long end_b = start_b + sb;
                 if (end_b > pos) {
                     const int lo = (int)(pos - start_b) + first_key;
@@ -270,7 +298,8 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
                         // [lo, hi) are loaded with the tile and masked.  Lane 0 does the work,
                         // with the next tile's page id looked up one tile ahead.
                         const int tlo = plo & ~(kTileKeys - 1);
-                        int pid_cur = lane == 0 ? load_pid(max(tlo, plo)) : -1;
+                        int pid_cur = -1;
+                        if (lane == 0) pid_cur = kMode == kGrouped && plo == first_key ? first_pid : load_pid(max(tlo, plo));
                         for (int t0 = tlo; t0 < phi; t0 += kTileKeys) {
                             const int stage = it % S, round = it / S;
                             const int t1 = t0 + kTileKeys;
@@ -283,7 +312,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
                                 const uint32_t full_bar = ptx::smem_u32(full + stage);
                                 TileMeta &md = meta[stage];
                                 md.b = b;
-                                md.slot = b + (int)blockIdx.x;
+                                md.slot = b + range;
                                 md.n = khi - klo;
                                 md.flags = (t0 == tlo && plo == lo ? kFirst : 0) | (t1 >= phi && phi == hi ? kLast : 0) | (ok ? 0 : kBad);
                                 md.mask = ok ? keys : 0u;
@@ -384,7 +413,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
                         if (lane == 0) {
                             TileMeta &md = meta[stage];
                             md.b = b;
-                            md.slot = b + (int)blockIdx.x;
+                            md.slot = b + range;
                             md.n = n;
                             md.flags = (t0 == lo ? kFirst : 0) | (t0 + kTileKeys >= hi ? kLast : 0) |
                                        (badm ? kBad : 0);
@@ -912,7 +941,7 @@ cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, cudaStrea
     (void)plan;
     if (L.smem > (size_t)kSmemBudget) return cudaErrorInvalidValue;
     if (phase != DecodePhase::kMerge) {
-        dim3 grid(L.ctas, hkv / L.hg);
+        const dim3 grid = a.group_start ? dim3(hkv / L.hg, L.ctas) : dim3(L.ctas, hkv / L.hg);
         auto kernel = a.group_start
                           ? (box ? decode_split_kernel<true, kGrouped> : decode_split_kernel<false, kGrouped>)
                           : (box ? decode_split_kernel<true, kPlain> : decode_split_kernel<false, kPlain>);

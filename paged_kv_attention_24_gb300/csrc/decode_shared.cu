@@ -200,6 +200,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int hkv = a.pool.hkv;
     const int R = a.rows_per_tile, G = a.group;
 
+    // ---- this CTA's units; none when the split kernel takes the shared keys too
+    BatchScan batch;
+    scan_batch<kThreads / 32>(rows, scratch, batch);
+    const Share share = share_plan(batch.total, a.share, hkv, rows.num_reqs);
+    const bool pays = share.prefix > 0;
+    const long long before = (batch.before.tiles & kTilesMask) * hkv, mine = (batch.mine.tiles & kTilesMask) * hkv;
+    const long long units = pays ? (batch.total.tiles & kTilesMask) * hkv : 0;
+    const long long per = pays ? (units + share.prefix - 1) / share.prefix : 1;
+    const long long u0 = per * blockIdx.x, u1 = min(units, u0 + per);
+    // (a CTA with nothing to do frees its SM for the split as soon as it can; the last one lays out
+    // the merge's plan)
+    if (u0 >= u1 && !last_cta) return;
+
     if (threadIdx.x == 0) {
         ptx::mbar_init(bar(kQFull), 1);
         ptx::mbar_init(bar(kQEmpty), 1);
@@ -239,15 +252,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::fence_proxy_async_smem();
     }
 
-    // ---- this CTA's units; none when the split kernel takes the shared keys too
-    BatchScan batch;
-    scan_batch<kThreads / 32>(rows, scratch, batch);
-    const Share share = share_plan(batch.total, a.share, hkv, rows.num_reqs);
-    const bool pays = share.prefix > 0;
-    const long long before = (batch.before.tiles & kTilesMask) * hkv, mine = (batch.mine.tiles & kTilesMask) * hkv;
-    const long long units = pays ? (batch.total.tiles & kTilesMask) * hkv : 0;
-    const long long per = pays ? (units + share.prefix - 1) / share.prefix : 1;
-    const long long u0 = per * blockIdx.x, u1 = min(units, u0 + per);
     // the warp whose rows hold the first unit lays out the first segments
     const unsigned owner = __ballot_sync(0xffffffffu, u0 < u1 && before <= u0 && u0 < before + mine);
     if (owner) {
