@@ -176,19 +176,22 @@ __device__ __forceinline__ Share share_plan(const BatchSums &s, const ShareModel
     const uint32_t own = ns((s.own / 16 + num_reqs / 2) * m.tile_ns + num_reqs * 600ll);
     const uint32_t all = ns((s.all / 16 + num_reqs / 2) * m.tile_ns + num_reqs * 600ll);
     const uint32_t pre = ns(units * 1550 + items * 2500), crowded = ns(units * 800);
+    // (32 candidates, closer together where there are few: a CTA more or less matters most there)
     uint32_t best = 0xffffffffu;   // time in units of 128 ns, then the prefix CTAs
-    for (int p = 1 + (threadIdx.x & 31); p <= m.sms - m.ngr; p += 32) {
+    const int lane = threadIdx.x & 31, most = m.sms - m.ngr;
+    const int p = 1 + lane + max(most - 32, 0) * lane * lane / 961;
+    if (p <= most) {
         const uint32_t k = min((m.sms - p) / m.ngr, m.gx);
         const uint32_t t = max(8000 + (pre + crowded / 100 * min(m.sms - p, 100)) / p, 5000 + max(hbm, own / k));
-        best = min(best, (min(t, (1u << 30) - 1) >> 7) << 8 | p);
+        best = (min(t, (1u << 30) - 1) >> 7) << 8 | p;
     }
     best = __reduce_min_sync(0xffffffffu, best);
     const uint32_t through = 5000 + max(hbm, all / m.gx);
     // (3 us for the pieces that sharing adds to the join)
     if (best == 0xffffffffu || (!m.always && through <= (best >> 8 << 7) + 3000))
         return m.always ? Share{m.sms, m.gx} : Share{0, m.gx};
-    const int p = best & 255;
-    return Share{p, min((m.sms - p) / m.ngr, m.gx)};
+    const int n = best & 255;
+    return Share{n, min((m.sms - n) / m.ngr, m.gx)};
 }
 
 // A batch as one block sees it: thread i has rows [b0, b1) = [i * k, (i + 1) * k).  `before` counts
@@ -199,7 +202,6 @@ struct BatchScan {
     BatchSums before, mine, total;
 };
 
-template <int kMaxWarps>
 __device__ __forceinline__ void scan_batch(const GroupRows &r, long long (*scratch)[4], BatchScan &s) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, threads = blockDim.x;
     const int k = (r.num_reqs + threads - 1) / threads;
@@ -207,11 +209,13 @@ __device__ __forceinline__ void scan_batch(const GroupRows &r, long long (*scrat
     s.b1 = min(r.num_reqs, s.b0 + k);
     s.mine = BatchSums{0, 0, 0, 0};
     for (int b = s.b0; b < s.b1; ++b) add_row(r, b, s.mine);
+    // (rolled loops: this runs at the start of every CTA, where each line of code not yet in the
+    // instruction cache costs more than the loop)
     long long x[4] = {s.mine.all, s.mine.own, s.mine.tiles, s.mine.shared};
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
+        for (int i = 0; i < 4; ++i) {
             const long long u = __shfl_up_sync(0xffffffffu, x[i], o);
             if (lane >= o) x[i] += u;
         }
@@ -219,23 +223,17 @@ __device__ __forceinline__ void scan_batch(const GroupRows &r, long long (*scrat
 #pragma unroll
         for (int i = 0; i < 4; ++i) scratch[warp][i] = x[i];
     __syncthreads();
-    long long before[4], total[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        before[i] = x[i];
-        total[i] = 0;
-    }
+    long long total[4] = {0, 0, 0, 0};
     const int warps = threads >> 5;
+#pragma unroll 1
+    for (int w = 0; w < warps; ++w)
 #pragma unroll
-    for (int w = 0; w < kMaxWarps; ++w)
-        if (w < warps)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const long long y = scratch[w][i];
-                total[i] += y;
-                if (w < warp) before[i] += y;
-            }
-    s.before = BatchSums{before[0] - s.mine.all, before[1] - s.mine.own, 0, before[2] - s.mine.tiles};
+        for (int i = 0; i < 4; ++i) {
+            const long long y = scratch[w][i];
+            total[i] += y;
+            if (w < warp) x[i] += y;
+        }
+    s.before = BatchSums{x[0] - s.mine.all, x[1] - s.mine.own, 0, x[2] - s.mine.tiles};
     s.total = BatchSums{total[0], total[1], total[3], total[2]};
 }
 

@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
     int ranges = gridDim.x;   // that the batch's keys are cut into
     if constexpr (kMode == kGrouped) {
         BatchScan batch;
-        scan_batch<kMaxHeadGroup + 1>(group_rows_of(a), s_scan, batch);
+        scan_batch(group_rows_of(a), s_scan, batch);
         const Share share = share_plan(batch.total, a.share, a.pool.hkv, a.num_reqs);
         own_only = share.prefix > 0;
         ranges = share.split;

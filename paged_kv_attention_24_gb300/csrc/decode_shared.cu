@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // ---- this CTA's units; none when the split kernel takes the shared keys too
     BatchScan batch;
-    scan_batch<kThreads / 32>(rows, scratch, batch);
+    scan_batch(rows, scratch, batch);
     const Share share = share_plan(batch.total, a.share, hkv, rows.num_reqs);
     const bool pays = share.prefix > 0;
     const long long before = (batch.before.tiles & kTilesMask) * hkv, mine = (batch.mine.tiles & kTilesMask) * hkv;
