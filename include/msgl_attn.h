@@ -409,7 +409,8 @@ MSGL_API msgl_status msgl_shared_prefixes(const msgl_page_table *pages, const in
  * MSGL_DEVERR_GROUP and is written as o = 0, lse = -inf, and so may be the rows
  * of its group behind it; a bad page among the shared keys does that to every
  * row of the group (MSGL_DEVERR_PAGE_RANGE).
- * The launch shapes depend on host scalars only.
+ * At most 65535 requests, max_seq_len at most 2^30.  The launch shapes depend on
+ * host scalars only.
  */
 #define MSGL_SHARE_AUTO 0
 #define MSGL_SHARE_ALWAYS 1
@@ -482,6 +483,29 @@ MSGL_API msgl_status msgl_check_extend_meta(int64_t num_slots, int32_t page_size
 MSGL_API msgl_status msgl_check_decode_meta(int64_t num_slots, int32_t page_size, const int32_t *page_ids,
                                             int32_t stride, int32_t width, const int32_t *seq_lens,
                                             int32_t num_reqs, int32_t max_seq_len);
+
+/*
+ * The same for the arguments of msgl_step_tables and msgl_attn_decode_shared
+ * (host copies of the arrays, nothing launched):
+ *
+ * msgl_check_step_meta:  rows in range and none twice, lengths >= 0, every
+ *   request within the table's width, the pages of its cached tokens in the
+ *   pool, total_tokens and num_free large enough, and every free page that the
+ *   step takes in the pool and not in use by a request of the step.
+ * msgl_check_groups_meta:  the rules of group_start and shared_lens, 1 <=
+ *   seq_lens[b] <= max_seq_len, and the pages of the keys as they are read
+ *   (shared ones through the group's first row) in range.
+ */
+MSGL_API msgl_status msgl_check_step_meta(int64_t num_slots, int32_t page_size, const int32_t *req_table,
+                                          int32_t num_rows, int32_t table_stride, int32_t table_width,
+                                          const int32_t *req_rows, const int32_t *cached_lens,
+                                          const int32_t *new_lens, int32_t num_reqs, const int32_t *free_pages,
+                                          int32_t num_free, int32_t total_tokens);
+
+MSGL_API msgl_status msgl_check_groups_meta(int64_t num_slots, int32_t page_size, const int32_t *page_ids,
+                                            int32_t stride, int32_t width, const int32_t *group_start,
+                                            const int32_t *shared_lens, const int32_t *seq_lens, int32_t num_reqs,
+                                            int32_t max_seq_len);
 
 /* Static description of a status code. */
 MSGL_API const char *msgl_status_string(msgl_status s);

@@ -448,19 +448,21 @@ msgl_status msgl_attn_decode_shared(const msgl_kv_pool *pool, const msgl_page_ta
     g_last_error[0] = 0;
     if (sharing < MSGL_SHARE_AUTO || sharing > MSGL_SHARE_NEVER)
         return fail(MSGL_ERR_INVALID_ARG, "sharing %d is not one of MSGL_SHARE_*", sharing);
-    // the workspace it needs includes a decode's, so the decode's check passes when this one does
-    if (num_reqs > 0 && pool && pool->num_kv_heads > 0 && num_q_heads > 0) {
-        if (!group_start || !shared_lens)
-            return fail(MSGL_ERR_INVALID_ARG, "group_start and shared_lens must be non-NULL");
+    if (num_reqs > 0 && (!group_start || !shared_lens))
+        return fail(MSGL_ERR_INVALID_ARG, "group_start and shared_lens must be non-NULL");
+    if (num_reqs > 65535) return fail(MSGL_ERR_UNSUPPORTED, "more than 65535 requests");
+    if (max_seq_len > (1 << 30)) return fail(MSGL_ERR_UNSUPPORTED, "max_seq_len may not pass 2^30");
+    msgl::DecodeSharedArgs a;
+    msgl::DecodePlan plan{};
+    msgl_status s = prepare_decode(pool, pages, q, num_q_heads, nullptr, nullptr, nullptr, seq_lens, num_reqs,
+                                   max_seq_len, scale, o, lse, workspace, workspace_bytes, status, a.dec, plan);
+    if (num_reqs > 0 && (!s || s == MSGL_ERR_WORKSPACE)) {
+        // (a decode's workspace is part of it)
         const size_t need = msgl::decode_shared_workspace_bytes(num_reqs, num_q_heads, pool->num_kv_heads);
         if (!workspace || workspace_bytes < need)
             return fail(MSGL_ERR_WORKSPACE, "decode_shared needs %zu workspace bytes, got %zu", need,
                         workspace ? workspace_bytes : (size_t)0);
     }
-    msgl::DecodeSharedArgs a;
-    msgl::DecodePlan plan{};
-    msgl_status s = prepare_decode(pool, pages, q, num_q_heads, nullptr, nullptr, nullptr, seq_lens, num_reqs,
-                                   max_seq_len, scale, o, lse, workspace, workspace_bytes, status, a.dec, plan);
     if (s || num_reqs == 0) return s;
     a.dec.group_start = group_start;
     a.dec.shared_lens = shared_lens;

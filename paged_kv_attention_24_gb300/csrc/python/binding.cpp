@@ -61,8 +61,11 @@ int32_t size32(int64_t v, const char *name) {
     return (int32_t)v;
 }
 
-uint32_t *status_ptr(PyObject *o) {
-    return o == Py_None ? nullptr : static_cast<uint32_t *>(tensor(o, "status").data_ptr());
+uint32_t *status_ptr(PyObject *o, int dev) {
+    if (o == Py_None) return nullptr;
+    const at::Tensor &t = checked(o, "status", at::kInt, dev);
+    if (t.numel() < 1) refuse("%s must have an entry", "status");
+    return static_cast<uint32_t *>(t.data_ptr());
 }
 
 // The device's current stream, or the one given (as the integer of its handle).
@@ -73,8 +76,20 @@ c10::cuda::CUDAStream stream_of(PyObject *o, int dev) {
     return c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(p), dev);
 }
 
-at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, int dev) {
-    return at::detail::empty_cuda(sizes, type, c10::Device(c10::kCUDA, (c10::DeviceIndex)dev), c10::nullopt);
+// A new tensor in `stream`'s order.  When the caller named a stream other than the current one, the
+// tensor's memory also waits for the current one before it is used again.
+at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, int dev, const c10::cuda::CUDAStream &stream) {
+    const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev);
+    const c10::Device device(c10::kCUDA, (c10::DeviceIndex)dev);
+    if (current == stream) return at::detail::empty_cuda(sizes, type, device, c10::nullopt);
+    c10::cuda::setCurrentCUDAStream(stream);
+    struct Back {
+        c10::cuda::CUDAStream s;
+        ~Back() { c10::cuda::setCurrentCUDAStream(s); }
+    } back{current};
+    at::Tensor t = at::detail::empty_cuda(sizes, type, device, c10::nullopt);
+    c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), current);
+    return t;
 }
 
 msgl_stream_t raw(const c10::cuda::CUDAStream &s) { return reinterpret_cast<msgl_stream_t>(s.stream()); }
@@ -152,7 +167,7 @@ PyObject *step_tables(PyObject *, PyObject *const *a, Py_ssize_t n) {
         out.total_tokens = size32(pos.numel(), "positions");
         const int64_t slots = integer(a[4]);
         const int32_t ps = integer32(a[5], "page_size");
-        uint32_t *status = status_ptr(a[13]);
+        uint32_t *status = status_ptr(a[13], dev);
         c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
         return done(msgl_step_tables(slots, ps, i32(table), size32(table.size(0), "req_table"), W, W, rows, i32(cached),
                                      added, B, i32(free_pages), size32(free_pages.numel(), "free_pages"), &out, status,
@@ -172,17 +187,14 @@ PyObject *shared_prefixes(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int32_t ps = integer32(a[2], "page_size"), max_seq = integer32(a[3], "max_seq_len"),
                       min_shared = integer32(a[4], "min_shared");
         c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
-        const at::Tensor first = a[5] == Py_None ? fresh(seq.sizes(), at::kInt, dev) : checked(a[5], "group_start", at::kInt, dev);
-        const at::Tensor shared = a[6] == Py_None ? fresh(seq.sizes(), at::kInt, dev) : checked(a[6], "shared_lens", at::kInt, dev);
+        const c10::cuda::CUDAStream stream = stream_of(a[8], dev);
+        const at::Tensor first =
+            a[5] == Py_None ? fresh(seq.sizes(), at::kInt, dev, stream) : checked(a[5], "group_start", at::kInt, dev);
+        const at::Tensor shared =
+            a[6] == Py_None ? fresh(seq.sizes(), at::kInt, dev, stream) : checked(a[6], "shared_lens", at::kInt, dev);
         if (pages.dim() != 2 || pages.size(0) != B || first.numel() != B || shared.numel() != B)
             refuse("%s must be [B, width]; seq_lens, group_start and shared_lens [B]", "page_table");
-        uint32_t *status = status_ptr(a[7]);
-        const c10::cuda::CUDAStream stream = stream_of(a[8], dev);
-        if (a[8] != Py_None) {
-            // allocated for the current stream, used on this one
-            if (a[5] == Py_None) c10::cuda::CUDACachingAllocator::recordStream(first.storage().data_ptr(), stream);
-            if (a[6] == Py_None) c10::cuda::CUDACachingAllocator::recordStream(shared.storage().data_ptr(), stream);
-        }
+        uint32_t *status = status_ptr(a[7], dev);
         msgl_page_table pt;
         pt.page_ids = i32(pages);
         pt.stride = pt.width = size32(pages.size(1), "page_table");
@@ -220,7 +232,7 @@ PyObject *attn_decode_shared(PyObject *, PyObject *const *a, Py_ssize_t n) {
                       sharing = integer32(a[15], "sharing");
         const double scale = PyFloat_AsDouble(a[9]);
         if (scale == -1.0 && PyErr_Occurred()) throw Refused{};
-        uint32_t *status = status_ptr(a[13]);
+        uint32_t *status = status_ptr(a[13], dev);
         msgl_kv_pool pool;
         pool.k_pool = k.data_ptr();
         pool.v_pool = v.data_ptr();
@@ -234,15 +246,12 @@ PyObject *attn_decode_shared(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
         c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
         const c10::cuda::CUDAStream stream = stream_of(a[14], dev);
-        const at::Tensor out = a[10] == Py_None ? fresh(q.sizes(), at::kBFloat16, dev) : checked(a[10], "out", at::kBFloat16, dev);
-        const at::Tensor lse = a[11] == Py_None ? fresh({q.size(0), q.size(1)}, at::kFloat, dev)
+        const at::Tensor out = a[10] == Py_None ? fresh(q.sizes(), at::kBFloat16, dev, stream)
+                                                : checked(a[10], "out", at::kBFloat16, dev);
+        const at::Tensor lse = a[11] == Py_None ? fresh({q.size(0), q.size(1)}, at::kFloat, dev, stream)
                                                 : checked(a[11], "lse", at::kFloat, dev);
         if (out.sizes() != q.sizes()) refuse("%s must be [B, Hq, D]", "out");
         if (lse.dim() != 2 || lse.size(0) != B || lse.size(1) != hq) refuse("%s must be [B, Hq]", "lse");
-        if (a[14] != Py_None) {
-            if (a[10] == Py_None) c10::cuda::CUDACachingAllocator::recordStream(out.storage().data_ptr(), stream);
-            if (a[11] == Py_None) c10::cuda::CUDACachingAllocator::recordStream(lse.storage().data_ptr(), stream);
-        }
         // Scratch, when the caller brings none: from the caching allocator in the stream's order, and
         // back to it once the kernels are queued (its next user on the stream comes behind them).
         struct Scratch {

@@ -140,4 +140,88 @@ msgl_status msgl_check_decode_meta(int64_t num_slots, int32_t page_size, const i
     return MSGL_OK;
 }
 
+msgl_status msgl_check_step_meta(int64_t num_slots, int32_t page_size, const int32_t *req_table, int32_t num_rows,
+                                 int32_t table_stride, int32_t table_width, const int32_t *req_rows,
+                                 const int32_t *cached_lens, const int32_t *new_lens, int32_t num_reqs,
+                                 const int32_t *free_pages, int32_t num_free, int32_t total_tokens) {
+    msgl::set_last_error("");
+    msgl_status rc = check_pool_scalars(num_slots, page_size, req_table, table_stride, table_width);
+    if (rc) return rc;
+    if (num_reqs < 0 || num_rows < 0 || num_free < 0 || total_tokens < 0) return bad(MSGL_ERR_INVALID_ARG, "negative size");
+    if (num_reqs > 0 && !cached_lens) return bad(MSGL_ERR_INVALID_ARG, "cached_lens is NULL");
+    if (num_free > 0 && !free_pages) return bad(MSGL_ERR_INVALID_ARG, "free_pages is NULL");
+    const int64_t num_pages = num_slots / page_size;
+    std::unordered_set<int32_t> rows, used;
+    int64_t tokens = 0, taken = 0;
+    for (int32_t b = 0; b < num_reqs; ++b) {
+        const int32_t row = req_rows ? req_rows[b] : b, cached = cached_lens[b], fresh = new_lens ? new_lens[b] : 1;
+        if (row < 0 || row >= num_rows)
+            return bad(MSGL_ERR_OUT_OF_RANGE, "request %d: row %d is outside [0, %d)", b, row, num_rows);
+        if (!rows.insert(row).second)
+            return bad(MSGL_ERR_INVALID_ARG, "request %d: row %d belongs to an earlier request too", b, row);
+        if (cached < 0 || fresh < 0)
+            return bad(MSGL_ERR_INVALID_ARG, "request %d: cached_len %d and new_len %d must be >= 0", b, cached, fresh);
+        const int64_t old_pages = ((int64_t)cached + page_size - 1) / page_size;
+        const int64_t pages = ((int64_t)cached + fresh + page_size - 1) / page_size;
+        if (pages > table_width)
+            return bad(MSGL_ERR_OUT_OF_RANGE, "request %d: %lld tokens need %lld pages but the table width is %d", b,
+                       (long long)cached + fresh, (long long)pages, table_width);
+        if ((rc = check_pages(num_pages, page_size, req_table, table_stride, table_width, row, cached))) return rc;
+        for (int64_t p = 0; p < old_pages; ++p) used.insert(req_table[(int64_t)row * table_stride + p]);
+        tokens += fresh;
+        taken += pages - old_pages;
+        if (tokens > total_tokens)
+            return bad(MSGL_ERR_INVALID_ARG, "request %d: %lld tokens so far but total_tokens = %d", b,
+                       (long long)tokens, total_tokens);
+        if (taken > num_free)
+            return bad(MSGL_ERR_OUT_OF_RANGE, "request %d: %lld pages so far but num_free = %d", b, (long long)taken,
+                       num_free);
+    }
+    for (int64_t p = 0; p < taken; ++p) {
+        if (free_pages[p] < 0 || free_pages[p] >= num_pages)
+            return bad(MSGL_ERR_OUT_OF_RANGE, "free_pages[%lld] = %d is outside [0, %lld)", (long long)p, free_pages[p],
+                       (long long)num_pages);
+        if (!used.insert(free_pages[p]).second)
+            return bad(MSGL_ERR_INVALID_ARG, "free_pages[%lld] = %d is in use", (long long)p, free_pages[p]);
+    }
+    return MSGL_OK;
+}
+
+msgl_status msgl_check_groups_meta(int64_t num_slots, int32_t page_size, const int32_t *page_ids, int32_t stride,
+                                   int32_t width, const int32_t *group_start, const int32_t *shared_lens,
+                                   const int32_t *seq_lens, int32_t num_reqs, int32_t max_seq_len) {
+    msgl::set_last_error("");
+    msgl_status rc = check_pool_scalars(num_slots, page_size, page_ids, stride, width);
+    if (rc) return rc;
+    if (num_reqs < 0) return bad(MSGL_ERR_INVALID_ARG, "num_reqs must be >= 0");
+    if (num_reqs > 0 && (!group_start || !shared_lens || !seq_lens))
+        return bad(MSGL_ERR_INVALID_ARG, "group_start, shared_lens and seq_lens must be non-NULL");
+    const int64_t num_pages = num_slots / page_size;
+    for (int32_t b = 0; b < num_reqs; ++b) {
+        const int32_t first = group_start[b], n = seq_lens[b];
+        if (n < 1 || n > max_seq_len)
+            return bad(MSGL_ERR_INVALID_ARG, "request %d: seq_len %d is outside [1, max_seq_len = %d]", b, n, max_seq_len);
+        if (first != b && (b == 0 || first != group_start[b - 1]))
+            return bad(MSGL_ERR_INVALID_ARG, "request %d: group_start %d is neither %d nor the row's before", b, first, b);
+        const bool alone = first == b && (b + 1 == num_reqs || group_start[b + 1] != b);
+        const int32_t shared = alone ? 0 : shared_lens[b];
+        if (shared < 0 || shared > n)
+            return bad(MSGL_ERR_INVALID_ARG, "request %d: shared_len %d is outside [0, seq_len = %d]", b, shared, n);
+        if (first != b && shared != shared_lens[first])
+            return bad(MSGL_ERR_INVALID_ARG, "request %d: shared_len %d but its group's first has %d", b, shared,
+                       shared_lens[first]);
+        // shared keys on the first row's pages, the others on its own
+        if (first == b && (rc = check_pages(num_pages, page_size, page_ids, stride, width, b, n))) return rc;
+        if (((int64_t)n + page_size - 1) / page_size > width)
+            return bad(MSGL_ERR_OUT_OF_RANGE, "request %d: %d keys do not fit the table width %d", b, n, width);
+        for (int64_t p = shared / page_size; p * page_size < n; ++p) {
+            const int32_t id = page_ids[(int64_t)b * stride + p];
+            if (id < 0 || id >= num_pages)
+                return bad(MSGL_ERR_OUT_OF_RANGE, "request %d: page_ids[%lld] = %d is outside [0, %lld)", b,
+                           (long long)p, id, (long long)num_pages);
+        }
+    }
+    return MSGL_OK;
+}
+
 }  // extern "C"

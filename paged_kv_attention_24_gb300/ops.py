@@ -106,6 +106,8 @@ SIGNATURES = {
     "msgl_check_store_meta": ([I64, P, I32], ctypes.c_int),
     "msgl_check_extend_meta": ([I64, I32, P, I32, I32, P, P, P, P, I32, I32, I32, I32], ctypes.c_int),
     "msgl_check_decode_meta": ([I64, I32, P, I32, I32, P, I32, I32], ctypes.c_int),
+    "msgl_check_step_meta": ([I64, I32, P, I32, I32, I32, P, P, P, I32, P, I32, I32], ctypes.c_int),
+    "msgl_check_groups_meta": ([I64, I32, P, I32, I32, P, P, P, I32, I32], ctypes.c_int),
 }
 
 
@@ -553,3 +555,32 @@ def check_decode_meta(num_slots: int, page_size: int, page_table: torch.Tensor, 
     seq, seqp = _host_i32(seq_lens)
     _check(load().msgl_check_decode_meta(int(num_slots), int(page_size), ptp, w, w, seqp, seq.numel(),
                                          int(max_seq_len)), "msgl_check_decode_meta")
+
+
+def check_step_meta(num_slots: int, page_size: int, req_table: torch.Tensor, req_rows: Optional[torch.Tensor],
+                    cached_lens: torch.Tensor, new_lens: Optional[torch.Tensor], free_pages: torch.Tensor,
+                    total_tokens: int):
+    """Copies a step's request lengths and tables back and checks them (rows, pages, sizes).  Raises MsglError."""
+    rt, rtp, w = _table(req_table)
+    rows, rowsp = _host_i32(req_rows)
+    c, cp = _host_i32(cached_lens)
+    n, np_ = _host_i32(new_lens)
+    f, fp = _host_i32(free_pages)
+    for name, t in (("req_rows", rows), ("new_lens", n)):
+        if t is not None and t.numel() != c.numel():
+            raise ValueError(f"{name} must have one entry per request")
+    _check(load().msgl_check_step_meta(int(num_slots), int(page_size), rtp, rt.numel() // w if w else 0, w, w, rowsp,
+                                       cp, np_, c.numel(), fp, f.numel(), int(total_tokens)), "msgl_check_step_meta")
+
+
+def check_groups_meta(num_slots: int, page_size: int, page_table: torch.Tensor, seq_lens: torch.Tensor,
+                      group_start: torch.Tensor, shared_lens: torch.Tensor, max_seq_len: int):
+    """Copies a shared-prefix decode's metadata back and checks it (groups, lengths, pages).  Raises MsglError."""
+    pt, ptp, w = _table(page_table)
+    seq, seqp = _host_i32(seq_lens)
+    first, firstp = _host_i32(group_start)
+    shared, sharedp = _host_i32(shared_lens)
+    if first.numel() != seq.numel() or shared.numel() != seq.numel():
+        raise ValueError("group_start and shared_lens must have one entry per request")
+    _check(load().msgl_check_groups_meta(int(num_slots), int(page_size), ptp, w, w, firstp, sharedp, seqp, seq.numel(),
+                                         int(max_seq_len)), "msgl_check_groups_meta")
