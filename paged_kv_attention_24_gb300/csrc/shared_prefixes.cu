@@ -6,13 +6,13 @@
 // the least m of its joined rows (the common prefix of a run of rows is the
 // least of its neighbours' common prefixes).
 //
-// Bound by latency (a batch's tables are at most a few megabytes).  Up to kClusterEntries table
-// entries, one launch: a cluster of 8 blocks, a warp per row compares it with the row before (1024
-// columns a round, done at the first round with a difference), and behind the cluster's barrier
-// its first block finds each group's start and least m by scans over the rows.  Above that,
-// eight blocks' loads take longer than a second launch: a block per row compares (2048 columns a
-// round), and the scans are a kernel of their own behind it.  m travels in shared_lens, which the
-// scans overwrite, so the call needs no scratch.
+// Bound by latency (a batch's tables are at most a few megabytes).  Two kernels: one block
+// per row compares it with the row before, 4096 columns a round, done at the first round with a
+// difference; one block then finds each group's start and least m by scans over the rows.  m
+// travels in shared_lens, which the scans overwrite, so the call needs no scratch.  64 requests:
+// 3.5 us up to 1024 columns, 6.4 us for 16384 equal ones.  (One cluster of 8 blocks with a barrier
+// in place of the second launch: 5.2 and 41 us.  Blocks of 256 threads: the same up to 2048 columns,
+// 8.4 us for 16384; of 1024: 5.7 us there, but 9.0 in place of 6.3 us for 1024 requests.)
 #include <limits.h>
 
 #include "kernels.h"
@@ -21,7 +21,7 @@ namespace msgl {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kPerThread = 8;
 
 __device__ __forceinline__ bool row_ok(const SharedPrefixesArgs &a, int s) {
@@ -67,9 +67,10 @@ __global__ void __launch_bounds__(kThreads) row_match_kernel(const SharedPrefixe
 // atomicMin on the start row's entry, which holds no m of its own.
 constexpr int kScanThreads = 1024;
 
-__device__ __forceinline__ void group_rows(const SharedPrefixesArgs &a) {
+__global__ void __launch_bounds__(kScanThreads) row_groups_kernel(const SharedPrefixesArgs a) {
     __shared__ int warp_max[32];
     __shared__ int carry;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) carry = 0;
     __syncthreads();
@@ -107,57 +108,9 @@ __device__ __forceinline__ void group_rows(const SharedPrefixesArgs &a) {
         if (__ldcg(a.shared_lens + b) == INT_MAX) a.shared_lens[b] = 0;
 }
 
-__global__ void __launch_bounds__(kScanThreads) row_groups_kernel(const SharedPrefixesArgs a) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    group_rows(a);
-}
-
-constexpr int kCluster = 8;
-constexpr long long kClusterEntries = 1ll << 20;
-constexpr int kRound = 32;   // columns a lane has in flight
-
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScanThreads)
-    shared_prefixes_cluster_kernel(const SharedPrefixesArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int warps = kCluster * kScanThreads / 32;
-    for (int b = blockIdx.x * (kScanThreads / 32) + (threadIdx.x >> 5); b < a.num_reqs; b += warps) {
-        const int s1 = __ldg(a.seq_lens + b), s0 = b > 0 ? __ldg(a.seq_lens + b - 1) : 0;
-        if (lane == 0) {
-            if (s1 < 1 || s1 > a.max_seq_len) report(a.status, MSGL_DEVERR_LENGTH);
-            else if (!row_ok(a, s1)) report(a.status, MSGL_DEVERR_PAGE_RANGE);
-        }
-        int m = 0;
-        if (b > 0 && row_ok(a, s0) && row_ok(a, s1)) {
-            const int both = min(s0, s1);
-            const int n = ((both - 1) >> a.log2_ps) + 1;
-            const int32_t *x = a.pages.ids + (long long)(b - 1) * a.pages.stride, *y = x + a.pages.stride;
-            int far = n;
-            for (int c0 = 0; c0 < n && far == n; c0 += 32 * kRound) {
-                int here = n;
-#pragma unroll
-                for (int u = kRound - 1; u >= 0; --u) {
-                    const int p = c0 + u * 32 + lane;
-                    if (p < n && __ldg(x + p) != __ldg(y + p)) here = p;
-                }
-                far = __reduce_min_sync(0xffffffffu, here);
-            }
-            m = (int)min((long long)far << a.log2_ps, (long long)both);
-        }
-        if (lane == 0) a.shared_lens[b] = m;
-    }
-    // every row's m is written before the first block reads them
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    if (blockIdx.x == 0) group_rows(a);
-}
-
 }  // namespace
 
 cudaError_t launch_shared_prefixes(const SharedPrefixesArgs &a, cudaStream_t stream) {
-    if ((long long)a.num_reqs * a.pages.width <= kClusterEntries) {
-        shared_prefixes_cluster_kernel<<<kCluster, kScanThreads, 0, stream>>>(a);
-        return cudaGetLastError();
-    }
     row_match_kernel<<<a.num_reqs, kThreads, 0, stream>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
