@@ -170,25 +170,28 @@ struct Share {
 __device__ __forceinline__ Share share_plan(const BatchSums &s, const ShareModel &m, int hkv, int num_reqs) {
     const long long units = (s.tiles & kTilesMask) * hkv, items = (s.tiles >> kPairShift) * hkv;
     if (m.sms == 0 || units == 0) return Share{0, m.gx};
-    auto ns = [](long long x) -> uint32_t { return (uint32_t)min(x, 1ll << 30); };
-    const uint32_t hbm = ns((s.own + s.shared) * (hkv * kHeadDim * 4) / 6400);
+    // times in units of 64 ns (of SMs: up to 68 s)
+    auto t64 = [](long long ns) -> uint32_t { return (uint32_t)min(ns >> 6, 1ll << 30); };
+    const uint32_t hbm = t64((s.own + s.shared) * (hkv * kHeadDim * 4) / 6400);
     // (a request's own keys end in a tile that is half empty on average)
-    const uint32_t own = ns((s.own / 16 + num_reqs / 2) * m.tile_ns + num_reqs * 600ll);
-    const uint32_t all = ns((s.all / 16 + num_reqs / 2) * m.tile_ns + num_reqs * 600ll);
-    const uint32_t pre = ns(units * 1550 + items * 2500), crowded = ns(units * 800);
+    const uint32_t own = t64((s.own / 16 + num_reqs / 2) * m.tile_ns + num_reqs * 600ll);
+    const uint32_t all = t64((s.all / 16 + num_reqs / 2) * m.tile_ns + num_reqs * 600ll);
+    const uint32_t pre = t64(units * 1550 + items * 2500), crowded = t64(units * 800);
+    constexpr uint32_t kPrefixStart = 8000 / 64, kSplitStart = 5000 / 64, kJoin = 3000 / 64;
     // (32 candidates, closer together where there are few: a CTA more or less matters most there)
-    uint32_t best = 0xffffffffu;   // time in units of 128 ns, then the prefix CTAs
+    uint32_t best = 0xffffffffu;   // the time, then the prefix CTAs
     const int lane = threadIdx.x & 31, most = m.sms - m.ngr;
     const int p = 1 + lane + max(most - 32, 0) * lane * lane / 961;
     if (p <= most) {
         const uint32_t k = min((m.sms - p) / m.ngr, m.gx);
-        const uint32_t t = max(8000 + (pre + crowded / 100 * min(m.sms - p, 100)) / p, 5000 + max(hbm, own / k));
-        best = (min(t, (1u << 30) - 1) >> 7) << 8 | p;
+        const uint32_t t = max(kPrefixStart + (pre + crowded / 100 * min(m.sms - p, 100)) / p,
+                               kSplitStart + max(hbm, own / k));
+        best = min(t, (1u << 23) - 1) << 8 | p;
     }
     best = __reduce_min_sync(0xffffffffu, best);
-    const uint32_t through = 5000 + max(hbm, all / m.gx);
-    // (3 us for the pieces that sharing adds to the join)
-    if (best == 0xffffffffu || (!m.always && through <= (best >> 8 << 7) + 3000))
+    const uint32_t through = kSplitStart + max(hbm, all / m.gx);
+    // (kJoin: for the pieces that sharing adds to the join)
+    if (best == 0xffffffffu || (!m.always && through <= (best >> 8) + kJoin))
         return m.always ? Share{m.sms, m.gx} : Share{0, m.gx};
     const int n = best & 255;
     return Share{n, min((m.sms - n) / m.ngr, m.gx)};

@@ -94,8 +94,8 @@ __device__ __forceinline__ long long warp_incl_scan(long long v, int lane) {
 
 // Which keys of a request the ranges cover, and through which page table.
 //   kPlain    all of them, through its own
-//   kGrouped  all of them, or those behind the prefix that its group shares (where the
-//             shared-prefix kernel takes that: prefix_pays); shared keys through the group's
+//   kGrouped  all of them, or those behind the prefix that its group shares (where
+//             share_plan leaves that to the prefix kernel); shared keys through the group's
 //             first request's table
 enum KeyMode { kPlain, kGrouped };
 

@@ -16,10 +16,21 @@
 //   (and from L2 after the first) instead of once per request.
 // * The merge joins all pieces of a row.
 //
-// The split kernel is launched behind the prefix kernel with programmatic
-// dependent launch: its CTAs take each SM as the prefix kernel's share there
-// ends (at once where there is none), and its last CTA outwaits the prefix
-// kernel, so that the merge behind it finds both done.
+// Each of the first two has SMs of its own (share_plan in common.cuh prices the
+// partitions; every CTA counts the batch and comes to the same one).  The split
+// is launched behind the prefix kernel with programmatic dependent launch, so
+// its CTAs start on the SMs that the plan leaves free while the prefix kernel
+// works on the others; its last CTA outwaits the prefix kernel, so that the merge
+// behind it finds both done.
+//
+// Reading a shared key once a request is not much worse than it sounds: after the
+// first it comes out of L2, and the split kernel takes about 10 TB/s from there
+// (0.93 us for a 64 KB tile and SM) against 6.4 from HBM.  So the plan also prices
+// the split kernel alone, small batches skip the rest (kThroughBytes), and short
+// requests take a kernel of a single launch (decode_short.cu).  Sharing pays when
+// the groups are large: 256 requests over 32768 shared tokens, 64 q heads: 0.23 ms
+// with, 2.5 ms without; 32 groups of 8 over up to 1024 (page size 1): 129 and 193 us;
+// 64 requests over 2048 of about 5600: 161 us either way (floor 142).
 #include <cuda.h>
 #include <limits.h>
 #include <math.h>
@@ -73,7 +84,8 @@ static_assert(kOffX % 16 == 0, "alignment of the exchange");
 constexpr int kQFull = 0, kQEmpty = 1, kKFull = 2, kKEmpty = 4, kVFull = 6, kVEmpty = 9, kSFull = 12, kPFull = 14,
               kOFull = 16, kXFull = 18, kDrain = 19, kNumBars = 20;
 
-// What the merge needs to know of a row, written by the prefix kernel's last CTA.
+// What the merge needs to know of a row, written by the prefix kernel's last CTA (a plan kernel in
+// front of everything cost 6 to 8 us more than counting the batch in every CTA).
 struct RowPlan {
     int32_t err, start;                    // status bits; first own key
     int32_t in_pair;                       // row within its pair of Q tiles, -1: no shared keys
@@ -930,6 +942,8 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Merge
     if (lane == 0) a.lse[row] = none ? -INFINITY : M + logf(L);
 }
 
+// Up to this many bytes of K/V to attend (by the host's bounds), the split kernel alone needs 14 to
+// 22 us, and the prefix kernel would take longer than that for its start, one tile and the join.
 constexpr long long kThroughBytes = 140ll << 20;
 
 // Where the one-launch kernel of short requests is taken.  Up to 128 keys its blocks are small
@@ -974,8 +988,6 @@ cudaError_t launch_decode_shared(const DecodeSharedArgs &a, cudaStream_t stream)
     const int hkv = d.pool.hkv, G = d.hq / hkv, R = kRows / G;
     const DecodePlan plan = plan_decode(d.num_reqs, d.hq, hkv, d.max_seq_len);
     d.pair_rows = 2 * R;
-    // Small batches: with at most kThroughBytes of K/V to attend, sharing cannot win back what its
-    // kernel costs, which is left out.
     const bool small =
         d.num_reqs == 1 || (long long)d.num_reqs * d.max_seq_len * hkv * kHeadDim * 4 <= kThroughBytes;
     if (a.sharing == MSGL_SHARE_NEVER || (a.sharing == MSGL_SHARE_AUTO && small))

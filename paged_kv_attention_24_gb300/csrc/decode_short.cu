@@ -11,6 +11,10 @@
 // cp.async at a pitch that keeps ldmatrix free of bank conflicts, two tiles in
 // flight a warp; the products are the decode's (S^T = K Q^T with M = 16 keys and
 // N = 8 q heads, O^T = V^T P^T).
+//
+// Bound by latency: lengths, page ids, keys, joins, each waiting for the one
+// before.  4 requests of 145 to 200 keys (16 q heads over 8): 7.5 us, against 12
+// to 14 for the split and its merge.
 #include <math.h>
 
 #include "kernels.h"
