@@ -10,9 +10,10 @@
 // per row compares it with the row before, 4096 columns a round, done at the first round with a
 // difference; one block then finds each group's start and least m by scans over the rows.  m
 // travels in shared_lens, which the scans overwrite, so the call needs no scratch.  64 requests:
-// 3.5 us up to 1024 columns, 6.4 us for 16384 equal ones.  (One cluster of 8 blocks with a barrier
-// in place of the second launch: 5.2 and 41 us.  Blocks of 256 threads: the same up to 2048 columns,
-// 8.4 us for 16384; of 1024: 5.7 us there, but 9.0 in place of 6.3 us for 1024 requests.)
+// 3.0 us up to 1024 columns, 5 us for 16384 equal ones.  Slower: one cluster of 8 blocks with a
+// barrier in place of the second launch (+1.7 and +35 us); one block for all rows of a small table
+// (+0.4 us at 128 columns, +1.4 at 256); blocks of 256 threads (+2 us at 16384 columns) or of 1024
+// (+2.7 us for 1024 requests).
 #include <limits.h>
 
 #include "kernels.h"
@@ -62,17 +63,41 @@ __global__ void __launch_bounds__(kThreads) row_match_kernel(const SharedPrefixe
     if (threadIdx.x == 0) a.shared_lens[b] = m;
 }
 
-// One block.  Rows are taken 1024 at a time; a row's group starts at the last row
-// that did not join (an inclusive max scan), and its least m is gathered by
-// atomicMin on the start row's entry, which holds no m of its own.
+// One block.  A row's group starts at the last row up to it that did not join (a max scan).
+// Up to 1024 rows, one a thread, the least m of a group is gathered in shared memory: 3.0 us a call
+// for 64 rows, against 4.4 in the global memory that larger batches use.  Those are taken 1024
+// rows at a time, and a group's least m by atomicMin on its start row's entry, which holds no m of
+// its own (1000 rows: 5.4 us; 1025: 7.7; 2048: 10.2).
 constexpr int kScanThreads = 1024;
 
 __global__ void __launch_bounds__(kScanThreads) row_groups_kernel(const SharedPrefixesArgs a) {
     __shared__ int warp_max[32];
     __shared__ int carry;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    __shared__ int least[kScanThreads];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    least[threadIdx.x] = INT_MAX;
     if (threadIdx.x == 0) carry = 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (a.num_reqs <= kScanThreads) {
+        // one row a thread, the least m of each group in shared memory
+        const int b = threadIdx.x;
+        const int m = b < a.num_reqs ? __ldcg(a.shared_lens + b) : 0;
+        const bool joined = b > 0 && m >= a.min_shared;
+        const uint32_t starts = __ballot_sync(0xffffffffu, !joined);
+        if (lane == 0) warp_max[warp] = starts ? b + 31 - __clz(starts) : 0;
+        __syncthreads();
+        const int before = (int)__reduce_max_sync(0xffffffffu, lane < warp ? (uint32_t)warp_max[lane] : 0u);
+        const uint32_t mine = starts & (0xffffffffu >> (31 - lane));
+        const int start = mine ? b - lane + 31 - __clz(mine) : before;
+        if (joined) atomicMin(&least[start], m);
+        __syncthreads();
+        if (b < a.num_reqs) {
+            const int shared = least[start];
+            a.group_start[b] = start;
+            a.shared_lens[b] = shared == INT_MAX ? 0 : shared;
+        }
+        return;
+    }
     __syncthreads();
     for (int c0 = 0; c0 < a.num_reqs; c0 += kScanThreads) {
         const int b = c0 + threadIdx.x;
