@@ -135,8 +135,16 @@ size_t decode_smem_bytes(int hg, int stages, bool box) {
            16;
 }
 
+// Warps that issue the copies of per-key stages (kGrouped).  A warp issues one copy at a time, about
+// one in 75 cycles: 32 rows of 2 KB take it 1.2 us, which is 55 GB/s an SM, and less with smaller rows.
+// Four warps take 0.58 us (two: 0.77; 16-byte cp.async copies by 4 or 8 warps: 0.9).  Ranges over all
+// SMs read rows of 2 KB from HBM at 43 GB/s an SM either way; a batch with shared keys has fewer SMs
+// for its ranges and reads more of its keys from L2.
+constexpr int kCopyWarps = 4;
+constexpr int copy_warps(bool box, KeyMode mode) { return !box && mode == kGrouped ? kCopyWarps : 0; }
+
 template <bool kBox, KeyMode kMode>
-__global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
+__global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1 + copy_warps(kBox, kMode)), 1)
     decode_split_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                         const DecodeKernelArgs a) {
     extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -151,6 +159,10 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
     uint64_t *empty = full + S;
     uint64_t *patch = empty + S;   // box path, append mode: the current token's tile lands here first
     volatile int *abort_flag = reinterpret_cast<volatile int *>(patch + 1);
+    // copy warps: a stage's pool slots (-1: not loaded), and the barrier that says they stand
+    constexpr bool kCopies = copy_warps(kBox, kMode) > 0;
+    __shared__ long long s_slot[kMaxStages][kTileKeys];
+    __shared__ __align__(8) uint64_t s_go[kMaxStages];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // which key range, of which group of kv heads (kGrouped: the groups of a range are neighbours in
@@ -165,6 +177,8 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
             ptx::mbar_init(ptx::smem_u32(full + s), 1);
             ptx::mbar_init(ptx::smem_u32(empty + s), hg * a.slices);
         }
+        if constexpr (kCopies)
+            for (int s = 0; s < S; ++s) ptx::mbar_init(ptx::smem_u32(s_go + s), 1);
         ptx::mbar_init(ptx::smem_u32(patch), 1);
         *abort_flag = 0;
         ptx::fence_mbar_init();
@@ -173,7 +187,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
 
     // kGrouped: the block counts the batch, and the thread whose rows hold the range's first key
     // says where that is
-    __shared__ long long s_scan[kMaxHeadGroup + 1][4], s_base;
+    __shared__ long long s_scan[kMaxHeadGroup + 1 + copy_warps(kBox, kMode)][4], s_base;
     __shared__ int s_row;
     long long total = 0;
     bool own_only = false;
@@ -421,6 +435,13 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
                             if (badm) report(a.status, MSGL_DEVERR_PAGE_RANGE);
                             ptx::mbar_arrive_expect_tx(full_bar, __popc(mask) * row_bytes * 2);
                         }
+                        if constexpr (kCopies) {
+                            if (lane < kTileKeys) s_slot[stage][lane] = slot;
+                            __syncwarp();
+                            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(s_go + stage));
+                            ++it;
+                            continue;
+                        }
                         __syncwarp();
                         // append mode: this tile holds the request's current token
                         const bool has_new = a.new_loc && t0 + n == sb;
@@ -469,6 +490,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
                 if (lane == 0) {
                     meta[stage].flags = kEnd;
                     ptx::mbar_arrive(ptx::smem_u32(full + stage));
+                    if constexpr (kCopies) ptx::mbar_arrive(ptx::smem_u32(s_go + stage));
                 }
                 ++it;
             } else {
@@ -487,6 +509,27 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1), 1)
         if constexpr (kMode == kGrouped) {
             if (a.share.sms > 0 && lane == 0 && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1)
                 asm volatile("griddepcontrol.wait;" ::: "memory");
+        }
+    } else if (kCopies && warp > n_consumers) {
+        // -------------------------------------------------------- copy warps
+        // rows 0 to 15 of a stage are K, 16 to 31 V
+        constexpr int kEach = 2 * kTileKeys / kCopyWarps;
+        const int row = (warp - n_consumers - 1) * kEach + lane;
+        const __nv_bfloat16 *pool = (row < kTileKeys ? a.pool.k : a.pool.v) + (long long)g0 * kHeadDim;
+        const long long slot_elems = (long long)a.pool.hkv * kHeadDim;
+        const uint64_t stream_policy = ptx::l2_evict_first_policy();
+        for (int it = 0;; ++it) {
+            const int stage = it % S, round = it / S;
+            if (*abort_flag) break;
+            if (!ptx::mbar_wait(ptx::smem_u32(s_go + stage), round & 1)) {
+                if (lane == 0) { report(a.status, MSGL_DEVERR_TIMEOUT); *abort_flag = 1; }
+                break;
+            }
+            if (meta[stage].flags & kEnd) break;
+            const long long slot = lane < kEach ? s_slot[stage][row % kTileKeys] : -1;
+            if (slot >= 0)
+                ptx::bulk_g2s_hint(ptx::smem_u32(smem + (size_t)stage * sbytes + row * pitch), pool + slot * slot_elems,
+                                   (uint32_t)hg * 256, ptx::smem_u32(full + stage), stream_policy);
         }
     } else if (warp < n_consumers) {
         // ----------------------------------------------------------- consumers
@@ -869,7 +912,7 @@ ShareModel decode_split_model(int32_t hq, const PoolView &pool) {
     ShareModel m{};
     m.gx = l.ctas;
     m.ngr = pool.hkv / l.hg;
-    m.tile_ns = box || l.hg < 5 ? 930 : 210 * l.hg;
+    m.tile_ns = box ? 930 : 400 + 100 * l.hg;
     return m;
 }
 
@@ -945,7 +988,7 @@ cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, cudaStrea
         auto kernel = a.group_start
                           ? (box ? decode_split_kernel<true, kGrouped> : decode_split_kernel<false, kGrouped>)
                           : (box ? decode_split_kernel<true, kPlain> : decode_split_kernel<false, kPlain>);
-        const int threads = 32 * (L.hg * slices + 1);
+        const int threads = 32 * (L.hg * slices + 1 + copy_warps(box, a.group_start ? kGrouped : kPlain));
         if (a.share.sms > 0) {
             // behind the shared-prefix kernel: SMs that it leaves free start at once
             cudaLaunchConfig_t cfg = {};
