@@ -145,10 +145,10 @@ __device__ __forceinline__ void add_row(const GroupRows &r, int i, BatchSums &s)
 
 // What a call's kernels know of each other's cost (whole nanoseconds, so that all of them come to
 // the same answer).  Measured: HBM gives 6.4 TB/s; a split CTA starts within 5 us, takes a 16-key tile
-// of its heads in tile_ns (0.93 us for page boxes, the per-key copies' 39 GB/s an SM below page size
-// 16) out of L2 or HBM, and 0.6 us more for every request it begins; a prefix CTA takes 8 us to its
-// first scores and out of its last piece, 1.55 us for a key tile (2.35 us while the other SMs
-// saturate HBM) and 2.5 us for every item it begins.
+// of its heads in tile_ns out of L2 or HBM (0.93 us for page boxes of 8 heads, 0.5 us for per-key rows
+// of one head and 0.1 us more for each further one) and 0.6 us more for every request it begins; a
+// prefix CTA takes 8 us to its first scores and out of its last piece, 1.55 us for a key tile (2.35 us
+// while the other SMs saturate HBM) and 2.5 us for every item it begins.
 struct ShareModel {
     int32_t sms;               // CTAs of the prefix grid, one an SM
     int32_t gx, ngr;           // the split's grid: key ranges, groups of kv heads

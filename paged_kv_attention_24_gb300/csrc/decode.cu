@@ -19,8 +19,8 @@
 //   - page_size >= 16 ("box" path): a 16-key tile aligned to 16 keys lies in
 //     one page, so its K (and V) arrive as two 3D TMA boxes of 64 dims x 16
 //     keys x the group's heads (128-byte swizzle, head-major rows).  Four
-//     copies per stage: a TMA unit issues about one copy per 80 cycles, which
-//     held per-key copies near 50 GB/s per SM.
+//     copies per stage: a warp issues about one copy per 75 cycles, which
+//     holds per-key copies of 2 KB near 55 GB/s per SM.
 //     In the append mode the tile holding the current token lands on a
 //     separate barrier, and the producer writes that key's rows from
 //     k_new / v_new over the loaded ones before handing the stage over.
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1 + copy_warps(kBox, kMo
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            ptx::mbar_init(ptx::smem_u32(full + s), 1);
+            ptx::mbar_init(ptx::smem_u32(full + s), 1 + copy_warps(kBox, kMode));
             ptx::mbar_init(ptx::smem_u32(empty + s), hg * a.slices);
         }
         if constexpr (kCopies)
@@ -525,11 +525,15 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1 + copy_warps(kBox, kMo
                 if (lane == 0) { report(a.status, MSGL_DEVERR_TIMEOUT); *abort_flag = 1; }
                 break;
             }
-            if (meta[stage].flags & kEnd) break;
-            const long long slot = lane < kEach ? s_slot[stage][row % kTileKeys] : -1;
+            const bool end = (meta[stage].flags & kEnd) != 0;
+            const long long slot = !end && lane < kEach ? s_slot[stage][row % kTileKeys] : -1;
             if (slot >= 0)
                 ptx::bulk_g2s_hint(ptx::smem_u32(smem + (size_t)stage * sbytes + row * pitch), pool + slot * slot_elems,
                                    (uint32_t)hg * 256, ptx::smem_u32(full + stage), stream_policy);
+            // (a warp without rows to copy arrives too: the stage is not reused before it has looked)
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(full + stage));
+            if (end) break;
         }
     } else if (warp < n_consumers) {
         // ----------------------------------------------------------- consumers

@@ -24,12 +24,12 @@
 // behind it finds both done.
 //
 // Reading a shared key once a request is not much worse than it sounds: after the
-// first it comes out of L2, and the split kernel takes about 10 TB/s from there
-// (0.93 us for a 64 KB tile and SM) against 6.4 from HBM.  So the plan also prices
+// first it comes out of L2, and the split kernel takes 10 to 13 TB/s from there
+// (0.73 to 0.93 us for a 64 KB tile and SM) against 6.4 from HBM.  So the plan also prices
 // the split kernel alone, small batches skip the rest (kThroughBytes), and short
 // requests take a kernel of a single launch (decode_short.cu).  Sharing pays when
 // the groups are large: 256 requests over 32768 shared tokens, 64 q heads: 0.23 ms
-// with, 2.5 ms without; 32 groups of 8 over up to 1024 (page size 1): 129 and 193 us;
+// with, 2.5 ms without; 32 groups of 8 over up to 1024 (page size 1): 115 and 147 us;
 // 64 requests over 2048 of about 5600: 161 us either way (floor 142).
 #include <cuda.h>
 #include <limits.h>
