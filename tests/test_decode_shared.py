@@ -89,6 +89,13 @@ def test_other_page_sizes(ps):
     check(shared_batch.make(40, 8, ps, [(333, [1, 20, 150]), (77, [5, 5])], seed=ps), f"ps {ps}")
 
 
+@pytest.mark.parametrize("hq,hkv,ps", [(8, 1, 1), (16, 8, 1), (5, 5, 2), (64, 1, 4), (64, 32, 8)])
+def test_many_short_requests_of_small_pages(hq, hkv, ps):
+    """Requests of a few keys each, so most 16-key tiles of a range are nearly empty."""
+    groups = [(20 + 3 * i, [1 + (7 * i + j) % (3 + i % 8) for j in range(30)]) for i in range(9)]
+    check(shared_batch.make(hq, hkv, ps, groups + [(700, [1, 33, 250])], seed=60 + hkv), f"{hq}/{hkv} ps {ps}")
+
+
 def test_many_groups_split_over_the_grid():
     groups = [(200 + 37 * i, [1 + (5 * i + j) % 23 for j in range(1 + i % 6)]) for i in range(60)]
     check(shared_batch.make(16, 8, 16, groups, seed=7))
