@@ -239,8 +239,8 @@ def check_groups(table, seq, ps, max_seq, min_shared):
 
 
 @pytest.mark.parametrize("ps", [1, 16, 256])
-@pytest.mark.parametrize("B,width", [(1, 1), (2, 3), (9, 40), (100, 70), (1024, 5), (1025, 5), (1500, 9), (2100, 33),
-                                     (12, 9000)])
+@pytest.mark.parametrize("B,width", [(1, 1), (2, 3), (9, 40), (100, 70), (128, 256), (129, 256), (128, 257), (12, 9000),
+                                     (1024, 5), (1025, 5), (1500, 9), (2100, 33)])
 def test_groups_match_the_loops(ps, B, width):
     rng = np.random.default_rng(B + width + ps)
     table = np.zeros((B, width), np.int32)
