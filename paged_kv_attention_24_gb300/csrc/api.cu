@@ -419,6 +419,7 @@ msgl_status msgl_shared_prefixes(const msgl_page_table *pages, const int32_t *se
     if (num_reqs == 0) return MSGL_OK;
     if ((s = check_pages(pages, num_reqs, a.pages))) return s;
     if (max_seq_len <= 0) return fail(MSGL_ERR_INVALID_ARG, "max_seq_len must be > 0");
+    if (max_seq_len > (1 << 30)) return fail(MSGL_ERR_UNSUPPORTED, "max_seq_len may not pass 2^30");
     if (min_shared <= 0) return fail(MSGL_ERR_INVALID_ARG, "min_shared must be > 0");
     if (!seq_lens || !group_start || !shared_lens)
         return fail(MSGL_ERR_INVALID_ARG, "seq_lens, group_start and shared_lens must be non-NULL");

@@ -69,6 +69,7 @@ def test_shared_prefixes_refusals(lib):
     for want, kw in [(INVALID, dict(pages=None)), (INVALID, dict(pages=ops._Pages(16, 4, 8))),
                      (INVALID, dict(pages=ops._Pages(None, 8, 8))), (INVALID, dict(seq=None)), (INVALID, dict(reqs=-1)),
                      (UNSUPPORTED, dict(ps=24)), (INVALID, dict(max_seq=0)), (INVALID, dict(least=0)),
+                     (UNSUPPORTED, dict(max_seq=2 ** 30 + 1)),
                      (INVALID, dict(first=None)), (INVALID, dict(shared=None))]:
         assert call(**kw) == want, kw
     assert call(reqs=0) == 0
