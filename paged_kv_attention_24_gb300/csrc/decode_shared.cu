@@ -949,9 +949,9 @@ constexpr long long kThroughBytes = 140ll << 20;
 // Where the one-launch kernel of short requests is taken.  Up to 128 keys its blocks are small
 // enough to keep several on an SM, and it was never behind the split and merge (32 keys, 256
 // requests: 13.4 against 22.7 us).  Longer ones have an SM to themselves, or nearly: ahead as long as
-// there are at most two a SM (512 keys: 8 requests 8.2 against 12.4 us, 32 requests 12.7 against 16.0,
-// 64 requests 23 against 20; 1024 keys: 16 requests 13.1 against 16.7, 32 requests 21.2 against
-// 20.5), and the split's many CTAs win on the longest.
+// there are at most two a SM (512 keys, 8 kv heads: 8 requests 8.2 against 11.5 us at page size 1 and
+// 13.8 at 16, 32 requests 13 against 17, 64 requests 23 against 21; 1024 keys: 16 requests 13.4 against
+// 17, but 2 requests 12.6 against 11.9 at page size 1), and the split's many CTAs win on the longest.
 bool takes_short(const DecodeArgs &d) {
     if (d.num_reqs > 65535) return false;
     const long long blocks = (long long)d.num_reqs * d.pool.hkv * ((d.hq / d.pool.hkv + 7) / 8);
