@@ -57,18 +57,6 @@ __host__ __device__ __forceinline__ long long keys_per_cta(long long total, long
     return share > kMinKeysPerCta ? share : kMinKeysPerCta;
 }
 
-// Shared-prefix decode: the keys of request b that only it attends, and the first of them.  A
-// request with a neighbour in its group starts behind the shared keys; entries that break the
-// group rules give no keys (the merge reports them).
-__device__ __forceinline__ int own_keys_shared(const int32_t *seq_lens, const int32_t *group_start,
-                                               const int32_t *shared_lens, int num_reqs, int max_seq, int b,
-                                               int &first) {
-    const int s = seq_valid(seq_lens, b, max_seq);
-    const bool grouped = __ldg(group_start + b) != b || (b + 1 < num_reqs && __ldg(group_start + b + 1) == b);
-    first = grouped ? __ldg(shared_lens + b) : 0;
-    return first >= 0 && first <= s ? s - first : 0;
-}
-
 // The rows of a shared-prefix decode.  A group's rows are cut into pairs of Q tiles of pair_rows / 2
 // rows each (the tiles of its tensor-core kernel; pair_rows = 2 * floor(128 / G)).
 struct GroupRows {
@@ -78,49 +66,68 @@ struct GroupRows {
 
 constexpr int kPrefixTileKeys = 128;
 
-// 128-key tiles of shared keys of the pair that starts at row b; 0 when none does.  Whatever the
-// group arrays hold, the entries used (group_start[b], shared_lens[b]) are in range.
-__device__ __forceinline__ int pair_tiles(const GroupRows &r, int b) {
-    const int lead = __ldg(r.group_start + b), s = __ldg(r.shared_lens + b);
-    const int next = b + 1 < r.num_reqs ? __ldg(r.group_start + b + 1) : -1;
-    const bool starts = lead >= 0 && lead <= b && (b - lead) % r.pair_rows == 0 && (lead != b || next == b);
-    return starts && s > 0 && s <= r.max_seq_len ? (s + kPrefixTileKeys - 1) / kPrefixTileKeys : 0;
+// What the arrays say of row b (all loads at once: one after the other, as the rules below need them,
+// they are most of the time that a CTA's count of the batch takes).
+struct GroupRow {
+    int32_t b, seq, lead, next, shared;   // next: the group of row b + 1, -1 behind the last row
+};
+
+__device__ __forceinline__ GroupRow group_row_at(const GroupRows &r, int b) {
+    const int after = min(b + 1, r.num_reqs - 1);
+    GroupRow x{b, __ldg(r.seq_lens + b), __ldg(r.group_start + b), __ldg(r.group_start + after), __ldg(r.shared_lens + b)};
+    if (after == b) x.next = -1;
+    return x;
 }
 
-// The status bits of row b: its length, the rules of group_start and shared_lens, and that the
+__device__ __forceinline__ int valid_seq(const GroupRows &r, const GroupRow &x) {
+    return x.seq >= 1 && x.seq <= r.max_seq_len ? x.seq : 0;
+}
+
+// The keys that only row x.b attends, and the first of them.  A request with a neighbour in its group
+// starts behind the shared keys; entries that break the group rules give no keys (the merge reports
+// them).
+__device__ __forceinline__ int own_keys(const GroupRows &r, const GroupRow &x, int &first) {
+    const int s = valid_seq(r, x);
+    first = x.lead != x.b || x.next == x.b ? x.shared : 0;
+    return first >= 0 && first <= s ? s - first : 0;
+}
+
+// All keys of row x.b where the shared ones are read through its group's first row; 0 when its
+// entries are out of range.  from: the first key that is read through its own.
+__device__ __forceinline__ int through_keys(const GroupRows &r, const GroupRow &x, int &from) {
+    const int own = own_keys(r, x, from), s = valid_seq(r, x);
+    return x.lead >= 0 && x.lead <= x.b && from >= 0 && own + from == s ? s : 0;
+}
+
+// 128-key tiles of shared keys of the pair that starts at row x.b; 0 when none does.  Whatever the
+// group arrays hold, the entries used (group_start[b], shared_lens[b]) are in range.
+__device__ __forceinline__ int pair_tiles(const GroupRows &r, const GroupRow &x) {
+    const bool starts = x.lead >= 0 && x.lead <= x.b && (x.b - x.lead) % r.pair_rows == 0 &&
+                        (x.lead != x.b || x.next == x.b);
+    return starts && x.shared > 0 && x.shared <= r.max_seq_len ? (x.shared + kPrefixTileKeys - 1) / kPrefixTileKeys : 0;
+}
+
+// The status bits of row x.b: its length, the rules of group_start and shared_lens, and that the
 // pair it belongs to can be worked on.  start: its first own key; pair: its pair's first row (-1:
 // no shared keys).
-__device__ __forceinline__ uint32_t group_row_errors(const GroupRows &r, int b, int &seq, int &start, int &pair) {
-    seq = __ldg(r.seq_lens + b);
+__device__ __forceinline__ uint32_t group_row_errors(const GroupRows &r, const GroupRow &x, int &start, int &pair) {
     start = 0;
     pair = -1;
-    if (seq < 1 || seq > r.max_seq_len) return MSGL_DEVERR_LENGTH;
-    const int lead = __ldg(r.group_start + b);
-    if (lead == b && !(b + 1 < r.num_reqs && __ldg(r.group_start + b + 1) == b)) return 0;   // alone
-    const int s = __ldg(r.shared_lens + b);
-    if (lead < 0 || lead > b || s < 0 || s > seq) return MSGL_DEVERR_GROUP;
-    if (lead != b && (__ldg(r.group_start + b - 1) != lead || __ldg(r.group_start + lead) != lead ||
-                      __ldg(r.shared_lens + lead) != s))
-        return MSGL_DEVERR_GROUP;
+    if (valid_seq(r, x) == 0) return MSGL_DEVERR_LENGTH;
+    const int b = x.b, lead = x.lead, s = x.shared;
+    if (lead == b && x.next != b) return 0;   // alone
+    if (lead < 0 || lead > b || s < 0 || s > x.seq) return MSGL_DEVERR_GROUP;
+    const int half = r.pair_rows / 2, first = lead + (b - lead) / r.pair_rows * r.pair_rows;
+    const int before = __ldg(r.group_start + max(b - 1, 0)), lead_lead = __ldg(r.group_start + lead),
+              lead_shared = __ldg(r.shared_lens + lead), second = __ldg(r.group_start + min(first + half, b));
+    const GroupRow p = group_row_at(r, first);
+    if (lead != b && (before != lead || lead_lead != lead || lead_shared != s)) return MSGL_DEVERR_GROUP;
     start = s;
     if (s == 0) return 0;
-    const int half = r.pair_rows / 2;
-    pair = lead + (b - lead) / r.pair_rows * r.pair_rows;
-    if (__ldg(r.group_start + pair) != lead || __ldg(r.shared_lens + pair) != s || pair_tiles(r, pair) == 0)
-        return MSGL_DEVERR_GROUP;
-    if (b - pair >= half && __ldg(r.group_start + pair + half) != lead) return MSGL_DEVERR_GROUP;
+    pair = first;
+    if (p.lead != lead || p.shared != s || pair_tiles(r, p) == 0) return MSGL_DEVERR_GROUP;
+    if (b - first >= half && second != lead) return MSGL_DEVERR_GROUP;
     return 0;
-}
-
-// All keys of row b where the shared ones are read through its group's first row; 0 when its
-// entries are out of range.  from: the first key that is read through its own.
-__device__ __forceinline__ int through_keys(const GroupRows &r, int b, int *from = nullptr) {
-    int split;
-    const int own = own_keys_shared(r.seq_lens, r.group_start, r.shared_lens, r.num_reqs, r.max_seq_len, b, split);
-    const int lead = __ldg(r.group_start + b);
-    if (from) *from = split;
-    const int s = seq_valid(r.seq_lens, b, r.max_seq_len);
-    return lead >= 0 && lead <= b && split >= 0 && own + split == s ? s : 0;
 }
 
 // What a batch asks for.
@@ -133,13 +140,14 @@ constexpr int kPairShift = 44;
 constexpr long long kTilesMask = (1ll << kPairShift) - 1;
 
 __device__ __forceinline__ void add_row(const GroupRows &r, int i, BatchSums &s) {
+    const GroupRow x = group_row_at(r, i);
     int from;
-    s.own += own_keys_shared(r.seq_lens, r.group_start, r.shared_lens, r.num_reqs, r.max_seq_len, i, from);
-    s.all += through_keys(r, i);
-    const int t = pair_tiles(r, i);
+    s.own += own_keys(r, x, from);
+    s.all += through_keys(r, x, from);
+    const int t = pair_tiles(r, x);
     if (t > 0) {
         s.tiles += t + (1ll << kPairShift);
-        if (__ldg(r.group_start + i) == i) s.shared += __ldg(r.shared_lens + i);
+        if (x.lead == i) s.shared += x.shared;
     }
 }
 

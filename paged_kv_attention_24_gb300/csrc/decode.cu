@@ -103,20 +103,23 @@ __device__ __forceinline__ GroupRows group_rows_of(const DecodeKernelArgs &a) {
     return GroupRows{a.seq_lens, a.group_start, a.shared_lens, a.num_reqs, a.max_seq_len, a.pair_rows};
 }
 
-// Request b's keys in the ranges (0: not a valid request), the first of them, and where those of its
-// own page table begin.
+// Request b's keys in the ranges (0: not a valid request), the first of them, where those of its own
+// page table begin, and the row whose table has the others.
 template <KeyMode kMode>
-__device__ __forceinline__ int range_keys(const DecodeKernelArgs &a, int b, bool own_only, int &first, int &own_from) {
+__device__ __forceinline__ int range_keys(const DecodeKernelArgs &a, int b, bool own_only, int &first, int &own_from,
+                                          int &shared_row) {
     first = own_from = 0;
+    shared_row = b;
     if constexpr (kMode == kGrouped) {
         // (rows whose entries break the group rules are written by the merge; here they only have to
         // stay in range)
-        if (own_only) {
-            const int n = own_keys_shared(a.seq_lens, a.group_start, a.shared_lens, a.num_reqs, a.max_seq_len, b, first);
-            own_from = first;
-            return n;
-        }
-        return through_keys(group_rows_of(a), b, &own_from);
+        const GroupRows rows = group_rows_of(a);
+        const GroupRow x = group_row_at(rows, b);
+        shared_row = x.lead;
+        if (!own_only) return through_keys(rows, x, own_from);
+        const int n = own_keys(rows, x, first);
+        own_from = first;
+        return n;
     } else {
         return seq_valid(a.seq_lens, b, a.max_seq_len);
     }
@@ -226,7 +229,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1 + copy_warps(kBox, kMo
         const long long r0 = per * range;
         const long long r1 = min(total, r0 + per);
         int it = 0;
-        int first_key, own_from;
+        int first_key, own_from, shared_row;
         uint32_t patch_uses = 0;
         bool patch_pending = false;
         bool aborted = false;
@@ -250,8 +253,8 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1 + copy_warps(kBox, kMo
                 base = s_base;
             }
             for (int c = c0; c < B && b < 0; c += 32) {
-                int f, o;
-                const int s = (c + lane < B) ? range_keys<kMode>(a, c + lane, own_only, f, o) : 0;
+                int f, o, l0;
+                const int s = (c + lane < B) ? range_keys<kMode>(a, c + lane, own_only, f, o, l0) : 0;
                 const long long incl = warp_incl_scan(s, lane);
                 const long long tot = __shfl_sync(0xffffffffu, incl, 31);
                 if (r0 < base + tot) {
@@ -264,7 +267,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1 + copy_warps(kBox, kMo
             }
             // kGrouped: a batch of short requests would wait for each one's numbers and first page id
             // in turn, so the lanes look up those of 32 requests at once
-            int info_b = INT_MIN / 2, info_n = 0, info_first = 0, info_from = 0, info_pid = -1;
+            int info_b = INT_MIN / 2, info_n = 0, info_first = 0, info_from = 0, info_row = 0, info_pid = -1;
             long long pos = r0;
             while (b >= 0 && b < B && pos < r1 && !aborted) {
                 int sb, first_pid = -1;
@@ -272,12 +275,12 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1 + copy_warps(kBox, kMo
                     if (b >= info_b + 32) {
                         info_b = b;
                         const int row = b + lane;
-                        info_n = info_first = info_from = 0;
+                        info_n = info_first = info_from = info_row = 0;
                         info_pid = -1;
-                        if (row < B) info_n = range_keys<kMode>(a, row, own_only, info_first, info_from);
+                        if (row < B) info_n = range_keys<kMode>(a, row, own_only, info_first, info_from, info_row);
                         if (kBox && info_n > 0) {
                             const int pidx = info_first >> a.pool.log2_ps;
-                            const int from = info_first < info_from ? __ldg(a.group_start + row) : row;
+                            const int from = info_first < info_from ? info_row : row;
                             if (pidx < a.pages.width)
                                 info_pid = __ldg(a.pages.ids + (int64_t)from * a.pages.stride + pidx);
                         }
@@ -286,9 +289,10 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1 + copy_warps(kBox, kMo
                     sb = __shfl_sync(0xffffffffu, info_n, l);
                     first_key = __shfl_sync(0xffffffffu, info_first, l);
                     own_from = __shfl_sync(0xffffffffu, info_from, l);
+                    shared_row = __shfl_sync(0xffffffffu, info_row, l);
                     first_pid = __shfl_sync(0xffffffffu, info_pid, l);
                 } else {
-                    sb = range_keys<kMode>(a, b, own_only, first_key, own_from);
+                    sb = range_keys<kMode>(a, b, own_only, first_key, own_from, shared_row);
                 }
                 const long long end_b = start_b + sb;
                 if (end_b > pos) {
@@ -296,7 +300,6 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1 + copy_warps(kBox, kMo
                     const int hi = (int)(min(r1, end_b) - start_b) + first_key;
                     // page id of key `key` of request b (-1 when the page index is past the
                     // table's width, which then reads as a bad page)
-                    const int shared_row = kMode == kGrouped ? __ldg(a.group_start + b) : b;
                     auto load_pid = [&](int key) -> int {
                         const int pidx = key >> a.pool.log2_ps;
                         const int row = kMode == kGrouped && key < own_from ? shared_row : b;
@@ -728,7 +731,8 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(
     // a request's keys in the split's ranges; the split's count of them, rule for rule
     auto keys_of = [&](int i) -> int {
         if constexpr (kThrough) {
-            return through_keys(rows, i);
+            int from;
+            return through_keys(rows, group_row_at(rows, i), from);
         } else {
             return seq_valid(rows.seq_lens, i, rows.max_seq_len);
         }
@@ -756,8 +760,8 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(
     __nv_bfloat16 *orow = o + row * kHeadDim + lane * 4;
     uint32_t err = sb == 0 ? MSGL_DEVERR_LENGTH : 0;
     if constexpr (kThrough) {
-        int seq, start, pair;
-        err = group_row_errors(rows, b, seq, start, pair);
+        int start, pair;
+        err = group_row_errors(rows, group_row_at(rows, b), start, pair);
     }
     if (err) {
         if (blockIdx.x == 0 && warp == 0 && lane == 0) report(status, err);

@@ -131,7 +131,7 @@ struct Walk {
         const int lane = threadIdx.x & 31;
         tiles = 0;
         for (; r < rows.num_reqs; r += 32) {
-            const int t = r + lane < rows.num_reqs ? pair_tiles(rows, r + lane) : 0;
+            const int t = r + lane < rows.num_reqs ? pair_tiles(rows, group_row_at(rows, r + lane)) : 0;
             const unsigned m = __ballot_sync(0xffffffffu, t > 0);
             if (m) {
                 row = r + __ffs(m) - 1;
@@ -284,17 +284,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         long long at = pays ? batch.before.own : batch.before.all, unit = before;
         for (int b = batch.b0; b < batch.b1; ++b) {
             a.plan[b].unit = unit;
-            unit += (long long)pair_tiles(rows, b) * hkv;
+            unit += (long long)pair_tiles(rows, group_row_at(rows, b)) * hkv;
         }
         __threadfence_block();
         __syncthreads();
         for (int b = batch.b0; b < batch.b1; ++b) {
-            int seq, start, pair, first;
-            const int n = pays ? own_keys_shared(rows.seq_lens, rows.group_start, rows.shared_lens, rows.num_reqs,
-                                                 rows.max_seq_len, b, first)
-                               : through_keys(rows, b);
+            int start, pair, first;
+            const GroupRow x = group_row_at(rows, b);
+            const int n = pays ? own_keys(rows, x, first) : through_keys(rows, x, first);
             const long long c0 = at / split_per;
-            a.plan[b].err = (int32_t)group_row_errors(rows, b, seq, start, pair);
+            a.plan[b].err = (int32_t)group_row_errors(rows, x, start, pair);
             if (!pays) pair = -1;
             a.plan[b].start = start;
             a.plan[b].in_pair = pair >= 0 ? b - pair : -1;

@@ -53,8 +53,8 @@ __global__ void __launch_bounds__(32 * kWarps) decode_short_kernel(const ShortAr
     const int b = blockIdx.y, g = blockIdx.x / a.slices, hoff = (blockIdx.x - g * a.slices) * 8;
     const int G = a.group, Gs = min(8, G - hoff);   // q heads of this block (slots past them are empty)
     int from;                                       // first key of the row's own pages
-    const int n = through_keys(a.rows, b, &from);
-    const int lead = __ldg(a.rows.group_start + b);
+    const GroupRow row = group_row_at(a.rows, b);
+    const int n = through_keys(a.rows, row, from), lead = row.lead;
     if (threadIdx.x == 0) s_bad = 0;
 
     // Q^T fragments: head slot lane / 4
@@ -104,8 +104,8 @@ __global__ void __launch_bounds__(32 * kWarps) decode_short_kernel(const ShortAr
     }
     // (the group rules are looked up while the first tiles are on their way)
     if (threadIdx.x == 0) {
-        int seq, start, pair;
-        s_err = group_row_errors(a.rows, b, seq, start, pair);
+        int start, pair;
+        s_err = group_row_errors(a.rows, row, start, pair);
     }
     const int krow = (lane & 7) + 8 * ((lane >> 3) & 1), kcol = 8 * (lane >> 4);
     const int vrow = (lane & 7) + 8 * (lane >> 4), vcol = 8 * ((lane >> 3) & 1);
