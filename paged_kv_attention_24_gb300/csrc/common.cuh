@@ -151,7 +151,7 @@ __device__ __forceinline__ void add_row(const GroupRows &r, int i, BatchSums &s)
     }
 }
 
-// What a call's kernels know of each other's cost (whole nanoseconds, so that all of them come to
+// What a call's kernels know of each other's cost (in whole numbers, so that all of them come to
 // the same answer).  Measured: HBM gives 6.4 TB/s; a split CTA starts within 5 us, takes a 16-key tile
 // of its heads in tile_ns out of L2 or HBM (0.93 us for page boxes of 8 heads, 0.5 us for per-key rows
 // of one head and 0.1 us more for each further one) and 0.6 us more for every request it begins; a

@@ -27,7 +27,8 @@ def run(g, **kw):
                                   g.scale, **kw)
 
 
-VARIANTS = {"always": ("always", 0), "short": ("never", 0), "split": ("never", 2000)}
+# sharing, and the least max_seq_len: "auto" by a bound that leaves the choice to the device
+VARIANTS = {"always": ("always", 0), "short": ("never", 0), "split": ("never", 2000), "auto": ("auto", 40000)}
 
 
 def varied(w, variant):
