@@ -762,6 +762,8 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(
     if constexpr (kThrough) {
         int start, pair;
         err = group_row_errors(rows, group_row_at(rows, b), start, pair);
+        // (the split works on the keys of rows in error too: this grid does not end before it)
+        if (err) asm volatile("griddepcontrol.wait;" ::: "memory");
     }
     if (err) {
         if (blockIdx.x == 0 && warp == 0 && lane == 0) report(status, err);

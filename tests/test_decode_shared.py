@@ -192,6 +192,22 @@ def test_rows_in_error_leave_the_others_alone(variant):
 
 
 @pytest.mark.parametrize("variant", list(VARIANTS))
+def test_every_row_in_error(variant):
+    w = shared_batch.make(16, 8, 16, [(160, [1, 40, 9])], seed=19)
+    w, kw = varied(w, variant)
+    g = w.cuda()
+    good = run(g, **kw)
+    status = ops.new_status()
+    bad = dataclasses.replace(g, seq=torch.tensor([0, 200, 169], dtype=torch.int32, device="cuda"),
+                              shared=torch.tensor([160, 150, 140], dtype=torch.int32, device="cuda"))
+    o, lse = run(bad, status=status, **kw)
+    again = run(g, **kw)
+    assert ops.read_status(status) == ops.DEVERR_LENGTH | ops.DEVERR_GROUP
+    assert torch.all(o == 0) and torch.all(lse == float("-inf"))
+    assert torch.equal(again[0], good[0]) and torch.equal(again[1], good[1])
+
+
+@pytest.mark.parametrize("variant", list(VARIANTS))
 def test_narrow_table_is_a_page_error(variant):
     w = shared_batch.make(16, 8, 16, [(160, [1, 40]), (0, [20])], seed=14)
     w, kw = varied(w, variant)
