@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1 + copy_warps(kBox, kMo
         total = own_only ? batch.total.own : batch.total.all;
         const long long at = own_only ? batch.before.own : batch.before.all;
         const long long n = own_only ? batch.mine.own : batch.mine.all;
-        const long long r0 = keys_per_cta(total, ranges) * range;
+        const long long r0 = grouped_keys_per_cta(total, ranges, a.num_reqs) * range;
         if (r0 < total && at <= r0 && r0 < at + n) {
             s_row = batch.b0;
             s_base = at;
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1 + copy_warps(kBox, kMo
             for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
         }
         const long long P = ranges;
-        const long long per = keys_per_cta(total, P);
+        const long long per = kMode == kGrouped ? grouped_keys_per_cta(total, P, B) : keys_per_cta(total, P);
         const long long r0 = per * range;
         const long long r1 = min(total, r0 + per);
         int it = 0;
@@ -720,7 +720,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1 + copy_warps(kBox, kMo
 // partials at a time so their loads overlap.
 constexpr int kMergeMaxParts = kMaxDecodeCtas + 1;
 
-template <bool kThrough>
+template <bool kThrough, int kAtOnce = 4>
 __global__ void __launch_bounds__(256) decode_merge_kernel(
     const GroupRows rows, int32_t hq, int32_t num_ctas, const float *__restrict__ part_o, const float *__restrict__ part_lse,
     __nv_bfloat16 *__restrict__ o, float *__restrict__ lse, uint32_t *status) {
@@ -773,7 +773,8 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(
     }
     // the split kernel's partials are complete and visible after this point
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const long long per = keys_per_cta(s_total, num_ctas);
+    const long long per =
+        kThrough ? grouped_keys_per_cta(s_total, num_ctas, rows.num_reqs) : keys_per_cta(s_total, num_ctas);
     const int first = (int)(s_start / per);
     const int count = (int)((s_start + sb - 1) / per) - first + 1;   // <= num_ctas
     if (count <= 4) {
@@ -844,6 +845,23 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(
         const float *base = part_o + ((long long)(b + first) * hq + h) * kHeadDim + lane * 4;
         const long long stride = (long long)hq * kHeadDim;
         int i = 0;
+        if constexpr (kAtOnce > 4) {
+            for (; i < count; i += kAtOnce) {
+                float4 v[kAtOnce];
+#pragma unroll
+                for (int u = 0; u < kAtOnce; ++u)
+                    v[u] = i + u < count ? *reinterpret_cast<const float4 *>(base + (i + u) * stride)
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int u = 0; u < kAtOnce; ++u) {
+                    const float w = i + u < count ? s_w[warp][i + u] : 0.f;
+                    acc[0] += w * v[u].x;
+                    acc[1] += w * v[u].y;
+                    acc[2] += w * v[u].z;
+                    acc[3] += w * v[u].w;
+                }
+            }
+        }
         for (; i + 4 <= count; i += 4) {
             float4 v[4];
 #pragma unroll
@@ -1030,8 +1048,13 @@ cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, cudaStrea
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const GroupRows rows{a.seq_lens, a.group_start, a.shared_lens, a.num_reqs, a.max_seq_len, a.pair_rows};
-    return cudaLaunchKernelEx(&cfg, a.group_start ? decode_merge_kernel<true> : decode_merge_kernel<false>, rows, a.hq,
-                              L.ctas, (const float *)a.part_o, (const float *)a.part_lse, a.o, a.lse, a.status);
+    // grouped: the pieces of a few rows are many each, and 16 at a time are fewer round trips (2 requests
+    // of 9000 keys: 33 -> 27 us a call; with every SM full of rows the registers cost more, 51 -> 55)
+    const bool few = (long long)cfg.gridDim.x * cfg.gridDim.y <= 2ll * sm_count();
+    auto merge = !a.group_start ? decode_merge_kernel<false>
+                                : few ? decode_merge_kernel<true, 16> : decode_merge_kernel<true>;
+    return cudaLaunchKernelEx(&cfg, merge, rows, a.hq, L.ctas, (const float *)a.part_o, (const float *)a.part_lse, a.o,
+                              a.lse, a.status);
 }
 
 }  // namespace msgl

@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (last_cta) {
         // the rows' places among the pieces, for the merge
-        const long long split_per = keys_per_cta(pays ? batch.total.own : batch.total.all, share.split);
+        const long long split_per = grouped_keys_per_cta(pays ? batch.total.own : batch.total.all, share.split, rows.num_reqs);
         long long at = pays ? batch.before.own : batch.before.all, unit = before;
         for (int b = batch.b0; b < batch.b1; ++b) {
             a.plan[b].unit = unit;
@@ -819,9 +819,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------- merge
-// One warp per (request, q head), each lane 4 of the 128 dims.  A row's pieces are taken
-// four at a time (their lse and values loaded together), with a running maximum and sum.
-// Bound by latency and the rows in flight: one round for most rows, four blocks an SM.  (With the
+// One warp per (request, q head), each lane 4 of the 128 dims.  A row's pieces are taken kAtOnce at
+// a time (their lse and values loaded together), with a running maximum and sum.  Bound by latency and
+// the rows in flight.  Large batches: four pieces, one round for most rows, four blocks an SM.  (With the
 // next four pieces loaded while these are joined, three blocks fit: +1 to 1.5 us a call.  Six blocks
 // spill: +3 us.)  256 requests of 64 q heads, 30 MB of pieces: 10 us of the call's 227.
 
@@ -842,7 +842,8 @@ __device__ __forceinline__ long long div_units(long long a, long long b) {
     return ((a | b) >> 32) ? a / b : (long long)((uint32_t)a / (uint32_t)b);
 }
 
-__global__ void __launch_bounds__(kMergeThreads, 4) shared_merge_kernel(const MergeArgs a) {
+template <int kAtOnce>
+__global__ void __launch_bounds__(kMergeThreads, kAtOnce > 4 ? 1 : 4) shared_merge_kernel(const MergeArgs a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = blockIdx.y;
     const int h = blockIdx.x * (kMergeThreads / 32) + warp;
@@ -893,7 +894,6 @@ __global__ void __launch_bounds__(kMergeThreads, 4) shared_merge_kernel(const Me
         x = *l;
         v = *reinterpret_cast<const float4 *>(o);
     };
-    constexpr int kAtOnce = 4;
     float M = -INFINITY, L = 0.f, acc0 = 0.f, acc1 = 0.f, acc2 = 0.f, acc3 = 0.f;
     bool failed = false;
     for (int i0 = 0; i0 < n; i0 += kAtOnce) {
@@ -1053,7 +1053,9 @@ cudaError_t launch_decode_shared(const DecodeSharedArgs &a, cudaStream_t stream)
     cfg.gridDim = dim3((d.hq + kMergeThreads / 32 - 1) / (kMergeThreads / 32), d.num_reqs);
     cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, shared_merge_kernel, g);
+    // (the pieces of a few rows are many each)
+    const bool few = (long long)cfg.gridDim.x * cfg.gridDim.y <= 2ll * sm_count();
+    return cudaLaunchKernelEx(&cfg, few ? shared_merge_kernel<16> : shared_merge_kernel<4>, g);
 }
 
 }  // namespace msgl
