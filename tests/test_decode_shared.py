@@ -129,6 +129,30 @@ def test_large_scores_and_scales():
     check(w)
 
 
+@pytest.mark.parametrize("ps", [1, 16, 64])
+def test_slots_whose_offsets_pass_32_bits(ps):
+    """Pages at both ends of pools of 9 GB: the same results as side by side in a small one."""
+    w = shared_batch.make(40, 8, ps, [(320, [1, 50, 3]), (0, [70, 200]), (700, [20, 7])], seed=9)
+    slots = 4400000 // ps * ps
+    assert slots * 8 * 128 > 2 ** 32
+    pages, n = slots // ps, w.k.shape[0] // ps
+    at = torch.arange(n)
+    at = torch.where(at % 2 == 0, at, pages - 1 - at)
+    free = torch.cuda.mem_get_info()[0]
+    if free < 40 << 30:
+        pytest.skip("needs 40 GB")
+    k = torch.empty(slots, 8, 128, dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    k.view(pages, -1)[at.cuda()] = w.k.view(n, -1).cuda()
+    v.view(pages, -1)[at.cuda()] = w.v.view(n, -1).cuda()
+    table = torch.where(w.table >= 0, at[w.table.clamp(min=0).long()].int(), w.table)
+    for variant in VARIANTS:
+        x, kw = varied(w, variant)
+        want = run(x.cuda(), **kw)
+        got = run(dataclasses.replace(x.cuda(), k=k, v=v, table=table.cuda()), **kw)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), variant
+
+
 @pytest.mark.parametrize("variant", list(VARIANTS))
 def test_repeats_are_bit_identical(variant):
     w = shared_batch.make(64, 8, 64, [(1600, rising(20, 1, 13)), (640, [5, 6])], seed=11)
