@@ -92,6 +92,15 @@ at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, int dev, const c10:
     return t;
 }
 
+// Row i of a contiguous [rows, n] tensor as a tensor of its own over the same memory (an allocation
+// costs about 0.9 us, this 0.2).
+at::Tensor row_of(const at::Tensor &t, int64_t i) {
+    auto impl = c10::make_intrusive<at::TensorImpl>(c10::Storage(t.storage()), t.key_set(), t.dtype());
+    impl->set_sizes_contiguous({t.size(1)});
+    impl->set_storage_offset(i * t.size(1));
+    return at::Tensor(std::move(impl));
+}
+
 msgl_stream_t raw(const c10::cuda::CUDAStream &s) { return reinterpret_cast<msgl_stream_t>(s.stream()); }
 
 PyObject *done(msgl_status rc) {
@@ -188,10 +197,15 @@ PyObject *shared_prefixes(PyObject *, PyObject *const *a, Py_ssize_t n) {
                       min_shared = integer32(a[4], "min_shared");
         c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
         const c10::cuda::CUDAStream stream = stream_of(a[8], dev);
-        const at::Tensor first =
-            a[5] == Py_None ? fresh(seq.sizes(), at::kInt, dev, stream) : checked(a[5], "group_start", at::kInt, dev);
-        const at::Tensor shared =
-            a[6] == Py_None ? fresh(seq.sizes(), at::kInt, dev, stream) : checked(a[6], "shared_lens", at::kInt, dev);
+        at::Tensor first, shared;
+        if (a[5] == Py_None && a[6] == Py_None) {
+            const at::Tensor both = fresh({2, B}, at::kInt, dev, stream);
+            first = row_of(both, 0);
+            shared = row_of(both, 1);
+        } else {
+            first = a[5] == Py_None ? fresh({B}, at::kInt, dev, stream) : checked(a[5], "group_start", at::kInt, dev);
+            shared = a[6] == Py_None ? fresh({B}, at::kInt, dev, stream) : checked(a[6], "shared_lens", at::kInt, dev);
+        }
         if (pages.dim() != 2 || pages.size(0) != B || first.numel() != B || shared.numel() != B)
             refuse("%s must be [B, width]; seq_lens, group_start and shared_lens [B]", "page_table");
         uint32_t *status = status_ptr(a[7], dev);
