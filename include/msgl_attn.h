@@ -326,7 +326,10 @@ MSGL_API msgl_status msgl_attn_decode_noalloc(const msgl_kv_pool *pool, const ms
  *   out          total_tokens entries of positions and out_loc; when the step has fewer tokens
  *                (a captured step padded to a bucket) the entries behind them are
  *                positions = 0, out_loc = -1, so that a store skips them
- * No output may overlap an input but req_table.  A request is refused when its
+ * No array that the step writes may overlap another of its arrays (MSGL_ERR_INVALID_ARG): a loop that
+ * passes the last step's seq_lens on as cached_lens alternates between two sets of outputs.  One
+ * exception: out->page_ids may be req_table itself, at the same stride and without req_rows.
+ * A request is refused when its
  * length is negative or needs more columns than either table has, or its row is
  * outside the table (MSGL_DEVERR_LENGTH), when its tokens pass total_tokens
  * (MSGL_DEVERR_LENGTH), or when free_pages does not reach its last new page

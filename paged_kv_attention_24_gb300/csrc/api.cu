@@ -90,6 +90,33 @@ msgl_status check_scale(float scale) {
     return MSGL_OK;
 }
 
+// int32 entries in device memory: `rows` rows of `width`, `pitch` apart.
+struct Span {
+    const int32_t *at;
+    int64_t rows, width, pitch;
+    const char *name;
+};
+
+Span flat(const int32_t *at, int64_t n, const char *name) { return Span{at, 1, n, n, name}; }
+
+// Do two arrays have an entry in common?  Exact, so that two tables may be columns of one allocation.
+bool overlap(const Span &a, const Span &b) {
+    if (!a.at || !b.at || a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
+    const int64_t size = sizeof(int32_t), a0 = (int64_t)(uintptr_t)a.at, b0 = (int64_t)(uintptr_t)b.at;
+    if (a0 + ((a.rows - 1) * a.pitch + a.width) * size <= b0 || b0 + ((b.rows - 1) * b.pitch + b.width) * size <= a0)
+        return false;
+    if (b.rows > a.rows) return overlap(b, a);
+    // the last row of a that begins in front of the end of b's row r is the only one that can reach it
+    for (int64_t r = 0; r < b.rows; ++r) {
+        const int64_t from = b0 + r * b.pitch * size, to = from + b.width * size;
+        if (to <= a0) continue;
+        const int64_t row = a.rows == 1 ? 0 : (to - 1 - a0) / (a.pitch * size);
+        const int64_t last = row < a.rows ? row : a.rows - 1;
+        if (a0 + (last * a.pitch + a.width) * size > from) return true;
+    }
+    return false;
+}
+
 }  // namespace
 
 namespace msgl {
@@ -384,6 +411,26 @@ msgl_status msgl_step_tables(int64_t num_slots, int32_t page_size, int32_t *req_
     if (num_free > 0 && !free_pages) return fail(MSGL_ERR_INVALID_ARG, "free_pages is NULL");
     if (out->total_tokens > msgl::kMaxStepItems || a.max_pages > msgl::kMaxStepItems)
         return fail(MSGL_ERR_UNSUPPORTED, "more than %lld tokens or columns", (long long)msgl::kMaxStepItems);
+    // Every block takes the sums over the lengths before its own while others write, so an output over an
+    // input would race with them.
+    const Span outs[] = {{out->page_ids, num_reqs, a.max_pages, out->stride, "out->page_ids"},
+                         {req_table, num_rows, a.max_pages, table_stride, "req_table"},
+                         flat(out->seq_lens, num_reqs, "out->seq_lens"),
+                         flat(out->cu_ext, (int64_t)num_reqs + 1, "out->cu_ext"),
+                         flat(out->positions, out->total_tokens, "out->positions"),
+                         flat(out->out_loc, out->total_tokens, "out->out_loc"),
+                         flat(out->pages_taken, 1, "out->pages_taken")};
+    const Span ins[] = {flat(cached_lens, num_reqs, "cached_lens"), flat(new_lens, num_reqs, "new_lens"),
+                        flat(req_rows, num_reqs, "req_rows"), flat(free_pages, num_free, "free_pages")};
+    const bool in_place = out->page_ids == req_table && out->stride == table_stride && !req_rows;
+    constexpr int kOuts = sizeof outs / sizeof outs[0];
+    for (int i = 0; i < kOuts; ++i) {
+        for (const Span &in : ins)
+            if (overlap(outs[i], in)) return fail(MSGL_ERR_INVALID_ARG, "%s overlaps %s", outs[i].name, in.name);
+        for (int j = 0; j < i; ++j)
+            if (!(j == 0 && i == 1 && in_place) && overlap(outs[i], outs[j]))
+                return fail(MSGL_ERR_INVALID_ARG, "%s overlaps %s", outs[j].name, outs[i].name);
+    }
     a.req_table = req_table;
     a.req_rows = req_rows;
     a.cached_lens = cached_lens;

@@ -420,7 +420,9 @@ def step_tables(req_table: torch.Tensor, cached_lens: torch.Tensor, new_lens: Op
     this step's new pages, taken from the front of ``free_pages``; request b is row
     ``req_rows[b]`` (b when None), has ``cached_lens[b]`` tokens and gets ``new_lens[b]``
     more (one each when None).  ``total_tokens`` and ``width`` size the outputs when
-    ``out`` is not given (W columns by default).
+    ``out`` is not given (W columns by default).  No output may overlap an input: a loop
+    whose ``cached_lens`` are the last step's ``seq_lens`` keeps two ``out`` and takes
+    them in turn.  ``out.page_table`` may be ``req_table`` itself when ``req_rows`` is None.
     """
     if out is None:
         if total_tokens is None:
