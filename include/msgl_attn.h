@@ -376,7 +376,8 @@ MSGL_API msgl_status msgl_step_tables(int64_t num_slots, int32_t page_size, int3
  *   seq_lens     device int32 [num_reqs]; a request whose length is outside
  *                [1, max_seq_len] (MSGL_DEVERR_LENGTH) or passes the table's width
  *                (MSGL_DEVERR_PAGE_RANGE) is a group of one; max_seq_len is at most 2^30
- *   group_start, shared_lens   device int32 [num_reqs] (output)
+ *   group_start, shared_lens   device int32 [num_reqs] (output); they may overlap neither each
+ *                other nor an input (MSGL_ERR_INVALID_ARG)
  */
 MSGL_API msgl_status msgl_shared_prefixes(const msgl_page_table *pages, const int32_t *seq_lens, int32_t num_reqs,
                                           int32_t page_size, int32_t max_seq_len, int32_t min_shared,

@@ -470,6 +470,14 @@ msgl_status msgl_shared_prefixes(const msgl_page_table *pages, const int32_t *se
     if (min_shared <= 0) return fail(MSGL_ERR_INVALID_ARG, "min_shared must be > 0");
     if (!seq_lens || !group_start || !shared_lens)
         return fail(MSGL_ERR_INVALID_ARG, "seq_lens, group_start and shared_lens must be non-NULL");
+    // (the common lengths travel in shared_lens while other blocks still read the inputs)
+    const Span ins[] = {flat(seq_lens, num_reqs, "seq_lens"),
+                        {a.pages.ids, num_reqs, a.pages.width, a.pages.stride, "page_ids"}};
+    const Span outs[] = {flat(group_start, num_reqs, "group_start"), flat(shared_lens, num_reqs, "shared_lens")};
+    for (const Span &out : outs)
+        for (const Span &in : ins)
+            if (overlap(out, in)) return fail(MSGL_ERR_INVALID_ARG, "%s overlaps %s", out.name, in.name);
+    if (overlap(outs[0], outs[1])) return fail(MSGL_ERR_INVALID_ARG, "group_start overlaps shared_lens");
     a.seq_lens = seq_lens;
     a.num_reqs = num_reqs;
     a.max_seq_len = max_seq_len;

@@ -1,4 +1,5 @@
-"""Which arrays of a step may share memory: msgl_step_tables refuses an output over an input."""
+"""Which arrays of a step may share memory: msgl_step_tables and msgl_shared_prefixes refuse an output over
+an input."""
 import ctypes
 
 import numpy as np
@@ -64,6 +65,21 @@ def test_rows_with_a_pitch(lib):
     at["cached_lens"] = (1 << 24) + 4 * (40 * 3 + 2 * W - 1)   # inside the last row's columns
     rc, text = call(lib, at, stride=40, table_stride=40)
     assert rc == 1 and "page_ids overlaps cached_lens" in text, text
+
+
+@pytest.mark.parametrize("out", ["group_start", "shared_lens"])
+@pytest.mark.parametrize("other", ["page_ids", "seq_lens", "group_start", "shared_lens"])
+def test_prefix_groups_over_another_array_are_refused(lib, out, other):
+    if out == other:
+        return
+    for shift in (0, B - 1, 1 - B):
+        at = dict(page_ids=1 << 20, seq_lens=2 << 20, group_start=3 << 20, shared_lens=4 << 20)
+        at[out] = at[other] + 4 * shift
+        pages = ops._Pages(at["page_ids"], 40, W)
+        rc = lib.msgl_shared_prefixes(ctypes.byref(pages), at["seq_lens"], B, 16, 128, 16, at["group_start"],
+                                      at["shared_lens"], None, None)
+        text = lib.msgl_last_error().decode()
+        assert rc == 1 and "overlaps" in text, (out, other, shift, text)
 
 
 @pytest.mark.gpu
