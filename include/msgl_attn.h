@@ -403,8 +403,11 @@ MSGL_API msgl_status msgl_shared_prefixes(const msgl_page_table *pages, const in
  *                the same for all rows of a group (of a group of one it is
  *                not used: all keys are its own)
  *   sharing      MSGL_SHARE_AUTO: by the batch's lengths and groups, found on the
- *                device; MSGL_SHARE_ALWAYS / MSGL_SHARE_NEVER: one or the other, for
- *                results that do not depend on what else is in the batch
+ *                device; MSGL_SHARE_ALWAYS / MSGL_SHARE_NEVER: one or the other, whatever
+ *                the batch.  None of them makes a row's bits independent of the rest of the
+ *                batch: where a row's keys are cut into pieces follows from the sums over
+ *                all rows, and each piece rounds its weights against a maximum of its own.
+ *                The same arguments give the same bits.
  *   workspace    device scratch of at least msgl_decode_shared_workspace_size()
  *                bytes, 256-byte aligned, fully rewritten by every call; two calls
  *                (or captured graphs) that may overlap need one each

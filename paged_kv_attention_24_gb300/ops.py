@@ -484,8 +484,10 @@ def attn_decode_shared(pool: KVPool, q: torch.Tensor, page_table: torch.Tensor, 
     ``shared_lens[b]`` the leading keys the group has in common, read through the first
     row's pages (:func:`shared_prefixes` finds both).  ``sharing`` = "always" or "never"
     settles whether a group's rows go through its shared keys together, which "auto"
-    does where the batch's lengths and groups make it pay.  Returns (o bf16 [B,Hq,D],
-    lse fp32 [B,Hq]).
+    does where the batch's lengths and groups make it pay.  A row's last bits depend on
+    the rest of the batch in all three (its keys are cut into pieces by the sums over all
+    rows); the same arguments give the same bits.  Returns (o bf16 [B,Hq,D], lse fp32
+    [B,Hq]).
     """
     r = (_native or _binding()).attn_decode_shared(pool.k, pool.v, pool.page_size, q, page_table, seq_lens, group_start,
                                                    shared_lens, max_seq_len, scale, out, lse, workspace, status,
