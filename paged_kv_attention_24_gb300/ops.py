@@ -19,9 +19,10 @@ from typing import NamedTuple, Optional
 
 import torch
 
+from .build import binding_path
+
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_build", "libmsgl_attn.so")
-BINDING_PATH = os.path.join(_PKG, "_build", "_msgl_binding.so")
 
 MSGL_OK = 0
 STATUS_NAMES = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "CUDA", 4: "OUT_OF_RANGE",
@@ -396,10 +397,11 @@ def _binding():
     """The native binding of the calls below (csrc/python/binding.cpp); raises if it has not been built."""
     global _native
     load()
-    if not os.path.exists(BINDING_PATH):
-        raise RuntimeError(f"the native binding is not built ({BINDING_PATH} missing); run "
+    path = binding_path()
+    if not os.path.exists(path):
+        raise RuntimeError(f"the native binding is not built ({path} missing); run "
                            "`python -c 'import __graft_entry__ as g; g.build()'`")
-    spec = importlib.util.spec_from_file_location("_msgl_binding", BINDING_PATH)
+    spec = importlib.util.spec_from_file_location("_msgl_binding", path)
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
     _native = module
