@@ -114,6 +114,12 @@ bool arity(Py_ssize_t n, Py_ssize_t want) {
     return false;
 }
 
+// Other Python threads run while the allocator and the launches may block (a full launch queue).
+struct NoGil {
+    PyThreadState *state = PyEval_SaveThread();
+    ~NoGil() { PyEval_RestoreThread(state); }
+};
+
 // Runs f; C++ exceptions (an allocation that fails) become Python ones.
 template <class F>
 PyObject *guarded(F f) {
@@ -178,9 +184,15 @@ PyObject *step_tables(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int32_t ps = integer32(a[5], "page_size");
         uint32_t *status = status_ptr(a[13], dev);
         c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
-        return done(msgl_step_tables(slots, ps, i32(table), size32(table.size(0), "req_table"), W, W, rows, i32(cached),
-                                     added, B, i32(free_pages), size32(free_pages.numel(), "free_pages"), &out, status,
-                                     raw(stream_of(a[14], dev))));
+        const c10::cuda::CUDAStream stream = stream_of(a[14], dev);
+        const int32_t num_rows = size32(table.size(0), "req_table"), num_free = size32(free_pages.numel(), "free_pages");
+        msgl_status rc;
+        {
+            NoGil no_gil;
+            rc = msgl_step_tables(slots, ps, i32(table), num_rows, W, W, rows, i32(cached), added, B, i32(free_pages),
+                                  num_free, &out, status, raw(stream));
+        }
+        return done(rc);
     });
 }
 
@@ -198,22 +210,28 @@ PyObject *shared_prefixes(PyObject *, PyObject *const *a, Py_ssize_t n) {
         c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
         const c10::cuda::CUDAStream stream = stream_of(a[8], dev);
         at::Tensor first, shared;
-        if (a[5] == Py_None && a[6] == Py_None) {
-            const at::Tensor both = fresh({2, B}, at::kInt, dev, stream);
-            first = row_of(both, 0);
-            shared = row_of(both, 1);
-        } else {
-            first = a[5] == Py_None ? fresh({B}, at::kInt, dev, stream) : checked(a[5], "group_start", at::kInt, dev);
-            shared = a[6] == Py_None ? fresh({B}, at::kInt, dev, stream) : checked(a[6], "shared_lens", at::kInt, dev);
-        }
-        if (pages.dim() != 2 || pages.size(0) != B || first.numel() != B || shared.numel() != B)
+        if (a[5] != Py_None) first = checked(a[5], "group_start", at::kInt, dev);
+        if (a[6] != Py_None) shared = checked(a[6], "shared_lens", at::kInt, dev);
+        if (pages.dim() != 2 || pages.size(0) != B || (first.defined() && first.numel() != B) ||
+            (shared.defined() && shared.numel() != B))
             refuse("%s must be [B, width]; seq_lens, group_start and shared_lens [B]", "page_table");
         uint32_t *status = status_ptr(a[7], dev);
         msgl_page_table pt;
         pt.page_ids = i32(pages);
         pt.stride = pt.width = size32(pages.size(1), "page_table");
-        const msgl_status rc = msgl_shared_prefixes(&pt, i32(seq), B, ps, max_seq, min_shared, i32(first), i32(shared),
-                                                    status, raw(stream));
+        msgl_status rc;
+        {
+            NoGil no_gil;
+            if (!first.defined() && !shared.defined()) {
+                const at::Tensor both = fresh({2, B}, at::kInt, dev, stream);
+                first = row_of(both, 0);
+                shared = row_of(both, 1);
+            }
+            if (!first.defined()) first = fresh({B}, at::kInt, dev, stream);
+            if (!shared.defined()) shared = fresh({B}, at::kInt, dev, stream);
+            rc = msgl_shared_prefixes(&pt, i32(seq), B, ps, max_seq, min_shared, i32(first), i32(shared), status,
+                                      raw(stream));
+        }
         if (rc != MSGL_OK) return done(rc);
         PyObject *x = THPVariable_Wrap(first), *y = THPVariable_Wrap(shared);
         PyObject *r = x && y ? PyTuple_Pack(2, x, y) : nullptr;
@@ -260,20 +278,11 @@ PyObject *attn_decode_shared(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
         c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
         const c10::cuda::CUDAStream stream = stream_of(a[14], dev);
-        const at::Tensor out = a[10] == Py_None ? fresh(q.sizes(), at::kBFloat16, dev, stream)
-                                                : checked(a[10], "out", at::kBFloat16, dev);
-        const at::Tensor lse = a[11] == Py_None ? fresh({q.size(0), q.size(1)}, at::kFloat, dev, stream)
-                                                : checked(a[11], "lse", at::kFloat, dev);
-        if (out.sizes() != q.sizes()) refuse("%s must be [B, Hq, D]", "out");
-        if (lse.dim() != 2 || lse.size(0) != B || lse.size(1) != hq) refuse("%s must be [B, Hq]", "lse");
-        // Scratch, when the caller brings none: from the caching allocator in the stream's order, and
-        // back to it once the kernels are queued (its next user on the stream comes behind them).
-        struct Scratch {
-            void *p = nullptr;
-            ~Scratch() {
-                if (p) c10::cuda::CUDACachingAllocator::raw_delete(p);
-            }
-        } scratch;
+        at::Tensor out, lse;
+        if (a[10] != Py_None) out = checked(a[10], "out", at::kBFloat16, dev);
+        if (a[11] != Py_None) lse = checked(a[11], "lse", at::kFloat, dev);
+        if (out.defined() && out.sizes() != q.sizes()) refuse("%s must be [B, Hq, D]", "out");
+        if (lse.defined() && (lse.dim() != 2 || lse.size(0) != B || lse.size(1) != hq)) refuse("%s must be [B, Hq]", "lse");
         void *ws = nullptr;
         size_t ws_bytes = 0;
         if (a[12] != Py_None) {
@@ -282,15 +291,30 @@ PyObject *attn_decode_shared(PyObject *, PyObject *const *a, Py_ssize_t n) {
                 refuse("%s must be contiguous and on q's device", "workspace");
             ws = t.data_ptr();
             ws_bytes = t.nbytes();
-        } else {
-            ws_bytes = msgl_decode_shared_workspace_size(B, hq, pool.num_kv_heads, pool.head_dim, max_seq);
-            if (ws_bytes)
-                ws = scratch.p = c10::cuda::CUDACachingAllocator::raw_alloc_with_stream(ws_bytes, stream.stream());
         }
-        const msgl_status rc =
-            msgl_attn_decode_shared(&pool, &pt, q.data_ptr(), hq, i32(first), i32(shared), i32(seq), B, max_seq, sharing,
-                                    (float)scale, out.data_ptr(), static_cast<float *>(lse.data_ptr()), ws, ws_bytes,
-                                    status, raw(stream));
+        const bool own_scratch = a[12] == Py_None;
+        msgl_status rc;
+        {
+            NoGil no_gil;
+            if (!out.defined()) out = fresh(q.sizes(), at::kBFloat16, dev, stream);
+            if (!lse.defined()) lse = fresh({q.size(0), q.size(1)}, at::kFloat, dev, stream);
+            // Scratch, when the caller brings none: from the caching allocator in the stream's order, and
+            // back to it once the kernels are queued (its next user on the stream comes behind them).
+            struct Scratch {
+                void *p = nullptr;
+                ~Scratch() {
+                    if (p) c10::cuda::CUDACachingAllocator::raw_delete(p);
+                }
+            } scratch;
+            if (own_scratch) {
+                ws_bytes = msgl_decode_shared_workspace_size(B, hq, pool.num_kv_heads, pool.head_dim, max_seq);
+                if (ws_bytes)
+                    ws = scratch.p = c10::cuda::CUDACachingAllocator::raw_alloc_with_stream(ws_bytes, stream.stream());
+            }
+            rc = msgl_attn_decode_shared(&pool, &pt, q.data_ptr(), hq, i32(first), i32(shared), i32(seq), B, max_seq,
+                                         sharing, (float)scale, out.data_ptr(), static_cast<float *>(lse.data_ptr()), ws,
+                                         ws_bytes, status, raw(stream));
+        }
         if (rc != MSGL_OK) return done(rc);
         PyObject *x = THPVariable_Wrap(out), *y = THPVariable_Wrap(lse);
         PyObject *r = x && y ? PyTuple_Pack(2, x, y) : nullptr;
