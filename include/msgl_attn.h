@@ -455,12 +455,14 @@ MSGL_API msgl_status msgl_selftest_wait_timeout(uint32_t *status, int64_t budget
 /*
  * Host-side checks of one step's metadata, for tests and debugging.  They
  * read HOST copies of the arrays (copy the device arrays back first), launch
- * nothing, need no GPU and allocate nothing.  The kernels check the same
+ * nothing, need no GPU and allocate no device memory.  The kernels check the same
  * conditions on the device and report them through the status word; these
  * calls name the first offending entry in msgl_last_error().  Each returns
  * MSGL_OK, MSGL_ERR_INVALID_ARG (NULL array, bad scalar, inconsistent
  * lengths, wrong position, duplicate slot) or MSGL_ERR_OUT_OF_RANGE (a slot,
- * page index or page id outside the pool or the table).
+ * page index or page id outside the pool or the table).  The store's and the
+ * step's keep what they have seen in host memory; where that runs out they
+ * return MSGL_ERR_UNSUPPORTED.
  *
  * msgl_check_store_meta:  every out_loc[t] lies in [0, num_slots) and no
  *   slot is named twice (the store's result would depend on which row wins).

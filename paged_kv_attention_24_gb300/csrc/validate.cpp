@@ -8,6 +8,7 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include <exception>
 #include <unordered_set>
 
 #include "../../include/msgl_attn.h"
@@ -58,11 +59,14 @@ msgl_status check_pool_scalars(int64_t num_slots, int32_t page_size, const int32
     return MSGL_OK;
 }
 
+// The sets of slots, rows and pages seen are the only thing here that can throw.
+msgl_status no_memory() { return bad(MSGL_ERR_UNSUPPORTED, "out of host memory for the check"); }
+
 }  // namespace
 
 extern "C" {
 
-msgl_status msgl_check_store_meta(int64_t num_slots, const int32_t *out_loc, int32_t n_tokens) {
+msgl_status msgl_check_store_meta(int64_t num_slots, const int32_t *out_loc, int32_t n_tokens) try {
     msgl::set_last_error("");
     if (n_tokens < 0 || num_slots < 0) return bad(MSGL_ERR_INVALID_ARG, "n_tokens and num_slots must be >= 0");
     if (n_tokens > 0 && !out_loc) return bad(MSGL_ERR_INVALID_ARG, "out_loc is NULL");
@@ -76,6 +80,8 @@ msgl_status msgl_check_store_meta(int64_t num_slots, const int32_t *out_loc, int
             return bad(MSGL_ERR_INVALID_ARG, "out_loc[%d] = %d names a slot an earlier row already writes", t, s);
     }
     return MSGL_OK;
+} catch (const std::exception &) {
+    return no_memory();
 }
 
 msgl_status msgl_check_extend_meta(int64_t num_slots, int32_t page_size, const int32_t *page_ids, int32_t stride,
@@ -143,7 +149,7 @@ msgl_status msgl_check_decode_meta(int64_t num_slots, int32_t page_size, const i
 msgl_status msgl_check_step_meta(int64_t num_slots, int32_t page_size, const int32_t *req_table, int32_t num_rows,
                                  int32_t table_stride, int32_t table_width, const int32_t *req_rows,
                                  const int32_t *cached_lens, const int32_t *new_lens, int32_t num_reqs,
-                                 const int32_t *free_pages, int32_t num_free, int32_t total_tokens) {
+                                 const int32_t *free_pages, int32_t num_free, int32_t total_tokens) try {
     msgl::set_last_error("");
     msgl_status rc = check_pool_scalars(num_slots, page_size, req_table, table_stride, table_width);
     if (rc) return rc;
@@ -185,6 +191,8 @@ msgl_status msgl_check_step_meta(int64_t num_slots, int32_t page_size, const int
             return bad(MSGL_ERR_INVALID_ARG, "free_pages[%lld] = %d is in use", (long long)p, free_pages[p]);
     }
     return MSGL_OK;
+} catch (const std::exception &) {
+    return no_memory();
 }
 
 msgl_status msgl_check_groups_meta(int64_t num_slots, int32_t page_size, const int32_t *page_ids, int32_t stride,
