@@ -32,15 +32,16 @@ msgl_status bad(msgl_status s, const char *fmt, ...) {
 
 bool pow2(int32_t x) { return x > 0 && (x & (x - 1)) == 0; }
 
-// Pages of keys 0..n_keys-1 of request b: index below width, id inside the pool.
+// Pages of keys 0..n_keys-1 of request b, which are row `row` of the table: index below width, id
+// inside the pool.
 msgl_status check_pages(int64_t num_pages, int32_t page_size, const int32_t *page_ids, int32_t stride,
-                        int32_t width, int32_t b, int64_t n_keys) {
+                        int32_t width, int32_t b, int32_t row, int64_t n_keys) {
     const int64_t n_pages = (n_keys + page_size - 1) / page_size;
     if (n_pages > width)
         return bad(MSGL_ERR_OUT_OF_RANGE, "request %d: %lld keys need %lld pages but the table width is %d", b,
                    (long long)n_keys, (long long)n_pages, width);
     for (int64_t p = 0; p < n_pages; ++p) {
-        const int32_t id = page_ids[(int64_t)b * stride + p];
+        const int32_t id = page_ids[(int64_t)row * stride + p];
         if (id < 0 || id >= num_pages)
             return bad(MSGL_ERR_OUT_OF_RANGE, "request %d: page_ids[%lld] = %d is outside [0, %lld)", b,
                        (long long)p, id, (long long)num_pages);
@@ -120,7 +121,7 @@ msgl_status msgl_check_extend_meta(int64_t num_slots, int32_t page_size, const i
                 if (positions[cu_ext[b] + i] != pre + i)
                     return bad(MSGL_ERR_INVALID_ARG, "request %d row %d: positions[%d] = %d, expected %d", b, i,
                                cu_ext[b] + i, positions[cu_ext[b] + i], pre + i);
-        if ((rc = check_pages(num_pages, page_size, page_ids, stride, width, b, (int64_t)pre + ext))) return rc;
+        if ((rc = check_pages(num_pages, page_size, page_ids, stride, width, b, b, (int64_t)pre + ext))) return rc;
     }
     if (cu_ext[num_reqs] != total_tokens)
         return bad(MSGL_ERR_INVALID_ARG, "cu_ext[%d] = %d but total_tokens = %d", num_reqs, cu_ext[num_reqs],
@@ -141,7 +142,7 @@ msgl_status msgl_check_decode_meta(int64_t num_slots, int32_t page_size, const i
         if (n < 1 || n > max_seq_len)
             return bad(MSGL_ERR_INVALID_ARG, "request %d: seq_len %d is outside [1, max_seq_len = %d]", b, n,
                        max_seq_len);
-        if ((rc = check_pages(num_pages, page_size, page_ids, stride, width, b, n))) return rc;
+        if ((rc = check_pages(num_pages, page_size, page_ids, stride, width, b, b, n))) return rc;
     }
     return MSGL_OK;
 }
@@ -172,7 +173,7 @@ msgl_status msgl_check_step_meta(int64_t num_slots, int32_t page_size, const int
         if (pages > table_width)
             return bad(MSGL_ERR_OUT_OF_RANGE, "request %d: %lld tokens need %lld pages but the table width is %d", b,
                        (long long)cached + fresh, (long long)pages, table_width);
-        if ((rc = check_pages(num_pages, page_size, req_table, table_stride, table_width, row, cached))) return rc;
+        if ((rc = check_pages(num_pages, page_size, req_table, table_stride, table_width, b, row, cached))) return rc;
         for (int64_t p = 0; p < old_pages; ++p) used.insert(req_table[(int64_t)row * table_stride + p]);
         tokens += fresh;
         taken += pages - old_pages;
@@ -219,7 +220,7 @@ msgl_status msgl_check_groups_meta(int64_t num_slots, int32_t page_size, const i
             return bad(MSGL_ERR_INVALID_ARG, "request %d: shared_len %d but its group's first has %d", b, shared,
                        shared_lens[first]);
         // shared keys on the first row's pages, the others on its own
-        if (first == b && (rc = check_pages(num_pages, page_size, page_ids, stride, width, b, n))) return rc;
+        if (first == b && (rc = check_pages(num_pages, page_size, page_ids, stride, width, b, b, n))) return rc;
         if (((int64_t)n + page_size - 1) / page_size > width)
             return bad(MSGL_ERR_OUT_OF_RANGE, "request %d: %d keys do not fit the table width %d", b, n, width);
         for (int64_t p = shared / page_size; p * page_size < n; ++p) {
