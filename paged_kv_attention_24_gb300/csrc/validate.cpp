@@ -168,6 +168,8 @@ msgl_status msgl_check_step_meta(int64_t num_slots, int32_t page_size, const int
             return bad(MSGL_ERR_INVALID_ARG, "request %d: row %d belongs to an earlier request too", b, row);
         if (cached < 0 || fresh < 0)
             return bad(MSGL_ERR_INVALID_ARG, "request %d: cached_len %d and new_len %d must be >= 0", b, cached, fresh);
+        if ((int64_t)cached + fresh > INT32_MAX)
+            return bad(MSGL_ERR_INVALID_ARG, "request %d: %lld tokens do not fit 32 bits", b, (long long)cached + fresh);
         const int64_t old_pages = ((int64_t)cached + page_size - 1) / page_size;
         const int64_t pages = ((int64_t)cached + fresh + page_size - 1) / page_size;
         if (pages > table_width)

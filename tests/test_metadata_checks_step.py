@@ -1,4 +1,4 @@
-"""msgl_check_step_meta names the request, not its row of the resident table."""
+"""msgl_check_step_meta names the request, not its row of the resident table, and refuses what the kernel refuses."""
 import pytest
 import torch
 
@@ -28,3 +28,15 @@ def test_the_request_is_named():
         with pytest.raises(ops.MsglError) as e:
             ops.check_step_meta(**dict(good, cached_lens=cached))
         assert e.value.status == OUT_OF_RANGE and fragment in str(e.value), str(e.value)
+
+
+def test_a_length_past_int32():
+    """The kernel refuses a request of more than 2^31 - 1 tokens however wide the table is."""
+    pages = 2 ** 31 // 256
+    table = torch.zeros(1, pages + 1, dtype=torch.int32)
+    args = dict(num_slots=256 * (pages + 2), page_size=256, req_table=table, req_rows=None,
+                cached_lens=i32(2 ** 31 - 1 - 200), free_pages=i32(1, 2), total_tokens=1000)
+    ops.check_step_meta(**dict(args, new_lens=i32(200)))
+    with pytest.raises(ops.MsglError) as e:
+        ops.check_step_meta(**dict(args, new_lens=i32(201)))
+    assert e.value.status == INVALID and "request 0" in str(e.value), str(e.value)
