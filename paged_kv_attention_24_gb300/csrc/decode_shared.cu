@@ -325,6 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // before the barrier).
     auto next_segs = [&]() -> bool {
         if (!*more_segs) return false;
+        __syncwarp();   // (the barrier counts whole warps)
         block_sync();
         if (*abort_flag) return false;
         if (warp == 0) {
