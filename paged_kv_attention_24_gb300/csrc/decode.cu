@@ -4,8 +4,9 @@
 // from prefill; §6.4: decode is replayed under CUDA graphs, so the launch
 // shape depends only on host scalars and the device (never on seq_lens).
 //
-// Design (bandwidth-bound: every cached K/V byte is read exactly once)
-// ---------------------------------------------------------------------
+// Design (bandwidth-bound: every key's K/V bytes are read once for each request that attends
+// it; kGrouped, below, may leave the keys that a group shares to the shared-prefix kernel)
+// -------------------------------------------------------------------------------------------
 // * Balanced split-KV.  The keys of all requests, laid end to end, are cut
 //   into P equal ranges (at least 32 keys each), one per persistent CTA
 //   (P = resident CTAs on the GPU).  A CTA's range covers one or more request segments; each segment
@@ -234,7 +235,11 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1 + copy_warps(kBox, kMo
         bool patch_pending = false;
         bool aborted = false;
         const uint32_t row_bytes = (uint32_t)hg * 256;
-        // every K/V byte is read once: evict-first keeps the stream from displacing other lines
+        // A request's own K/V are read once: evict-first keeps the stream from displacing other lines.
+        // kGrouped: where the ranges take the shared keys too, those come again for every request of
+        // the group.  Without the hint there, 256 requests over 32768 shared tokens of 8 heads took 2.35
+        // ms in place of 2.54, but rows of 1 to 4 heads 4 to 13% more, and batches that leave the shared
+        // keys to their own kernel, the usual ones, up to 6 us more.
         const uint64_t stream_policy = ptx::l2_evict_first_policy();
         const long long slot_elems = (long long)a.pool.hkv * kHeadDim;
 

@@ -397,9 +397,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     int64_t slot0;
                     if (lsu) {
                         // 16-byte cp.async copies into the SWIZZLE_128B K-major layout (see extend.cu).
-                        // Warps 0 and 2 copy the K tiles of one stage each, warp 3 the V tiles; a
-                        // tile is handed over when the warp's next one has been issued, so that the
-                        // copies of two overlap.
+                        // Warps 0 and 2 copy the K tiles of one stage each and hand a tile over when
+                        // its copies have landed; warp 3 copies the V tiles and hands one over when its
+                        // next has been issued.  Either way the copies of two tiles overlap.
                         const __nv_bfloat16 *pool = is_v ? a.pool.v : a.pool.k;
                         const int step = is_v ? 1 : 2;
                         const int first = is_v ? 0 : (int)((tile0 ^ (warp == 2 ? 1u : 0u)) & 1u);
@@ -939,9 +939,13 @@ __global__ void __launch_bounds__(kMergeThreads, kAtOnce > 4 ? 1 : 4) shared_mer
 // 22 us, and the prefix kernel would take longer than that for its start, one tile and the join.
 constexpr long long kThroughBytes = 140ll << 20;
 
-// Where the one-launch kernel of short requests is taken.  Up to 128 keys its blocks are small
-// enough to keep several on an SM, and it was never behind the split and merge (32 keys, 256
-// requests: 13.4 against 22.7 us).  Longer ones have an SM to themselves, or nearly: ahead as long as
+// Where the one-launch kernel of short requests is taken instead of the split and merge (by
+// "never", and by "auto" up to kThroughBytes).  Up to 128 keys its blocks are small enough to keep
+// several on an SM (about 128 keys, page size 1: 16/8 heads 64 requests 12.3 against 16.0 us, 2000
+// requests 163 against 172, 256 to 600 requests 28 to 55 against 26 to 47; 64/8 and 16/2 heads ahead at
+// every size, 35 against 41 and 15 against 23 us for 300 requests).  Batches of that kind beyond
+// kThroughBytes go by the device's plan in three launches: 40 us in place of 55 for 600 requests of 16/8
+// heads, 42 in place of 35 for 300 of 64/8, 76 in place of 54 for 2000 of 16/2.  Longer requests have an SM to themselves, or nearly: ahead as long as
 // there are at most two a SM (512 keys, 8 kv heads: 8 requests 8.2 against 11.5 us at page size 1 and
 // 13.8 at 16, 32 requests 13 against 17, 64 requests 23 against 21; 1024 keys: 16 requests 13.4 against
 // 17, but 2 requests 12.6 against 11.9 at page size 1), and the split's many CTAs win on the longest.
