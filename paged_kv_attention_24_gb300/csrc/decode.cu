@@ -662,6 +662,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadGroup + 1 + copy_warps(kBox, kMo
             m2[1] = mn1;
             l[0] = l[0] * al0 + p00 + p10;
             l[1] = l[1] * al1 + p01 + p11;
+            // P is rounded to bf16 for the product (at most 2^-8 of each weight); the sums are not
             const uint32_t pb0 = ptx::movmatrix_t(ptx::pack_bf16(p00, p01));   // keys 0-7
             const uint32_t pb1 = ptx::movmatrix_t(ptx::pack_bf16(p10, p11));   // keys 8-15
             // zero V^T fragment entries of keys that were not loaded
