@@ -416,8 +416,9 @@ MSGL_API msgl_status msgl_shared_prefixes(const msgl_page_table *pages, const in
  * MSGL_DEVERR_GROUP and is written as o = 0, lse = -inf, and so may be the rows
  * of its group behind it; a bad page among the shared keys does that to every
  * row of the group (MSGL_DEVERR_PAGE_RANGE).
- * At most 65535 requests, max_seq_len at most 2^30.  The launch shapes depend on
- * host scalars only.
+ * At most 65535 requests, max_seq_len at most 2^30.  A CTA that would work on one
+ * group's shared keys for more than about 2 s (some 170 million keys) gives up with
+ * MSGL_DEVERR_TIMEOUT.  The launch shapes depend on host scalars only.
  */
 #define MSGL_SHARE_AUTO 0
 #define MSGL_SHARE_ALWAYS 1
