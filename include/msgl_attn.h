@@ -77,7 +77,10 @@ typedef enum msgl_status {
 #define MSGL_DEVERR_TIMEOUT 0x10u    /* a bounded in-kernel wait gave up */
 #define MSGL_DEVERR_APPEND_SLOT 0x20u /* decode_append: new_loc[b] is not the slot of key seq_lens[b]-1 */
 #define MSGL_DEVERR_GROUP 0x40u      /* group_start / shared_lens do not describe a group (decode_shared) */
-#define MSGL_DEVERR_NO_PAGES 0x80u   /* step_tables: the free pages do not reach this far */
+#define MSGL_DEVERR_NO_PAGES 0x80u   /* step_tables, fork: the free pages do not reach this far */
+#define MSGL_DEVERR_ROW 0x100u       /* fork, free, compact: a row outside the table, or one that forks collide on */
+#define MSGL_DEVERR_TOKEN 0x200u     /* verify_drafts: a drafted token outside the vocabulary */
+#define MSGL_DEVERR_PROBS 0x400u     /* verify_drafts: a row without a positive finite sum */
 
 /*
  * The unified KV pool of one layer.  k_pool and v_pool are device bf16
@@ -360,6 +363,217 @@ MSGL_API msgl_status msgl_step_tables(int64_t num_slots, int32_t page_size, int3
                                       uint32_t *status, msgl_stream_t stream);
 
 /*
+ * Store step with the rotation in it: q and k of the new tokens turned by their
+ * positions, q written to q_out, k and v to the pool ("不懂SGLang？从miniSGLang开始",
+ * §1.3 items 1 and 3: the positions are an input of the forward, the new K/V
+ * become part of the pool).  Pair j of a head, (x_j, y_j), turns by
+ *   angle_j = positions[axis_j][t] * f_j:
+ *   x' = factor * (x cos - y sin),  y' = factor * (y cos + x sin)
+ * with x_j, y_j = dims j and j + num_pairs, or (adjacent) 2j and 2j + 1; dims from
+ * 2 * num_pairs on stay as they are.  With q_norm / k_norm a head is first
+ * replaced by x * w / sqrt(mean(x^2) + eps).  All of it is computed in 32 bits (the
+ * angle modulo a turn exactly) and rounded to bf16 once; v is copied.
+ *
+ *   turns        host uint64 [num_pairs]: f_j / (2 pi) * 2^64 modulo 2^64
+ *   axes         host uint8 [num_pairs]: axis_j < num_axes, or NULL (all 0)
+ *   num_pairs    8, 16, .. 64;  num_axes 1..4
+ *   q, k, v      device bf16 [n_tokens, heads, head_dim], token t at t * stride elements
+ *                (strides: multiples of 8, at least heads * head_dim), so that they may
+ *                be columns of one projection's output
+ *   q_out        the same for the turned q; may be q itself (same stride), and may not
+ *                otherwise overlap an input
+ *   positions    device int32, axis a of token t at a * axis_stride + t; any int32 value
+ *   out_loc      device int32 [n_tokens]: the token's pool slot.  -1: not a token (the
+ *                padding of msgl_step_tables, and the tokens of a request that it
+ *                refused): nothing is read or written for it, its row of q_out
+ *                stays as it was.  Another slot out of range sets
+ *                MSGL_DEVERR_SLOT_RANGE: q is turned, nothing stored.
+ *   q_norm, k_norm  device bf16 [head_dim] or NULL
+ * Duplicate slots are undefined (one of the rows wins).
+ */
+typedef struct msgl_rope {
+    const uint64_t *turns;         /* host */
+    const uint8_t *axes;           /* host, or NULL */
+    int32_t num_pairs, num_axes;
+    int32_t adjacent;
+    float factor;                  /* normally 1 */
+} msgl_rope;
+
+typedef struct msgl_new_tokens {
+    const void *q, *k, *v;         /* device bf16 */
+    void *q_out;
+    int64_t q_stride, k_stride, v_stride, out_stride;   /* elements */
+    const int32_t *positions;      /* device int32 [num_axes, n_tokens], rows axis_stride apart */
+    int64_t axis_stride;
+    const int32_t *out_loc;        /* device int32 [n_tokens] */
+    int32_t n_tokens, num_q_heads;
+} msgl_new_tokens;
+
+MSGL_API msgl_status msgl_rope_store_kv(const msgl_kv_pool *pool, const msgl_new_tokens *tokens, const msgl_rope *rope,
+                                        const void *q_norm, const void *k_norm, float eps, uint32_t *status,
+                                        msgl_stream_t stream);
+
+/*
+ * Drafted tokens accepted or replaced by the target's probabilities, from given
+ * random numbers, without the host (a decode step is a graph replay: "Mini-SGLang
+ * 实战指南", §6.4).  A step fed request b's last token and its drafts, so rows
+ * first = cu_ext[b] .. cu_ext[b+1]-1 of the step are its: tokens[first] the token
+ * before the drafts, tokens[first + i + 1] draft i, and row first + i of the
+ * target's probabilities is the distribution that draft i is held against (the
+ * last row: that of the token behind all drafts).  Draft i stands when
+ *   accept_u[first + i] * q(x) < p(x),   x = tokens[first + i + 1],
+ * p and q rows first + i of target and draft.  With a the number of drafts in
+ * front of the first one that does not stand, and r = first + a:
+ *   w = max(p_r - q_r, 0) when a draft was refused, p_r when none was or when
+ *       that is zero everywhere;
+ *   the new token = the first v with w_0 + .. + w_v > sample_u[b] * sum(w)
+ *       (the last one with w > 0 when there is none, as for sample_u >= 1)
+ *   accepted[b] = a;  kv_lens[b] = cached_lens[b] + a + 1
+ *   out_tokens[first + i] = draft i for i < a, the new token at i = a, -1 behind it
+ * kv_lens counts the tokens whose K/V of this step are kept: the cached_lens of the
+ * next msgl_step_tables (the new token's K/V are stored by that step).
+ * Weights are taken in 32 bits, sums to 48 or more.  What is not a number weighs nothing.
+ *
+ *   target, draft  device fp32 or bf16 (both the same) [total_tokens, vocab], rows
+ *                  stride elements apart; they need not sum to 1.  draft NULL: the
+ *                  drafts were not drawn at random, q(x) = 1 for each draft x itself
+ *   tokens         device int32 [total_tokens];  cu_ext device int32 [num_reqs + 1]
+ *   accept_u       device fp32 [total_tokens] (a request's last entry is not used)
+ *   sample_u       device fp32 [num_reqs], in [0, 1)
+ *   cached_lens    device int32 [num_reqs] or NULL (0)
+ *   accepted, kv_lens  device int32 [num_reqs];  out_tokens device int32 [total_tokens]
+ * The outputs may overlap neither an input nor each other (kv_lens may be
+ * cached_lens itself).  Rows outside all requests are not touched.  A request without rows
+ * gets accepted = 0 and kv_lens = cached_lens; so does one whose cu_ext
+ * entries are out of order or range (MSGL_DEVERR_LENGTH).  A draft outside
+ * [0, vocab) does not stand (MSGL_DEVERR_TOKEN).  Where w has no positive
+ * finite sum the new token is -1 (MSGL_DEVERR_PROBS).  vocab is at most 2^30.
+ */
+typedef struct msgl_draft_batch {
+    const void *target, *draft;
+    int64_t target_stride, draft_stride;
+    int32_t vocab, is_bf16;
+    const int32_t *tokens, *cu_ext;
+    const float *accept_u, *sample_u;
+    const int32_t *cached_lens;
+    int32_t num_reqs, total_tokens;
+    int32_t *accepted, *out_tokens, *kv_lens;
+} msgl_draft_batch;
+
+MSGL_API msgl_status msgl_verify_drafts(const msgl_draft_batch *batch, uint32_t *status, msgl_stream_t stream);
+
+/*
+ * Requests that continue other requests on the same pages (parallel samples of a
+ * prompt, beams): fork i gives row child_rows[i] of req_table the first lens[i]
+ * tokens of row parent_rows[i].  Whole pages are shared ("Mini-SGLang 实战指南", §6.5:
+ * requests hold the same prefix pages); a partly filled last page would be written by
+ * both, so the child gets a page of its own for it:
+ *   F = lens[i] / page_size, tail = lens[i] % page_size
+ *   req_table[child][p] = req_table[parent][p]             for p < F
+ *   tail > 0: req_table[child][F] = free_pages[k], k the number of earlier forks with a tail;
+ *             copy_src[i] = req_table[parent][F], copy_dst[i] = that page, copy_tokens[i] = tail
+ *   else      copy_src[i] = copy_dst[i] = -1, copy_tokens[i] = 0
+ *   pages_taken[0] = how many of free_pages are now in use
+ * The copies are the arguments of msgl_copy_pages.  Later columns of the child's row stay
+ * as they are.
+ *   req_table    device int32 [num_rows, table_stride], table_width valid columns (in and out)
+ *   parent_rows, child_rows, lens   device int32 [num_forks]; both rows -1: no fork (padding)
+ * Refused are a fork whose rows are outside the table, or whose child is also a parent
+ * or another fork's child (MSGL_DEVERR_ROW); one whose length is negative or passes
+ * table_width (MSGL_DEVERR_LENGTH); one that free_pages does not reach
+ * (MSGL_DEVERR_NO_PAGES); and one whose new page or partly filled page is
+ * outside [0, num_slots / page_size) (MSGL_DEVERR_PAGE_RANGE).  A refused fork's
+ * row is left as it was and nothing is copied for it; its place among the free
+ * pages is kept.  The outputs may overlap neither an input nor each other.
+ */
+typedef struct msgl_fork_out {
+    int32_t *copy_src, *copy_dst, *copy_tokens;   /* device int32 [num_forks] */
+    int32_t *pages_taken;                         /* device int32 [1] */
+} msgl_fork_out;
+
+MSGL_API msgl_status msgl_fork_requests(int64_t num_slots, int32_t page_size, int32_t *req_table, int32_t num_rows,
+                                        int32_t table_stride, int32_t table_width, const int32_t *parent_rows,
+                                        const int32_t *child_rows, const int32_t *lens, int32_t num_forks,
+                                        const int32_t *free_pages, int32_t num_free, const msgl_fork_out *out,
+                                        uint32_t *status, msgl_stream_t stream);
+
+/*
+ * Copies pages within the pools of several layers (one page table serves all layers:
+ * "Mini-SGLang 实战指南", §6.2): in every pool, the first tokens[i] slots of page src[i], K
+ * and V, go to page dst[i], bit for bit.
+ *   pools        host array [num_pools] of the same num_slots, page_size and heads, at most
+ *                2^15 of them
+ *   src, dst     device int32 [num_pairs]; both -1: no copy (padding)
+ *   tokens       device int32 [num_pairs], 0..page_size, or NULL (whole pages)
+ *   count        device int32 [1] or NULL: only the first count[0] pairs
+ * A page id outside the pool (MSGL_DEVERR_PAGE_RANGE) or a count of tokens out of
+ * range (MSGL_DEVERR_LENGTH) skips the pair.  A page that is written and
+ * is also another pair's src or dst is undefined (some order wins).
+ */
+MSGL_API msgl_status msgl_copy_pages(const msgl_kv_pool *pools, int32_t num_pools, const int32_t *src,
+                                     const int32_t *dst, const int32_t *tokens, int32_t num_pairs,
+                                     const int32_t *count, uint32_t *status, msgl_stream_t stream);
+
+/*
+ * The pages that no running request holds, in ascending order: the free_pages of the next
+ * msgl_step_tables or msgl_fork_requests.  Request b holds the first
+ * ceil(lens[b] / page_size) entries of its row, so pages come back by what the
+ * tables no longer say: a finished request is left out, a request whose drafts
+ * were refused comes with its shorter length, a page that forks share is free
+ * when none of them holds it.
+ *   req_table    device int32 [num_rows, table_stride], table_width valid columns
+ *   req_rows     device int32 [num_reqs] or NULL (row b); -1: no request (padding)
+ *   lens         device int32 [num_reqs]
+ *   held         device uint8 [num_slots / page_size] or NULL: not 0 for a page that something
+ *                else holds (a radix cache's pages, a request that waits)
+ *   pages        device int32 [num_slots / page_size] (output): the free pages' ids, -1 behind them
+ *   num_free     device int32 [1] (output): how many there are
+ * A row outside the table (MSGL_DEVERR_ROW) holds nothing; a request whose length is
+ * negative or passes table_width (MSGL_DEVERR_LENGTH) holds all of its row, so that none
+ * of its pages is given away; an id outside the pool (MSGL_DEVERR_PAGE_RANGE) is
+ * skipped.  The outputs may overlap neither an input nor each other.
+ */
+MSGL_API msgl_status msgl_free_pages(int64_t num_slots, int32_t page_size, const int32_t *req_table, int32_t num_rows,
+                                     int32_t table_stride, int32_t table_width, const int32_t *req_rows,
+                                     const int32_t *lens, int32_t num_reqs, const uint8_t *held, int32_t *pages,
+                                     int32_t *num_free, uint32_t *status, msgl_stream_t stream);
+
+/*
+ * The pages in use moved to the front of the pool, so that the pool may shrink
+ * or grow, or pages be handed out as long runs.  With U the number of pages that
+ * requests hold (as above) or `held` names: the pages that requests hold and
+ * `held` does not, with ids from U on, in ascending order, move to the first free
+ * ids below U, in ascending order.
+ *   out->src, out->dst      the moves (the arguments of msgl_copy_pages, with
+ *                           count = out->num_moves), -1 behind them
+ *   out->remap[p]           page p's id from now on (p itself when it stays), -1 when it is free
+ *   out->page_ids           the rows of the requests with the new ids in their pages' columns;
+ *                           may be req_table itself at the same stride.  An id outside the
+ *                           pool stays; other columns and rows are left as they were
+ *   out->num_used[0]        U
+ * A page that `held` names stays where it is (ids from U on may then be in use).
+ * The pages have to be copied before they are read or written again.
+ * Requests, errors and overlaps are those of msgl_free_pages (a request that holds
+ * all of its row gets new ids in all of it); a row may be named twice.  At most
+ * MSGL_COMPACT_MAX_PAGES pages (MSGL_ERR_UNSUPPORTED).
+ */
+#define MSGL_COMPACT_MAX_PAGES 1310720
+
+typedef struct msgl_compact_out {
+    int32_t *page_ids;             /* device int32 [num_rows, stride] */
+    int32_t stride;
+    int32_t *remap;                /* device int32 [num_slots / page_size] */
+    int32_t *src, *dst;            /* device int32 [num_slots / page_size / 2] */
+    int32_t *num_moves, *num_used; /* device int32 [1] */
+} msgl_compact_out;
+
+MSGL_API msgl_status msgl_compact_pages(int64_t num_slots, int32_t page_size, const int32_t *req_table,
+                                        int32_t num_rows, int32_t table_stride, int32_t table_width,
+                                        const int32_t *req_rows, const int32_t *lens, int32_t num_reqs,
+                                        const uint8_t *held, const msgl_compact_out *out, uint32_t *status,
+                                        msgl_stream_t stream);
+
+/*
  * Groups of neighbouring requests whose page tables begin with the same pages:
  * the input of msgl_attn_decode_shared.  A radix-cache hit gives requests the
  * same prefix pages ("Mini-SGLang 实战指南", §6.5 "Radix Cache"), so the tables
@@ -516,6 +730,38 @@ MSGL_API msgl_status msgl_check_groups_meta(int64_t num_slots, int32_t page_size
                                             int32_t stride, int32_t width, const int32_t *group_start,
                                             const int32_t *shared_lens, const int32_t *seq_lens, int32_t num_reqs,
                                             int32_t max_seq_len);
+
+/*
+ * The same for the arguments of msgl_fork_requests, msgl_copy_pages, msgl_free_pages and
+ * msgl_compact_pages, and msgl_verify_drafts (host copies of the arrays, nothing
+ * launched; padding entries of -1 are passed over):
+ *
+ * msgl_check_fork_meta:  rows in range, no child a parent or another fork's child,
+ *   0 <= lens[i] and within the table's width, the parents' pages in the pool,
+ *   num_free large enough, and every free page that the forks take in the pool, taken
+ *   once and not a page of a parent.
+ * msgl_check_copy_meta:  pages in range, 0 <= tokens[i] <= page_size, and no page that is
+ *   written is another pair's src or dst.
+ * msgl_check_held_meta:  (free, compact) rows in range, lengths within the table's
+ *   width, and the requests' pages in the pool.
+ * msgl_check_draft_meta:  cu_ext in order and within total_tokens, drafted tokens in
+ *   [0, vocab), accept_u and sample_u in [0, 1) where they are used.
+ */
+MSGL_API msgl_status msgl_check_fork_meta(int64_t num_slots, int32_t page_size, const int32_t *req_table,
+                                          int32_t num_rows, int32_t table_stride, int32_t table_width,
+                                          const int32_t *parent_rows, const int32_t *child_rows, const int32_t *lens,
+                                          int32_t num_forks, const int32_t *free_pages, int32_t num_free);
+
+MSGL_API msgl_status msgl_check_copy_meta(int64_t num_slots, int32_t page_size, const int32_t *src, const int32_t *dst,
+                                          const int32_t *tokens, int32_t num_pairs);
+
+MSGL_API msgl_status msgl_check_held_meta(int64_t num_slots, int32_t page_size, const int32_t *req_table,
+                                          int32_t num_rows, int32_t table_stride, int32_t table_width,
+                                          const int32_t *req_rows, const int32_t *lens, int32_t num_reqs);
+
+MSGL_API msgl_status msgl_check_draft_meta(int32_t vocab, const int32_t *tokens, const int32_t *cu_ext,
+                                           const float *accept_u, const float *sample_u, int32_t num_reqs,
+                                           int32_t total_tokens);
 
 /* Static description of a status code. */
 MSGL_API const char *msgl_status_string(msgl_status s);

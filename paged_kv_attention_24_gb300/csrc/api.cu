@@ -117,6 +117,67 @@ bool overlap(const Span &a, const Span &b) {
     return false;
 }
 
+// Do n rows, `stride` elements apart, reach further than any memory (so that offsets stay within 64 bits)?
+bool too_far(int64_t n, int64_t stride) { return stride > (1ll << 50) / (n > 0 ? n : 1); }
+
+// A byte array as the 32-bit words that it touches.
+Span bytes_span(const uint8_t *at, int64_t n, const char *name) {
+    const uintptr_t from = (uintptr_t)at & ~(uintptr_t)3;
+    return flat(reinterpret_cast<const int32_t *>(from), ((int64_t)((uintptr_t)at - from) + n + 3) / 4, name);
+}
+
+// No output over an input or another output.
+msgl_status check_overlaps(const Span *outs, int n_outs, const Span *ins, int n_ins) {
+    for (int i = 0; i < n_outs; ++i) {
+        for (int j = 0; j < n_ins; ++j)
+            if (overlap(outs[i], ins[j])) return fail(MSGL_ERR_INVALID_ARG, "%s overlaps %s", outs[i].name, ins[j].name);
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i], outs[j])) return fail(MSGL_ERR_INVALID_ARG, "%s overlaps %s", outs[j].name, outs[i].name);
+    }
+    return MSGL_OK;
+}
+
+msgl_status check_page_count(int64_t num_slots, int32_t page_size, int32_t &log2_ps, int32_t &num_pages) {
+    msgl_status s = check_page_size(page_size, log2_ps);
+    if (s) return s;
+    if (num_slots < 0 || num_slots % page_size != 0)
+        return fail(MSGL_ERR_INVALID_ARG, "num_slots must be a non-negative multiple of page_size");
+    if (num_slots / page_size > INT32_MAX) return fail(MSGL_ERR_UNSUPPORTED, "more than 2^31-1 pages");
+    num_pages = (int32_t)(num_slots / page_size);
+    return MSGL_OK;
+}
+
+msgl_status check_req_table(const int32_t *table, int32_t rows, int32_t stride, int32_t width) {
+    if (rows < 0) return fail(MSGL_ERR_INVALID_ARG, "negative size");
+    if (width < 0 || stride < width) return fail(MSGL_ERR_INVALID_ARG, "req_table needs 0 <= table_width <= table_stride");
+    if (rows > 0 && width > 0 && !table) return fail(MSGL_ERR_INVALID_ARG, "req_table is NULL");
+    return MSGL_OK;
+}
+
+// The arguments that msgl_free_pages and msgl_compact_pages share.
+msgl_status prepare_page_map(int64_t num_slots, int32_t page_size, const int32_t *req_table, int32_t num_rows,
+                             int32_t table_stride, int32_t table_width, const int32_t *req_rows, const int32_t *lens,
+                             int32_t num_reqs, const uint8_t *held, uint32_t *status, msgl::PageMapArgs &a) {
+    msgl_status s = check_page_count(num_slots, page_size, a.log2_ps, a.num_pages);
+    if (s) return s;
+    if ((s = check_req_table(req_table, num_rows, table_stride, table_width))) return s;
+    if (num_reqs < 0) return fail(MSGL_ERR_INVALID_ARG, "negative size");
+    if (num_reqs > 0 && !lens) return fail(MSGL_ERR_INVALID_ARG, "lens is NULL");
+    if (num_reqs > INT32_MAX - 1024) return fail(MSGL_ERR_UNSUPPORTED, "num_reqs passes int32");
+    if (table_width > msgl::kMaxStepItems)
+        return fail(MSGL_ERR_UNSUPPORTED, "more than %lld columns", (long long)msgl::kMaxStepItems);
+    a.table = req_table;
+    a.req_rows = req_rows;
+    a.lens = lens;
+    a.held = held;
+    a.num_rows = num_rows;
+    a.table_stride = table_stride;
+    a.table_width = table_width;
+    a.num_reqs = num_reqs;
+    a.status = status;
+    return MSGL_OK;
+}
+
 }  // namespace
 
 namespace msgl {
@@ -526,6 +587,306 @@ msgl_status msgl_attn_decode_shared(const msgl_kv_pool *pool, const msgl_page_ta
     a.workspace = workspace;
     cudaError_t e = msgl::launch_decode_shared(a, (cudaStream_t)stream);
     return e == cudaSuccess ? MSGL_OK : cuda_fail(e, "decode_shared launch");
+}
+
+msgl_status msgl_rope_store_kv(const msgl_kv_pool *pool, const msgl_new_tokens *tokens, const msgl_rope *rope,
+                               const void *q_norm, const void *k_norm, float eps, uint32_t *status,
+                               msgl_stream_t stream) {
+    g_last_error[0] = 0;
+    if (!tokens || !rope) return fail(MSGL_ERR_INVALID_ARG, "tokens and rope must be non-NULL");
+    const msgl_new_tokens &n = *tokens;
+    msgl::RopeStoreArgs a{};
+    msgl_status s = check_pool(pool, a.pool);
+    if (s) return s;
+    if ((s = check_heads(n.num_q_heads, a.pool.hkv))) return s;
+    if (!rope->turns) return fail(MSGL_ERR_INVALID_ARG, "rope->turns is NULL");
+    if (rope->num_pairs <= 0 || rope->num_pairs > msgl::kHeadDim / 2)
+        return fail(MSGL_ERR_INVALID_ARG, "num_pairs %d is outside [1, %d]", rope->num_pairs, msgl::kHeadDim / 2);
+    if (rope->num_pairs % 8) return fail(MSGL_ERR_UNSUPPORTED, "num_pairs %d is not a multiple of 8", rope->num_pairs);
+    if (rope->num_axes < 1 || rope->num_axes > 4)
+        return fail(MSGL_ERR_INVALID_ARG, "num_axes %d is outside [1, 4]", rope->num_axes);
+    if (!isfinite(rope->factor)) return fail(MSGL_ERR_INVALID_ARG, "factor must be finite");
+    if ((q_norm || k_norm) && !(eps >= 0.f && isfinite(eps)))
+        return fail(MSGL_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    if (n.n_tokens < 0) return fail(MSGL_ERR_INVALID_ARG, "n_tokens < 0");
+    for (int j = 0; j < rope->num_pairs; ++j) {
+        const uint32_t axis = rope->axes ? rope->axes[j] : 0;
+        if (axis >= (uint32_t)rope->num_axes)
+            return fail(MSGL_ERR_INVALID_ARG, "axes[%d] = %u but num_axes = %d", j, axis, rope->num_axes);
+        a.turns[j] = rope->turns[j];
+        a.axis_bits[j / 16] |= axis << (2 * (j % 16));
+    }
+    if (n.n_tokens == 0) return MSGL_OK;
+    if (!n.q || !n.k || !n.v || !n.q_out || !n.positions || !n.out_loc)
+        return fail(MSGL_ERR_INVALID_ARG, "q, k, v, q_out, positions and out_loc must be non-NULL");
+    if (!aligned16(n.q) || !aligned16(n.k) || !aligned16(n.v) || !aligned16(n.q_out) || !aligned16(q_norm) ||
+        !aligned16(k_norm))
+        return fail(MSGL_ERR_INVALID_ARG, "q, k, v, q_out and the norms must be 16-byte aligned");
+    const int64_t q_row = (int64_t)n.num_q_heads * msgl::kHeadDim, kv_row = (int64_t)a.pool.hkv * msgl::kHeadDim;
+    const struct {
+        int64_t stride, row;
+        const char *name;
+    } strides[] = {{n.q_stride, q_row, "q_stride"}, {n.k_stride, kv_row, "k_stride"}, {n.v_stride, kv_row, "v_stride"},
+                   {n.out_stride, q_row, "out_stride"}};
+    for (const auto &x : strides)
+        if (x.stride % 8 || x.stride < x.row || too_far(n.n_tokens, x.stride))
+            return fail(MSGL_ERR_INVALID_ARG, "%s %lld is not a multiple of 8 from %lld on that memory can hold", x.name,
+                        (long long)x.stride, (long long)x.row);
+    if (rope->num_axes > 1 && (n.axis_stride < n.n_tokens || too_far(rope->num_axes, n.axis_stride)))
+        return fail(MSGL_ERR_INVALID_ARG, "axis_stride %lld is below n_tokens %d (or past all memory)",
+                    (long long)n.axis_stride, n.n_tokens);
+    // (two bf16 an entry; tokens are turned by blocks of their own, in any order)
+    auto span = [&](const void *p, int64_t row, int64_t stride, const char *name) {
+        return Span{static_cast<const int32_t *>(p), n.n_tokens, row / 2, stride / 2, name};
+    };
+    const Span out = span(n.q_out, q_row, n.out_stride, "q_out");
+    const Span ins[] = {span(n.q, q_row, n.q_stride, "q"), span(n.k, kv_row, n.k_stride, "k"),
+                        span(n.v, kv_row, n.v_stride, "v"),
+                        flat(static_cast<const int32_t *>(q_norm), msgl::kHeadDim / 2, "q_norm"),
+                        flat(static_cast<const int32_t *>(k_norm), msgl::kHeadDim / 2, "k_norm"),
+                        {n.positions, rope->num_axes, n.n_tokens, rope->num_axes > 1 ? n.axis_stride : n.n_tokens, "positions"},
+                        flat(n.out_loc, n.n_tokens, "out_loc"),
+                        {static_cast<const int32_t *>(pool->k_pool), pool->num_slots, kv_row / 2, kv_row / 2, "the K pool"},
+                        {static_cast<const int32_t *>(pool->v_pool), pool->num_slots, kv_row / 2, kv_row / 2, "the V pool"}};
+    for (const Span &in : ins) {
+        if (in.at == ins[0].at && n.q_out == n.q && n.out_stride == n.q_stride) continue;   // in place
+        if (overlap(out, in)) return fail(MSGL_ERR_INVALID_ARG, "q_out overlaps %s", in.name);
+    }
+    a.k_pool = static_cast<__nv_bfloat16 *>(pool->k_pool);
+    a.v_pool = static_cast<__nv_bfloat16 *>(pool->v_pool);
+    a.q = static_cast<const __nv_bfloat16 *>(n.q);
+    a.k = static_cast<const __nv_bfloat16 *>(n.k);
+    a.v = static_cast<const __nv_bfloat16 *>(n.v);
+    a.q_norm = static_cast<const __nv_bfloat16 *>(q_norm);
+    a.k_norm = static_cast<const __nv_bfloat16 *>(k_norm);
+    a.q_out = static_cast<__nv_bfloat16 *>(n.q_out);
+    a.q_stride = n.q_stride;
+    a.k_stride = n.k_stride;
+    a.v_stride = n.v_stride;
+    a.out_stride = n.out_stride;
+    a.positions = n.positions;
+    a.out_loc = n.out_loc;
+    a.axis_stride = rope->num_axes > 1 ? n.axis_stride : 0;
+    a.pairs = rope->num_pairs;
+    a.adjacent = rope->adjacent != 0;
+    a.n_tokens = n.n_tokens;
+    a.hq = n.num_q_heads;
+    a.factor = rope->factor;
+    a.eps = eps;
+    a.status = status;
+    cudaError_t e = msgl::launch_rope_store(a, (cudaStream_t)stream);
+    return e == cudaSuccess ? MSGL_OK : cuda_fail(e, "rope_store launch");
+}
+
+msgl_status msgl_verify_drafts(const msgl_draft_batch *batch, uint32_t *status, msgl_stream_t stream) {
+    g_last_error[0] = 0;
+    if (!batch) return fail(MSGL_ERR_INVALID_ARG, "batch is NULL");
+    const msgl_draft_batch &d = *batch;
+    if (d.num_reqs < 0 || d.total_tokens < 0) return fail(MSGL_ERR_INVALID_ARG, "negative size");
+    if (d.vocab <= 0) return fail(MSGL_ERR_INVALID_ARG, "vocab must be > 0");
+    if (d.vocab > (1 << 30)) return fail(MSGL_ERR_UNSUPPORTED, "vocab may not pass 2^30");
+    if (d.num_reqs > msgl::kMaxDraftReqs) return fail(MSGL_ERR_UNSUPPORTED, "more than %d requests", msgl::kMaxDraftReqs);
+    if (d.num_reqs == 0) return MSGL_OK;
+    if (!d.cu_ext || !d.sample_u || !d.accepted || !d.kv_lens)
+        return fail(MSGL_ERR_INVALID_ARG, "cu_ext, sample_u, accepted and kv_lens must be non-NULL");
+    if (d.total_tokens > 0 && (!d.target || !d.tokens || !d.accept_u || !d.out_tokens))
+        return fail(MSGL_ERR_INVALID_ARG, "target, tokens, accept_u and out_tokens must be non-NULL");
+    if (d.target_stride < d.vocab || too_far(d.total_tokens, d.target_stride))
+        return fail(MSGL_ERR_INVALID_ARG, "target_stride %lld is below vocab %d (or past all memory)",
+                    (long long)d.target_stride, d.vocab);
+    if (d.draft && (d.draft_stride < d.vocab || too_far(d.total_tokens, d.draft_stride)))
+        return fail(MSGL_ERR_INVALID_ARG, "draft_stride %lld is below vocab %d (or past all memory)",
+                    (long long)d.draft_stride, d.vocab);
+    const uintptr_t size = d.is_bf16 ? 2 : 4;
+    if ((uintptr_t)d.target % size || (uintptr_t)d.draft % size)
+        return fail(MSGL_ERR_INVALID_ARG, "target and draft must be aligned to their type");
+    // (every block of a request reads its inputs while another writes its outputs)
+    const Span outs[] = {flat(d.accepted, d.num_reqs, "accepted"), flat(d.kv_lens, d.num_reqs, "kv_lens"),
+                         flat(d.out_tokens, d.total_tokens, "out_tokens")};
+    auto probs = [&](const void *p, int64_t stride, const char *name) {
+        const int64_t bytes = p && d.total_tokens > 0 ? ((d.total_tokens - 1) * stride + d.vocab) * (int64_t)size : 0;
+        const uintptr_t at = (uintptr_t)p & ~(uintptr_t)3;
+        return flat(reinterpret_cast<const int32_t *>(at), ((int64_t)((uintptr_t)p - at) + bytes + 3) / 4, name);
+    };
+    const Span ins[] = {flat(d.tokens, d.total_tokens, "tokens"), flat(d.cu_ext, (int64_t)d.num_reqs + 1, "cu_ext"),
+                        flat(reinterpret_cast<const int32_t *>(d.accept_u), d.total_tokens, "accept_u"),
+                        flat(reinterpret_cast<const int32_t *>(d.sample_u), d.num_reqs, "sample_u"),
+                        flat(d.cached_lens, d.num_reqs, "cached_lens"), probs(d.target, d.target_stride, "target"),
+                        probs(d.draft, d.draft_stride, "draft")};
+    for (int i = 0; i < 3; ++i) {
+        for (const Span &in : ins)
+            if (!(outs[i].at == d.kv_lens && in.at == d.kv_lens && d.kv_lens == d.cached_lens) && overlap(outs[i], in))
+                return fail(MSGL_ERR_INVALID_ARG, "%s overlaps %s", outs[i].name, in.name);
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i], outs[j])) return fail(MSGL_ERR_INVALID_ARG, "%s overlaps %s", outs[j].name, outs[i].name);
+    }
+    msgl::VerifyArgs a{};
+    a.target = d.target;
+    a.draft = d.draft;
+    a.target_stride = d.target_stride;
+    a.draft_stride = d.draft_stride;
+    a.tokens = d.tokens;
+    a.cu_ext = d.cu_ext;
+    a.cached_lens = d.cached_lens;
+    a.accept_u = d.accept_u;
+    a.sample_u = d.sample_u;
+    a.num_reqs = d.num_reqs;
+    a.total_tokens = d.total_tokens;
+    a.vocab = d.vocab;
+    a.bf16 = d.is_bf16 != 0;
+    a.accepted = d.accepted;
+    a.out_tokens = d.out_tokens;
+    a.kv_lens = d.kv_lens;
+    a.status = status;
+    cudaError_t e = msgl::launch_verify_drafts(a, (cudaStream_t)stream);
+    return e == cudaSuccess ? MSGL_OK : cuda_fail(e, "verify_drafts launch");
+}
+
+msgl_status msgl_fork_requests(int64_t num_slots, int32_t page_size, int32_t *req_table, int32_t num_rows,
+                               int32_t table_stride, int32_t table_width, const int32_t *parent_rows,
+                               const int32_t *child_rows, const int32_t *lens, int32_t num_forks,
+                               const int32_t *free_pages, int32_t num_free, const msgl_fork_out *out,
+                               uint32_t *status, msgl_stream_t stream) {
+    g_last_error[0] = 0;
+    if (!out) return fail(MSGL_ERR_INVALID_ARG, "out is NULL");
+    msgl::ForkArgs a{};
+    msgl_status s = check_page_count(num_slots, page_size, a.log2_ps, a.num_pages);
+    if (s) return s;
+    if ((s = check_req_table(req_table, num_rows, table_stride, table_width))) return s;
+    if (num_forks < 0 || num_free < 0) return fail(MSGL_ERR_INVALID_ARG, "negative size");
+    if (num_forks == INT32_MAX) return fail(MSGL_ERR_UNSUPPORTED, "num_forks + 1 passes int32");
+    if (table_width > msgl::kMaxStepItems)
+        return fail(MSGL_ERR_UNSUPPORTED, "more than %lld columns", (long long)msgl::kMaxStepItems);
+    if (!out->pages_taken) return fail(MSGL_ERR_INVALID_ARG, "out->pages_taken must be non-NULL");
+    if (num_forks > 0 && (!parent_rows || !child_rows || !lens || !out->copy_src || !out->copy_dst || !out->copy_tokens))
+        return fail(MSGL_ERR_INVALID_ARG, "parent_rows, child_rows, lens and the copies must be non-NULL");
+    if (num_free > 0 && !free_pages) return fail(MSGL_ERR_INVALID_ARG, "free_pages is NULL");
+    const Span outs[] = {{req_table, num_rows, table_width, table_stride, "req_table"},
+                         flat(out->copy_src, num_forks, "out->copy_src"),
+                         flat(out->copy_dst, num_forks, "out->copy_dst"),
+                         flat(out->copy_tokens, num_forks, "out->copy_tokens"),
+                         flat(out->pages_taken, 1, "out->pages_taken")};
+    const Span ins[] = {flat(parent_rows, num_forks, "parent_rows"), flat(child_rows, num_forks, "child_rows"),
+                        flat(lens, num_forks, "lens"), flat(free_pages, num_free, "free_pages")};
+    if ((s = check_overlaps(outs, 5, ins, 4))) return s;
+    a.req_table = req_table;
+    a.parent_rows = parent_rows;
+    a.child_rows = child_rows;
+    a.lens = lens;
+    a.free_pages = free_pages;
+    a.num_rows = num_rows;
+    a.table_stride = table_stride;
+    a.table_width = table_width;
+    a.num_forks = num_forks;
+    a.num_free = num_free;
+    a.copy_src = out->copy_src;
+    a.copy_dst = out->copy_dst;
+    a.copy_tokens = out->copy_tokens;
+    a.pages_taken = out->pages_taken;
+    a.status = status;
+    cudaError_t e = msgl::launch_fork(a, (cudaStream_t)stream);
+    return e == cudaSuccess ? MSGL_OK : cuda_fail(e, "fork_requests launch");
+}
+
+msgl_status msgl_copy_pages(const msgl_kv_pool *pools, int32_t num_pools, const int32_t *src, const int32_t *dst,
+                            const int32_t *tokens, int32_t num_pairs, const int32_t *count, uint32_t *status,
+                            msgl_stream_t stream) {
+    g_last_error[0] = 0;
+    if (num_pools < 0 || num_pairs < 0) return fail(MSGL_ERR_INVALID_ARG, "negative size");
+    if (num_pools > 1 << 15) return fail(MSGL_ERR_UNSUPPORTED, "more than 2^15 pools");
+    if (num_pools > 0 && !pools) return fail(MSGL_ERR_INVALID_ARG, "pools is NULL");
+    msgl::PoolView view{};
+    for (int i = 0; i < num_pools; ++i) {
+        msgl_status s = check_pool(pools + i, view);
+        if (s) return s;
+        if (pools[i].num_slots != pools[0].num_slots || pools[i].page_size != pools[0].page_size ||
+            pools[i].num_kv_heads != pools[0].num_kv_heads)
+            return fail(MSGL_ERR_INVALID_ARG, "pool %d has another num_slots, page_size or num_kv_heads than pool 0", i);
+    }
+    if (num_pools == 0 || num_pairs == 0) return MSGL_OK;
+    if (!src || !dst) return fail(MSGL_ERR_INVALID_ARG, "src and dst must be non-NULL");
+    msgl::CopyPagesArgs a;
+    a.src = src;
+    a.dst = dst;
+    a.tokens = tokens;
+    a.count = count;
+    a.row_vecs = view.hkv * msgl::kHeadDim * 2 / 16;
+    a.page_size = pools[0].page_size;
+    a.page_vecs = (int64_t)a.row_vecs * a.page_size;
+    a.num_pages = view.num_pages;
+    a.num_pairs = num_pairs;
+    a.status = status;
+    for (int i0 = 0; i0 < num_pools; i0 += msgl::kMaxCopyPools) {
+        const int n = num_pools - i0 < msgl::kMaxCopyPools ? num_pools - i0 : msgl::kMaxCopyPools;
+        for (int i = 0; i < n; ++i) {
+            a.buffers[2 * i] = pools[i0 + i].k_pool;
+            a.buffers[2 * i + 1] = pools[i0 + i].v_pool;
+        }
+        a.num_buffers = 2 * n;
+        cudaError_t e = msgl::launch_copy_pages(a, (cudaStream_t)stream);
+        if (e != cudaSuccess) return cuda_fail(e, "copy_pages launch");
+    }
+    return MSGL_OK;
+}
+
+msgl_status msgl_free_pages(int64_t num_slots, int32_t page_size, const int32_t *req_table, int32_t num_rows,
+                            int32_t table_stride, int32_t table_width, const int32_t *req_rows, const int32_t *lens,
+                            int32_t num_reqs, const uint8_t *held, int32_t *pages, int32_t *num_free,
+                            uint32_t *status, msgl_stream_t stream) {
+    g_last_error[0] = 0;
+    msgl::PageMapArgs a{};
+    msgl_status s = prepare_page_map(num_slots, page_size, req_table, num_rows, table_stride, table_width, req_rows, lens,
+                                     num_reqs, held, status, a);
+    if (s) return s;
+    if (!num_free || (a.num_pages > 0 && !pages))
+        return fail(MSGL_ERR_INVALID_ARG, "pages and num_free must be non-NULL");
+    const Span outs[] = {flat(pages, a.num_pages, "pages"), flat(num_free, 1, "num_free")};
+    const Span ins[] = {{req_table, num_rows, table_width, table_stride, "req_table"}, flat(req_rows, num_reqs, "req_rows"),
+                        flat(lens, num_reqs, "lens"), bytes_span(held, a.num_pages, "held")};
+    if ((s = check_overlaps(outs, 2, ins, 4))) return s;
+    a.pages_out = pages;
+    a.count_out = num_free;
+    cudaError_t e = msgl::launch_free_pages(a, (cudaStream_t)stream);
+    return e == cudaSuccess ? MSGL_OK : cuda_fail(e, "free_pages launch");
+}
+
+msgl_status msgl_compact_pages(int64_t num_slots, int32_t page_size, const int32_t *req_table, int32_t num_rows,
+                               int32_t table_stride, int32_t table_width, const int32_t *req_rows,
+                               const int32_t *lens, int32_t num_reqs, const uint8_t *held,
+                               const msgl_compact_out *out, uint32_t *status, msgl_stream_t stream) {
+    g_last_error[0] = 0;
+    if (!out) return fail(MSGL_ERR_INVALID_ARG, "out is NULL");
+    msgl::PageMapArgs a{};
+    msgl_status s = prepare_page_map(num_slots, page_size, req_table, num_rows, table_stride, table_width, req_rows, lens,
+                                     num_reqs, held, status, a);
+    if (s) return s;
+    static_assert(msgl::kMaxMapPages == MSGL_COMPACT_MAX_PAGES, "the header says what the kernel holds");
+    if (a.num_pages > msgl::kMaxMapPages)
+        return fail(MSGL_ERR_UNSUPPORTED, "%d pages: compact_pages takes at most %d", a.num_pages, msgl::kMaxMapPages);
+    if (!out->num_moves || !out->num_used || (a.num_pages > 0 && !out->remap) ||
+        (a.num_pages > 1 && (!out->src || !out->dst)) || (num_rows > 0 && table_width > 0 && !out->page_ids))
+        return fail(MSGL_ERR_INVALID_ARG, "out's arrays must be non-NULL");
+    if (out->stride < table_width) return fail(MSGL_ERR_INVALID_ARG, "out needs stride >= table_width");
+    const bool in_place = out->page_ids == req_table;
+    if (in_place && out->stride != table_stride)
+        return fail(MSGL_ERR_INVALID_ARG, "out->page_ids overlaps req_table at another stride");
+    const Span outs[] = {flat(out->remap, a.num_pages, "out->remap"), flat(out->src, a.num_pages / 2, "out->src"),
+                         flat(out->dst, a.num_pages / 2, "out->dst"), flat(out->num_moves, 1, "out->num_moves"),
+                         flat(out->num_used, 1, "out->num_used"),
+                         {out->page_ids, num_rows, table_width, out->stride, "out->page_ids"}};
+    const Span ins[] = {flat(req_rows, num_reqs, "req_rows"), flat(lens, num_reqs, "lens"),
+                        bytes_span(held, a.num_pages, "held"),
+                        {in_place ? nullptr : req_table, num_rows, table_width, table_stride, "req_table"}};
+    if ((s = check_overlaps(outs, 6, ins, 4))) return s;
+    a.pages_out = out->remap;
+    a.count_out = out->num_moves;
+    a.used_out = out->num_used;
+    a.src = out->src;
+    a.dst = out->dst;
+    a.table_out = out->page_ids;
+    a.out_stride = out->stride;
+    cudaError_t e = msgl::launch_compact_pages(a, (cudaStream_t)stream);
+    return e == cudaSuccess ? MSGL_OK : cuda_fail(e, "compact_pages launch");
 }
 
 msgl_status msgl_read_status(const uint32_t *status, uint32_t *flags, msgl_stream_t stream) {

@@ -98,6 +98,72 @@ struct SharedPrefixesArgs {
 };
 cudaError_t launch_shared_prefixes(const SharedPrefixesArgs &a, cudaStream_t stream);
 
+// ------------------------------------------- around the step: rotary store, drafts, pages
+struct RopeStoreArgs {
+    PoolView pool;
+    __nv_bfloat16 *k_pool, *v_pool;
+    const __nv_bfloat16 *q, *k, *v, *q_norm, *k_norm;
+    __nv_bfloat16 *q_out;
+    int64_t q_stride, k_stride, v_stride, out_stride;   // elements from token to token
+    const int32_t *positions, *out_loc;
+    int64_t axis_stride;
+    uint64_t turns[kHeadDim / 2];         // a pair's frequency: turns per position * 2^64, modulo 2^64
+    uint32_t axis_bits[kHeadDim / 32];    // a pair's axis, two bits each
+    int32_t pairs, adjacent, n_tokens, hq;
+    float factor, eps;
+    uint32_t *status;
+};
+cudaError_t launch_rope_store(const RopeStoreArgs &a, cudaStream_t stream);
+
+constexpr int kMaxDraftReqs = 1 << 24;    // a cluster of up to 8 blocks each (grid.x)
+
+struct VerifyArgs {
+    const void *target, *draft;           // [total_tokens, vocab] float or bf16; draft may be NULL
+    int64_t target_stride, draft_stride;
+    const int32_t *tokens, *cu_ext, *cached_lens;
+    const float *accept_u, *sample_u;
+    int32_t num_reqs, total_tokens, vocab, bf16;
+    int32_t *accepted, *out_tokens, *kv_lens;
+    uint32_t *status;
+};
+cudaError_t launch_verify_drafts(const VerifyArgs &a, cudaStream_t stream);
+
+struct ForkArgs {
+    int32_t *req_table;
+    const int32_t *parent_rows, *child_rows, *lens, *free_pages;
+    int32_t num_rows, table_stride, table_width, num_forks, num_free, num_pages, log2_ps;
+    int32_t *copy_src, *copy_dst, *copy_tokens, *pages_taken;
+    uint32_t *status;
+};
+cudaError_t launch_fork(const ForkArgs &a, cudaStream_t stream);
+
+constexpr int kMaxCopyPools = 128;        // pools of one copy launch (their addresses are kernel arguments)
+
+struct CopyPagesArgs {
+    void *buffers[2 * kMaxCopyPools];     // K and V of each pool
+    const int32_t *src, *dst, *tokens, *count;
+    int64_t page_vecs;                    // 16-byte vectors of a page and of a slot's row
+    int32_t row_vecs, page_size, num_pages, num_pairs, num_buffers;
+    int32_t pieces;                       // set by the launcher
+    uint32_t *status;
+};
+cudaError_t launch_copy_pages(CopyPagesArgs &a, cudaStream_t stream);
+
+constexpr int32_t kMaxMapPages = 1310720; // pages whose bits fit the shared memory of a block
+
+struct PageMapArgs {
+    const int32_t *table, *req_rows, *lens;
+    const uint8_t *held;
+    int32_t num_rows, table_stride, table_width, num_reqs, num_pages, log2_ps;
+    int32_t *pages_out;                   // [num_pages]: the free pages; compact: each page's new id
+    int32_t *count_out;                   // [1]: free pages; compact: pages that move
+    int32_t *table_out, *src, *dst, *used_out;   // compact
+    int32_t out_stride;
+    uint32_t *status;
+};
+cudaError_t launch_free_pages(const PageMapArgs &a, cudaStream_t stream);
+cudaError_t launch_compact_pages(const PageMapArgs &a, cudaStream_t stream);
+
 // -------------------------------------------------------- shared-prefix decode
 size_t decode_shared_workspace_bytes(int32_t num_reqs, int32_t hq, int32_t hkv);
 

@@ -1,0 +1,169 @@
+// Requests that continue other requests on the same pages, and copies of pages.
+//
+// "Mini-SGLang 实战指南", §6.2 and §6.5: requests that begin alike hold the same pages of
+// the one pool.  Whole pages are never written again, so a fork takes them over by
+// id; the last, partly filled page would be written by both, so the fork gets a
+// new one and a copy of what is in it.
+//
+// Both are copies: of table rows (latency: rows, lengths, ids, stores) and of pool
+// rows (HBM: every byte read once and written once).
+#include <limits.h>
+
+#include "kernels.h"
+
+namespace msgl {
+
+namespace {
+
+// ---------------------------------------------------------------------- fork
+//
+// One block per fork and 2048 columns of its row, as in the step tables.  A fork
+// needs one new page or none, so its place among the free pages is the number of
+// earlier forks with a partly filled page, counted again by every block; the same
+// loop sees whether its child's row is named by another fork.
+constexpr int kForkThreads = 256;
+constexpr int kPerThread = 8;
+constexpr int kChunk = kForkThreads * kPerThread;
+
+struct Fork {
+    int32_t parent, child, tokens;
+    int32_t full, tail;     // whole pages, tokens on the last one
+    bool none, rows_ok, len_ok;
+};
+
+__device__ __forceinline__ Fork fork_at(const ForkArgs &a, int i) {
+    Fork f;
+    f.parent = __ldg(a.parent_rows + i);
+    f.child = __ldg(a.child_rows + i);
+    f.tokens = __ldg(a.lens + i);
+    f.none = f.parent == -1 && f.child == -1;
+    f.rows_ok = f.parent >= 0 && f.parent < a.num_rows && f.child >= 0 && f.child < a.num_rows;
+    const int mask = (1 << a.log2_ps) - 1;
+    f.full = f.tokens >> a.log2_ps;
+    f.tail = f.tokens & mask;
+    f.len_ok = f.tokens >= 0 && (int64_t)f.full + (f.tail > 0) <= a.table_width;
+    if (f.none || !f.rows_ok || !f.len_ok) f.full = f.tail = 0;
+    return f;
+}
+
+__global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkArgs a) {
+    const int b = blockIdx.x, at0 = blockIdx.y * kChunk + (int)threadIdx.x;
+    Fork f{};
+    if (b < a.num_forks) {
+        f = fork_at(a, b);
+        if (blockIdx.y > 0 && blockIdx.y * kChunk > f.full) return;
+    } else if (blockIdx.y > 0) {
+        return;
+    }
+    __shared__ int before, clash;
+    if (threadIdx.x == 0) before = clash = 0;
+    __syncthreads();
+    int n = 0;
+    bool twice = false;
+    for (int i = threadIdx.x; i < a.num_forks; i += kForkThreads) {
+        const Fork x = fork_at(a, i);
+        n += i < b && x.tail > 0;
+        twice |= b < a.num_forks && (f.child == x.parent || (i != b && f.child == x.child));
+    }
+    if (n) atomicAdd(&before, n);
+    if (twice) clash = 1;
+    __syncthreads();
+    if (b == a.num_forks) {
+        if (threadIdx.x == 0) a.pages_taken[0] = min(before, a.num_free);
+        return;
+    }
+    const bool rows_ok = f.rows_ok && !clash, paged = f.tail == 0 || before < a.num_free;
+    bool served = !f.none && rows_ok && f.len_ok && paged;
+    int32_t *mine = a.req_table + (int64_t)max(f.child, 0) * a.table_stride;
+    const int32_t *theirs = a.req_table + (int64_t)max(f.parent, 0) * a.table_stride;
+    int32_t fresh = -1, source = -1;
+    bool pages_ok = true;
+    if (served && f.tail > 0) {
+        fresh = __ldg(a.free_pages + before);
+        source = theirs[f.full];
+        pages_ok = fresh >= 0 && fresh < a.num_pages && source >= 0 && source < a.num_pages;
+        served = pages_ok;
+    }
+    if (blockIdx.y == 0 && threadIdx.x == 0) {
+        const bool copies = served && f.tail > 0;
+        a.copy_src[b] = copies ? source : -1;
+        a.copy_dst[b] = copies ? fresh : -1;
+        a.copy_tokens[b] = copies ? f.tail : 0;
+        if (!f.none) {
+            if (!rows_ok) report(a.status, MSGL_DEVERR_ROW);
+            else if (!f.len_ok) report(a.status, MSGL_DEVERR_LENGTH);
+            else if (!paged) report(a.status, MSGL_DEVERR_NO_PAGES);
+            else if (!pages_ok) report(a.status, MSGL_DEVERR_PAGE_RANGE);
+        }
+    }
+    if (!served) return;
+    int32_t id[kPerThread];
+#pragma unroll
+    for (int u = 0; u < kPerThread; ++u) {
+        const int p = at0 + u * kForkThreads;
+        id[u] = p < f.full ? theirs[p] : fresh;
+    }
+#pragma unroll
+    for (int u = 0; u < kPerThread; ++u) {
+        const int p = at0 + u * kForkThreads;
+        if (p < f.full + (f.tail > 0)) mine[p] = id[u];
+    }
+}
+
+// ---------------------------------------------------------------------- copy
+//
+// A warp takes 4 KB of one page's K or V in one pool, all its loads before its
+// stores; the pools and their K and V are the grid's second axis, so that a
+// block's addresses differ by the page only.
+constexpr int kCopyThreads = 256;
+constexpr int kCopyUnroll = 8;
+constexpr int kPiece = 32 * kCopyUnroll;           // 16-byte vectors
+
+__global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_constant__ CopyPagesArgs a) {
+    const int lane = threadIdx.x & 31;
+    uint4 *pool = static_cast<uint4 *>(a.buffers[blockIdx.y]);
+    const int n = a.count ? min(max(__ldg(a.count), 0), a.num_pairs) : a.num_pairs;
+    const int64_t units = (int64_t)n * a.pieces, warps = (int64_t)gridDim.x * (kCopyThreads / 32);
+    for (int64_t w = ((int64_t)blockIdx.x * kCopyThreads + threadIdx.x) >> 5; w < units; w += warps) {
+        const int pair = (int)(w / a.pieces), piece = (int)(w - (int64_t)pair * a.pieces);
+        const int64_t src = __ldg(a.src + pair), dst = __ldg(a.dst + pair);
+        if (src == -1 && dst == -1) continue;
+        const int tokens = a.tokens ? __ldg(a.tokens + pair) : a.page_size;
+        if (src < 0 || src >= a.num_pages || dst < 0 || dst >= a.num_pages) {
+            if (lane == 0 && piece == 0) report(a.status, MSGL_DEVERR_PAGE_RANGE);
+            continue;
+        }
+        if (tokens < 0 || tokens > a.page_size) {
+            if (lane == 0 && piece == 0) report(a.status, MSGL_DEVERR_LENGTH);
+            continue;
+        }
+        const int most = tokens * a.row_vecs, at = piece * kPiece + lane;
+        const uint4 *from = pool + src * a.page_vecs;
+        uint4 *to = pool + dst * a.page_vecs;
+        uint4 r[kCopyUnroll];
+#pragma unroll
+        for (int u = 0; u < kCopyUnroll; ++u)
+            if (at + u * 32 < most) r[u] = ld_stream_16(from + at + u * 32);
+#pragma unroll
+        for (int u = 0; u < kCopyUnroll; ++u)
+            if (at + u * 32 < most) st_stream_16(to + at + u * 32, r[u]);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_fork(const ForkArgs &a, cudaStream_t stream) {
+    const long long chunks = ((long long)max(a.table_width, 1) + kChunk - 1) / kChunk;
+    fork_kernel<<<dim3(a.num_forks + 1, (unsigned)chunks), kForkThreads, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_copy_pages(CopyPagesArgs &a, cudaStream_t stream) {
+    a.pieces = (int32_t)((a.page_vecs + kPiece - 1) / kPiece);
+    const int64_t blocks = ((int64_t)a.num_pairs * a.pieces + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
+    const int64_t cap = ((int64_t)sm_count() * 4 + a.num_buffers - 1) / a.num_buffers;
+    copy_pages_kernel<<<dim3((unsigned)(blocks < cap ? blocks : cap), a.num_buffers), kCopyThreads, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace msgl

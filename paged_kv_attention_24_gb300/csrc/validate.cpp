@@ -9,6 +9,7 @@
 #include <stdio.h>
 
 #include <exception>
+#include <initializer_list>
 #include <unordered_set>
 
 #include "../../include/msgl_attn.h"
@@ -231,6 +232,126 @@ msgl_status msgl_check_groups_meta(int64_t num_slots, int32_t page_size, const i
                 return bad(MSGL_ERR_OUT_OF_RANGE, "request %d: page_ids[%lld] = %d is outside [0, %lld)", b,
                            (long long)p, id, (long long)num_pages);
         }
+    }
+    return MSGL_OK;
+}
+
+msgl_status msgl_check_fork_meta(int64_t num_slots, int32_t page_size, const int32_t *req_table, int32_t num_rows,
+                                 int32_t table_stride, int32_t table_width, const int32_t *parent_rows,
+                                 const int32_t *child_rows, const int32_t *lens, int32_t num_forks,
+                                 const int32_t *free_pages, int32_t num_free) try {
+    msgl::set_last_error("");
+    msgl_status rc = check_pool_scalars(num_slots, page_size, req_table, table_stride, table_width);
+    if (rc) return rc;
+    if (num_forks < 0 || num_rows < 0 || num_free < 0) return bad(MSGL_ERR_INVALID_ARG, "negative size");
+    if (num_forks > 0 && (!parent_rows || !child_rows || !lens))
+        return bad(MSGL_ERR_INVALID_ARG, "parent_rows, child_rows and lens must be non-NULL");
+    if (num_free > 0 && !free_pages) return bad(MSGL_ERR_INVALID_ARG, "free_pages is NULL");
+    const int64_t num_pages = num_slots / page_size;
+    std::unordered_set<int32_t> parents, children, used;
+    int64_t taken = 0;
+    auto none = [&](int32_t i) { return parent_rows[i] == -1 && child_rows[i] == -1; };
+    for (int32_t i = 0; i < num_forks; ++i)
+        if (!none(i)) parents.insert(parent_rows[i]);
+    for (int32_t i = 0; i < num_forks; ++i) {
+        if (none(i)) continue;
+        for (const int32_t row : {parent_rows[i], child_rows[i]})
+            if (row < 0 || row >= num_rows)
+                return bad(MSGL_ERR_OUT_OF_RANGE, "fork %d: row %d is outside [0, %d)", i, row, num_rows);
+        if (parents.count(child_rows[i]))
+            return bad(MSGL_ERR_INVALID_ARG, "fork %d: row %d is a parent too", i, child_rows[i]);
+        if (!children.insert(child_rows[i]).second)
+            return bad(MSGL_ERR_INVALID_ARG, "fork %d: row %d is an earlier fork's child too", i, child_rows[i]);
+        if (lens[i] < 0) return bad(MSGL_ERR_INVALID_ARG, "fork %d: length %d must be >= 0", i, lens[i]);
+        if ((rc = check_pages(num_pages, page_size, req_table, table_stride, table_width, i, parent_rows[i], lens[i])))
+            return rc;
+        for (int64_t p = 0; p * page_size < lens[i]; ++p)
+            used.insert(req_table[(int64_t)parent_rows[i] * table_stride + p]);
+        taken += lens[i] % page_size != 0;
+        if (taken > num_free)
+            return bad(MSGL_ERR_OUT_OF_RANGE, "fork %d: %lld pages so far but num_free = %d", i, (long long)taken, num_free);
+    }
+    for (int64_t p = 0; p < taken; ++p) {
+        if (free_pages[p] < 0 || free_pages[p] >= num_pages)
+            return bad(MSGL_ERR_OUT_OF_RANGE, "free_pages[%lld] = %d is outside [0, %lld)", (long long)p, free_pages[p],
+                       (long long)num_pages);
+        if (!used.insert(free_pages[p]).second)
+            return bad(MSGL_ERR_INVALID_ARG, "free_pages[%lld] = %d is in use", (long long)p, free_pages[p]);
+    }
+    return MSGL_OK;
+} catch (const std::exception &) {
+    return no_memory();
+}
+
+msgl_status msgl_check_copy_meta(int64_t num_slots, int32_t page_size, const int32_t *src, const int32_t *dst,
+                                 const int32_t *tokens, int32_t num_pairs) try {
+    msgl::set_last_error("");
+    msgl_status rc = check_pool_scalars(num_slots, page_size, nullptr, 0, 0);
+    if (rc) return rc;
+    if (num_pairs < 0) return bad(MSGL_ERR_INVALID_ARG, "negative size");
+    if (num_pairs > 0 && (!src || !dst)) return bad(MSGL_ERR_INVALID_ARG, "src and dst must be non-NULL");
+    const int64_t num_pages = num_slots / page_size;
+    std::unordered_set<int32_t> read, written;
+    for (int32_t i = 0; i < num_pairs; ++i) {
+        if (src[i] == -1 && dst[i] == -1) continue;
+        for (const int32_t page : {src[i], dst[i]})
+            if (page < 0 || page >= num_pages)
+                return bad(MSGL_ERR_OUT_OF_RANGE, "pair %d: page %d is outside [0, %lld)", i, page, (long long)num_pages);
+        if (tokens && (tokens[i] < 0 || tokens[i] > page_size))
+            return bad(MSGL_ERR_INVALID_ARG, "pair %d: %d tokens are outside [0, page_size = %d]", i, tokens[i], page_size);
+        if (!written.insert(dst[i]).second)
+            return bad(MSGL_ERR_INVALID_ARG, "pair %d: page %d is an earlier pair's dst too", i, dst[i]);
+        read.insert(src[i]);
+    }
+    for (int32_t i = 0; i < num_pairs; ++i)
+        if (dst[i] >= 0 && read.count(dst[i]))
+            return bad(MSGL_ERR_INVALID_ARG, "pair %d: page %d is written and read", i, dst[i]);
+    return MSGL_OK;
+} catch (const std::exception &) {
+    return no_memory();
+}
+
+msgl_status msgl_check_held_meta(int64_t num_slots, int32_t page_size, const int32_t *req_table, int32_t num_rows,
+                                 int32_t table_stride, int32_t table_width, const int32_t *req_rows,
+                                 const int32_t *lens, int32_t num_reqs) {
+    msgl::set_last_error("");
+    msgl_status rc = check_pool_scalars(num_slots, page_size, req_table, table_stride, table_width);
+    if (rc) return rc;
+    if (num_reqs < 0 || num_rows < 0) return bad(MSGL_ERR_INVALID_ARG, "negative size");
+    if (num_reqs > 0 && !lens) return bad(MSGL_ERR_INVALID_ARG, "lens is NULL");
+    for (int32_t b = 0; b < num_reqs; ++b) {
+        const int32_t row = req_rows ? req_rows[b] : b;
+        if (row == -1) continue;
+        if (row < 0 || row >= num_rows)
+            return bad(MSGL_ERR_OUT_OF_RANGE, "request %d: row %d is outside [0, %d)", b, row, num_rows);
+        if (lens[b] < 0) return bad(MSGL_ERR_INVALID_ARG, "request %d: length %d must be >= 0", b, lens[b]);
+        if ((rc = check_pages(num_slots / page_size, page_size, req_table, table_stride, table_width, b, row, lens[b])))
+            return rc;
+    }
+    return MSGL_OK;
+}
+
+msgl_status msgl_check_draft_meta(int32_t vocab, const int32_t *tokens, const int32_t *cu_ext, const float *accept_u,
+                                  const float *sample_u, int32_t num_reqs, int32_t total_tokens) {
+    msgl::set_last_error("");
+    if (num_reqs < 0 || total_tokens < 0 || vocab <= 0)
+        return bad(MSGL_ERR_INVALID_ARG, "num_reqs and total_tokens must be >= 0 and vocab > 0");
+    if (num_reqs == 0) return MSGL_OK;
+    if (!cu_ext || !sample_u || (total_tokens > 0 && (!tokens || !accept_u)))
+        return bad(MSGL_ERR_INVALID_ARG, "tokens, cu_ext, accept_u and sample_u must be non-NULL");
+    for (int32_t b = 0; b < num_reqs; ++b) {
+        const int32_t first = cu_ext[b], end = cu_ext[b + 1];
+        if (first < 0 || first > end || end > total_tokens)
+            return bad(MSGL_ERR_INVALID_ARG, "request %d: rows [%d, %d) are not rows of [0, %d)", b, first, end, total_tokens);
+        for (int32_t r = first; r + 1 < end; ++r) {
+            if (tokens[r + 1] < 0 || tokens[r + 1] >= vocab)
+                return bad(MSGL_ERR_OUT_OF_RANGE, "request %d: tokens[%d] = %d is outside [0, %d)", b, r + 1, tokens[r + 1],
+                           vocab);
+            if (!(accept_u[r] >= 0.f && accept_u[r] < 1.f))
+                return bad(MSGL_ERR_INVALID_ARG, "request %d: accept_u[%d] = %g is outside [0, 1)", b, r, accept_u[r]);
+        }
+        if (first < end && !(sample_u[b] >= 0.f && sample_u[b] < 1.f))
+            return bad(MSGL_ERR_INVALID_ARG, "request %d: sample_u = %g is outside [0, 1)", b, sample_u[b]);
     }
     return MSGL_OK;
 }

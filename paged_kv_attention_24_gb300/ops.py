@@ -5,14 +5,16 @@ scalars, calls the C ABI declared in ``include/msgl_attn.h`` with the
 current CUDA stream, and turns a non-OK status into :class:`MsglError`.
 All compute happens in the library's CUDA kernels; there is no CPU or
 PyTorch fallback, and calling anything here without the built library
-raises immediately.  The step tables, the prefix groups and the
-shared-prefix decode, whose kernels are short, marshal their arguments in
-a native extension over the same C ABI (``csrc/python/binding.cpp``).
+raises immediately.  The step tables, the prefix groups, the shared-prefix
+decode, the rotary store, the draft verification and the page calls, whose
+kernels are short, marshal their arguments in a native extension over the
+same C ABI (``csrc/python/binding.cpp``).
 """
 from __future__ import annotations
 
 import ctypes
 import importlib.util
+import math
 import os
 import threading
 from typing import NamedTuple, Optional
@@ -35,6 +37,9 @@ DEVERR_TIMEOUT = 0x10
 DEVERR_APPEND_SLOT = 0x20
 DEVERR_GROUP = 0x40
 DEVERR_NO_PAGES = 0x80
+DEVERR_ROW = 0x100
+DEVERR_TOKEN = 0x200
+DEVERR_PROBS = 0x400
 
 
 class MsglError(RuntimeError):
@@ -75,6 +80,38 @@ class _StepOut(ctypes.Structure):
                 ("total_tokens", ctypes.c_int32)]
 
 
+class _Rope(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("axes", ctypes.c_void_p), ("num_pairs", ctypes.c_int32),
+                ("num_axes", ctypes.c_int32), ("adjacent", ctypes.c_int32), ("factor", ctypes.c_float)]
+
+
+class _NewTokens(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("out_stride", ctypes.c_int64), ("positions", ctypes.c_void_p), ("axis_stride", ctypes.c_int64),
+                ("out_loc", ctypes.c_void_p), ("n_tokens", ctypes.c_int32), ("num_q_heads", ctypes.c_int32)]
+
+
+class _DraftBatch(ctypes.Structure):
+    _fields_ = [("target", ctypes.c_void_p), ("draft", ctypes.c_void_p), ("target_stride", ctypes.c_int64),
+                ("draft_stride", ctypes.c_int64), ("vocab", ctypes.c_int32), ("is_bf16", ctypes.c_int32),
+                ("tokens", ctypes.c_void_p), ("cu_ext", ctypes.c_void_p), ("accept_u", ctypes.c_void_p),
+                ("sample_u", ctypes.c_void_p), ("cached_lens", ctypes.c_void_p), ("num_reqs", ctypes.c_int32),
+                ("total_tokens", ctypes.c_int32), ("accepted", ctypes.c_void_p), ("out_tokens", ctypes.c_void_p),
+                ("kv_lens", ctypes.c_void_p)]
+
+
+class _ForkOut(ctypes.Structure):
+    _fields_ = [("copy_src", ctypes.c_void_p), ("copy_dst", ctypes.c_void_p), ("copy_tokens", ctypes.c_void_p),
+                ("pages_taken", ctypes.c_void_p)]
+
+
+class _CompactOut(ctypes.Structure):
+    _fields_ = [("page_ids", ctypes.c_void_p), ("stride", ctypes.c_int32), ("remap", ctypes.c_void_p),
+                ("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("num_moves", ctypes.c_void_p),
+                ("num_used", ctypes.c_void_p)]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -99,6 +136,14 @@ SIGNATURES = {
     "msgl_shared_prefixes": ([PT, P, I32, I32, I32, I32, P, P, P, P], ctypes.c_int),
     "msgl_decode_shared_workspace_size": ([I32, I32, I32, I32, I32], SZ),
     "msgl_attn_decode_shared": ([PP, PT, P, I32, P, P, P, I32, I32, I32, F32, P, P, P, SZ, P, P], ctypes.c_int),
+    "msgl_rope_store_kv": ([PP, ctypes.POINTER(_NewTokens), ctypes.POINTER(_Rope), P, P, F32, P, P], ctypes.c_int),
+    "msgl_verify_drafts": ([ctypes.POINTER(_DraftBatch), P, P], ctypes.c_int),
+    "msgl_fork_requests": ([I64, I32, P, I32, I32, I32, P, P, P, I32, P, I32, ctypes.POINTER(_ForkOut), P, P],
+                           ctypes.c_int),
+    "msgl_copy_pages": ([PP, I32, P, P, P, I32, P, P, P], ctypes.c_int),
+    "msgl_free_pages": ([I64, I32, P, I32, I32, I32, P, P, I32, P, P, P, P, P], ctypes.c_int),
+    "msgl_compact_pages": ([I64, I32, P, I32, I32, I32, P, P, I32, P, ctypes.POINTER(_CompactOut), P, P],
+                           ctypes.c_int),
     "msgl_selftest_wait_timeout": ([P, I64, P], ctypes.c_int),
     "msgl_read_status": ([P, ctypes.POINTER(ctypes.c_uint32), P], ctypes.c_int),
     "msgl_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -109,6 +154,10 @@ SIGNATURES = {
     "msgl_check_decode_meta": ([I64, I32, P, I32, I32, P, I32, I32], ctypes.c_int),
     "msgl_check_step_meta": ([I64, I32, P, I32, I32, I32, P, P, P, I32, P, I32, I32], ctypes.c_int),
     "msgl_check_groups_meta": ([I64, I32, P, I32, I32, P, P, P, I32, I32], ctypes.c_int),
+    "msgl_check_fork_meta": ([I64, I32, P, I32, I32, I32, P, P, P, I32, P, I32], ctypes.c_int),
+    "msgl_check_copy_meta": ([I64, I32, P, P, P, I32], ctypes.c_int),
+    "msgl_check_held_meta": ([I64, I32, P, I32, I32, I32, P, P, I32], ctypes.c_int),
+    "msgl_check_draft_meta": ([I32, P, P, P, P, I32, I32], ctypes.c_int),
 }
 
 
@@ -499,6 +548,173 @@ def attn_decode_shared(pool: KVPool, q: torch.Tensor, page_table: torch.Tensor, 
     return r
 
 
+# ------------------------------- rotary store, drafts, pages between the steps
+
+class Rope:
+    """How heads turn by position: made once, an argument of :func:`rope_store_kv`.
+
+    ``inv_freq``: radians per position of each of a head's pairs (8, 16, .. 64 of them; any
+    scaling of positions or frequencies is the caller's, in 64 bits).  ``axes``: the row
+    of ``positions`` that a pair goes by (all 0 when None): ``[0] * 16 + [1] * 24 + [2] * 24`` for
+    sections of time, height and width, ``[0, 1, 2] * 16 + ..`` for interleaved ones.  Pair j is
+    dims j and j + pairs, or 2j and 2j + 1 when ``adjacent``; later dims do not turn.
+    ``factor`` scales what turns.
+    """
+
+    def __init__(self, inv_freq, axes=None, adjacent: bool = False, factor: float = 1.0):
+        freq = [float(f) for f in (inv_freq.tolist() if isinstance(inv_freq, torch.Tensor) else inv_freq)]
+        axes = [0] * len(freq) if axes is None else [int(a) for a in axes]
+        if not freq or len(freq) > 64 or len(freq) % 8:
+            raise ValueError("inv_freq must have 8, 16, .. 64 entries")
+        if not all(math.isfinite(f) for f in freq) or not math.isfinite(factor):
+            raise ValueError("inv_freq and factor must be finite")
+        if len(axes) != len(freq) or min(axes) < 0 or max(axes) > 3:
+            raise ValueError("axes must have an entry in [0, 3] for each of inv_freq")
+        # a fraction of a turn in 64 bits: whole turns of an integer position drop out of the product
+        turns = [int(math.fmod(f / (2 * math.pi), 1.0) * 2.0 ** 64) % 2 ** 64 for f in freq]
+        self.turns = b"".join(ctypes.c_uint64(t) for t in turns)
+        self.axes, self.adjacent, self.factor = bytes(axes), bool(adjacent), float(factor)
+
+
+def rope_store_kv(pool: KVPool, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                  out_loc: torch.Tensor, rope: Rope, q_out: Optional[torch.Tensor] = None,
+                  q_norm: Optional[torch.Tensor] = None, k_norm: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                  status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """:func:`store_kv` of k and v with k turned by position on the way, and q turned into q_out, which it returns.
+
+    q [T,Hq,D], k and v [T,Hkv,D] may be columns of one tensor (tokens any multiple of 8
+    elements apart); ``q_out`` may be q itself.  ``positions`` int32 [T] or [axes, T].  ``q_norm`` and
+    ``k_norm`` bf16 [D] norm each head first.  A token with out_loc -1 is none (padding): its row of
+    q_out is not written.
+    """
+    r = (_native or _binding()).rope_store_kv(pool.k, pool.v, pool.page_size, q, k, v, positions, out_loc, rope.turns,
+                                              rope.axes, rope.adjacent, rope.factor, q_out, q_norm, k_norm, eps, status,
+                                              _handle(stream))
+    if type(r) is int:
+        _check(r, "msgl_rope_store_kv")
+    return r
+
+
+class Verified(NamedTuple):
+    """The outputs of :func:`verify_drafts` (all int32): keep one and pass it as ``out`` to reuse its buffers."""
+    accepted: torch.Tensor     # [B]  drafts that stand
+    tokens: torch.Tensor       # [T]  a request's rows: its accepted drafts, the new token, -1
+    kv_lens: torch.Tensor      # [B]  tokens whose K/V are kept: the next step's cached_lens
+
+
+def verify_drafts(target_probs: torch.Tensor, draft_probs: Optional[torch.Tensor], tokens: torch.Tensor,
+                  cu_ext: torch.Tensor, accept_u: torch.Tensor, sample_u: torch.Tensor,
+                  cached_lens: Optional[torch.Tensor] = None, out: Optional[Verified] = None,
+                  status: Optional[torch.Tensor] = None, stream=None) -> Verified:
+    """Drafted tokens accepted or replaced by the target's probabilities (msgl_verify_drafts).
+
+    Request b's rows of a step, ``cu_ext[b]`` to ``cu_ext[b+1] - 1``, were fed its last token and its
+    drafts (``tokens`` int32 [T]).  ``target_probs`` and ``draft_probs`` float32 or bfloat16 [T, vocab]: row r is the
+    distribution that token r + 1 is held against, and was drawn from (``draft_probs`` None: drafts
+    that were not drawn at random).  ``accept_u`` [T] and ``sample_u`` [B] are float32 numbers in
+    [0, 1).  ``out.kv_lens`` may be ``cached_lens`` itself, which a loop then goes on with.
+    """
+    a, x, n = (None, None, None) if out is None else out
+    r = (_native or _binding()).verify_drafts(target_probs, draft_probs, tokens, cu_ext, accept_u, sample_u, cached_lens,
+                                              a, x, n, status, _handle(stream))
+    if type(r) is int:
+        _check(r, "msgl_verify_drafts")
+    return out if r is None else Verified(*r)
+
+
+class Forked(NamedTuple):
+    """The outputs of :func:`fork_requests` (all int32); the first three are arguments of :func:`copy_pages`."""
+    src: torch.Tensor          # [N]  page to copy, -1 where none is
+    dst: torch.Tensor          # [N]
+    tokens: torch.Tensor       # [N]  tokens on it
+    pages_taken: torch.Tensor  # [1]  how many of the free pages are now in use
+
+
+def fork_requests(req_table: torch.Tensor, parent_rows: torch.Tensor, child_rows: torch.Tensor, lens: torch.Tensor,
+                  free_pages: torch.Tensor, num_slots: int, page_size: int, out: Optional[Forked] = None,
+                  status: Optional[torch.Tensor] = None, stream=None) -> Forked:
+    """Row ``child_rows[i]`` of ``req_table`` continues the first ``lens[i]`` tokens of row ``parent_rows[i]``.
+
+    Whole pages are shared; a partly filled last one is replaced by a page from the front of
+    ``free_pages`` and has to be copied (msgl_fork_requests): ``copy_pages(pools, f.src, f.dst, f.tokens)``.
+    """
+    s, d, n, t = (None,) * 4 if out is None else out
+    r = (_native or _binding()).fork_requests(req_table, parent_rows, child_rows, lens, free_pages, num_slots, page_size,
+                                              s, d, n, t, status, _handle(stream))
+    if type(r) is int:
+        _check(r, "msgl_fork_requests")
+    return out if r is None else Forked(*r)
+
+
+def copy_pages(pools, src: torch.Tensor, dst: torch.Tensor, tokens: Optional[torch.Tensor] = None,
+               count: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Pages ``src[i]`` to ``dst[i]`` in every pool (a :class:`KVPool` or a sequence of them, one a layer).
+
+    ``tokens`` int32 [N]: only the first of a page's slots; ``count`` int32 [1]: only the first pairs.
+    Pairs of -1 are passed over (msgl_copy_pages).
+    """
+    pools = [pools] if isinstance(pools, KVPool) else pools
+    ps = pools[0].page_size if pools else 1
+    if any(p.page_size != ps for p in pools):
+        raise ValueError("pools must have one page_size")
+    rc = (_native or _binding()).copy_pages(pools, ps, src, dst, tokens, count, status, _handle(stream))
+    if rc is not None:
+        _check(rc, "msgl_copy_pages")
+
+
+class FreePages(NamedTuple):
+    """The outputs of :func:`free_pages` (int32)."""
+    pages: torch.Tensor        # [num_pages]  ids in ascending order, -1 behind them
+    num_free: torch.Tensor     # [1]
+
+
+def free_pages(req_table: torch.Tensor, lens: torch.Tensor, num_slots: int, page_size: int,
+               req_rows: Optional[torch.Tensor] = None, held: Optional[torch.Tensor] = None,
+               out: Optional[FreePages] = None, status: Optional[torch.Tensor] = None, stream=None) -> FreePages:
+    """The pages that no request holds (msgl_free_pages): the ``free_pages`` of :func:`step_tables` and
+    :func:`fork_requests`.
+
+    Request b holds the pages of its first ``lens[b]`` tokens in row ``req_rows[b]`` (b when
+    None; -1: padding).  ``held`` uint8 or bool [num_pages]: pages in use beside them.
+    """
+    p, c = (None, None) if out is None else out
+    r = (_native or _binding()).free_pages(req_table, lens, num_slots, page_size, req_rows, held, p, c, status,
+                                           _handle(stream))
+    if type(r) is int:
+        _check(r, "msgl_free_pages")
+    return out if r is None else FreePages(*r)
+
+
+COMPACT_MAX_PAGES = 1310720
+
+
+class Compaction(NamedTuple):
+    """The outputs of :func:`compact_pages` (int32)."""
+    page_table: torch.Tensor   # [rows, W]       the requests' rows with the new ids
+    remap: torch.Tensor        # [num_pages]     a page's new id, -1 for a free one
+    src: torch.Tensor          # [num_pages//2]  the moves, -1 behind them
+    dst: torch.Tensor          # [num_pages//2]
+    num_moves: torch.Tensor    # [1]
+    num_used: torch.Tensor     # [1]             pages in use
+
+
+def compact_pages(req_table: torch.Tensor, lens: torch.Tensor, num_slots: int, page_size: int,
+                  req_rows: Optional[torch.Tensor] = None, held: Optional[torch.Tensor] = None,
+                  out: Optional[Compaction] = None, status: Optional[torch.Tensor] = None, stream=None) -> Compaction:
+    """Moves the requests' pages to the front of the pool (msgl_compact_pages).
+
+    The table is rewritten in place unless ``out`` has another; the pages themselves move by
+    ``copy_pages(pools, c.src, c.dst, count=c.num_moves)``.  Requests and ``held`` (pages that stay where they
+    are) as in :func:`free_pages`.
+    """
+    t, m, s, d, n, u = (req_table,) + (None,) * 5 if out is None else out
+    r = (_native or _binding()).compact_pages(req_table, lens, num_slots, page_size, req_rows, held, t, m, s, d, n, u,
+                                              status, _handle(stream))
+    if type(r) is int:
+        _check(r, "msgl_compact_pages")
+    return out if r is None else Compaction(req_table, *r)
+
+
 def selftest_wait_timeout(status: torch.Tensor, budget_cycles: int = 10_000_000, stream=None) -> None:
     """Run the bounded-wait self-test; the status word then holds DEVERR_TIMEOUT."""
     rc = load().msgl_selftest_wait_timeout(_ptr(status), int(budget_cycles), _stream(stream))
@@ -590,3 +806,53 @@ def check_groups_meta(num_slots: int, page_size: int, page_table: torch.Tensor, 
         raise ValueError("group_start and shared_lens must have one entry per request")
     _check(load().msgl_check_groups_meta(int(num_slots), int(page_size), ptp, w, w, firstp, sharedp, seqp, seq.numel(),
                                          int(max_seq_len)), "msgl_check_groups_meta")
+
+
+def check_fork_meta(num_slots: int, page_size: int, req_table: torch.Tensor, parent_rows: torch.Tensor,
+                    child_rows: torch.Tensor, lens: torch.Tensor, free_pages: torch.Tensor):
+    """Copies the forks' rows, lengths and tables back and checks them.  Raises MsglError."""
+    rt, rtp, w = _table(req_table)
+    a, ap = _host_i32(parent_rows)
+    b, bp = _host_i32(child_rows)
+    n, np_ = _host_i32(lens)
+    f, fp = _host_i32(free_pages)
+    if b.numel() != a.numel() or n.numel() != a.numel():
+        raise ValueError("child_rows and lens must have an entry for each of parent_rows")
+    _check(load().msgl_check_fork_meta(int(num_slots), int(page_size), rtp, rt.numel() // w if w else 0, w, w, ap, bp,
+                                       np_, a.numel(), fp, f.numel()), "msgl_check_fork_meta")
+
+
+def check_copy_meta(num_slots: int, page_size: int, src: torch.Tensor, dst: torch.Tensor,
+                    tokens: Optional[torch.Tensor] = None):
+    """Copies the pairs of pages back and checks them.  Raises MsglError."""
+    s, sp = _host_i32(src)
+    d, dp = _host_i32(dst)
+    n, np_ = _host_i32(tokens)
+    if d.numel() != s.numel() or (n is not None and n.numel() != s.numel()):
+        raise ValueError("dst and tokens must have an entry for each of src")
+    _check(load().msgl_check_copy_meta(int(num_slots), int(page_size), sp, dp, np_, s.numel()), "msgl_check_copy_meta")
+
+
+def check_held_meta(num_slots: int, page_size: int, req_table: torch.Tensor, lens: torch.Tensor,
+                    req_rows: Optional[torch.Tensor] = None):
+    """Copies what :func:`free_pages` and :func:`compact_pages` go by back and checks it.  Raises MsglError."""
+    rt, rtp, w = _table(req_table)
+    n, np_ = _host_i32(lens)
+    r, rp = _host_i32(req_rows)
+    if r is not None and r.numel() != n.numel():
+        raise ValueError("req_rows must have one entry per request")
+    _check(load().msgl_check_held_meta(int(num_slots), int(page_size), rtp, rt.numel() // w if w else 0, w, w, rp, np_,
+                                       n.numel()), "msgl_check_held_meta")
+
+
+def check_draft_meta(vocab: int, tokens: torch.Tensor, cu_ext: torch.Tensor, accept_u: torch.Tensor,
+                     sample_u: torch.Tensor):
+    """Copies a draft batch's tokens, rows and random numbers back and checks them.  Raises MsglError."""
+    t, tp = _host_i32(tokens)
+    cu, cup = _host_i32(cu_ext)
+    a = accept_u.detach().to("cpu", torch.float32).contiguous()
+    s = sample_u.detach().to("cpu", torch.float32).contiguous()
+    if a.numel() != t.numel() or cu.numel() != s.numel() + 1:
+        raise ValueError("accept_u must be [T], and cu_ext [B + 1] for sample_u [B]")
+    _check(load().msgl_check_draft_meta(int(vocab), tp, cup, ctypes.c_void_p(a.data_ptr()),
+                                        ctypes.c_void_p(s.data_ptr()), s.numel(), t.numel()), "msgl_check_draft_meta")
