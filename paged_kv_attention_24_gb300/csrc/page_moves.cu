@@ -17,12 +17,12 @@ namespace {
 
 // ---------------------------------------------------------------------- fork
 //
-// One block per fork and 2048 columns of its row, as in the step tables.  A fork
+// One block per fork and 4096 columns of its row, as in the step tables.  A fork
 // needs one new page or none, so its place among the free pages is the number of
 // earlier forks with a partly filled page, counted again by every block; the same
 // loop sees whether its child's row is named by another fork.
 constexpr int kForkThreads = 256;
-constexpr int kPerThread = 8;
+constexpr int kPerThread = 16;
 constexpr int kChunk = kForkThreads * kPerThread;
 
 struct Fork {
@@ -55,9 +55,15 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkArgs a) {
     } else if (blockIdx.y > 0) {
         return;
     }
-    __shared__ int before, clash;
-    if (threadIdx.x == 0) before = clash = 0;
-    __syncthreads();
+    // (f.full is 0 unless rows and length are in range, so these are read before the counts below are known)
+    const int32_t *theirs = a.req_table + (int64_t)max(f.parent, 0) * a.table_stride;
+    int32_t id[kPerThread];
+#pragma unroll
+    for (int u = 0; u < kPerThread; ++u) {
+        const int p = at0 + u * kForkThreads;
+        if (p < f.full) id[u] = theirs[p];
+    }
+    const int32_t source = f.tail > 0 ? theirs[f.full] : -1;
     int n = 0;
     bool twice = false;
     for (int i = threadIdx.x; i < a.num_forks; i += kForkThreads) {
@@ -65,22 +71,22 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkArgs a) {
         n += i < b && x.tail > 0;
         twice |= b < a.num_forks && (f.child == x.parent || (i != b && f.child == x.child));
     }
-    if (n) atomicAdd(&before, n);
-    if (twice) clash = 1;
-    __syncthreads();
+    __shared__ int part[kForkThreads / 32];
+    n = __reduce_add_sync(0xffffffffu, n);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = n;
+    const bool clash = __syncthreads_or(twice);
+    int before = 0;
+#pragma unroll
+    for (int w = 0; w < kForkThreads / 32; ++w) before += part[w];
     if (b == a.num_forks) {
         if (threadIdx.x == 0) a.pages_taken[0] = min(before, a.num_free);
         return;
     }
     const bool rows_ok = f.rows_ok && !clash, paged = f.tail == 0 || before < a.num_free;
-    bool served = !f.none && rows_ok && f.len_ok && paged;
-    int32_t *mine = a.req_table + (int64_t)max(f.child, 0) * a.table_stride;
-    const int32_t *theirs = a.req_table + (int64_t)max(f.parent, 0) * a.table_stride;
-    int32_t fresh = -1, source = -1;
-    bool pages_ok = true;
+    bool served = !f.none && rows_ok && f.len_ok && paged, pages_ok = true;
+    int32_t fresh = -1;
     if (served && f.tail > 0) {
         fresh = __ldg(a.free_pages + before);
-        source = theirs[f.full];
         pages_ok = fresh >= 0 && fresh < a.num_pages && source >= 0 && source < a.num_pages;
         served = pages_ok;
     }
@@ -97,26 +103,21 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkArgs a) {
         }
     }
     if (!served) return;
-    int32_t id[kPerThread];
+    int32_t *mine = a.req_table + (int64_t)f.child * a.table_stride;
 #pragma unroll
     for (int u = 0; u < kPerThread; ++u) {
         const int p = at0 + u * kForkThreads;
-        id[u] = p < f.full ? theirs[p] : fresh;
-    }
-#pragma unroll
-    for (int u = 0; u < kPerThread; ++u) {
-        const int p = at0 + u * kForkThreads;
-        if (p < f.full + (f.tail > 0)) mine[p] = id[u];
+        if (p < f.full + (f.tail > 0)) mine[p] = p < f.full ? id[u] : fresh;
     }
 }
 
 // ---------------------------------------------------------------------- copy
 //
-// A warp takes 4 KB of one page's K or V in one pool, all its loads before its
+// A warp takes 2 KB of one page's K or V in one pool, all its loads before its
 // stores; the pools and their K and V are the grid's second axis, so that a
 // block's addresses differ by the page only.
 constexpr int kCopyThreads = 256;
-constexpr int kCopyUnroll = 8;
+constexpr int kCopyUnroll = 4;
 constexpr int kPiece = 32 * kCopyUnroll;           // 16-byte vectors
 
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_constant__ CopyPagesArgs a) {
@@ -161,7 +162,7 @@ cudaError_t launch_fork(const ForkArgs &a, cudaStream_t stream) {
 cudaError_t launch_copy_pages(CopyPagesArgs &a, cudaStream_t stream) {
     a.pieces = (int32_t)((a.page_vecs + kPiece - 1) / kPiece);
     const int64_t blocks = ((int64_t)a.num_pairs * a.pieces + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
-    const int64_t cap = ((int64_t)sm_count() * 4 + a.num_buffers - 1) / a.num_buffers;
+    const int64_t cap = ((int64_t)sm_count() * 64 + a.num_buffers - 1) / a.num_buffers;
     copy_pages_kernel<<<dim3((unsigned)(blocks < cap ? blocks : cap), a.num_buffers), kCopyThreads, 0, stream>>>(a);
     return cudaGetLastError();
 }
