@@ -374,7 +374,7 @@ MSGL_API msgl_status msgl_step_tables(int64_t num_slots, int32_t page_size, int3
  * replaced by x * w / sqrt(mean(x^2) + eps).  All of it is computed in 32 bits (the
  * angle modulo a turn exactly) and rounded to bf16 once; v is copied.
  *
- *   turns        host uint64 [num_pairs]: f_j / (2 pi) * 2^64 modulo 2^64
+ *   turns        device uint64 [num_pairs]: f_j / (2 pi) * 2^64 modulo 2^64
  *   axes         host uint8 [num_pairs]: axis_j < num_axes, or NULL (all 0)
  *   num_pairs    8, 16, .. 64;  num_axes 1..4
  *   q, k, v      device bf16 [n_tokens, heads, head_dim], token t at t * stride elements
@@ -392,7 +392,7 @@ MSGL_API msgl_status msgl_step_tables(int64_t num_slots, int32_t page_size, int3
  * Duplicate slots are undefined (one of the rows wins).
  */
 typedef struct msgl_rope {
-    const uint64_t *turns;         /* host */
+    const uint64_t *turns;         /* device */
     const uint8_t *axes;           /* host, or NULL */
     int32_t num_pairs, num_axes;
     int32_t adjacent;
@@ -532,11 +532,17 @@ MSGL_API msgl_status msgl_copy_pages(const msgl_kv_pool *pools, int32_t num_pool
  * negative or passes table_width (MSGL_DEVERR_LENGTH) holds all of its row, so that none
  * of its pages is given away; an id outside the pool (MSGL_DEVERR_PAGE_RANGE) is
  * skipped.  The outputs may overlap neither an input nor each other.
+ *   workspace    device scratch of at least msgl_page_map_workspace_size() bytes, 256-byte
+ *                aligned, fully rewritten by every call; two calls (or captured graphs)
+ *                that may overlap need one each
  */
+MSGL_API size_t msgl_page_map_workspace_size(int64_t num_slots, int32_t page_size);
+
 MSGL_API msgl_status msgl_free_pages(int64_t num_slots, int32_t page_size, const int32_t *req_table, int32_t num_rows,
                                      int32_t table_stride, int32_t table_width, const int32_t *req_rows,
                                      const int32_t *lens, int32_t num_reqs, const uint8_t *held, int32_t *pages,
-                                     int32_t *num_free, uint32_t *status, msgl_stream_t stream);
+                                     int32_t *num_free, void *workspace, size_t workspace_bytes, uint32_t *status,
+                                     msgl_stream_t stream);
 
 /*
  * The pages in use moved to the front of the pool, so that the pool may shrink
@@ -553,12 +559,9 @@ MSGL_API msgl_status msgl_free_pages(int64_t num_slots, int32_t page_size, const
  *   out->num_used[0]        U
  * A page that `held` names stays where it is (ids from U on may then be in use).
  * The pages have to be copied before they are read or written again.
- * Requests, errors and overlaps are those of msgl_free_pages (a request that holds
- * all of its row gets new ids in all of it); a row may be named twice.  At most
- * MSGL_COMPACT_MAX_PAGES pages (MSGL_ERR_UNSUPPORTED).
+ * Requests, errors, overlaps and the workspace are those of msgl_free_pages (a request
+ * that holds all of its row gets new ids in all of it); a row may be named twice.
  */
-#define MSGL_COMPACT_MAX_PAGES 1310720
-
 typedef struct msgl_compact_out {
     int32_t *page_ids;             /* device int32 [num_rows, stride] */
     int32_t stride;
@@ -570,8 +573,8 @@ typedef struct msgl_compact_out {
 MSGL_API msgl_status msgl_compact_pages(int64_t num_slots, int32_t page_size, const int32_t *req_table,
                                         int32_t num_rows, int32_t table_stride, int32_t table_width,
                                         const int32_t *req_rows, const int32_t *lens, int32_t num_reqs,
-                                        const uint8_t *held, const msgl_compact_out *out, uint32_t *status,
-                                        msgl_stream_t stream);
+                                        const uint8_t *held, const msgl_compact_out *out, void *workspace,
+                                        size_t workspace_bytes, uint32_t *status, msgl_stream_t stream);
 
 /*
  * Groups of neighbouring requests whose page tables begin with the same pages:

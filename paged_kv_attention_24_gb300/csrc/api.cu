@@ -154,6 +154,14 @@ msgl_status check_req_table(const int32_t *table, int32_t rows, int32_t stride, 
     return MSGL_OK;
 }
 
+msgl_status check_map_workspace(const void *workspace, size_t bytes, int32_t num_pages) {
+    const size_t need = msgl::page_map_workspace_bytes(num_pages);
+    if (need && (!workspace || bytes < need))
+        return fail(MSGL_ERR_WORKSPACE, "needs %zu workspace bytes, got %zu", need, workspace ? bytes : (size_t)0);
+    if ((uintptr_t)workspace % 256) return fail(MSGL_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    return MSGL_OK;
+}
+
 // The arguments that msgl_free_pages and msgl_compact_pages share.
 msgl_status prepare_page_map(int64_t num_slots, int32_t page_size, const int32_t *req_table, int32_t num_rows,
                              int32_t table_stride, int32_t table_width, const int32_t *req_rows, const int32_t *lens,
@@ -613,7 +621,6 @@ msgl_status msgl_rope_store_kv(const msgl_kv_pool *pool, const msgl_new_tokens *
         const uint32_t axis = rope->axes ? rope->axes[j] : 0;
         if (axis >= (uint32_t)rope->num_axes)
             return fail(MSGL_ERR_INVALID_ARG, "axes[%d] = %u but num_axes = %d", j, axis, rope->num_axes);
-        a.turns[j] = rope->turns[j];
         a.axis_bits[j / 16] |= axis << (2 * (j % 16));
     }
     if (n.n_tokens == 0) return MSGL_OK;
@@ -622,6 +629,7 @@ msgl_status msgl_rope_store_kv(const msgl_kv_pool *pool, const msgl_new_tokens *
     if (!aligned16(n.q) || !aligned16(n.k) || !aligned16(n.v) || !aligned16(n.q_out) || !aligned16(q_norm) ||
         !aligned16(k_norm))
         return fail(MSGL_ERR_INVALID_ARG, "q, k, v, q_out and the norms must be 16-byte aligned");
+    if ((uintptr_t)rope->turns % 8) return fail(MSGL_ERR_INVALID_ARG, "rope->turns must be 8-byte aligned");
     const int64_t q_row = (int64_t)n.num_q_heads * msgl::kHeadDim, kv_row = (int64_t)a.pool.hkv * msgl::kHeadDim;
     const struct {
         int64_t stride, row;
@@ -646,6 +654,7 @@ msgl_status msgl_rope_store_kv(const msgl_kv_pool *pool, const msgl_new_tokens *
                         flat(static_cast<const int32_t *>(k_norm), msgl::kHeadDim / 2, "k_norm"),
                         {n.positions, rope->num_axes, n.n_tokens, rope->num_axes > 1 ? n.axis_stride : n.n_tokens, "positions"},
                         flat(n.out_loc, n.n_tokens, "out_loc"),
+                        flat(reinterpret_cast<const int32_t *>(rope->turns), 2 * rope->num_pairs, "rope->turns"),
                         {static_cast<const int32_t *>(pool->k_pool), pool->num_slots, kv_row / 2, kv_row / 2, "the K pool"},
                         {static_cast<const int32_t *>(pool->v_pool), pool->num_slots, kv_row / 2, kv_row / 2, "the V pool"}};
     for (const Span &in : ins) {
@@ -664,6 +673,7 @@ msgl_status msgl_rope_store_kv(const msgl_kv_pool *pool, const msgl_new_tokens *
     a.k_stride = n.k_stride;
     a.v_stride = n.v_stride;
     a.out_stride = n.out_stride;
+    a.turns = rope->turns;
     a.positions = n.positions;
     a.out_loc = n.out_loc;
     a.axis_stride = rope->num_axes > 1 ? n.axis_stride : 0;
@@ -829,10 +839,15 @@ msgl_status msgl_copy_pages(const msgl_kv_pool *pools, int32_t num_pools, const 
     return MSGL_OK;
 }
 
+size_t msgl_page_map_workspace_size(int64_t num_slots, int32_t page_size) {
+    if (page_size <= 0 || num_slots < 0 || num_slots / page_size > INT32_MAX) return 0;
+    return msgl::page_map_workspace_bytes((int32_t)(num_slots / page_size));
+}
+
 msgl_status msgl_free_pages(int64_t num_slots, int32_t page_size, const int32_t *req_table, int32_t num_rows,
                             int32_t table_stride, int32_t table_width, const int32_t *req_rows, const int32_t *lens,
                             int32_t num_reqs, const uint8_t *held, int32_t *pages, int32_t *num_free,
-                            uint32_t *status, msgl_stream_t stream) {
+                            void *workspace, size_t workspace_bytes, uint32_t *status, msgl_stream_t stream) {
     g_last_error[0] = 0;
     msgl::PageMapArgs a{};
     msgl_status s = prepare_page_map(num_slots, page_size, req_table, num_rows, table_stride, table_width, req_rows, lens,
@@ -844,25 +859,24 @@ msgl_status msgl_free_pages(int64_t num_slots, int32_t page_size, const int32_t 
     const Span ins[] = {{req_table, num_rows, table_width, table_stride, "req_table"}, flat(req_rows, num_reqs, "req_rows"),
                         flat(lens, num_reqs, "lens"), bytes_span(held, a.num_pages, "held")};
     if ((s = check_overlaps(outs, 2, ins, 4))) return s;
+    if ((s = check_map_workspace(workspace, workspace_bytes, a.num_pages))) return s;
     a.pages_out = pages;
     a.count_out = num_free;
-    cudaError_t e = msgl::launch_free_pages(a, (cudaStream_t)stream);
+    cudaError_t e = msgl::launch_free_pages(a, workspace, (cudaStream_t)stream);
     return e == cudaSuccess ? MSGL_OK : cuda_fail(e, "free_pages launch");
 }
 
 msgl_status msgl_compact_pages(int64_t num_slots, int32_t page_size, const int32_t *req_table, int32_t num_rows,
                                int32_t table_stride, int32_t table_width, const int32_t *req_rows,
                                const int32_t *lens, int32_t num_reqs, const uint8_t *held,
-                               const msgl_compact_out *out, uint32_t *status, msgl_stream_t stream) {
+                               const msgl_compact_out *out, void *workspace, size_t workspace_bytes,
+                               uint32_t *status, msgl_stream_t stream) {
     g_last_error[0] = 0;
     if (!out) return fail(MSGL_ERR_INVALID_ARG, "out is NULL");
     msgl::PageMapArgs a{};
     msgl_status s = prepare_page_map(num_slots, page_size, req_table, num_rows, table_stride, table_width, req_rows, lens,
                                      num_reqs, held, status, a);
     if (s) return s;
-    static_assert(msgl::kMaxMapPages == MSGL_COMPACT_MAX_PAGES, "the header says what the kernel holds");
-    if (a.num_pages > msgl::kMaxMapPages)
-        return fail(MSGL_ERR_UNSUPPORTED, "%d pages: compact_pages takes at most %d", a.num_pages, msgl::kMaxMapPages);
     if (!out->num_moves || !out->num_used || (a.num_pages > 0 && !out->remap) ||
         (a.num_pages > 1 && (!out->src || !out->dst)) || (num_rows > 0 && table_width > 0 && !out->page_ids))
         return fail(MSGL_ERR_INVALID_ARG, "out's arrays must be non-NULL");
@@ -878,6 +892,7 @@ msgl_status msgl_compact_pages(int64_t num_slots, int32_t page_size, const int32
                         bytes_span(held, a.num_pages, "held"),
                         {in_place ? nullptr : req_table, num_rows, table_width, table_stride, "req_table"}};
     if ((s = check_overlaps(outs, 6, ins, 4))) return s;
+    if ((s = check_map_workspace(workspace, workspace_bytes, a.num_pages))) return s;
     a.pages_out = out->remap;
     a.count_out = out->num_moves;
     a.used_out = out->num_used;
@@ -885,7 +900,7 @@ msgl_status msgl_compact_pages(int64_t num_slots, int32_t page_size, const int32
     a.dst = out->dst;
     a.table_out = out->page_ids;
     a.out_stride = out->stride;
-    cudaError_t e = msgl::launch_compact_pages(a, (cudaStream_t)stream);
+    cudaError_t e = msgl::launch_compact_pages(a, workspace, (cudaStream_t)stream);
     return e == cudaSuccess ? MSGL_OK : cuda_fail(e, "compact_pages launch");
 }
 

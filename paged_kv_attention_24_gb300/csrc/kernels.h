@@ -107,7 +107,7 @@ struct RopeStoreArgs {
     int64_t q_stride, k_stride, v_stride, out_stride;   // elements from token to token
     const int32_t *positions, *out_loc;
     int64_t axis_stride;
-    uint64_t turns[kHeadDim / 2];         // a pair's frequency: turns per position * 2^64, modulo 2^64
+    const uint64_t *turns;                // a pair's frequency: turns per position * 2^64, modulo 2^64
     uint32_t axis_bits[kHeadDim / 32];    // a pair's axis, two bits each
     int32_t pairs, adjacent, n_tokens, hq;
     float factor, eps;
@@ -149,8 +149,6 @@ struct CopyPagesArgs {
 };
 cudaError_t launch_copy_pages(CopyPagesArgs &a, cudaStream_t stream);
 
-constexpr int32_t kMaxMapPages = 1310720; // pages whose bits fit the shared memory of a block
-
 struct PageMapArgs {
     const int32_t *table, *req_rows, *lens;
     const uint8_t *held;
@@ -159,10 +157,12 @@ struct PageMapArgs {
     int32_t *count_out;                   // [1]: free pages; compact: pages that move
     int32_t *table_out, *src, *dst, *used_out;   // compact
     int32_t out_stride;
+    uint32_t *used_bits, *stay_bits, *moves_before;   // in the workspace (set by the launchers)
     uint32_t *status;
 };
-cudaError_t launch_free_pages(const PageMapArgs &a, cudaStream_t stream);
-cudaError_t launch_compact_pages(const PageMapArgs &a, cudaStream_t stream);
+size_t page_map_workspace_bytes(int32_t num_pages);
+cudaError_t launch_free_pages(PageMapArgs a, void *workspace, cudaStream_t stream);
+cudaError_t launch_compact_pages(PageMapArgs a, void *workspace, cudaStream_t stream);
 
 // -------------------------------------------------------- shared-prefix decode
 size_t decode_shared_workspace_bytes(int32_t num_reqs, int32_t hq, int32_t hkv);

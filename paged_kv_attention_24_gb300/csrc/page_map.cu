@@ -6,56 +6,31 @@
 // page is free when no request's table names it, whatever forks, rejected drafts
 // and finished requests did before.
 //
-// One cluster of 8 blocks, one launch: every block takes its share of the table
-// entries and marks their pages in a bitmap in its own shared memory; the blocks
-// then join their bitmaps, an eighth of the pages each, count, and write what is
-// theirs.  Pools of more pages than a bitmap has bits take a round for each part.
+// A bitmap of the pool, one bit a page, in the workspace: set from `held`, then every
+// table entry marks its page, then each block lists its share of the pages, its place in the
+// lists from a count of all bits before its own (the bitmap of a million pages is 128 KB,
+// which every block reads out of L2).  The kernels follow each other by programmatic dependent
+// launch; each waits for the one before, all of whose blocks did, before it touches
+// what that one wrote.
 //
-// Bound by latency up to some thousand entries (lengths, entries, two or three
-// exchanges between the blocks, stores), by the 8 SMs' loads and stores beyond.
+// Bound by latency up to some ten thousand entries, by scattered atomics and the
+// lists' stores beyond.  Both want many SMs: one cluster of 8 blocks that kept the bitmap in
+// shared memory, a launch less, took the same 6.5 us for 64 requests, but 32 us for half
+// a million entries (16 blocks 23: a shared-memory atomic takes a cycle a lane).
 #include "kernels.h"
 
 namespace msgl {
 
 namespace {
 
-constexpr int kCluster = 8;
-constexpr int kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kBatch = kThreads;                     // requests looked at together
+constexpr int kListThreads = 1024, kListWarps = kListThreads / 32;
 constexpr int kPerLane = 8;
 constexpr int kUnit = 32 * kPerLane;                 // table entries of one warp's turn
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
-
-__device__ __forceinline__ uint32_t peer(const void *p, int rank) {
-    uint32_t a;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
-    return a;
-}
-
-__device__ __forceinline__ uint32_t ld_peer(uint32_t at) {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-    return v;
-}
-
-__device__ __forceinline__ void st_peer(uint32_t at, uint32_t v) {
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
-}
-
-struct Shared {
-    int32_t row[kThreads], pages[kThreads], unit[kThreads];   // requests of the present batch
-    uint32_t warp[2][kWarps];
-    uint32_t counts[2][2][kCluster];                          // exchanged, two numbers a block
-};
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // x summed over the warp's lanes up to this one.
 __device__ __forceinline__ uint32_t warp_scan(uint32_t x) {
@@ -68,260 +43,421 @@ __device__ __forceinline__ uint32_t warp_scan(uint32_t x) {
     return x;
 }
 
-// f(entry's address in the table, its place in the output) for every table entry of a request, 8 to a lane.
-template <class F>
-__device__ __forceinline__ void for_entries(const PageMapArgs &a, Shared &s, bool tell, F f) {
+// ----------------------------------------------------------- table entries
+
+// The row and the number of table entries of request b.
+__device__ __forceinline__ int entries_of(const PageMapArgs &a, int b, bool tell, int &row) {
+    row = a.req_rows ? __ldg(a.req_rows + b) : b;
+    const int len = __ldg(a.lens + b);
+    const int64_t need = ((int64_t)len + (1 << a.log2_ps) - 1) >> a.log2_ps;
+    const bool row_ok = row >= 0 && row < a.num_rows, len_ok = len >= 0 && need <= a.table_width;
+    if (tell && row != -1 && !row_ok) report(a.status, MSGL_DEVERR_ROW);
+    if (tell && row_ok && !len_ok) report(a.status, MSGL_DEVERR_LENGTH);
+    // a request of a length that cannot be keeps whatever its row names: nothing of it is given away
+    return row_ok ? (len_ok ? (int)need : a.table_width) : 0;
+}
+
+struct Batch {
+    int32_t row[kBatch], pages[kBatch], unit[kBatch], warp[kWarps];
+};
+
+// The table entries of a row from column c0 on, kPerLane to a lane.
+struct Unit {
+    int row, c0, n;
+    int32_t id[kPerLane];
+    __device__ __forceinline__ void load(const PageMapArgs &a) {
+        const int col = c0 + (int)(threadIdx.x & 31);
+        const int64_t at = (int64_t)row * a.table_stride + col;
+#pragma unroll
+        for (int k = 0; k < kPerLane; ++k)
+            if (col + 32 * k < n) id[k] = a.table[at + 32 * k];
+    }
+    __device__ __forceinline__ bool has(int k) const { return c0 + (int)(threadIdx.x & 31) + 32 * k < n; }
+    __device__ __forceinline__ int64_t place(const PageMapArgs &a, int k) const {   // in the output
+        return (int64_t)row * a.out_stride + c0 + (int)(threadIdx.x & 31) + 32 * k;
+    }
+};
+
+// f(unit) for all table entries of the requests, over all warps of the grid's first
+// `blocks` blocks; ready(), once, by every thread (one without
+// entries too: the grid's end then says that the grid before has ended), in front of the first f, but behind the
+// first loads.  Where a warp gets a few units even if every row were full, it looks its requests up
+// itself; else the rows' units are counted first and dealt out evenly.
+template <class R, class F>
+__device__ __forceinline__ void for_entries(const PageMapArgs &a, Batch &s, int blocks, bool tell, R ready, F f) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int first = cluster_rank() * kWarps + warp;
-    for (int b0 = 0; b0 < a.num_reqs; b0 += kThreads) {
+    const int first = blockIdx.x * kWarps + warp, warps = blocks * kWarps;
+    const int chunks = max(1, (a.table_width + kUnit - 1) / kUnit);
+    Unit x;
+    x.n = 0;
+    if ((int64_t)a.num_reqs * chunks <= 2 * warps) {
+        auto look = [&](int u) {
+            const int b = u / chunks;
+            x.c0 = (u - b * chunks) * kUnit;
+            x.n = u < a.num_reqs * chunks ? entries_of(a, b, tell && x.c0 == 0 && lane == 0, x.row) : 0;
+            x.load(a);
+        };
+        look(first);
+        ready();
+        f(x);
+        for (int u = first + warps; u < a.num_reqs * chunks; u += warps) {
+            look(u);
+            f(x);
+        }
+        return;
+    }
+    for (int b0 = 0; b0 < a.num_reqs; b0 += kBatch) {
         const int b = b0 + threadIdx.x;
         int row = -1, pages = 0;
-        if (b < a.num_reqs) {
-            row = a.req_rows ? __ldg(a.req_rows + b) : b;
-            const int len = __ldg(a.lens + b);
-            const int64_t need = ((int64_t)len + (1 << a.log2_ps) - 1) >> a.log2_ps;
-            const bool row_ok = row >= 0 && row < a.num_rows, len_ok = len >= 0 && need <= a.table_width;
-            // a request of a length that cannot be keeps whatever its row names: nothing of it is given away
-            pages = row_ok ? (len_ok ? (int)need : a.table_width) : 0;
-            if (tell && row != -1 && !row_ok) report(a.status, MSGL_DEVERR_ROW);
-            if (tell && row_ok && !len_ok) report(a.status, MSGL_DEVERR_LENGTH);
-        }
+        if (b < a.num_reqs) pages = entries_of(a, b, tell && blockIdx.x == 0, row);
         const uint32_t units = (pages + kUnit - 1) / kUnit, upto = warp_scan(units);
         __syncthreads();                                       // the batch before is done with
-        if (lane == 31) s.warp[0][warp] = upto;
+        if (lane == 31) s.warp[warp] = upto;
         s.row[threadIdx.x] = row;
         s.pages[threadIdx.x] = pages;
         __syncthreads();
-        if (warp == 0) s.warp[1][lane] = warp_scan(s.warp[0][lane]);
+        const uint32_t all = warp_scan(lane < kWarps ? s.warp[lane] : 0);
+        const uint32_t before = __shfl_sync(0xffffffffu, all, (warp + 31) & 31);
+        s.unit[threadIdx.x] = (warp ? before : 0) + upto;      // units up to and with this request
+        const int total = __shfl_sync(0xffffffffu, all, 31);
         __syncthreads();
-        s.unit[threadIdx.x] = (warp ? s.warp[1][warp - 1] : 0) + upto;   // units up to and with this request
-        const int total = s.warp[1][kWarps - 1];
-        __syncthreads();
-        for (int u = first; u < total; u += kCluster * kWarps) {
+        auto look = [&](int u) {
             int lo = 0;                                        // the first request whose units pass u
 #pragma unroll
-            for (int step = kThreads / 2; step > 0; step >>= 1)
+            for (int step = kBatch / 2; step > 0; step >>= 1)
                 if (s.unit[lo + step - 1] <= u) lo += step;
-            const int col = (u - (lo ? s.unit[lo - 1] : 0)) * kUnit + lane, n = s.pages[lo];
-            const int64_t at = (int64_t)s.row[lo] * a.table_stride + col;
-            int32_t id[kPerLane];
-#pragma unroll
-            for (int k = 0; k < kPerLane; ++k)
-                if (col + 32 * k < n) id[k] = a.table[at + 32 * k];
-#pragma unroll
-            for (int k = 0; k < kPerLane; ++k)
-                if (col + 32 * k < n) f(id[k], (int64_t)s.row[lo] * a.out_stride + col + 32 * k);
+            x.row = s.row[lo];
+            x.c0 = (u - (lo ? s.unit[lo - 1] : 0)) * kUnit;
+            x.n = u < total ? s.pages[lo] : 0;
+            x.load(a);
+        };
+        look(first);
+        if (b0 == 0) ready();
+        f(x);
+        for (int u = first + warps; u < total; u += warps) {
+            look(u);
+            f(x);
         }
     }
 }
 
-// Bits of 32 pages from p0 on that something beside the requests holds.
+// -------------------------------------------------------------- the bitmaps
+
+// Bits of 32 pages from p0 on (a multiple of 32) that something beside the requests holds.
 __device__ __forceinline__ uint32_t held_word(const PageMapArgs &a, int64_t p0) {
-    if (!a.held) return 0;
     uint32_t bits = 0;
-    for (int i = 0; i < 32; ++i)
-        if (p0 + i < a.num_pages && __ldg(a.held + p0 + i)) bits |= 1u << i;
+    if (!a.held) return 0;
+    if (p0 + 32 <= a.num_pages && (reinterpret_cast<uintptr_t>(a.held) & 15) == 0) {
+        const uint4 *h = reinterpret_cast<const uint4 *>(a.held + p0);
+        const uint4 x = __ldg(h), y = __ldg(h + 1);
+        const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) bits |= ((__vcmpne4(w[i], 0) & 0x08040201u) * 0x01010101u >> 24) << (4 * i);
+        return bits;
+    }
+    for (int i = 0; i < 32 && p0 + i < a.num_pages; ++i)
+        if (__ldg(a.held + p0 + i)) bits |= 1u << i;
     return bits;
 }
 
-// Marks the pages [p0, p0 + 32 * kCluster * slice) that the requests hold, and leaves this block's slice of
-// them, joined, in bits[rank * slice ..].
-__device__ __forceinline__ void mark(const PageMapArgs &a, Shared &s, uint32_t *bits, int slice, int64_t p0, bool tell) {
-    for (int i = threadIdx.x; i < kCluster * slice; i += kThreads) bits[i] = 0;
+// Words of the bitmap: whole 16-byte vectors.
+__host__ __device__ __forceinline__ int64_t words_of(int32_t num_pages) { return ((int64_t)num_pages + 127) / 128 * 4; }
+
+// stays = the pages that `held` names and the bits behind the last page, which nothing moves or gives away; used
+// begins as the same.
+__global__ void __launch_bounds__(256) begin_kernel(const PageMapArgs a) {
+    let_next_start();
+    const int64_t w = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (w >= words_of(a.num_pages)) return;
+    const int64_t left = a.num_pages - 32 * w;
+    const uint32_t bits = held_word(a, 32 * w) | (left >= 32 ? 0u : left > 0 ? 0xffffffffu << left : 0xffffffffu);
+    a.used_bits[w] = bits;
+    if (a.stay_bits) a.stay_bits[w] = bits;
+}
+
+__global__ void __launch_bounds__(kThreads) mark_kernel(const PageMapArgs a) {
+    __shared__ Batch s;
+    let_next_start();
+    for_entries(a, s, gridDim.x, true, [] { wait_for_last(); }, [&](const Unit &x) {
+        bool bad = false;
+#pragma unroll
+        for (int k = 0; k < kPerLane; ++k) {
+            if (!x.has(k)) continue;
+            const int32_t id = x.id[k];
+            if (id >= 0 && id < a.num_pages) atomicOr(a.used_bits + (id >> 5), 1u << (id & 31));
+            else bad = true;
+        }
+        if (bad) report(a.status, MSGL_DEVERR_PAGE_RANGE);
+    });
+}
+
+// ----------------------------------------------------------------- the lists
+
+// Sums over the whole block of up to three numbers; every thread gets them.  Not called twice without a barrier
+// of the caller's between.
+template <int N>
+__device__ __forceinline__ void block_sums(uint32_t (&x)[N], uint32_t (*part)[kListWarps]) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = __reduce_add_sync(0xffffffffu, x[i]);
+    if (lane == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i) part[i][warp] = x[i];
     __syncthreads();
-    for_entries(a, s, tell, [&](int32_t id, int64_t) {
-        if (id < 0 || id >= a.num_pages) {
-            if (tell) report(a.status, MSGL_DEVERR_PAGE_RANGE);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = __reduce_add_sync(0xffffffffu, lane < kListWarps ? part[i][lane] : 0);
+}
+
+// f(first word, four words of x, four of y) for all vectors of one or two bitmaps, by the whole block, 4 of a thread's
+// loads of each at a time (y: zeros where it is not given).
+template <bool kBoth, class F>
+__device__ __forceinline__ void for_words(const uint32_t *x, const uint32_t *y, int64_t words, F f) {
+    constexpr int kLoads = 4;
+    for (int64_t v0 = threadIdx.x; v0 < words / 4; v0 += kLoads * kListThreads) {
+        uint4 r[kLoads], s[kLoads];
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int64_t v = v0 + i * kListThreads;
+            s[i] = make_uint4(0, 0, 0, 0);
+            if (v >= words / 4) continue;
+            r[i] = __ldcg(reinterpret_cast<const uint4 *>(x) + v);
+            if (kBoth) s[i] = __ldcg(reinterpret_cast<const uint4 *>(y) + v);
+        }
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            if (v0 + i * kListThreads < words / 4) f(4 * (v0 + i * kListThreads), r[i], s[i]);
+    }
+}
+
+__device__ __forceinline__ uint32_t ones(const uint4 &x) { return __popc(x.x) + __popc(x.y) + __popc(x.z) + __popc(x.w); }
+
+// out[place + i] = the i-th page of a word's set bits; most: entries from there on are not written.
+__device__ __forceinline__ void write_bits(uint32_t word, int64_t page, uint32_t place, int32_t *out, uint32_t most) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t to = place + __popc(word & ((1u << lane) - 1));
+    if (word >> lane & 1 && to < most) out[to] = (int32_t)(page + lane);
+}
+
+// -1 in out[from, to), by all threads of the grid.
+__device__ __forceinline__ void fill(int32_t *out, int64_t from, int64_t to) {
+    const int64_t me = (int64_t)blockIdx.x * kListThreads + threadIdx.x, all = (int64_t)gridDim.x * kListThreads;
+    const int64_t head = min(to, from + (-((reinterpret_cast<uintptr_t>(out) >> 2) + (uint64_t)from) & 3));
+    const int64_t quads = (to - head) / 4, tail = head + 4 * quads;
+    if (me < head - from) out[from + me] = -1;
+    if (me < to - tail) out[tail + me] = -1;
+    for (int64_t i = me; i < quads; i += all) *reinterpret_cast<int4 *>(out + head + 4 * i) = make_int4(-1, -1, -1, -1);
+}
+
+// A block's share of the words.  It goes over them 32 at a time: every warp looks at all 32, a lane each, so that
+// all know where each word's pages go without a word between them, and writes one of them.
+struct Share {
+    int64_t w0, w1, words;
+};
+__device__ __forceinline__ Share share_of(const PageMapArgs &a) {
+    Share s;
+    s.words = words_of(a.num_pages);
+    const int64_t each = ((s.words + gridDim.x - 1) / gridDim.x + 31) / 32 * 32;
+    s.w0 = min((int64_t)blockIdx.x * each, s.words);
+    s.w1 = min(s.w0 + each, s.words);
+    return s;
+}
+static_assert(kListWarps == 32, "a word for each warp");
+
+__global__ void __launch_bounds__(kListThreads) free_list_kernel(const PageMapArgs a) {
+    __shared__ uint32_t part[2][kListWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Share s = share_of(a);
+    wait_for_last();
+    uint32_t n[2] = {0, 0};                                       // free pages before the share, and all
+    for_words<false>(a.used_bits, nullptr, s.words, [&](int64_t w, const uint4 &x, const uint4 &) {
+        const uint32_t free = 128 - ones(x);
+        n[1] += free;
+        if (w < s.w0) n[0] += free;
+    });
+    uint32_t word = s.w0 + lane < s.w1 ? ~__ldcg(a.used_bits + s.w0 + lane) : 0;
+    block_sums(n, part);
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.count_out[0] = (int32_t)n[1];
+    uint32_t place = n[0];
+    for (int64_t w0 = s.w0; w0 < s.w1; w0 += 32) {
+        const uint32_t next = w0 + 32 + lane < s.w1 ? ~__ldcg(a.used_bits + w0 + 32 + lane) : 0;
+        const uint32_t mine = __popc(word), upto = warp_scan(mine);
+        write_bits(__shfl_sync(0xffffffffu, word, warp), 32 * (w0 + warp),
+                   place + __shfl_sync(0xffffffffu, upto - mine, warp), a.pages_out, 0xffffffffu);
+        place += __shfl_sync(0xffffffffu, upto, 31);
+        word = next;
+    }
+    fill(a.pages_out, n[1], a.num_pages);
+}
+
+// The pages of word w in front of page `used`.
+__device__ __forceinline__ uint32_t below(uint32_t used, int64_t w) {
+    const int64_t left = (int64_t)used - 32 * w;
+    return left >= 32 ? 0xffffffffu : left > 0 ? (1u << left) - 1 : 0;
+}
+
+// The moves: the movable pages from page `used` on go to the free pages in front of it, both in order.  Leaves for
+// every word the number of moves before it.
+__global__ void __launch_bounds__(kListThreads) moves_kernel(const PageMapArgs a) {
+    __shared__ uint32_t part[3][kListWarps];
+    let_next_start();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Share s = share_of(a);
+    wait_for_last();
+    uint32_t n[1] = {0};
+    for_words<false>(a.used_bits, nullptr, s.words, [&](int64_t, const uint4 &x, const uint4 &) { n[0] += ones(x); });
+    block_sums(n, part);
+    const uint32_t used = n[0] - (uint32_t)(32 * s.words - a.num_pages);
+    uint32_t m[3] = {0, 0, 0};                                    // moves before the share, holes before it, all moves
+    __syncthreads();
+    for_words<true>(a.used_bits, a.stay_bits, s.words, [&](int64_t w, const uint4 &x, const uint4 &y) {
+        if (32 * (w + 4) <= used) {
+            if (w < s.w0) m[1] += 128 - ones(x);
             return;
         }
-        const int64_t at = id - p0;
-        if (at >= 0 && at < 32ll * kCluster * slice) atomicOr(bits + (at >> 5), 1u << (at & 31));
+        const uint32_t u[4] = {x.x, x.y, x.z, x.w}, stays[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t front = below(used, w + i), moves = __popc(u[i] & ~stays[i] & ~front);
+            m[2] += moves;
+            if (w < s.w0) {
+                m[0] += moves;
+                m[1] += __popc(~u[i] & front);
+            }
+        }
     });
-    cluster_sync();
-    const int rank = cluster_rank();
-    for (int i = threadIdx.x; i < slice; i += kThreads) {
-        uint32_t *mine = bits + rank * slice + i, v = *mine;
-#pragma unroll
-        for (int k = 1; k < kCluster; ++k) v |= ld_peer(peer(mine, (rank + k) % kCluster));
-        *mine = v;
-    }
-    __syncthreads();
-}
-
-// Sums of x and y over the block's warps before this one and over the blocks before this one; every block's
-// totals.  which: two exchanges in a row use different places.
-struct Places {
-    uint32_t x, y, all_x, all_y;
-};
-__device__ __forceinline__ Places exchange(Shared &s, uint32_t x, uint32_t y, int which) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = cluster_rank();
-    if (lane == 0) {
-        s.warp[0][warp] = x;
-        s.warp[1][warp] = y;
-    }
-    __syncthreads();
-    const uint32_t wx = s.warp[0][lane], wy = s.warp[1][lane];
-    Places p;
-    p.x = __reduce_add_sync(0xffffffffu, lane < warp ? wx : 0);
-    p.y = __reduce_add_sync(0xffffffffu, lane < warp ? wy : 0);
-    if (warp == 0) {
-        const uint32_t bx = __reduce_add_sync(0xffffffffu, wx), by = __reduce_add_sync(0xffffffffu, wy);
-        if (lane < kCluster) {
-            st_peer(peer(&s.counts[which][0][rank], lane), bx);
-            st_peer(peer(&s.counts[which][1][rank], lane), by);
-        }
-    }
-    cluster_sync();
-    p.all_x = p.all_y = 0;
-#pragma unroll
-    for (int k = 0; k < kCluster; ++k) {
-        const uint32_t bx = s.counts[which][0][k], by = s.counts[which][1][k];
-        if (k < rank) {
-            p.x += bx;
-            p.y += by;
-        }
-        p.all_x += bx;
-        p.all_y += by;
-    }
-    return p;
-}
-
-// out[place + i] = the i-th page of the word's set bits, for the 32 words that a warp's lanes hold; most: entries
-// from there on are not written.  Returns the place behind them.
-__device__ __forceinline__ uint32_t write_bits(uint32_t word, int64_t page, uint32_t place, int32_t *out, uint32_t most) {
-    const int lane = threadIdx.x & 31;
-    const uint32_t n = __popc(word), upto = warp_scan(n);
-#pragma unroll 4
-    for (int i = 0; i < 32; ++i) {
-        const uint32_t w = __shfl_sync(0xffffffffu, word, i), at = place + __shfl_sync(0xffffffffu, upto - n, i);
-        const uint32_t to = at + __popc(w & ((1u << lane) - 1));
-        if (w >> lane & 1 && to < most) out[to] = (int32_t)(page + 32 * i + lane);
-    }
-    return place + __shfl_sync(0xffffffffu, upto, 31);
-}
-
-__device__ __forceinline__ void fill(int32_t *out, int64_t from, int64_t to) {
-    for (int64_t i = from + (int64_t)cluster_rank() * kThreads + threadIdx.x; i < to; i += kCluster * kThreads) out[i] = -1;
-}
-
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) free_pages_kernel(const PageMapArgs a, int slice) {
-    extern __shared__ uint32_t bits[];
-    __shared__ Shared s;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = cluster_rank();
-    const int run = ((slice + kWarps - 1) / kWarps + 31) / 32 * 32;   // words of a warp
-    uint32_t before = 0;
-    int round = 0;
-    for (int64_t p0 = 0; p0 < a.num_pages; p0 += 32ll * kCluster * slice, ++round) {
-        mark(a, s, bits, slice, p0, round == 0);
-        uint32_t *mine = bits + rank * slice;
-        const int w0 = min(warp * run, slice), w1 = min(w0 + run, slice);
-        uint32_t n = 0;
-        for (int w = w0 + lane; w < w1; w += 32) {
-            const int64_t page = p0 + 32ll * (rank * slice + w), left = a.num_pages - page;
-            const uint32_t inside = left >= 32 ? 0xffffffffu : left > 0 ? (1u << left) - 1 : 0;
-            const uint32_t free = ~(mine[w] | held_word(a, page)) & inside;
-            mine[w] = free;
-            n += __popc(free);
-        }
-        const Places p = exchange(s, __reduce_add_sync(0xffffffffu, n), 0, round & 1);
-        uint32_t place = before + p.x;
-        for (int w = w0; w < w1; w += 32) {
-            const uint32_t word = w + lane < w1 ? mine[w + lane] : 0;
-            place = write_bits(word, p0 + 32ll * (rank * slice + w), place, a.pages_out, 0xffffffffu);
-        }
-        before += p.all_x;
-        // (the next round clears bitmaps that a slower block may still be reading)
-        cluster_sync();
-    }
-    fill(a.pages_out, before, a.num_pages);
-    if (rank == 0 && threadIdx.x == 0) a.count_out[0] = (int32_t)before;
-}
-
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
-    compact_pages_kernel(const PageMapArgs a, int slice) {
-    extern __shared__ uint32_t bits[];
-    __shared__ Shared s;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = cluster_rank();
-    uint32_t *stays = bits + kCluster * slice;                       // this block's slice: in use but not movable
-    mark(a, s, bits, slice, 0, true);
-    uint32_t *mine = bits + rank * slice;
-    const int run = ((slice + kWarps - 1) / kWarps + 31) / 32 * 32;
-    const int w0 = min(warp * run, slice), w1 = min(w0 + run, slice);
-    uint32_t n = 0;
-    for (int w = w0 + lane; w < w1; w += 32) {
-        stays[w] = held_word(a, 32ll * (rank * slice + w));
-        n += __popc(mine[w] | stays[w]);
-    }
-    const uint32_t used = exchange(s, __reduce_add_sync(0xffffffffu, n), 0, 0).all_x;
-    // the pages behind the first `used` ones go to the free pages among those, both in order
-    auto below = [&](int w) -> uint32_t {                            // the word's pages in front of page `used`
-        const int64_t left = (int64_t)used - 32ll * (rank * slice + w);
-        return left >= 32 ? 0xffffffffu : left > 0 ? (1u << left) - 1 : 0;
-    };
-    auto holes = [&](int w) { return w < w1 ? ~(mine[w] | stays[w]) & below(w) : 0; };
-    auto moves = [&](int w) { return w < w1 ? mine[w] & ~stays[w] & ~below(w) : 0; };
-    uint32_t from = 0, to = 0;
-    for (int w = w0 + lane; w < w1; w += 32) {
-        from += __popc(moves(w));
-        to += __popc(holes(w));
-    }
-    const Places p = exchange(s, __reduce_add_sync(0xffffffffu, from), __reduce_add_sync(0xffffffffu, to), 1);
-    uint32_t src = p.x, dst = p.y;
-    for (int w = w0; w < w1; w += 32) {
-        const int64_t page = 32ll * (rank * slice + w);
-        src = write_bits(moves(w + lane), page, src, a.src, p.all_x);
-        dst = write_bits(holes(w + lane), page, dst, a.dst, p.all_x);
-        const uint32_t all = w + lane < w1 ? mine[w + lane] | stays[w + lane] : 0, go = moves(w + lane);
-        for (int i = 0; i < 32 && w + i < w1; ++i) {
-            const uint32_t u = __shfl_sync(0xffffffffu, all, i), m = __shfl_sync(0xffffffffu, go, i);
-            const int64_t at = page + 32 * i + lane;
-            if (at < a.num_pages && !(m >> lane & 1)) a.pages_out[at] = u >> lane & 1 ? (int32_t)at : -1;
-        }
-    }
-    fill(a.src, p.all_x, a.num_pages / 2);
-    fill(a.dst, p.all_x, a.num_pages / 2);
-    if (rank == 0 && threadIdx.x == 0) {
-        a.count_out[0] = (int32_t)p.all_x;
+    block_sums(m, part);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        a.count_out[0] = (int32_t)m[2];
         a.used_out[0] = (int32_t)used;
     }
-    cluster_sync();
-    for (uint32_t i = rank * kThreads + threadIdx.x; i < p.all_x; i += kCluster * kThreads)
-        a.pages_out[__ldcg(a.src + i)] = __ldcg(a.dst + i);
-    cluster_sync();
-    // A page that did not move keeps its id, and so does one that this loop has already renamed (a row that is
-    // named twice): its new id was free, so the map says -1 there.
-    for_entries(a, s, false, [&](int32_t id, int64_t at) {
-        const int32_t now = id >= (int32_t)used && id < a.num_pages ? __ldcg(a.pages_out + id) : -1;
-        if (now >= 0) a.table_out[at] = now;
-        else if (a.table_out != a.table) a.table_out[at] = id;
-    });
+    uint32_t from = m[0], to = m[1];
+    for (int64_t w0 = s.w0; w0 < s.w1; w0 += 32) {
+        const int64_t w = w0 + lane;
+        uint32_t u = 0xffffffffu, stays = 0xffffffffu;
+        if (w < s.w1) {
+            u = __ldcg(a.used_bits + w);
+            stays = __ldcg(a.stay_bits + w);
+        }
+        const uint32_t front = below(used, w), moves = u & ~stays & ~front, holes = ~u & front;
+        const uint32_t moved = from + warp_scan(__popc(moves)), filled = to + warp_scan(__popc(holes));
+        if (warp == 0 && w < s.w1) a.moves_before[w] = moved - __popc(moves);
+        const int64_t page = 32 * (w0 + warp) + lane;
+        const uint32_t x = __shfl_sync(0xffffffffu, u, warp), y = __shfl_sync(0xffffffffu, moves, warp),
+                       z = __shfl_sync(0xffffffffu, holes, warp);
+        write_bits(y, page - lane, __shfl_sync(0xffffffffu, moved, warp) - __popc(y), a.src, m[2]);
+        write_bits(z, page - lane, __shfl_sync(0xffffffffu, filled, warp) - __popc(z), a.dst, m[2]);
+        if (page < a.num_pages && w0 + warp < s.w1 && !(y >> lane & 1)) a.pages_out[page] = x >> lane & 1 ? (int32_t)page : -1;
+        from = __shfl_sync(0xffffffffu, moved, 31);
+        to = __shfl_sync(0xffffffffu, filled, 31);
+    }
+    fill(a.src, m[2], a.num_pages / 2);
+    fill(a.dst, m[2], a.num_pages / 2);
 }
 
-// Bitmaps of at most this many words, 8 slices.
-constexpr int kMostWords = kMaxMapPages / 32;
-static_assert(kMostWords % (32 * kCluster) == 0, "slices of whole 32-word groups");
+// The new ids: of all pages in the requests' tables (the first entry_blocks blocks), and of those that move in the
+// map (the others).
+__global__ void __launch_bounds__(kThreads) rename_kernel(const PageMapArgs a, int entry_blocks) {
+    __shared__ Batch s;
+    if (blockIdx.x >= entry_blocks) {
+        wait_for_last();
+        const int moves = __ldcg(a.count_out), blocks = gridDim.x - entry_blocks;
+        for (int64_t i = (int64_t)(blockIdx.x - entry_blocks) * kThreads + threadIdx.x; i < moves; i += (int64_t)blocks * kThreads)
+            a.pages_out[__ldcg(a.src + i)] = __ldcg(a.dst + i);
+        return;
+    }
+    int32_t used = 0;
+    for_entries(
+        a, s, entry_blocks, false,
+        [&] {
+            wait_for_last();
+            used = __ldcg(a.used_out);
+        },
+        [&](const Unit &x) {
+            // (an id that was given out here, in a row that is named twice, is in front of page `used` and stays)
+            int32_t to[kPerLane];                              // the move's number, -1: none
+#pragma unroll
+            for (int k = 0; k < kPerLane; ++k) {
+                const int32_t id = x.has(k) ? x.id[k] : -1;
+                const bool may = id >= used && id >= 0 && id < a.num_pages;
+                const int w = may ? id >> 5 : 0;
+                const uint32_t bit = 1u << (id & 31);
+                const uint32_t moves = may ? __ldcg(a.used_bits + w) & ~__ldcg(a.stay_bits + w) : 0;
+                const uint32_t before = may ? __ldcg(a.moves_before + w) : 0;
+                to[k] = moves & bit ? (int32_t)(before + __popc(moves & (bit - 1) & ~below(used, w))) : -1;
+            }
+#pragma unroll
+            for (int k = 0; k < kPerLane; ++k)
+                if (to[k] >= 0) to[k] = __ldcg(a.dst + to[k]);
+#pragma unroll
+            for (int k = 0; k < kPerLane; ++k)
+                if (x.has(k) && (to[k] >= 0 || a.table_out != a.table)) a.table_out[x.place(a, k)] = to[k] >= 0 ? to[k] : x.id[k];
+        });
+}
 
-template <class K>
-cudaError_t launch_map(K kernel, const PageMapArgs &a, bool with_stays, cudaStream_t stream) {
-    const int64_t words = ((int64_t)a.num_pages + 31) / 32;
-    const int64_t most = words < kMostWords ? words : kMostWords;
-    const int slice = (int)((most + kCluster - 1) / kCluster);
-    const size_t bytes = ((size_t)kCluster + with_stays) * slice * 4;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)((kCluster + 1) * (size_t)(kMostWords / kCluster) * 4));
-    if (e != cudaSuccess) return e;
-    kernel<<<kCluster, kThreads, bytes, stream>>>(a, slice);
-    return cudaGetLastError();
+template <class... A>
+cudaError_t launch_after(void (*kernel)(A...), int blocks, int threads, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Sets and marks the bitmaps; entry_blocks: for the kernels that go over the table entries.
+cudaError_t launch_marks(const PageMapArgs &a, int entry_blocks, cudaStream_t stream) {
+    begin_kernel<<<(unsigned)(words_of(a.num_pages) / 256 + 1), 256, 0, stream>>>(a);
+    cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? launch_after(mark_kernel, entry_blocks, kThreads, stream, a) : e;
+}
+
+// A block for every kWarps units that full rows would have, at most two an SM.
+int entry_blocks(const PageMapArgs &a) {
+    const int64_t chunks = a.table_width > 0 ? (a.table_width + kUnit - 1) / kUnit : 1;
+    const int64_t want = ((int64_t)a.num_reqs * chunks + kWarps - 1) / kWarps, most = 2 * sm_count();
+    return (int)(want < 1 ? 1 : want < most ? want : most);
+}
+
+// A block for every 32 words, at most one an SM.
+int list_blocks(const PageMapArgs &a) {
+    const int64_t want = (words_of(a.num_pages) + 31) / 32;
+    return (int)(want < 1 ? 1 : want < sm_count() ? want : sm_count());
+}
+
+// A thread for every four moves that there may be, at most a block an SM.
+int move_blocks(const PageMapArgs &a) {
+    const int64_t want = a.num_pages / 2 / (4 * kThreads) + 1;
+    return (int)(want < sm_count() ? want : sm_count());
 }
 
 }  // namespace
 
-cudaError_t launch_free_pages(const PageMapArgs &a, cudaStream_t stream) {
-    return launch_map(free_pages_kernel, a, false, stream);
+size_t page_map_workspace_bytes(int32_t num_pages) {
+    return ((size_t)words_of(num_pages) * 4 * 3 + 255) / 256 * 256;
 }
 
-cudaError_t launch_compact_pages(const PageMapArgs &a, cudaStream_t stream) {
-    return launch_map(compact_pages_kernel, a, true, stream);
+static void set_workspace(PageMapArgs &a, void *workspace, bool compact) {
+    a.used_bits = static_cast<uint32_t *>(workspace);
+    a.stay_bits = compact ? a.used_bits + words_of(a.num_pages) : nullptr;
+    a.moves_before = compact ? a.stay_bits + words_of(a.num_pages) : nullptr;
+}
+
+cudaError_t launch_free_pages(PageMapArgs a, void *workspace, cudaStream_t stream) {
+    set_workspace(a, workspace, false);
+    cudaError_t e = launch_marks(a, entry_blocks(a), stream);
+    return e == cudaSuccess ? launch_after(free_list_kernel, list_blocks(a), kListThreads, stream, a) : e;
+}
+
+cudaError_t launch_compact_pages(PageMapArgs a, void *workspace, cudaStream_t stream) {
+    set_workspace(a, workspace, true);
+    const int blocks = entry_blocks(a);
+    cudaError_t e = launch_marks(a, blocks, stream);
+    if (e == cudaSuccess) e = launch_after(moves_kernel, list_blocks(a), kListThreads, stream, a);
+    return e == cudaSuccess ? launch_after(rename_kernel, blocks + move_blocks(a), kThreads, stream, a, blocks) : e;
 }
 
 }  // namespace msgl

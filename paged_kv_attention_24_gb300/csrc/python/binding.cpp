@@ -39,7 +39,7 @@ const at::Tensor &checked(PyObject *o, const char *name, at::ScalarType type, in
     const at::Tensor &t = tensor(o, name);
     if (!t.is_cuda()) refuse("%s must be a CUDA tensor", name);
     if (t.scalar_type() != type)
-        refuse("%s must be torch.%s", name, type == at::kInt ? "int32" : type == at::kFloat ? "float32" : "bfloat16");
+        refuse("%s must be torch.%s", name, type == at::kInt ? "int32" : type == at::kLong ? "int64" : type == at::kFloat ? "float32" : "bfloat16");
     if (dev < 0) dev = t.get_device();
     if (t.get_device() != dev) refuse("%s must be on the same CUDA device as the other tensors", name);
     if (!t.is_contiguous()) refuse("%s must be contiguous", name);
@@ -405,7 +405,9 @@ PyObject *rope_store_kv(PyObject *, PyObject *const *a, Py_ssize_t n) {
         msgl_rope rope{};
         rope.num_pairs = size32(PyBytes_Check(a[9]) ? PyBytes_GET_SIZE(a[9]) : -1, "axes");
         rope.axes = reinterpret_cast<const uint8_t *>(bytes_of(a[9], "axes", rope.num_pairs));
-        rope.turns = reinterpret_cast<const uint64_t *>(bytes_of(a[8], "turns", 8 * (Py_ssize_t)rope.num_pairs));
+        const at::Tensor &turns = checked(a[8], "rope.turns", at::kLong, dev);
+        if (turns.numel() != rope.num_pairs) refuse("%s must have an entry for each of rope.axes", "rope.turns");
+        rope.turns = static_cast<const uint64_t *>(turns.data_ptr());
         rope.num_axes = pos.dim() == 2 ? size32(pos.size(0), "positions") : 1;
         rope.adjacent = (int32_t)integer(a[10]);
         rope.factor = (float)number(a[11]);
@@ -643,6 +645,32 @@ PyObject *copy_pages(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// The workspace that the caller brings, or scratch in `stream`'s order for the length of a call (its next user on
+// the stream comes behind the call's kernels).
+struct Workspace {
+    void *p = nullptr, *own = nullptr;
+    size_t bytes = 0;
+    bool brought = false;
+    Workspace(PyObject *o, int dev) {
+        if (o == Py_None) return;
+        const at::Tensor &t = tensor(o, "workspace");
+        if (!t.is_cuda() || t.get_device() != dev || !t.is_contiguous())
+            refuse("%s must be contiguous and on the other tensors' device", "workspace");
+        p = t.data_ptr();
+        bytes = t.nbytes();
+        brought = true;
+    }
+    Workspace(const Workspace &) = delete;
+    void need(size_t n, const c10::cuda::CUDAStream &stream) {
+        if (brought || !n) return;
+        p = own = c10::cuda::CUDACachingAllocator::raw_alloc_with_stream(n, stream.stream());
+        bytes = n;
+    }
+    ~Workspace() {
+        if (own) c10::cuda::CUDACachingAllocator::raw_delete(own);
+    }
+};
+
 // The arguments that free_pages and compact_pages begin with: (req_table, lens, num_slots, page_size, req_rows | None,
 // held | None).
 struct PageMap {
@@ -676,16 +704,17 @@ PageMap page_map(PyObject *const *a, int &dev) {
     return m;
 }
 
-// (.. , pages | None, num_free | None, status | None, stream | None) -> (pages, num_free), None when they were given,
+// (.. , pages | None, num_free | None, workspace | None, status | None, stream | None) -> (pages, num_free), None when they were given,
 // or the status
 PyObject *free_pages(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (!arity(n, 10)) return nullptr;
+    if (!arity(n, 11)) return nullptr;
     return guarded([&]() -> PyObject * {
         int dev = -1;
         const PageMap m = page_map(a, dev);
-        uint32_t *status = status_ptr(a[8], dev);
+        uint32_t *status = status_ptr(a[9], dev);
         c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
-        const c10::cuda::CUDAStream stream = stream_of(a[9], dev);
+        const c10::cuda::CUDAStream stream = stream_of(a[10], dev);
+        Workspace ws(a[8], dev);
         at::Tensor pages, count;
         const bool given = a[6] != Py_None;
         if (given) {
@@ -700,8 +729,9 @@ PyObject *free_pages(PyObject *, PyObject *const *a, Py_ssize_t n) {
                 pages = fresh({m.pages}, at::kInt, dev, stream);
                 count = fresh({1}, at::kInt, dev, stream);
             }
+            ws.need(msgl_page_map_workspace_size(m.slots, m.ps), stream);
             rc = msgl_free_pages(m.slots, m.ps, m.table.at, m.table.rows, m.table.width, m.table.width, m.rows, m.lens,
-                                 m.reqs, m.held, i32(pages), i32(count), status, raw(stream));
+                                 m.reqs, m.held, i32(pages), i32(count), ws.p, ws.bytes, status, raw(stream));
         }
         if (rc != MSGL_OK) return done(rc);
         if (given) Py_RETURN_NONE;
@@ -709,18 +739,19 @@ PyObject *free_pages(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// (.. , table_out, remap | None, src | None, dst | None, num_moves | None, num_used | None, status | None,
-//  stream | None) -> (remap, src, dst, num_moves, num_used), None when they were given, or the status
+// (.. , table_out, remap | None, src | None, dst | None, num_moves | None, num_used | None, workspace | None,
+//  status | None, stream | None) -> (remap, src, dst, num_moves, num_used), None when they were given, or the status
 PyObject *compact_pages(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (!arity(n, 14)) return nullptr;
+    if (!arity(n, 15)) return nullptr;
     return guarded([&]() -> PyObject * {
         int dev = -1;
         const PageMap m = page_map(a, dev);
         const Table to = table_of(a[6], "out.page_table", dev);
         if (to.rows != m.table.rows || to.width != m.table.width) refuse("%s must have req_table's size", "out.page_table");
-        uint32_t *status = status_ptr(a[12], dev);
+        uint32_t *status = status_ptr(a[13], dev);
         c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
-        const c10::cuda::CUDAStream stream = stream_of(a[13], dev);
+        const c10::cuda::CUDAStream stream = stream_of(a[14], dev);
+        Workspace ws(a[12], dev);
         at::Tensor remap, src, dst, moves, used;
         const bool given = a[7] != Py_None;
         if (given) {
@@ -753,8 +784,9 @@ PyObject *compact_pages(PyObject *, PyObject *const *a, Py_ssize_t n) {
             out.dst = i32(dst);
             out.num_moves = i32(moves);
             out.num_used = i32(used);
+            ws.need(msgl_page_map_workspace_size(m.slots, m.ps), stream);
             rc = msgl_compact_pages(m.slots, m.ps, m.table.at, m.table.rows, m.table.width, m.table.width, m.rows, m.lens,
-                                    m.reqs, m.held, &out, status, raw(stream));
+                                    m.reqs, m.held, &out, ws.p, ws.bytes, status, raw(stream));
         }
         if (rc != MSGL_OK) return done(rc);
         if (given) Py_RETURN_NONE;

@@ -13,145 +13,232 @@
 // position; its upper 32 bits go through sincospif (an error of 2^-25 of the angle).
 // Everything is in 32 bits up to the one rounding to bf16.
 //
-// Bound by HBM for many tokens, by latency for few.  One block per token: a thread's
-// loads of its heads are issued first, the angles are computed once a token under
-// them, and 8 lanes hold a head so that both halves of every pair are in one lane.
+// Bound by HBM for many tokens, by latency for few.  A warp takes a token, or a part
+// of its heads where tokens are few, 4 heads a turn: 8 lanes hold a head, so that
+// both halves of every pair are in one lane, and a lane's part of the rotation
+// (the weights of the norm multiplied in) stays in its registers from head to head.
+// No block-wide wait: a block of 8 warps that shared the angles of its tokens through
+// shared memory, and read cosines, sines and weights again for every head, issued
+// 370 instructions a turn and was bound by them (8256 tokens of 64/8 heads: 70 us).
 #include "kernels.h"
 
 namespace msgl {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128, kWarps = kThreads / 32;
 constexpr int kLanes = 8;                          // lanes of a head: two 16-byte chunks each
-constexpr int kHeadsPerPass = kThreads / kLanes;
-constexpr int kUnroll = 3;                         // passes whose loads are issued together
+constexpr int kHeads = 32 / kLanes;                // heads of a warp's turn
+constexpr int kAhead = 6;                          // turns whose heads are on their way
+constexpr int kBlocks = 5;                         // blocks an SM
 
-__device__ __forceinline__ void unpack8(const uint4 &r, float (&x)[8]) {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = bf16_lo(w[i]);
-        x[2 * i + 1] = bf16_hi(w[i]);
-    }
+// Two floats, for the instructions that take both at once.
+struct Two {
+    uint64_t v;
+    __device__ __forceinline__ float lo() const { return __uint_as_float((uint32_t)v); }
+    __device__ __forceinline__ float hi() const { return __uint_as_float((uint32_t)(v >> 32)); }
+};
+__device__ __forceinline__ Two two(uint32_t lo, uint32_t hi) { return Two{(uint64_t)hi << 32 | lo}; }
+__device__ __forceinline__ Two two(float lo, float hi) { return two(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ Two swapped(Two a) { return Two{a.v << 32 | a.v >> 32}; }
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+    Two d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+    Two d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return d;
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+// 8 bf16 as four pairs of floats, and back.
+__device__ __forceinline__ void unpack8(const uint4 &r, Two (&x)[4]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = two(w[i] << 16, w[i] & 0xffff0000u);
+}
+__device__ __forceinline__ uint4 pack8(const Two (&x)[4]) {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&p);
-    }
+    for (int i = 0; i < 4; ++i)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x[i].hi()), "f"(x[i].lo()));
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__global__ void __launch_bounds__(kThreads) rope_store_kernel(const __grid_constant__ RopeStoreArgs a) {
-    __shared__ float cosines[kHeadDim / 2], sines[kHeadDim / 2];
-    const int64_t t = blockIdx.x;
-    const int64_t slot = __ldg(a.out_loc + t);
-    if (slot == -1) return;                        // not a token: a bucket's padding
-    const bool stored = slot >= 0 && slot < a.pool.num_slots;
-    if (!stored && threadIdx.x == 0) report(a.status, MSGL_DEVERR_SLOT_RANGE);
-    const int lane = threadIdx.x % kLanes, head0 = threadIdx.x / kLanes;
+// 16 bytes into the lane's own place in shared memory, past L1 (not the read-only path: q may be turned in place).
+// behind: what was read from that place before, so that the copy is not issued until it has arrived.
+__device__ __forceinline__ void copy16(void *to, const void *from, uint32_t behind) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from),
+                 "r"(behind)
+                 : "memory");
+}
+__device__ __forceinline__ void end_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_group() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// What a lane does to its chunks x and y: x' = x * a + other(x) * b, y' = y * c + other(y) * d, where the
+// other of x is y (and of y x), or, for adjacent pairs, the chunk with its neighbours exchanged.
+struct Rotation {
+    Two a[4], b[4], c[4], d[4];
+};
+
+// kind: 0 for q, 1 for k.
+template <bool kAdjacent>
+__device__ __forceinline__ void rotation_of(const RopeStoreArgs &args, int kind, const float *cosines, const float *sines,
+                                            int c0, int c1, bool turns, Rotation &r) {
+    const __nv_bfloat16 *weight = kind == 0 ? args.q_norm : args.k_norm;
+    Two wx[4], wy[4];
+    if (weight) {
+        unpack8(__ldg(reinterpret_cast<const uint4 *>(weight) + c0), wx);
+        unpack8(__ldg(reinterpret_cast<const uint4 *>(weight) + c1), wy);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) wx[i] = wy[i] = two(1.f, 1.f);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (!turns) {
+            r.a[i] = wx[i];
+            r.c[i] = wy[i];
+            r.b[i] = r.d[i] = two(0.f, 0.f);
+        } else if (kAdjacent) {
+            const float cx = cosines[4 * c0 + i], sx = sines[4 * c0 + i], cy = cosines[4 * c1 + i], sy = sines[4 * c1 + i];
+            r.a[i] = wx[i] * two(cx, cx);
+            r.b[i] = swapped(wx[i]) * two(-sx, sx);
+            r.c[i] = wy[i] * two(cy, cy);
+            r.d[i] = swapped(wy[i]) * two(-sy, sy);
+        } else {
+            const float2 co = *reinterpret_cast<const float2 *>(cosines + 8 * c0 + 2 * i);
+            const float2 si = *reinterpret_cast<const float2 *>(sines + 8 * c0 + 2 * i);
+            r.a[i] = wx[i] * two(co.x, co.y);
+            r.b[i] = wy[i] * two(-si.x, -si.y);
+            r.c[i] = wy[i] * two(co.x, co.y);
+            r.d[i] = wx[i] * two(si.x, si.y);
+        }
+    }
+}
+
+template <bool kAdjacent, bool kNorm>
+__global__ void __launch_bounds__(kThreads, kBlocks) rope_store_kernel(const __grid_constant__ RopeStoreArgs a, int parts) {
+    __shared__ __align__(16) float angles[kWarps][2][kHeadDim / 2];
+    __shared__ uint4 places[kWarps][kAhead][2][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x % kLanes, head0 = (threadIdx.x & 31) / kLanes;
+    const int64_t unit = (int64_t)blockIdx.x * kWarps + warp, t = unit / parts;
+    if (t >= a.n_tokens) return;
+    const int part = (int)(unit - t * parts);
     // the lane's two chunks of 8 dims: a pair's halves where it turns, neighbours behind the turned dims
     const int turning = a.pairs / 8;
     const bool turns = lane < turning;
     const int c0 = turns ? lane : 2 * lane, c1 = turns ? lane + turning : 2 * lane + 1;
     const int hkv = a.pool.hkv, heads = a.hq + 2 * hkv;
-    bool ready = false;
-    for (int h0 = 0; h0 < heads; h0 += kHeadsPerPass * kUnroll) {
-        uint4 r[kUnroll][2];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int h = h0 + u * kHeadsPerPass + head0;
-            if (h >= heads) continue;
-            const __nv_bfloat16 *row = h < a.hq         ? a.q + t * a.q_stride + h * kHeadDim
-                                       : h < a.hq + hkv ? a.k + t * a.k_stride + (h - a.hq) * kHeadDim
-                                                        : a.v + t * a.v_stride + (h - a.hq - hkv) * kHeadDim;
-            r[u][0] = *reinterpret_cast<const uint4 *>(row + 8 * c0);
-            r[u][1] = *reinterpret_cast<const uint4 *>(row + 8 * c1);
+    const __nv_bfloat16 *q = a.q + t * a.q_stride, *k = a.k + t * a.k_stride - a.hq * kHeadDim,
+                        *v = a.v + t * a.v_stride - (a.hq + hkv) * kHeadDim;
+    const int64_t slot = __ldg(a.out_loc + t);
+    const int step = parts * kHeads;
+    uint4 (*place)[2][32] = places[warp];
+    // (read before the slot is known, whatever that says: one wait less)
+    auto load = [&](int h, int at, uint32_t behind0, uint32_t behind1) {
+        if (h < heads) {
+            const __nv_bfloat16 *row = (h < a.hq ? q : h < a.hq + hkv ? k : v) + h * kHeadDim;
+            copy16(&place[at][0][threadIdx.x & 31], row + 8 * c0, behind0);
+            copy16(&place[at][1][threadIdx.x & 31], row + 8 * c1, behind1);
         }
-        if (!ready) {
-            if (threadIdx.x < a.pairs) {
-                const int j = threadIdx.x, axis = a.axis_bits[j / 16] >> (2 * (j % 16)) & 3;
-                const int64_t pos = __ldg(a.positions + axis * a.axis_stride + t);
-                const uint64_t turn = a.turns[j] * (uint64_t)pos;
-                float s, c;
-                sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
-                cosines[j] = c * a.factor;
-                sines[j] = s * a.factor;
-            }
-            __syncthreads();
-            ready = true;
-        }
+        end_group();
+    };
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int h = h0 + u * kHeadsPerPass + head0;
-            // (a head's 8 lanes go the same way, but the shuffles below take the whole warp)
-            const bool is_q = h < a.hq, is_k = !is_q && h < a.hq + hkv, live = h < heads;
-            float x[8], y[8];
-            unpack8(r[u][0], x);
-            unpack8(r[u][1], y);
-            const __nv_bfloat16 *weight = is_q ? a.q_norm : is_k ? a.k_norm : nullptr;
-            if (a.q_norm || a.k_norm) {
-                float sum = 0.f;
+    for (int u = 0; u < kAhead; ++u) load(part * kHeads + head0 + u * step, u, 0, 0);
+    // the token's angles, two a lane
+    float *cosines = angles[warp][0], *sines = angles[warp][1];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum += x[i] * x[i] + y[i] * y[i];
-#pragma unroll
-                for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                if (live && weight) {
-                    const float scale = 1.f / sqrtf(sum * (1.f / kHeadDim) + a.eps);
-                    float wx[8], wy[8];
-                    unpack8(__ldg(reinterpret_cast<const uint4 *>(weight) + c0), wx);
-                    unpack8(__ldg(reinterpret_cast<const uint4 *>(weight) + c1), wy);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        x[i] *= scale * wx[i];
-                        y[i] *= scale * wy[i];
-                    }
-                }
-            }
-            if (!live) continue;
-            if (is_q || is_k) {
-                if (turns && !a.adjacent) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float c = cosines[8 * c0 + i], s = sines[8 * c0 + i];
-                        const float p = x[i] * c - y[i] * s, q = y[i] * c + x[i] * s;
-                        x[i] = p;
-                        y[i] = q;
-                    }
-                } else if (turns) {
-#pragma unroll
-                    for (int i = 0; i < 8; i += 2) {
-                        const float cx = cosines[4 * c0 + i / 2], sx = sines[4 * c0 + i / 2];
-                        const float cy = cosines[4 * c1 + i / 2], sy = sines[4 * c1 + i / 2];
-                        const float p = x[i] * cx - x[i + 1] * sx, q = x[i + 1] * cx + x[i] * sx;
-                        const float v = y[i] * cy - y[i + 1] * sy, w = y[i + 1] * cy + y[i] * sy;
-                        x[i] = p;
-                        x[i + 1] = q;
-                        y[i] = v;
-                        y[i + 1] = w;
-                    }
-                }
-                r[u][0] = pack8(x);
-                r[u][1] = pack8(y);
-            }
-            if (!is_q && !stored) continue;
-            __nv_bfloat16 *row = is_q   ? a.q_out + t * a.out_stride + h * kHeadDim
-                                 : is_k ? a.k_pool + (slot * hkv + h - a.hq) * kHeadDim
-                                        : a.v_pool + (slot * hkv + h - a.hq - hkv) * kHeadDim;
-            *reinterpret_cast<uint4 *>(row + 8 * c0) = r[u][0];
-            *reinterpret_cast<uint4 *>(row + 8 * c1) = r[u][1];
-        }
+    for (int i = 0; i < 2; ++i) {
+        const int j = threadIdx.x % 32 + 32 * i;
+        if (j >= a.pairs) break;
+        // (all four words are there for every lane: an index of its own would be read lane by lane)
+        const uint32_t bits = j % 32 < 16 ? a.axis_bits[2 * i] : a.axis_bits[2 * i + 1];
+        const int axis = bits >> (2 * (j % 16)) & 3;
+        const int64_t pos = __ldg(a.positions + axis * a.axis_stride + t);
+        const uint64_t turn = __ldg(a.turns + j) * (uint64_t)pos;
+        float s, c;
+        sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
+        cosines[j] = c * a.factor;
+        sines[j] = s * a.factor;
     }
+    if (slot == -1) {
+        wait_group<0>();
+        return;                                    // not a token: a bucket's padding
+    }
+    if (part == 0 && threadIdx.x % 32 == 0 && (slot < 0 || slot >= a.pool.num_slots))
+        report(a.status, MSGL_DEVERR_SLOT_RANGE);
+    __syncwarp();
+    Rotation rotation;
+    int kind = -1;
+    int at = 0;
+    for (int h = part * kHeads + head0; h - head0 < heads; h += step) {
+            const bool live = h < heads, is_q = h < a.hq, is_k = !is_q && h < a.hq + hkv;
+            wait_group<kAhead - 1>();
+            uint4 r0 = place[at][0][threadIdx.x & 31], r1 = place[at][1][threadIdx.x & 31];
+            load(h + step * kAhead, at, r0.x, r1.x);
+            at = at + 1 == kAhead ? 0 : at + 1;
+            if (h - head0 < a.hq + hkv) {          // (else the whole turn is v's, or behind it)
+                const int now = is_q || !kNorm ? 0 : 1;
+                if (now != kind) {
+                    rotation_of<kAdjacent>(a, now, cosines, sines, c0, c1, turns, rotation);
+                    kind = now;
+                }
+                Two x[4], y[4];
+                unpack8(r0, x);
+                unpack8(r1, y);
+                float scale = 1.f;
+                if (kNorm) {
+                    Two sum = two(0.f, 0.f);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sum = fma2(y[i], y[i], fma2(x[i], x[i], sum));
+                    float all = sum.lo() + sum.hi();
+#pragma unroll
+                    for (int o = 1; o < kLanes; o <<= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+                    if (is_q ? a.q_norm : a.k_norm) scale = 1.f / sqrtf(all * (1.f / kHeadDim) + a.eps);
+                }
+                if (is_q || is_k) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const Two xo = kAdjacent ? swapped(x[i]) : y[i], yo = kAdjacent ? swapped(y[i]) : x[i];
+                        Two p = x[i] * rotation.a[i], q = y[i] * rotation.c[i];
+                        if (turns) {               // (what does not turn takes nothing of the other chunk, infinities neither)
+                            p = fma2(xo, rotation.b[i], p);
+                            q = fma2(yo, rotation.d[i], q);
+                        }
+                        x[i] = kNorm ? p * two(scale, scale) : p;
+                        y[i] = kNorm ? q * two(scale, scale) : q;
+                    }
+                    r0 = pack8(x);
+                    r1 = pack8(y);
+                }
+            }
+            if (live && (is_q || (slot >= 0 && slot < a.pool.num_slots))) {
+                __nv_bfloat16 *row = is_q   ? a.q_out + t * a.out_stride + h * kHeadDim
+                                     : is_k ? a.k_pool + (slot * hkv + h - a.hq) * kHeadDim
+                                            : a.v_pool + (slot * hkv + h - a.hq - hkv) * kHeadDim;
+                *reinterpret_cast<uint4 *>(row + 8 * c0) = r0;
+                *reinterpret_cast<uint4 *>(row + 8 * c1) = r1;
+            }
+    }
+    wait_group<0>();
 }
 
 }  // namespace
 
 cudaError_t launch_rope_store(const RopeStoreArgs &a, cudaStream_t stream) {
-    rope_store_kernel<<<a.n_tokens, kThreads, 0, stream>>>(a);
+    const int turns = (a.hq + 2 * a.pool.hkv + kHeads - 1) / kHeads;
+    // As many warps as the GPU holds at once (5 blocks of 4 an SM): a token's heads in parts where tokens are
+    // few, whole tokens where they are enough (64/8 heads, us with 1, 2, 4, 10, 20 parts: 64 tokens 11.0, 6.9, 5.2,
+    // 4.1, 3.3; 256 tokens 11.4, 7.2, 5.7, 4.7, 6.0; 4096 tokens 33.7, 34.1, 39.6, 49.9, 71).
+    const int64_t fit = (int64_t)sm_count() * 5 * kWarps / a.n_tokens;
+    const int parts = (int)(fit < 1 ? 1 : fit < turns ? fit : turns);
+    const unsigned blocks = (unsigned)(((int64_t)a.n_tokens * parts + kWarps - 1) / kWarps);
+    auto kernel = a.q_norm || a.k_norm ? (a.adjacent ? rope_store_kernel<true, true> : rope_store_kernel<false, true>)
+                                       : (a.adjacent ? rope_store_kernel<true, false> : rope_store_kernel<false, false>);
+    kernel<<<blocks, kThreads, 0, stream>>>(a, parts);
     return cudaGetLastError();
 }
 

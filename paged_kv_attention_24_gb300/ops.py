@@ -141,8 +141,9 @@ SIGNATURES = {
     "msgl_fork_requests": ([I64, I32, P, I32, I32, I32, P, P, P, I32, P, I32, ctypes.POINTER(_ForkOut), P, P],
                            ctypes.c_int),
     "msgl_copy_pages": ([PP, I32, P, P, P, I32, P, P, P], ctypes.c_int),
-    "msgl_free_pages": ([I64, I32, P, I32, I32, I32, P, P, I32, P, P, P, P, P], ctypes.c_int),
-    "msgl_compact_pages": ([I64, I32, P, I32, I32, I32, P, P, I32, P, ctypes.POINTER(_CompactOut), P, P],
+    "msgl_page_map_workspace_size": ([I64, I32], SZ),
+    "msgl_free_pages": ([I64, I32, P, I32, I32, I32, P, P, I32, P, P, P, P, SZ, P, P], ctypes.c_int),
+    "msgl_compact_pages": ([I64, I32, P, I32, I32, I32, P, P, I32, P, ctypes.POINTER(_CompactOut), P, SZ, P, P],
                            ctypes.c_int),
     "msgl_selftest_wait_timeout": ([P, I64, P], ctypes.c_int),
     "msgl_read_status": ([P, ctypes.POINTER(ctypes.c_uint32), P], ctypes.c_int),
@@ -558,10 +559,11 @@ class Rope:
     of ``positions`` that a pair goes by (all 0 when None): ``[0] * 16 + [1] * 24 + [2] * 24`` for
     sections of time, height and width, ``[0, 1, 2] * 16 + ..`` for interleaved ones.  Pair j is
     dims j and j + pairs, or 2j and 2j + 1 when ``adjacent``; later dims do not turn.
-    ``factor`` scales what turns.
+    ``factor`` scales what turns.  The frequencies are kept on ``device`` (the current CUDA device
+    when None), where the tensors of the calls have to be.
     """
 
-    def __init__(self, inv_freq, axes=None, adjacent: bool = False, factor: float = 1.0):
+    def __init__(self, inv_freq, axes=None, adjacent: bool = False, factor: float = 1.0, device=None):
         freq = [float(f) for f in (inv_freq.tolist() if isinstance(inv_freq, torch.Tensor) else inv_freq)]
         axes = [0] * len(freq) if axes is None else [int(a) for a in axes]
         if not freq or len(freq) > 64 or len(freq) % 8:
@@ -572,7 +574,7 @@ class Rope:
             raise ValueError("axes must have an entry in [0, 3] for each of inv_freq")
         # a fraction of a turn in 64 bits: whole turns of an integer position drop out of the product
         turns = [int(math.fmod(f / (2 * math.pi), 1.0) * 2.0 ** 64) % 2 ** 64 for f in freq]
-        self.turns = b"".join(ctypes.c_uint64(t) for t in turns)
+        self.turns = torch.tensor([t - 2 ** 64 if t >> 63 else t for t in turns], dtype=torch.int64, device=device or "cuda")
         self.axes, self.adjacent, self.factor = bytes(axes), bool(adjacent), float(factor)
 
 
@@ -668,9 +670,15 @@ class FreePages(NamedTuple):
     num_free: torch.Tensor     # [1]
 
 
+def page_map_workspace_size(num_slots: int, page_size: int) -> int:
+    """Workspace bytes of :func:`free_pages` and :func:`compact_pages`."""
+    return int(load().msgl_page_map_workspace_size(num_slots, page_size))
+
+
 def free_pages(req_table: torch.Tensor, lens: torch.Tensor, num_slots: int, page_size: int,
                req_rows: Optional[torch.Tensor] = None, held: Optional[torch.Tensor] = None,
-               out: Optional[FreePages] = None, status: Optional[torch.Tensor] = None, stream=None) -> FreePages:
+               out: Optional[FreePages] = None, workspace: Optional[torch.Tensor] = None,
+               status: Optional[torch.Tensor] = None, stream=None) -> FreePages:
     """The pages that no request holds (msgl_free_pages): the ``free_pages`` of :func:`step_tables` and
     :func:`fork_requests`.
 
@@ -678,14 +686,11 @@ def free_pages(req_table: torch.Tensor, lens: torch.Tensor, num_slots: int, page
     None; -1: padding).  ``held`` uint8 or bool [num_pages]: pages in use beside them.
     """
     p, c = (None, None) if out is None else out
-    r = (_native or _binding()).free_pages(req_table, lens, num_slots, page_size, req_rows, held, p, c, status,
-                                           _handle(stream))
+    r = (_native or _binding()).free_pages(req_table, lens, num_slots, page_size, req_rows, held, p, c, workspace,
+                                           status, _handle(stream))
     if type(r) is int:
         _check(r, "msgl_free_pages")
     return out if r is None else FreePages(*r)
-
-
-COMPACT_MAX_PAGES = 1310720
 
 
 class Compaction(NamedTuple):
@@ -700,7 +705,8 @@ class Compaction(NamedTuple):
 
 def compact_pages(req_table: torch.Tensor, lens: torch.Tensor, num_slots: int, page_size: int,
                   req_rows: Optional[torch.Tensor] = None, held: Optional[torch.Tensor] = None,
-                  out: Optional[Compaction] = None, status: Optional[torch.Tensor] = None, stream=None) -> Compaction:
+                  out: Optional[Compaction] = None, workspace: Optional[torch.Tensor] = None,
+                  status: Optional[torch.Tensor] = None, stream=None) -> Compaction:
     """Moves the requests' pages to the front of the pool (msgl_compact_pages).
 
     The table is rewritten in place unless ``out`` has another; the pages themselves move by
@@ -709,7 +715,7 @@ def compact_pages(req_table: torch.Tensor, lens: torch.Tensor, num_slots: int, p
     """
     t, m, s, d, n, u = (req_table,) + (None,) * 5 if out is None else out
     r = (_native or _binding()).compact_pages(req_table, lens, num_slots, page_size, req_rows, held, t, m, s, d, n, u,
-                                              status, _handle(stream))
+                                              workspace, status, _handle(stream))
     if type(r) is int:
         _check(r, "msgl_compact_pages")
     return out if r is None else Compaction(req_table, *r)
