@@ -36,15 +36,15 @@ bool pow2(int32_t x) { return x > 0 && (x & (x - 1)) == 0; }
 // Pages of keys 0..n_keys-1 of request b, which are row `row` of the table: index below width, id
 // inside the pool.
 msgl_status check_pages(int64_t num_pages, int32_t page_size, const int32_t *page_ids, int32_t stride,
-                        int32_t width, int32_t b, int32_t row, int64_t n_keys) {
+                        int32_t width, int32_t b, int32_t row, int64_t n_keys, const char *who = "request") {
     const int64_t n_pages = (n_keys + page_size - 1) / page_size;
     if (n_pages > width)
-        return bad(MSGL_ERR_OUT_OF_RANGE, "request %d: %lld keys need %lld pages but the table width is %d", b,
+        return bad(MSGL_ERR_OUT_OF_RANGE, "%s %d: %lld keys need %lld pages but the table width is %d", who, b,
                    (long long)n_keys, (long long)n_pages, width);
     for (int64_t p = 0; p < n_pages; ++p) {
         const int32_t id = page_ids[(int64_t)row * stride + p];
         if (id < 0 || id >= num_pages)
-            return bad(MSGL_ERR_OUT_OF_RANGE, "request %d: page_ids[%lld] = %d is outside [0, %lld)", b,
+            return bad(MSGL_ERR_OUT_OF_RANGE, "%s %d: page_ids[%lld] = %d is outside [0, %lld)", who, b,
                        (long long)p, id, (long long)num_pages);
     }
     return MSGL_OK;
@@ -263,7 +263,8 @@ msgl_status msgl_check_fork_meta(int64_t num_slots, int32_t page_size, const int
         if (!children.insert(child_rows[i]).second)
             return bad(MSGL_ERR_INVALID_ARG, "fork %d: row %d is an earlier fork's child too", i, child_rows[i]);
         if (lens[i] < 0) return bad(MSGL_ERR_INVALID_ARG, "fork %d: length %d must be >= 0", i, lens[i]);
-        if ((rc = check_pages(num_pages, page_size, req_table, table_stride, table_width, i, parent_rows[i], lens[i])))
+        if ((rc = check_pages(num_pages, page_size, req_table, table_stride, table_width, i, parent_rows[i], lens[i],
+                              "fork")))
             return rc;
         for (int64_t p = 0; p * page_size < lens[i]; ++p)
             used.insert(req_table[(int64_t)parent_rows[i] * table_stride + p]);
