@@ -640,9 +640,10 @@ msgl_status msgl_rope_store_kv(const msgl_kv_pool *pool, const msgl_new_tokens *
         if (x.stride % 8 || x.stride < x.row || too_far(n.n_tokens, x.stride))
             return fail(MSGL_ERR_INVALID_ARG, "%s %lld is not a multiple of 8 from %lld on that memory can hold", x.name,
                         (long long)x.stride, (long long)x.row);
-    if (rope->num_axes > 1 && (n.axis_stride < n.n_tokens || too_far(rope->num_axes, n.axis_stride)))
-        return fail(MSGL_ERR_INVALID_ARG, "axis_stride %lld is below n_tokens %d (or past all memory)",
+    if (rope->num_axes > 1 && n.axis_stride != 0 && (n.axis_stride < n.n_tokens || too_far(rope->num_axes, n.axis_stride)))
+        return fail(MSGL_ERR_INVALID_ARG, "axis_stride %lld is neither 0 nor n_tokens %d or more (or past all memory)",
                     (long long)n.axis_stride, n.n_tokens);
+    const bool one_axis = rope->num_axes == 1 || n.axis_stride == 0;
     // (two bf16 an entry; tokens are turned by blocks of their own, in any order)
     auto span = [&](const void *p, int64_t row, int64_t stride, const char *name) {
         return Span{static_cast<const int32_t *>(p), n.n_tokens, row / 2, stride / 2, name};
@@ -652,7 +653,7 @@ msgl_status msgl_rope_store_kv(const msgl_kv_pool *pool, const msgl_new_tokens *
                         span(n.v, kv_row, n.v_stride, "v"),
                         flat(static_cast<const int32_t *>(q_norm), msgl::kHeadDim / 2, "q_norm"),
                         flat(static_cast<const int32_t *>(k_norm), msgl::kHeadDim / 2, "k_norm"),
-                        {n.positions, rope->num_axes, n.n_tokens, rope->num_axes > 1 ? n.axis_stride : n.n_tokens, "positions"},
+                        {n.positions, one_axis ? 1 : rope->num_axes, n.n_tokens, one_axis ? n.n_tokens : n.axis_stride, "positions"},
                         flat(n.out_loc, n.n_tokens, "out_loc"),
                         flat(reinterpret_cast<const int32_t *>(rope->turns), 2 * rope->num_pairs, "rope->turns"),
                         {static_cast<const int32_t *>(pool->k_pool), pool->num_slots, kv_row / 2, kv_row / 2, "the K pool"},
@@ -676,7 +677,7 @@ msgl_status msgl_rope_store_kv(const msgl_kv_pool *pool, const msgl_new_tokens *
     a.turns = rope->turns;
     a.positions = n.positions;
     a.out_loc = n.out_loc;
-    a.axis_stride = rope->num_axes > 1 ? n.axis_stride : 0;
+    a.axis_stride = one_axis ? 0 : n.axis_stride;
     a.pairs = rope->num_pairs;
     a.adjacent = rope->adjacent != 0;
     a.n_tokens = n.n_tokens;
@@ -815,7 +816,8 @@ msgl_status msgl_copy_pages(const msgl_kv_pool *pools, int32_t num_pools, const 
     }
     if (num_pools == 0 || num_pairs == 0) return MSGL_OK;
     if (!src || !dst) return fail(MSGL_ERR_INVALID_ARG, "src and dst must be non-NULL");
-    msgl::CopyPagesArgs a;
+    msgl::CopyPagesArgs a{};
+    void *buffers[2 * msgl::kMaxCopyPools];
     a.src = src;
     a.dst = dst;
     a.tokens = tokens;
@@ -829,11 +831,11 @@ msgl_status msgl_copy_pages(const msgl_kv_pool *pools, int32_t num_pools, const 
     for (int i0 = 0; i0 < num_pools; i0 += msgl::kMaxCopyPools) {
         const int n = num_pools - i0 < msgl::kMaxCopyPools ? num_pools - i0 : msgl::kMaxCopyPools;
         for (int i = 0; i < n; ++i) {
-            a.buffers[2 * i] = pools[i0 + i].k_pool;
-            a.buffers[2 * i + 1] = pools[i0 + i].v_pool;
+            buffers[2 * i] = pools[i0 + i].k_pool;
+            buffers[2 * i + 1] = pools[i0 + i].v_pool;
         }
         a.num_buffers = 2 * n;
-        cudaError_t e = msgl::launch_copy_pages(a, (cudaStream_t)stream);
+        cudaError_t e = msgl::launch_copy_pages(a, buffers, (cudaStream_t)stream);
         if (e != cudaSuccess) return cuda_fail(e, "copy_pages launch");
     }
     return MSGL_OK;

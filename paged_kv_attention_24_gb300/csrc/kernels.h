@@ -140,14 +140,14 @@ cudaError_t launch_fork(const ForkArgs &a, cudaStream_t stream);
 constexpr int kMaxCopyPools = 128;        // pools of one copy launch (their addresses are kernel arguments)
 
 struct CopyPagesArgs {
-    void *buffers[2 * kMaxCopyPools];     // K and V of each pool
     const int32_t *src, *dst, *tokens, *count;
     int64_t page_vecs;                    // 16-byte vectors of a page and of a slot's row
     int32_t row_vecs, page_size, num_pages, num_pairs, num_buffers;
     int32_t pieces;                       // set by the launcher
     uint32_t *status;
 };
-cudaError_t launch_copy_pages(CopyPagesArgs &a, cudaStream_t stream);
+// buffers: K and V of each pool, a.num_buffers (at most 2 * kMaxCopyPools) in all
+cudaError_t launch_copy_pages(CopyPagesArgs a, void *const *buffers, cudaStream_t stream);
 
 struct PageMapArgs {
     const int32_t *table, *req_rows, *lens;

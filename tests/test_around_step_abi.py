@@ -82,6 +82,7 @@ def test_rope_store_refusals(lib):
                      (INVALID, dict(q_stride=16 * 128 - 8)), (INVALID, dict(k_stride=8 * 128 + 4)), (INVALID, dict(v_stride=0)),
                      (INVALID, dict(out_stride=2 ** 62)), (INVALID, dict(q_stride=-8)),
                      (INVALID, dict(ax=second, num_axes=2, axis_stride=3)), (INVALID, dict(ax=second, num_axes=2, axis_stride=2 ** 60)),
+                     (INVALID, dict(ax=second, num_axes=2, axis_stride=-4)),
                      # q_out over an input, and over part of q
                      (INVALID, dict(q_out=at(4))), (INVALID, dict(q_out=at(5) + 3 * 2048)), (INVALID, dict(q_out=at(3) + 16)),
                      (INVALID, dict(q_out=at(3), out_stride=16 * 128 + 8)), (INVALID, dict(q_out=at(0) + 2048)),

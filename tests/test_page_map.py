@@ -66,6 +66,27 @@ def test_free_without_rows_and_with_shared_pages():
     run_free(table, [rows[0], rows[0], -1], [lens[0], lens[0], 5], 700, 4)
 
 
+@pytest.mark.parametrize("first", [0, 5, 31, 1000])
+def test_free_of_pages_in_a_row(first):
+    """Neighbouring pages share words of the bitmap: whole rows of them, broken runs, one page many times."""
+    table = np.tile(np.arange(first, first + 300, dtype=np.int32), (40, 1))
+    table[1::2] = table[1::2, ::-1]
+    table[3, 10:200] = first + 7
+    table[5, ::3] = -1
+    lens = [300] * 40
+    run_free(table, None, lens, 1500, 1, flags=ops.DEVERR_PAGE_RANGE)
+    run_free(table[:3], None, [300, 299, 33], 1500, 1)
+    run_compact(table[:3], None, [300, 299, 33], 1500, 1)
+    run_compact(table, None, lens, 1500, 1, flags=ops.DEVERR_PAGE_RANGE)
+
+
+def test_held_as_bools():
+    held = torch.zeros(64, dtype=torch.bool, device="cuda")
+    held[[3, 40]] = True
+    out = ops.free_pages(i32([[5, 6]], "cuda"), i32([2], "cuda"), 64, 1, held=held)
+    assert out.pages[:out.num_free.item()].tolist() == [p for p in range(64) if p not in (3, 5, 6, 40)]
+
+
 def test_free_at_the_ends():
     empty = np.zeros((0, 0), np.int32)
     run_free(empty, None, [], 0, 16)

@@ -118,6 +118,19 @@ def test_positions_out_of_a_larger_buffer():
     check(q, k, v, buf[:, :6], loc, pool, out, freqs(64), axes)
 
 
+def test_one_row_of_positions_for_all_axes():
+    q, k, v, pos, loc, pool = case(5, 8, 4, seed=17)
+    axes = [j % 3 for j in range(64)]
+    out = ops.rope_store_kv(pool, q, k, v, pos.expand(3, 5), loc, ops.Rope(freqs(64), axes))
+    check(q, k, v, pos.expand(3, 5).contiguous(), loc, pool, out, freqs(64), axes)
+
+
+def test_most_heads():
+    q, k, v, pos, loc, pool = case(2, 64 * 64, 64, seed=18)
+    out = ops.rope_store_kv(pool, q, k, v, pos[0], loc, ops.Rope(freqs(64)))
+    check(q, k, v, pos, loc, pool, out, freqs(64))
+
+
 def test_padding_and_bad_slots():
     q, k, v, pos, loc, pool = case(8, 8, 8, seed=8)
     loc[3] = -1
