@@ -143,7 +143,7 @@ struct CopyPagesArgs {
     const int32_t *src, *dst, *tokens, *count;
     int64_t page_vecs;                    // 16-byte vectors of a page and of a slot's row
     int32_t row_vecs, page_size, num_pages, num_pairs, num_buffers;
-    int32_t pieces;                       // set by the launcher
+    int32_t pieces, group, span, turns;   // set by the launcher
     uint32_t *status;
 };
 // buffers: K and V of each pool, a.num_buffers (at most 2 * kMaxCopyPools) in all

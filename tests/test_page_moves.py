@@ -163,6 +163,23 @@ def test_padding_and_counts():
         run_copy(p, [1, 2, 3, 4, -1], [21, 22, 23, 24, -1], count=count)
 
 
+def test_long_lists_are_taken_in_groups():
+    """Enough pairs that a warp looks at 32 of them; most are padding, some are wrong, the last group is not full."""
+    ps, pages = 64, 300
+    p = pools(3, pages * ps, 8, ps)
+    n = 200001
+    src, dst, tokens = np.full(n, -1), np.full(n, -1), np.full(n, -7)
+    at = np.random.default_rng(3).permutation(n)[:100]
+    at[:3] = 0, n - 1, n - 33
+    src[at], dst[at], tokens[at] = np.arange(100), np.arange(150, 250), np.arange(100) % (ps + 1)
+    bad = [i for i in range(40, 2000, 97) if src[i] == -1]
+    src[bad[::2]] = 5
+    dst[bad[1::2]] = pages
+    run_copy(p, src.tolist(), dst.tolist(), tokens.tolist(), flags=ops.DEVERR_PAGE_RANGE)
+    src[bad], dst[bad] = -1, -1
+    run_copy(p, src.tolist(), dst.tolist())
+
+
 def test_bad_pairs_are_passed_over():
     p = pools(2, 20 * 16, 8, 16)
     run_copy(p, [1, 20, 3], [11, 12, 13], flags=ops.DEVERR_PAGE_RANGE)
