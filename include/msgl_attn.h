@@ -524,7 +524,7 @@ MSGL_API msgl_status msgl_copy_pages(const msgl_kv_pool *pools, int32_t num_pool
  * when none of them holds it.
  *   req_table    device int32 [num_rows, table_stride], table_width valid columns
  *   req_rows     device int32 [num_reqs] or NULL (row b); -1: no request (padding)
- *   lens         device int32 [num_reqs]
+ *   lens         device int32 [num_reqs], at most 2^24 of them
  *   held         device uint8 [num_slots / page_size] or NULL: not 0 for a page that something
  *                else holds (a radix cache's pages, a request that waits)
  *   pages        device int32 [num_slots / page_size] (output): the free pages' ids, -1 behind them

@@ -171,7 +171,7 @@ msgl_status prepare_page_map(int64_t num_slots, int32_t page_size, const int32_t
     if ((s = check_req_table(req_table, num_rows, table_stride, table_width))) return s;
     if (num_reqs < 0) return fail(MSGL_ERR_INVALID_ARG, "negative size");
     if (num_reqs > 0 && !lens) return fail(MSGL_ERR_INVALID_ARG, "lens is NULL");
-    if (num_reqs > INT32_MAX - 1024) return fail(MSGL_ERR_UNSUPPORTED, "num_reqs passes int32");
+    if (num_reqs > 1 << 24) return fail(MSGL_ERR_UNSUPPORTED, "more than 2^24 requests");
     if (table_width > msgl::kMaxStepItems)
         return fail(MSGL_ERR_UNSUPPORTED, "more than %lld columns", (long long)msgl::kMaxStepItems);
     a.table = req_table;

@@ -78,11 +78,11 @@ struct Unit {
     }
 };
 
-// f(unit) for all table entries of the requests, over all warps of the grid's first
-// `blocks` blocks; ready(), once, by every thread (one without
-// entries too: the grid's end then says that the grid before has ended), in front of the first f, but behind the
-// first loads.  Where a warp gets a few units even if every row were full, it looks its requests up
-// itself; else the rows' units are counted first and dealt out evenly.
+// f(unit) for all table entries of the requests, over all warps of the grid's first `blocks` blocks; ready(), once, by
+// every thread (one without entries too: the grid's end then says that the grid before has ended), in front of the
+// first f, but behind the first loads.  Where full rows would give a warp no more units than twice the batches of
+// requests, it looks each unit's request up itself (20000 requests of 4 pages: 88 -> 11 us); else (rows much wider than
+// what is in them) the rows' units are counted first, a batch of requests at a time, and dealt out evenly.
 template <class R, class F>
 __device__ __forceinline__ void for_entries(const PageMapArgs &a, Batch &s, int blocks, bool tell, R ready, F f) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -90,7 +90,8 @@ __device__ __forceinline__ void for_entries(const PageMapArgs &a, Batch &s, int 
     const int chunks = max(1, (a.table_width + kUnit - 1) / kUnit);
     Unit x;
     x.n = 0;
-    if ((int64_t)a.num_reqs * chunks <= 2 * warps) {
+    const int64_t rounds = ((int64_t)a.num_reqs * chunks + warps - 1) / warps;
+    if (rounds <= 2 * ((a.num_reqs + kBatch - 1) / kBatch)) {
         auto look = [&](int u) {
             const int b = u / chunks;
             x.c0 = (u - b * chunks) * kUnit;

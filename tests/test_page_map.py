@@ -80,6 +80,16 @@ def test_free_of_pages_in_a_row(first):
     run_compact(table, None, lens, 1500, 1, flags=ops.DEVERR_PAGE_RANGE)
 
 
+@pytest.mark.parametrize("batch", [70, 601])
+def test_tables_much_wider_than_what_is_in_them(batch):
+    """The rows' units are counted and dealt out, in one batch of requests and in two."""
+    table, rows, lens, rng = requests(batch, 1, 900, 300000, batch, width=60000)
+    lens[5], lens[-1], rows[9] = 0, -4, -1
+    table[rows[-1]] = rng.integers(0, 300000, 60000)
+    run_free(table, rows, lens, 300000, 1, flags=ops.DEVERR_LENGTH)
+    run_compact(table, rows, lens, 300000, 1, some_held(rng, 300000, 0.2), flags=ops.DEVERR_LENGTH)
+
+
 def test_held_as_bools():
     held = torch.zeros(64, dtype=torch.bool, device="cuda")
     held[[3, 40]] = True
