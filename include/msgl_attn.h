@@ -476,7 +476,8 @@ MSGL_API msgl_status msgl_verify_drafts(const msgl_draft_batch *batch, uint32_t 
  *   else      copy_src[i] = copy_dst[i] = -1, copy_tokens[i] = 0
  *   pages_taken[0] = how many of free_pages are now in use
  * The copies are the arguments of msgl_copy_pages.  Later columns of the child's row stay
- * as they are.
+ * as they are.  lens[i] counts tokens that the parent keeps: a page that it will write
+ * again (under drafts that may yet be refused) is not to be shared.
  *   req_table    device int32 [num_rows, table_stride], table_width valid columns (in and out)
  *   parent_rows, child_rows, lens   device int32 [num_forks]; both rows -1: no fork (padding)
  * Refused are a fork whose rows are outside the table, or whose child is also a parent

@@ -13,10 +13,12 @@
 // launch; each waits for the one before, all of whose blocks did, before it touches
 // what that one wrote.
 //
-// Bound by latency up to some ten thousand entries, by scattered atomics and the
-// lists' stores beyond.  Both want many SMs: one cluster of 8 blocks that kept the bitmap in
-// shared memory, a launch less, took the same 6.5 us for 64 requests, but 32 us for half
-// a million entries (16 blocks 23: a shared-memory atomic takes a cycle a lane).
+// Bound by latency up to some ten thousand entries (64 requests, 12 thousand pages: free 5.9 us;
+// 32 requests: compaction 9), by scattered atomics and the lists' stores beyond (half a million
+// entries, 740 thousand pages: free 14 us; 280 thousand and 550 thousand: compaction 18).
+// Both want many SMs: one cluster of 8 blocks that kept the bitmap in shared memory, two launches
+// less, took 6.5 us for the 64 requests, but 32 us for the half million entries (16 blocks 23: a
+// shared-memory atomic takes a cycle a lane).
 #include "kernels.h"
 
 namespace msgl {
@@ -226,11 +228,11 @@ __device__ __forceinline__ void block_sums(uint32_t (&x)[N], uint32_t (*part)[kL
     for (int i = 0; i < N; ++i) x[i] = __reduce_add_sync(0xffffffffu, lane < kListWarps ? part[i][lane] : 0);
 }
 
-// f(first word, four words of x, four of y) for all vectors of one or two bitmaps, by the whole block, 4 of a thread's
-// loads of each at a time (y: zeros where it is not given).
+// f(first word, four words of x, four of y) for all vectors of one or two bitmaps, by the whole block, as many of a
+// thread's loads together as registers allow: one round up to 786 (655) thousand pages (y: zeros where it is not given).
 template <bool kBoth, class F>
 __device__ __forceinline__ void for_words(const uint32_t *x, const uint32_t *y, int64_t words, F f) {
-    constexpr int kLoads = 4;
+    constexpr int kLoads = kBoth ? 5 : 6;
     for (int64_t v0 = threadIdx.x; v0 < words / 4; v0 += kLoads * kListThreads) {
         uint4 r[kLoads], s[kLoads];
 #pragma unroll
@@ -266,8 +268,9 @@ __device__ __forceinline__ void fill(int32_t *out, int64_t from, int64_t to) {
     for (int64_t i = me; i < quads; i += all) *reinterpret_cast<int4 *>(out + head + 4 * i) = make_int4(-1, -1, -1, -1);
 }
 
-// A block's share of the words.  It goes over them 32 at a time: every warp looks at all 32, a lane each, so that
-// all know where each word's pages go without a word between them, and writes one of them.
+// A block's share of the words.  It goes over them 1024 at a time: a thread looks at one, a scan says where its pages
+// go, and then each warp writes every 32nd word's.  (Every warp scanning for itself saves two barriers, but 32 warps
+// with the same scan keep the SM's issue slots busy: 6.7 against 5.7 us for the list of 740 thousand pages.)
 struct Share {
     int64_t w0, w1, words;
 };
@@ -279,11 +282,22 @@ __device__ __forceinline__ Share share_of(const PageMapArgs &a) {
     s.w1 = min(s.w0 + each, s.words);
     return s;
 }
-static_assert(kListWarps == 32, "a word for each warp");
+static_assert(kListWarps == 32, "a lane for each warp's count");
+
+// x summed over the block's threads before this one; all: over the whole block.
+__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t *part, uint32_t &all) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t upto = warp_scan(x);
+    if (lane == 31) part[warp] = upto;
+    __syncthreads();
+    const uint32_t w = part[lane];
+    all = __reduce_add_sync(0xffffffffu, w);
+    return __reduce_add_sync(0xffffffffu, lane < warp ? w : 0) + upto - x;
+}
 
 __global__ void __launch_bounds__(kListThreads) free_list_kernel(const PageMapArgs a) {
-    __shared__ uint32_t part[2][kListWarps];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ uint32_t part[2][kListWarps], words[kListThreads], places[kListThreads];
+    const int warp = threadIdx.x >> 5;
     const Share s = share_of(a);
     wait_for_last();
     uint32_t n[2] = {0, 0};                                       // free pages before the share, and all
@@ -292,17 +306,20 @@ __global__ void __launch_bounds__(kListThreads) free_list_kernel(const PageMapAr
         n[1] += free;
         if (w < s.w0) n[0] += free;
     });
-    uint32_t word = s.w0 + lane < s.w1 ? ~__ldcg(a.used_bits + s.w0 + lane) : 0;
+    uint32_t word = s.w0 + threadIdx.x < s.w1 ? ~__ldcg(a.used_bits + s.w0 + threadIdx.x) : 0;
     block_sums(n, part);
     if (blockIdx.x == 0 && threadIdx.x == 0) a.count_out[0] = (int32_t)n[1];
-    uint32_t place = n[0];
-    for (int64_t w0 = s.w0; w0 < s.w1; w0 += 32) {
-        const uint32_t next = w0 + 32 + lane < s.w1 ? ~__ldcg(a.used_bits + w0 + 32 + lane) : 0;
-        const uint32_t mine = __popc(word), upto = warp_scan(mine);
-        write_bits(__shfl_sync(0xffffffffu, word, warp), 32 * (w0 + warp),
-                   place + __shfl_sync(0xffffffffu, upto - mine, warp), a.pages_out, 0xffffffffu);
-        place += __shfl_sync(0xffffffffu, upto, 31);
-        word = next;
+    uint32_t place = n[0], all;
+    for (int64_t w0 = s.w0; w0 < s.w1; w0 += kListThreads) {
+        if (w0 > s.w0) word = w0 + threadIdx.x < s.w1 ? ~__ldcg(a.used_bits + w0 + threadIdx.x) : 0;
+        __syncthreads();
+        const uint32_t before = block_scan(__popc(word), part[0], all);
+        words[threadIdx.x] = word;
+        places[threadIdx.x] = place + before;
+        __syncthreads();
+        const int mine = (int)min((int64_t)kListThreads, s.w1 - w0);
+        for (int i = warp; i < mine; i += kListWarps) write_bits(words[i], 32 * (w0 + i), places[i], a.pages_out, 0xffffffffu);
+        place += all;
     }
     fill(a.pages_out, n[1], a.num_pages);
 }
@@ -316,7 +333,8 @@ __device__ __forceinline__ uint32_t below(uint32_t used, int64_t w) {
 // The moves: the movable pages from page `used` on go to the free pages in front of it, both in order.  Leaves for
 // every word the number of moves before it.
 __global__ void __launch_bounds__(kListThreads) moves_kernel(const PageMapArgs a) {
-    __shared__ uint32_t part[3][kListWarps];
+    __shared__ uint32_t part[3][kListWarps], used_words[kListThreads];
+    __shared__ uint4 words[kListThreads];
     let_next_start();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Share s = share_of(a);
@@ -343,30 +361,39 @@ __global__ void __launch_bounds__(kListThreads) moves_kernel(const PageMapArgs a
             }
         }
     });
+    uint32_t u, stays;
+    auto load = [&](int64_t w) {
+        u = w < s.w1 ? __ldcg(a.used_bits + w) : 0xffffffffu;
+        stays = w < s.w1 ? __ldcg(a.stay_bits + w) : 0xffffffffu;
+    };
+    load(s.w0 + threadIdx.x);
     block_sums(m, part);
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         a.count_out[0] = (int32_t)m[2];
         a.used_out[0] = (int32_t)used;
     }
-    uint32_t from = m[0], to = m[1];
-    for (int64_t w0 = s.w0; w0 < s.w1; w0 += 32) {
-        const int64_t w = w0 + lane;
-        uint32_t u = 0xffffffffu, stays = 0xffffffffu;
-        if (w < s.w1) {
-            u = __ldcg(a.used_bits + w);
-            stays = __ldcg(a.stay_bits + w);
-        }
+    uint32_t from = m[0], to = m[1], all_moves, all_holes;
+    for (int64_t w0 = s.w0; w0 < s.w1; w0 += kListThreads) {
+        const int64_t w = w0 + threadIdx.x;
+        if (w0 > s.w0) load(w);
         const uint32_t front = below(used, w), moves = u & ~stays & ~front, holes = ~u & front;
-        const uint32_t moved = from + warp_scan(__popc(moves)), filled = to + warp_scan(__popc(holes));
-        if (warp == 0 && w < s.w1) a.moves_before[w] = moved - __popc(moves);
-        const int64_t page = 32 * (w0 + warp) + lane;
-        const uint32_t x = __shfl_sync(0xffffffffu, u, warp), y = __shfl_sync(0xffffffffu, moves, warp),
-                       z = __shfl_sync(0xffffffffu, holes, warp);
-        write_bits(y, page - lane, __shfl_sync(0xffffffffu, moved, warp) - __popc(y), a.src, m[2]);
-        write_bits(z, page - lane, __shfl_sync(0xffffffffu, filled, warp) - __popc(z), a.dst, m[2]);
-        if (page < a.num_pages && w0 + warp < s.w1 && !(y >> lane & 1)) a.pages_out[page] = x >> lane & 1 ? (int32_t)page : -1;
-        from = __shfl_sync(0xffffffffu, moved, 31);
-        to = __shfl_sync(0xffffffffu, filled, 31);
+        __syncthreads();
+        const uint32_t moved = from + block_scan(__popc(moves), part[0], all_moves),
+                       filled = to + block_scan(__popc(holes), part[1], all_holes);
+        if (w < s.w1) a.moves_before[w] = moved;
+        words[threadIdx.x] = make_uint4(moves, moved, holes, filled);
+        used_words[threadIdx.x] = u;
+        __syncthreads();
+        const int mine = (int)min((int64_t)kListThreads, s.w1 - w0);
+        for (int i = warp; i < mine; i += kListWarps) {
+            const uint4 x = words[i];
+            const int64_t page = 32 * (w0 + i) + lane;
+            write_bits(x.x, page - lane, x.y, a.src, m[2]);
+            write_bits(x.z, page - lane, x.w, a.dst, m[2]);
+            if (page < a.num_pages && !(x.x >> lane & 1)) a.pages_out[page] = used_words[i] >> lane & 1 ? (int32_t)page : -1;
+        }
+        from += all_moves;
+        to += all_holes;
     }
     fill(a.src, m[2], a.num_pages / 2);
     fill(a.dst, m[2], a.num_pages / 2);

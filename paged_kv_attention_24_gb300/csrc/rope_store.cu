@@ -17,9 +17,12 @@
 // of its heads where tokens are few, 4 heads a turn: 8 lanes hold a head, so that
 // both halves of every pair are in one lane, and a lane's part of the rotation
 // (the weights of the norm multiplied in) stays in its registers from head to head.
-// No block-wide wait: a block of 8 warps that shared the angles of its tokens through
-// shared memory, and read cosines, sines and weights again for every head, issued
-// 370 instructions a turn and was bound by them (8256 tokens of 64/8 heads: 70 us).
+// Heads come 6 turns ahead by cp.async into the lane's own places in shared memory, so
+// that no thread waits for another.  8256 tokens of 64/8 heads, normed: 55 us (6.1 TB/s of
+// the 338 MB; ncu: DRAM 66% busy, 28% of the warps), 4 tokens of 16/8 heads 2.4 us.  Slower:
+// angles shared by a block through shared memory, cosines, sines and weights read
+// again for every head (370 instructions a turn in place of 200: 70 us); heads ahead in
+// registers, 2 to 5 turns (66 to 72 us); 4 turns ahead, or 6 or 7 blocks an SM (56 to 59).
 #include "kernels.h"
 
 namespace msgl {

@@ -17,7 +17,9 @@
 // is read once), by latency for small ones.  A cluster of blocks takes a request,
 // so that a row is read by many SMs; each warp sums a run of neighbouring tokens,
 // the blocks exchange their warps' sums, and only the run in which the draw falls
-// is read again (out of L2).
+// is read again (out of L2).  128 requests over 131072 tokens of fp32: 27 us (the rows alone
+// 18 us at the copy rate; lookups in front, exchange and draw behind take the rest); 4 over
+// 50001 of bf16: 7.2 us.  With 64-bit sums: 72 and 14 us.
 #include "kernels.h"
 
 namespace msgl {
