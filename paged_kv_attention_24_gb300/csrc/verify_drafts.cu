@@ -19,7 +19,7 @@
 // the blocks exchange their warps' sums, and only the run in which the draw falls
 // is read again (out of L2).  128 requests over 131072 tokens of fp32: 27 us (the rows alone
 // 18 us at the copy rate; lookups in front, exchange and draw behind take the rest); 4 over
-// 50001 of bf16: 7.2 us.  With 64-bit sums: 72 and 14 us.
+// 50001 of bf16: 6.8 us.  With 64-bit sums: 72 and 14 us.
 #include "kernels.h"
 
 namespace msgl {
@@ -27,7 +27,6 @@ namespace msgl {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kMaxRuns = 8 * kWarps;   // warps of a cluster
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -72,7 +71,7 @@ __device__ __forceinline__ Sum shfl(const Sum &a, int lane) {
     return Sum{__shfl_sync(0xffffffffu, a.hi, lane), __shfl_sync(0xffffffffu, a.lo, lane)};
 }
 
-// Sums over the warp's lanes before this one (x) and up to this one (returned).
+// Sums over the warp's lanes before this one (before) and up to this one (returned).
 __device__ __forceinline__ Sum warp_scan(Sum x, Sum &before) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -83,6 +82,13 @@ __device__ __forceinline__ Sum warp_scan(Sum x, Sum &before) {
     before = Sum{__shfl_up_sync(0xffffffffu, x.hi, 1), __shfl_up_sync(0xffffffffu, x.lo, 1)};
     if (lane == 0) before = Sum{0.f, 0.f};
     return x;
+}
+
+// The first lane with any weight x at which the running sum `upto` passes the draw, else the last one with any; -1
+// when there is none.
+__device__ __forceinline__ int drawn_lane(const Sum &x, const Sum &upto, const Sum &draw) {
+    const uint32_t heavy = __ballot_sync(0xffffffffu, x.hi > 0), over = __ballot_sync(0xffffffffu, x.hi > 0 && upto > draw);
+    return over ? __ffs(over) - 1 : 31 - __clz(heavy);
 }
 
 // max(p - q, 0); what is no number counts nothing.
@@ -150,13 +156,16 @@ struct Row {
         const float w = weight(x[k], y[k]);
         return token(vector) + k == without ? 0.f : w;
     }
+    __device__ __forceinline__ float at(int i) const {   // token i, by itself
+        return i < 0 || i >= vocab || i == without ? 0.f : weight(value(p[i]), q ? value(q[i]) : 0.f);
+    }
 };
 
 struct Shared {
-    Sum sums[kWarps];                // this block's runs
+    Sum sums[kWarps], total;         // of this block's runs, and of the block
     Sum warp[kWarps];
     Sum draw, before;                // u * total; the weights in front of the drawn run
-    int accepted, run, drawn, last;
+    int accepted, run, drawn, last;  // run: of this block's, -1 when the draw is in another block
     bool bad;
 };
 
@@ -219,11 +228,12 @@ __device__ __forceinline__ int standing(const VerifyArgs &a, int first, int draf
 }
 
 template <class T>
-__global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a, int cluster) {
-    constexpr int kN = Vec<T>::kN;
+__global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a, int log2_cluster) {
+    const int cluster = 1 << log2_cluster, log2_runs = log2_cluster + 4;
+    static_assert(kWarps == 16, "a block of 16 runs");
     __shared__ Shared s;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = cluster_rank(), b = blockIdx.x / cluster;
+    const int rank = cluster_rank(), b = blockIdx.x >> log2_cluster;
     const int first = __ldg(a.cu_ext + b), end = __ldg(a.cu_ext + b + 1);
     const bool ok = first >= 0 && first <= end && end <= a.total_tokens;
     if (!ok || first == end) {
@@ -254,13 +264,20 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
     Row<T> r;
     r.set(p, refused && a.draft ? static_cast<const T *>(a.draft) + row * a.draft_stride : nullptr,
           refused && !a.draft ? __ldg(a.tokens + row + 1) : -1, a.vocab);
-    const int runs = cluster * kWarps, vectors = r.vectors();
-    const int length = ((vectors + runs - 1) / runs + 31) / 32 * 32;   // whole rounds of a warp
+    const int vectors = r.vectors();
+    const int length = ((vectors - 1) >> log2_runs) / 32 * 32 + 32;       // whole rounds of a warp
     const int mine = rank * kWarps + warp;
     for (bool second = false;; second = true) {
         const int n0 = (int)min((int64_t)mine * length, (int64_t)vectors), n1 = min(n0 + length, vectors);
         const Sum sum = run_sum(r, n0, n1);
         if (lane == 0) s.sums[warp] = sum;
+        __syncthreads();
+        Sum x{0.f, 0.f}, upto, lower;
+        if (warp == 0) {
+            if (lane < kWarps) x = s.sums[lane];
+            upto = warp_scan(x, lower);
+            if (lane == 31) s.total = upto;
+        }
         cluster_arrive();
         if (rank == 0 && !second) {
             // (written here, where the block waits anyway)
@@ -272,46 +289,30 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
             }
         }
         cluster_wait();
-        // every block goes through all runs' sums in the same order and so comes to the same end
+        // Every block goes through all blocks' sums in the same order and so comes to the same end; the one that
+        // the draw falls into goes on to its runs.  (One warp over all runs' sums at once, four a lane, was more
+        // code than it was worth: 7.2 against 6.8 us for 4 requests.  Rolled scans: 8.0.)
         if (warp == 0) {
-            constexpr int kEach = kMaxRuns / 32;
-            const int each = (runs + 31) / 32;                          // runs of a lane
-            Sum x[kEach], upto[kEach], sum{0.f, 0.f}, lower;
-#pragma unroll
-            for (int k = 0; k < kEach; ++k) {
-                const int i = lane * each + k;
-                x[k] = Sum{0.f, 0.f};
-                if (k < each && i < runs) {
-                    uint32_t at;
-                    asm("mapa.shared::cluster.u32 %0, %1, %2;"
-                        : "=r"(at)
-                        : "r"((uint32_t)__cvta_generic_to_shared(&s.sums[i % kWarps])), "r"(i / kWarps));
-                    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(x[k].hi), "=f"(x[k].lo) : "r"(at) : "memory");
-                }
+            Sum y{0.f, 0.f}, ahead;
+            if (lane < cluster) {
+                uint32_t at;
+                asm("mapa.shared::cluster.u32 %0, %1, %2;"
+                    : "=r"(at)
+                    : "r"((uint32_t)__cvta_generic_to_shared(&s.total)), "r"(lane));
+                asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(y.hi), "=f"(y.lo) : "r"(at) : "memory");
             }
-#pragma unroll
-            for (int k = 0; k < kEach; ++k) {
-                if (k < each) sum = sum + x[k];
-                upto[k] = sum;
+            const Sum blocks = warp_scan(y, ahead), total = shfl(blocks, 31), draw = times(sample, total);
+            const bool bad = !(total.hi > 0 && total.hi <= 3.4e38f);
+            int run = -1;
+            if (!bad && drawn_lane(y, blocks, draw) == rank) {
+                const Sum base = shfl(ahead, rank);
+                run = drawn_lane(x, base + upto, draw);
+                if (lane == run) s.before = base + lower;
             }
-            const Sum total = shfl(warp_scan(sum, lower), 31), draw = times(sample, total);
-            // the first run at which the sum passes the draw, else the last one with any weight
-            int run = INT32_MAX, heavy = -1;
-#pragma unroll
-            for (int k = kEach - 1; k >= 0; --k) {
-                if (k >= each || !(x[k].hi > 0)) continue;
-                if (lower + upto[k] > draw) run = lane * each + k;
-                if (heavy < 0) heavy = lane * each + k;
-            }
-            const int found = __reduce_min_sync(0xffffffffu, run), final = __reduce_max_sync(0xffffffffu, heavy);
-            const int chosen = found != INT32_MAX ? found : final;
-#pragma unroll
-            for (int k = 0; k < kEach; ++k)
-                if (k < each && lane * each + k == chosen) s.before = k ? lower + upto[k ? k - 1 : 0] : lower;
             if (lane == 0) {
                 s.draw = draw;
-                s.run = chosen;
-                s.bad = !(total.hi > 0 && total.hi <= 3.4e38f);
+                s.run = run;
+                s.bad = bad;
             }
         }
         // (no block leaves, or sums anew, while another may still read its sums)
@@ -327,39 +328,35 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
             a.out_tokens[row] = -1;
             report(a.status, MSGL_DEVERR_PROBS);
         }
-    } else if (s.run / kWarps == rank) {
-        // the token within the run: a vector a thread
-        const int n1 = min(s.run * length + length, vectors);
+    } else if (s.run >= 0) {
+        // the token within the run: four a thread
+        constexpr int kEach = 4;
+        const int n0 = (rank * kWarps + s.run) * length, i1 = r.token(min(n0 + length, vectors));
         Sum before = s.before;
-        for (int t = s.run * length; t < n1; t += kThreads) {
-            const int n = t + threadIdx.x;
-            float w[kN];
+        for (int t = r.token(n0); t < i1; t += kEach * kThreads) {
+            const int i = t + kEach * (int)threadIdx.x;
+            float w[kEach];
             Sum own{0.f, 0.f}, lower, ahead;
-            if (n < n1) {
-                const Vec<T> x = r.target(n), y = r.draft(n);
 #pragma unroll
-                for (int k = 0; k < kN; ++k) {
-                    w[k] = r.at(n, k, x, y);
-                    own = own + Sum{w[k], 0.f};
-                }
-            }
+            for (int k = 0; k < kEach; ++k) w[k] = i + k < i1 ? r.at(i + k) : 0.f;
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) own = own + Sum{w[k], 0.f};
             const Sum upto = warp_scan(own, lower);
             if (lane == 31) s.warp[warp] = upto;
             __syncthreads();
             const Sum warps = warp_scan(lane < kWarps ? s.warp[lane] : Sum{0.f, 0.f}, ahead);
             Sum sum = (before + shfl(ahead, warp)) + lower;
             before = before + shfl(warps, 31);
-            if (n < n1) {
+            if (own.hi > 0) {
                 int drawn = INT32_MAX, last = -1;
 #pragma unroll
-                for (int k = 0; k < kN; ++k) {
-                    if (!(w[k] > 0)) continue;
+                for (int k = 0; k < kEach; ++k) {
                     sum = sum + Sum{w[k], 0.f};
-                    last = r.token(n) + k;
-                    if (drawn == INT32_MAX && sum > s.draw) drawn = last;
+                    if (w[k] > 0) last = i + k;
+                    if (w[k] > 0 && drawn == INT32_MAX && sum > s.draw) drawn = i + k;
                 }
                 if (drawn != INT32_MAX) atomicMin(&s.drawn, drawn);
-                if (last >= 0) atomicMax(&s.last, last);
+                atomicMax(&s.last, last);
             }
             __syncthreads();
             if (s.drawn != INT32_MAX) break;
@@ -378,20 +375,20 @@ cudaError_t launch_verify_drafts(const VerifyArgs &a, cudaStream_t stream) {
     // 12.0; 64 (bf16) 24.2, 15.7, 14.7, 20.2; 128 36.6, 27.9, 31.2, 41.8; 37 (100003 tokens) 28.8, 18.7, 15.0, 18.0.
     // Blocks of 256 threads, four an SM, are at most 3% ahead (small batches) and up to 18% behind.
     const int sms = sm_count(), n = a.num_reqs;
-    int cluster = n <= sms * 4 / 19 ? 8 : n <= sms * 9 / 19 ? 4 : n <= sms ? 2 : 1;
-    while (cluster > 1 && a.vocab < cluster * 2048) cluster /= 2;
+    int log2_cluster = n <= sms * 4 / 19 ? 3 : n <= sms * 9 / 19 ? 2 : n <= sms ? 1 : 0;
+    while (log2_cluster > 0 && a.vocab < 2048 << log2_cluster) --log2_cluster;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)a.num_reqs * cluster);
+    cfg.gridDim = dim3((unsigned)a.num_reqs << log2_cluster);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.x = 1u << log2_cluster;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return a.bf16 ? cudaLaunchKernelEx(&cfg, verify_kernel<__nv_bfloat16>, a, cluster)
-                  : cudaLaunchKernelEx(&cfg, verify_kernel<float>, a, cluster);
+    return a.bf16 ? cudaLaunchKernelEx(&cfg, verify_kernel<__nv_bfloat16>, a, log2_cluster)
+                  : cudaLaunchKernelEx(&cfg, verify_kernel<float>, a, log2_cluster);
 }
 
 }  // namespace msgl
