@@ -13,12 +13,11 @@
 // launch; each waits for the one before, all of whose blocks did, before it touches
 // what that one wrote.
 //
-// Bound by latency up to some ten thousand entries (64 requests, 12 thousand pages: free 5.9 us;
-// 32 requests: compaction 9), by scattered atomics and the lists' stores beyond (half a million
-// entries, 740 thousand pages: free 14 us; 280 thousand and 550 thousand: compaction 18).
-// Both want many SMs: one cluster of 8 blocks that kept the bitmap in shared memory, two launches
-// less, took 6.5 us for the 64 requests, but 32 us for the half million entries (16 blocks 23: a
-// shared-memory atomic takes a cycle a lane).
+// Bound by scattered atomics and the lists' stores (half a million entries, 740 thousand pages:
+// free 14 us; 280 thousand and 550 thousand: compaction 18), which want many SMs: one cluster of 8
+// blocks with the bitmap in shared memory took 32 and 63 us (16 blocks 23 and 44: a shared-memory
+// atomic takes a cycle a lane).  Pools of up to 32 thousand pages under small tables are bound by latency and
+// launches, and such a cluster does them in one launch (small_pool_kernel).
 #include "kernels.h"
 
 namespace msgl {
@@ -178,45 +177,48 @@ __global__ void __launch_bounds__(256) begin_kernel(const PageMapArgs a) {
     if (a.stay_bits) a.stay_bits[w] = bits;
 }
 
+// Marks the pages of a unit in a bitmap (in global or in shared memory).
+__device__ __forceinline__ void mark_unit(const PageMapArgs &a, const Unit &x, uint32_t *bitmap) {
+    bool bad = false;
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) {
+        const bool has = x.has(k), fine = has && x.id[k] >= 0 && x.id[k] < a.num_pages;
+        bad |= has && !fine;
+        // Neighbouring pages, as a list in ascending order hands them out, are bits of one word, and the atomics on a
+        // word are taken one by one: where runs of lanes have a word in common, the first lane of a run marks for
+        // all (256 requests over 2048 common pages in a row: 315 -> 16 us).
+        const int word = fine ? x.id[k] >> 5 : -1 - lane;
+        uint32_t bits = 1u << (x.id[k] & 31);
+        bool marks = fine;
+        const uint32_t heads = __ballot_sync(0xffffffffu, lane == 0 | word != __shfl_up_sync(0xffffffffu, word, 1));
+        if (__popc(heads) <= 16) {
+            const uint32_t later = heads & ~((2u << lane) - 1);
+            const int end = later ? __ffs(later) - 1 : 32;   // of the lane's run
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_down_sync(0xffffffffu, bits, o);
+                if (lane + o < end) bits |= y;
+            }
+            marks = fine && heads >> lane & 1;
+        }
+        if (marks) atomicOr(bitmap + word, bits);
+    }
+    if (bad) report(a.status, MSGL_DEVERR_PAGE_RANGE);
+}
+
 __global__ void __launch_bounds__(kThreads) mark_kernel(const PageMapArgs a) {
     __shared__ Batch s;
     let_next_start();
-    for_entries(a, s, gridDim.x, true, [] { wait_for_last(); }, [&](const Unit &x) {
-        bool bad = false;
-        const int lane = threadIdx.x & 31;
-#pragma unroll
-        for (int k = 0; k < kPerLane; ++k) {
-            const bool has = x.has(k), fine = has && x.id[k] >= 0 && x.id[k] < a.num_pages;
-            bad |= has && !fine;
-            // Neighbouring pages, as a list in ascending order hands them out, are bits of one word, and the L2 takes
-            // the atomics on a word one by one: where runs of lanes have a word in common, the first lane of a run
-            // marks for all (256 requests over 2048 common pages in a row: 315 -> 16 us).
-            const int word = fine ? x.id[k] >> 5 : -1 - lane;
-            uint32_t bits = 1u << (x.id[k] & 31);
-            bool marks = fine;
-            const uint32_t heads = __ballot_sync(0xffffffffu, lane == 0 | word != __shfl_up_sync(0xffffffffu, word, 1));
-            if (__popc(heads) <= 16) {
-                const uint32_t later = heads & ~((2u << lane) - 1);
-                const int end = later ? __ffs(later) - 1 : 32;   // of the lane's run
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint32_t y = __shfl_down_sync(0xffffffffu, bits, o);
-                    if (lane + o < end) bits |= y;
-                }
-                marks = fine && heads >> lane & 1;
-            }
-            if (marks) atomicOr(a.used_bits + word, bits);
-        }
-        if (bad) report(a.status, MSGL_DEVERR_PAGE_RANGE);
-    });
+    for_entries(a, s, gridDim.x, true, [] { wait_for_last(); }, [&](const Unit &x) { mark_unit(a, x, a.used_bits); });
 }
 
 // ----------------------------------------------------------------- the lists
 
 // Sums over the whole block of up to three numbers; every thread gets them.  Not called twice without a barrier
 // of the caller's between.
-template <int N>
-__device__ __forceinline__ void block_sums(uint32_t (&x)[N], uint32_t (*part)[kListWarps]) {
+template <int W, int N>
+__device__ __forceinline__ void block_sums(uint32_t (&x)[N], uint32_t (*part)[W]) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = __reduce_add_sync(0xffffffffu, x[i]);
@@ -225,7 +227,7 @@ __device__ __forceinline__ void block_sums(uint32_t (&x)[N], uint32_t (*part)[kL
         for (int i = 0; i < N; ++i) part[i][warp] = x[i];
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = __reduce_add_sync(0xffffffffu, lane < kListWarps ? part[i][lane] : 0);
+    for (int i = 0; i < N; ++i) x[i] = __reduce_add_sync(0xffffffffu, lane < W ? part[i][lane] : 0);
 }
 
 // f(first word, four words of x, four of y) for all vectors of one or two bitmaps, by the whole block, as many of a
@@ -259,8 +261,8 @@ __device__ __forceinline__ void write_bits(uint32_t word, int64_t page, uint32_t
 }
 
 // -1 in out[from, to), by all threads of the grid.
-__device__ __forceinline__ void fill(int32_t *out, int64_t from, int64_t to) {
-    const int64_t me = (int64_t)blockIdx.x * kListThreads + threadIdx.x, all = (int64_t)gridDim.x * kListThreads;
+__device__ __forceinline__ void fill(int32_t *out, int64_t from, int64_t to, int threads) {
+    const int64_t me = (int64_t)blockIdx.x * threads + threadIdx.x, all = (int64_t)gridDim.x * threads;
     const int64_t head = min(to, from + (-((reinterpret_cast<uintptr_t>(out) >> 2) + (uint64_t)from) & 3));
     const int64_t quads = (to - head) / 4, tail = head + 4 * quads;
     if (me < head - from) out[from + me] = -1;
@@ -282,15 +284,15 @@ __device__ __forceinline__ Share share_of(const PageMapArgs &a) {
     s.w1 = min(s.w0 + each, s.words);
     return s;
 }
-static_assert(kListWarps == 32, "a lane for each warp's count");
 
-// x summed over the block's threads before this one; all: over the whole block.
-__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t *part, uint32_t &all) {
+// x summed over the threads before this one of a block of W warps; all: over the whole block.
+template <int W>
+__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t (&part)[W], uint32_t &all) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t upto = warp_scan(x);
     if (lane == 31) part[warp] = upto;
     __syncthreads();
-    const uint32_t w = part[lane];
+    const uint32_t w = lane < W ? part[lane] : 0;
     all = __reduce_add_sync(0xffffffffu, w);
     return __reduce_add_sync(0xffffffffu, lane < warp ? w : 0) + upto - x;
 }
@@ -307,13 +309,13 @@ __global__ void __launch_bounds__(kListThreads) free_list_kernel(const PageMapAr
         if (w < s.w0) n[0] += free;
     });
     uint32_t word = s.w0 + threadIdx.x < s.w1 ? ~__ldcg(a.used_bits + s.w0 + threadIdx.x) : 0;
-    block_sums(n, part);
+    block_sums<kListWarps>(n, part);
     if (blockIdx.x == 0 && threadIdx.x == 0) a.count_out[0] = (int32_t)n[1];
     uint32_t place = n[0], all;
     for (int64_t w0 = s.w0; w0 < s.w1; w0 += kListThreads) {
         if (w0 > s.w0) word = w0 + threadIdx.x < s.w1 ? ~__ldcg(a.used_bits + w0 + threadIdx.x) : 0;
         __syncthreads();
-        const uint32_t before = block_scan(__popc(word), part[0], all);
+        const uint32_t before = block_scan<kListWarps>(__popc(word), part[0], all);
         words[threadIdx.x] = word;
         places[threadIdx.x] = place + before;
         __syncthreads();
@@ -321,7 +323,7 @@ __global__ void __launch_bounds__(kListThreads) free_list_kernel(const PageMapAr
         for (int i = warp; i < mine; i += kListWarps) write_bits(words[i], 32 * (w0 + i), places[i], a.pages_out, 0xffffffffu);
         place += all;
     }
-    fill(a.pages_out, n[1], a.num_pages);
+    fill(a.pages_out, n[1], a.num_pages, kListThreads);
 }
 
 // The pages of word w in front of page `used`.
@@ -341,7 +343,7 @@ __global__ void __launch_bounds__(kListThreads) moves_kernel(const PageMapArgs a
     wait_for_last();
     uint32_t n[1] = {0};
     for_words<false>(a.used_bits, nullptr, s.words, [&](int64_t, const uint4 &x, const uint4 &) { n[0] += ones(x); });
-    block_sums(n, part);
+    block_sums<kListWarps>(n, part);
     const uint32_t used = n[0] - (uint32_t)(32 * s.words - a.num_pages);
     uint32_t m[3] = {0, 0, 0};                                    // moves before the share, holes before it, all moves
     __syncthreads();
@@ -367,7 +369,7 @@ __global__ void __launch_bounds__(kListThreads) moves_kernel(const PageMapArgs a
         stays = w < s.w1 ? __ldcg(a.stay_bits + w) : 0xffffffffu;
     };
     load(s.w0 + threadIdx.x);
-    block_sums(m, part);
+    block_sums<kListWarps>(m, part);
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         a.count_out[0] = (int32_t)m[2];
         a.used_out[0] = (int32_t)used;
@@ -378,8 +380,8 @@ __global__ void __launch_bounds__(kListThreads) moves_kernel(const PageMapArgs a
         if (w0 > s.w0) load(w);
         const uint32_t front = below(used, w), moves = u & ~stays & ~front, holes = ~u & front;
         __syncthreads();
-        const uint32_t moved = from + block_scan(__popc(moves), part[0], all_moves),
-                       filled = to + block_scan(__popc(holes), part[1], all_holes);
+        const uint32_t moved = from + block_scan<kListWarps>(__popc(moves), part[0], all_moves),
+                       filled = to + block_scan<kListWarps>(__popc(holes), part[1], all_holes);
         if (w < s.w1) a.moves_before[w] = moved;
         words[threadIdx.x] = make_uint4(moves, moved, holes, filled);
         used_words[threadIdx.x] = u;
@@ -395,8 +397,33 @@ __global__ void __launch_bounds__(kListThreads) moves_kernel(const PageMapArgs a
         from += all_moves;
         to += all_holes;
     }
-    fill(a.src, m[2], a.num_pages / 2);
-    fill(a.dst, m[2], a.num_pages / 2);
+    fill(a.src, m[2], a.num_pages / 2, kListThreads);
+    fill(a.dst, m[2], a.num_pages / 2, kListThreads);
+}
+
+// The new ids of a unit's pages: page `used` and those behind it that may move take the place of their number among
+// the moves (bits and numbers in global or in shared memory).
+__device__ __forceinline__ void rename_unit(const PageMapArgs &a, const Unit &x, int32_t used, const uint32_t *used_bits,
+                                            const uint32_t *stay_bits, const uint32_t *moves_before) {
+    // (an id that was given out here, in a row that is named twice, is in front of page `used` and stays)
+    int32_t to[kPerLane];                                      // the move's number, -1: none
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) {
+        const int32_t id = x.has(k) ? x.id[k] : -1;
+        const bool may = id >= used && id >= 0 && id < a.num_pages;
+        const int w = may ? id >> 5 : 0;
+        const uint32_t bit = 1u << (id & 31);
+        // (through L1: requests that share pages look up the same words)
+        const uint32_t moves = may ? used_bits[w] & ~stay_bits[w] : 0;
+        const uint32_t before = may ? moves_before[w] : 0;
+        to[k] = moves & bit ? (int32_t)(before + __popc(moves & (bit - 1) & ~below(used, w))) : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k)
+        if (to[k] >= 0) to[k] = a.dst[to[k]];
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k)
+        if (x.has(k) && (to[k] >= 0 || a.table_out != a.table)) a.table_out[x.place(a, k)] = to[k] >= 0 ? to[k] : x.id[k];
 }
 
 // The new ids: of all pages in the requests' tables (the first entry_blocks blocks), and of those that move in the
@@ -417,27 +444,150 @@ __global__ void __launch_bounds__(kThreads) rename_kernel(const PageMapArgs a, i
             wait_for_last();
             used = __ldcg(a.used_out);
         },
-        [&](const Unit &x) {
-            // (an id that was given out here, in a row that is named twice, is in front of page `used` and stays)
-            int32_t to[kPerLane];                              // the move's number, -1: none
+        [&](const Unit &x) { rename_unit(a, x, used, a.used_bits, a.stay_bits, a.moves_before); });
+}
+
+// --------------------------------------------------------------- small pools
+
+// All of it in one launch, for small pools and tables: a cluster of 8 blocks, each of which marks its share of the
+// entries in a bitmap in its own shared memory, joins all 8 (so that each knows every page), and lists and renames
+// its share.  Free pages of 64 requests in 15 thousand pages: 5.9 -> 4.9 us in a graph, launched one by one 8.3 ->
+// 6.4; compaction of 32 requests in 13 thousand: 9.2 -> 8.9 and 12.3 -> 10.3.  At 32 thousand pages the three or
+// four launches are level (free 6.9 to 7.4 against 5.4 to 6.9 in a graph, compaction 10.5 to 11.3 against 10.3 to 12.4),
+// at 60 thousand ahead (6.1 against 6.6, 11.3 against 13.1).
+constexpr int kCluster = 8, kSmallWords = 1024, kSmallUnits = 2 * kCluster * kWarps;
+static_assert(kSmallWords == 2 * kThreads, "two words a thread");
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
+// 8 bytes out of another block's shared memory.
+__device__ __forceinline__ uint2 ld_peer(const void *p, int rank) {
+    uint32_t at;
+    uint2 v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+    return v;
+}
+
+template <bool kCompact>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) small_pool_kernel(const PageMapArgs a) {
+    __shared__ __align__(16) uint32_t mine[kSmallWords], held[kSmallWords / kCluster], used[kSmallWords];
+    __shared__ __align__(16) uint32_t stays[kCompact ? kSmallWords : 4], places[kSmallWords], moved[kCompact ? kSmallWords : 4];
+    __shared__ uint32_t part[2][kWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = cluster_rank(), t2 = 2 * threadIdx.x;
+    const int words = (int)words_of(a.num_pages), share = (words / 2 + kCluster - 1) / kCluster * 2;
+    const int w0 = min(rank * share, words), w1 = min(w0 + share, words);
+    const int chunks = max(1, (a.table_width + kUnit - 1) / kUnit), units = a.num_reqs * chunks;
+    *reinterpret_cast<uint2 *>(mine + t2) = make_uint2(0, 0);
+    // the pages held beside the requests' and the bits behind the last page: this block's share
+    for (int w = w0 + threadIdx.x; w < w1; w += kThreads) {
+        const int64_t left = (int64_t)a.num_pages - 32 * w;
+        held[w - w0] = held_word(a, 32 * w) | (left >= 32 ? 0u : left > 0 ? 0xffffffffu << left : 0xffffffffu);
+    }
+    Unit x[2];
 #pragma unroll
-            for (int k = 0; k < kPerLane; ++k) {
-                const int32_t id = x.has(k) ? x.id[k] : -1;
-                const bool may = id >= used && id >= 0 && id < a.num_pages;
-                const int w = may ? id >> 5 : 0;
-                const uint32_t bit = 1u << (id & 31);
-                // (through L1: requests that share pages look up the same words)
-                const uint32_t moves = may ? a.used_bits[w] & ~a.stay_bits[w] : 0;
-                const uint32_t before = may ? a.moves_before[w] : 0;
-                to[k] = moves & bit ? (int32_t)(before + __popc(moves & (bit - 1) & ~below(used, w))) : -1;
-            }
+    for (int i = 0; i < 2; ++i) {
+        const int u = rank + kCluster * (warp + i * kWarps), b = u / chunks;
+        x[i].c0 = (u - b * chunks) * kUnit;
+        x[i].n = u < units ? entries_of(a, b, x[i].c0 == 0 && lane == 0, x[i].row) : 0;
+        x[i].load(a);
+    }
+    __syncthreads();
 #pragma unroll
-            for (int k = 0; k < kPerLane; ++k)
-                if (to[k] >= 0) to[k] = a.dst[to[k]];
+    for (int i = 0; i < 2; ++i)
+        if (rank + kCluster * (warp + i * kWarps) < units) mark_unit(a, x[i], mine);
+    cluster_arrive();
+    cluster_wait();
+    // two words a thread: of all blocks' marks, and of the block that looked up what is held there
+    uint32_t u[2] = {}, st[2] = {0xffffffffu, 0xffffffffu};
+    if (t2 < words) {
+        const uint2 h = ld_peer(held + t2 % share, t2 / share);
+        st[0] = h.x, st[1] = h.y;
+        uint2 v[kCluster];
 #pragma unroll
-            for (int k = 0; k < kPerLane; ++k)
-                if (x.has(k) && (to[k] >= 0 || a.table_out != a.table)) a.table_out[x.place(a, k)] = to[k] >= 0 ? to[k] : x.id[k];
-        });
+        for (int k = 0; k < kCluster; ++k) v[k] = ld_peer(mine + t2, k);
+#pragma unroll
+        for (int k = 0; k < kCluster; ++k) u[0] |= v[k].x, u[1] |= v[k].y;
+    }
+    // (no block leaves while another may still read its bitmap)
+    cluster_arrive();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) u[i] |= st[i];
+    if constexpr (!kCompact) {
+        uint32_t all, n = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) n += __popc(~u[i]);
+        uint32_t place = block_scan<kWarps>(n, part[0], all);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            used[t2 + i] = u[i];
+            places[t2 + i] = place;
+            place += __popc(~u[i]);
+        }
+        __syncthreads();
+        for (int w = w0 + warp; w < w1; w += kWarps) write_bits(~used[w], 32ll * w, places[w], a.pages_out, 0xffffffffu);
+        fill(a.pages_out, all, a.num_pages, kThreads);
+        if (rank == 0 && threadIdx.x == 0) a.count_out[0] = (int32_t)all;
+        cluster_wait();
+    } else {
+        uint32_t n[1] = {0};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) n[0] += __popc(u[i]);
+        block_sums<kWarps>(n, part);
+        const uint32_t total = n[0] - (uint32_t)(32 * kSmallWords - a.num_pages);
+        uint32_t go = 0, to = 0, all_go, all_to;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t front = below(total, t2 + i);
+            go += __popc(u[i] & ~st[i] & ~front);
+            to += __popc(~u[i] & front);
+        }
+        __syncthreads();
+        uint32_t from = block_scan<kWarps>(go, part[0], all_go), place = block_scan<kWarps>(to, part[1], all_to);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t front = below(total, t2 + i);
+            used[t2 + i] = u[i];
+            stays[t2 + i] = st[i];
+            moved[t2 + i] = from;
+            places[t2 + i] = place;
+            from += __popc(u[i] & ~st[i] & ~front);
+            place += __popc(~u[i] & front);
+        }
+        __syncthreads();
+        for (int w = w0 + warp; w < w1; w += kWarps) {
+            const uint32_t front = below(total, w), go = used[w] & ~stays[w] & ~front;
+            const int page = 32 * w + lane;
+            write_bits(go, 32ll * w, moved[w], a.src, all_go);
+            write_bits(~used[w] & front, 32ll * w, places[w], a.dst, all_go);
+            if (page < a.num_pages && !(go >> lane & 1)) a.pages_out[page] = used[w] >> lane & 1 ? page : -1;
+        }
+        fill(a.src, all_go, a.num_pages / 2, kThreads);
+        fill(a.dst, all_go, a.num_pages / 2, kThreads);
+        if (rank == 0 && threadIdx.x == 0) {
+            a.count_out[0] = (int32_t)all_go;
+            a.used_out[0] = (int32_t)total;
+        }
+        cluster_wait();
+        // (the moves of all blocks are there)
+        cluster_arrive();
+        cluster_wait();
+        for (uint32_t i = rank * kThreads + threadIdx.x; i < all_go; i += kCluster * kThreads)
+            a.pages_out[__ldcg(a.src + i)] = __ldcg(a.dst + i);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) rename_unit(a, x[i], (int32_t)total, used, stays, moved);
+    }
+}
+
+bool takes_small(const PageMapArgs &a) {
+    const int64_t chunks = a.table_width > 0 ? (a.table_width + kUnit - 1) / kUnit : 1;
+    return words_of(a.num_pages) <= kSmallWords && a.num_reqs * chunks <= kSmallUnits;
 }
 
 template <class... A>
@@ -493,12 +643,20 @@ static void set_workspace(PageMapArgs &a, void *workspace, bool compact) {
 }
 
 cudaError_t launch_free_pages(PageMapArgs a, void *workspace, cudaStream_t stream) {
+    if (takes_small(a)) {
+        small_pool_kernel<false><<<kCluster, kThreads, 0, stream>>>(a);
+        return cudaGetLastError();
+    }
     set_workspace(a, workspace, false);
     cudaError_t e = launch_marks(a, entry_blocks(a), stream);
     return e == cudaSuccess ? launch_after(free_list_kernel, list_blocks(a), kListThreads, stream, a) : e;
 }
 
 cudaError_t launch_compact_pages(PageMapArgs a, void *workspace, cudaStream_t stream) {
+    if (takes_small(a)) {
+        small_pool_kernel<true><<<kCluster, kThreads, 0, stream>>>(a);
+        return cudaGetLastError();
+    }
     set_workspace(a, workspace, true);
     const int blocks = entry_blocks(a);
     cudaError_t e = launch_marks(a, blocks, stream);
