@@ -596,10 +596,10 @@ PyObject *fork_requests(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// (pools: sequence of objects with k and v, page_size, src, dst, tokens | None, count | None, status | None,
+// (pools: sequence of objects with k, v and page_size, src, dst, tokens | None, count | None, status | None,
 //  stream | None)
 PyObject *copy_pages(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (!arity(n, 8)) return nullptr;
+    if (!arity(n, 7)) return nullptr;
     return guarded([&]() -> PyObject * {
         struct Ref {
             PyObject *p;
@@ -609,32 +609,33 @@ PyObject *copy_pages(PyObject *, PyObject *const *a, Py_ssize_t n) {
             Ref(const Ref &) = delete;
             ~Ref() { Py_DECREF(p); }
         };
-        static PyObject *const names[2] = {PyUnicode_InternFromString("k"), PyUnicode_InternFromString("v")};
+        static PyObject *const names[3] = {PyUnicode_InternFromString("k"), PyUnicode_InternFromString("v"),
+                                           PyUnicode_InternFromString("page_size")};
         int dev = -1;
-        const at::Tensor &src = checked(a[2], "src", at::kInt, dev);
-        const at::Tensor &dst = checked(a[3], "dst", at::kInt, dev);
+        const at::Tensor &src = checked(a[1], "src", at::kInt, dev);
+        const at::Tensor &dst = checked(a[2], "dst", at::kInt, dev);
         const int64_t N = src.numel();
         if (dst.numel() != N) refuse("%s must have an entry for each of src", "dst");
-        const int32_t *tokens = entries(a[4], "tokens", N, dev), *count = entries(a[5], "count", 1, dev);
-        const int32_t ps = integer32(a[1], "page_size");
+        const int32_t *tokens = entries(a[3], "tokens", N, dev), *count = entries(a[4], "count", 1, dev);
         const Ref seq(PySequence_Fast(a[0], "pools must be a sequence of KVPool"));
         const Py_ssize_t pools = PySequence_Fast_GET_SIZE(seq.p);
         std::vector<msgl_kv_pool> c((size_t)pools);
         for (Py_ssize_t i = 0; i < pools; ++i) {
             PyObject *pool = PySequence_Fast_GET_ITEM(seq.p, i);
-            const Ref ko(PyObject_GetAttr(pool, names[0])), vo(PyObject_GetAttr(pool, names[1]));
+            const Ref ko(PyObject_GetAttr(pool, names[0])), vo(PyObject_GetAttr(pool, names[1])),
+                po(PyObject_GetAttr(pool, names[2]));
             const at::Tensor &k = checked(ko.p, "k_pool", at::kBFloat16, dev), &v = checked(vo.p, "v_pool", at::kBFloat16, dev);
             if (k.dim() != 3 || v.sizes() != k.sizes()) refuse("%s and v_pool must both be [num_slots, Hkv, D]", "k_pool");
             c[i].k_pool = k.data_ptr();
             c[i].v_pool = v.data_ptr();
             c[i].num_slots = k.size(0);
-            c[i].page_size = ps;
+            c[i].page_size = integer32(po.p, "page_size");
             c[i].num_kv_heads = size32(k.size(1), "k_pool");
             c[i].head_dim = size32(k.size(2), "k_pool");
         }
-        uint32_t *status = status_ptr(a[6], dev);
+        uint32_t *status = status_ptr(a[5], dev);
         c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
-        const c10::cuda::CUDAStream stream = stream_of(a[7], dev);
+        const c10::cuda::CUDAStream stream = stream_of(a[6], dev);
         const int32_t pairs = size32(N, "src"), num_pools = size32(pools, "pools");
         msgl_status rc;
         {

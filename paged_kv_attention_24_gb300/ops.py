@@ -655,11 +655,9 @@ def copy_pages(pools, src: torch.Tensor, dst: torch.Tensor, tokens: Optional[tor
     ``tokens`` int32 [N]: only the first of a page's slots; ``count`` int32 [1]: only the first pairs.
     Pairs of -1 are passed over (msgl_copy_pages).
     """
-    pools = [pools] if isinstance(pools, KVPool) else pools
-    ps = pools[0].page_size if pools else 1
-    if any(p.page_size != ps for p in pools):
-        raise ValueError("pools must have one page_size")
-    rc = (_native or _binding()).copy_pages(pools, ps, src, dst, tokens, count, status, _handle(stream))
+    if isinstance(pools, KVPool):
+        pools = (pools,)
+    rc = (_native or _binding()).copy_pages(pools, src, dst, tokens, count, status, _handle(stream))
     if rc is not None:
         _check(rc, "msgl_copy_pages")
 
