@@ -15,11 +15,13 @@
 //
 // Bound by HBM for large batches (one row of p, and of q where a draft was refused,
 // is read once), by latency for small ones.  A cluster of blocks takes a request,
-// so that a row is read by many SMs; each warp sums a run of neighbouring tokens,
-// the blocks exchange their warps' sums, and only the run in which the draw falls
-// is read again (out of L2).  128 requests over 131072 tokens of fp32: 27 us (the rows alone
-// 18 us at the copy rate; lookups in front, exchange and draw behind take the rest); 4 over
-// 50001 of bf16: 6.8 us.  With 64-bit sums: 72 and 14 us.
+// so that a row is read by many SMs; each warp sums a run of neighbouring tokens and
+// writes its sum into the shared memory of all the cluster's blocks, each of which
+// then finds the run in which the draw falls; only that one is read again (out of L2), by
+// the block that summed it.  128 requests over 131072 tokens of fp32: 24.3 us (the rows
+// alone 18 us at the copy rate; lookups in front, exchange and draw behind take the
+// rest); 4 over 50001 of bf16: 5.6 us.  With 64-bit sums: 72 and 14 us.  Sums sent by
+// st.async and waited for by one warp, in place of the cluster's barrier: 25.8 and 5.3.
 #include "kernels.h"
 
 namespace msgl {
@@ -58,6 +60,13 @@ __device__ __forceinline__ Sum operator+(const Sum &a, const Sum &b) {
     return settled(s, two_sum_error(a.hi, b.hi, s) + (a.lo + b.lo));
 }
 
+// The same without settling (lo a few units of hi's last place), for sums of a few that settle at the end: a third
+// fewer instructions in the chains behind the rows (6.0 -> 5.5 us for 4 requests).
+__device__ __forceinline__ Sum loose(const Sum &a, const Sum &b) {
+    const float s = a.hi + b.hi;
+    return Sum{s, two_sum_error(a.hi, b.hi, s) + (a.lo + b.lo)};
+}
+
 __device__ __forceinline__ Sum times(float u, const Sum &a) {
     const float p = u * a.hi;
     return settled(p, fmaf(u, a.lo, fmaf(u, a.hi, -p)));
@@ -77,8 +86,9 @@ __device__ __forceinline__ Sum warp_scan(Sum x, Sum &before) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const Sum y{__shfl_up_sync(0xffffffffu, x.hi, o), __shfl_up_sync(0xffffffffu, x.lo, o)};
-        if (lane >= o) x = y + x;
+        if (lane >= o) x = loose(y, x);
     }
+    x = settled(x.hi, x.lo);
     before = Sum{__shfl_up_sync(0xffffffffu, x.hi, 1), __shfl_up_sync(0xffffffffu, x.lo, 1)};
     if (lane == 0) before = Sum{0.f, 0.f};
     return x;
@@ -162,10 +172,13 @@ struct Row {
 };
 
 struct Shared {
-    Sum sums[kWarps], total;         // of this block's runs, and of the block
+    Sum runs[8 * kWarps];            // the sums of all the cluster's runs
     Sum warp[kWarps];
     Sum draw, before;                // u * total; the weights in front of the drawn run
-    int accepted, run, drawn, last;  // run: of this block's, -1 when the draw is in another block
+    int first, drafts;               // the request's first row, its drafts
+    int accepted, refused;           // drafts that stand, the token of the one that does not
+    float sample;
+    int run, last;                   // the drawn run; the last token with any weight in the tiles gone by
     bool bad;
 };
 
@@ -177,6 +190,7 @@ __device__ __forceinline__ Sum run_sum(const Row<T> &r, int n0, int n1) {
     // (four sums, so that one does not wait for the last; as two pairs, by the instructions that add two floats at once,
     // 39 us in place of 27 for 128 requests)
     float hi[4] = {}, lo[4] = {};
+    // (four vectors of each row on the way; 128 requests: three 25.2 us, two 26.6, six, which spill, 29.2)
     for (int n = n0 + lane; n < n1; n += 32 * kUnroll) {
         Vec<T> x[kUnroll], y[kUnroll];
 #pragma unroll
@@ -195,24 +209,25 @@ __device__ __forceinline__ Sum run_sum(const Row<T> &r, int n0, int n1) {
                     hi[k % 4] = s;
                 }
     }
-    Sum sum = (settled(hi[0], lo[0]) + settled(hi[1], lo[1])) + (settled(hi[2], lo[2]) + settled(hi[3], lo[3]));
+    Sum sum = loose(loose(Sum{hi[0], lo[0]}, Sum{hi[1], lo[1]}), loose(Sum{hi[2], lo[2]}, Sum{hi[3], lo[3]}));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
-        sum = sum + Sum{__shfl_xor_sync(0xffffffffu, sum.hi, o), __shfl_xor_sync(0xffffffffu, sum.lo, o)};
-    return sum;
+        sum = loose(sum, Sum{__shfl_xor_sync(0xffffffffu, sum.hi, o), __shfl_xor_sync(0xffffffffu, sum.lo, o)});
+    return settled(sum.hi, sum.lo);
 }
 
-// How many drafts stand: the first one that does not, or all.
+// How many drafts stand: the first one that does not (its token in `refused`), or all.
 template <class T>
-__device__ __forceinline__ int standing(const VerifyArgs &a, int first, int drafts, bool &bad_token) {
+__device__ __forceinline__ int standing(const VerifyArgs &a, int first, int drafts, int &refused, bool &bad_token) {
     const int lane = threadIdx.x & 31;
     const T *p = static_cast<const T *>(a.target), *q = static_cast<const T *>(a.draft);
     for (int i0 = 0; i0 < drafts; i0 += 32) {
         const int i = i0 + lane;
         bool ok = true, bad = false;
+        int x = -1;
         if (i < drafts) {
             const int64_t row = first + i;
-            const int x = __ldg(a.tokens + row + 1);
+            x = __ldg(a.tokens + row + 1);
             const float u = __ldg(a.accept_u + row);
             bad = x < 0 || x >= a.vocab;
             ok = false;
@@ -224,9 +239,58 @@ __device__ __forceinline__ int standing(const VerifyArgs &a, int first, int draf
         }
         bad_token |= __any_sync(0xffffffffu, bad);
         const uint32_t fails = ~__ballot_sync(0xffffffffu, ok);
-        if (fails) return i0 + __ffs(fails) - 1;
+        if (fails) {
+            refused = __shfl_sync(0xffffffffu, x, __ffs(fails) - 1);
+            return i0 + __ffs(fails) - 1;
+        }
     }
+    refused = -1;
     return drafts;
+}
+
+// The token at which the running sum passes the draw, of tokens [i0, i1) of the drawn run, E a thread in each tile:
+// the block's warps scan a tile, and the warp that the draw falls into goes on to its lanes.  By the whole block.
+template <int E, class T>
+__device__ __forceinline__ void draw_token(const Row<T> &r, Shared &s, int i0, int i1, int32_t *out) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Sum draw = s.draw;
+    Sum before = s.before;
+    for (int t = i0;; t += E * kThreads) {
+        const int i = t + E * (int)threadIdx.x;
+        float w[E];
+        Sum own{0.f, 0.f}, lower, ahead;
+#pragma unroll
+        for (int k = 0; k < E; ++k) w[k] = i + k < i1 ? r.at(i + k) : 0.f;
+#pragma unroll
+        for (int k = 0; k < E; ++k) own = loose(own, Sum{w[k], 0.f});
+        const Sum upto = warp_scan(own, lower);
+        if (lane == 31) s.warp[warp] = upto;
+        __syncthreads();
+        const Sum x = lane < kWarps ? s.warp[lane] : Sum{0.f, 0.f}, warps = warp_scan(x, ahead);
+        // (where rounding lets no token pass, the last one with any weight counts)
+        const int chosen = drawn_lane(x, before + warps, draw);
+        const bool passes = __any_sync(0xffffffffu, x.hi > 0 && before + warps > draw), ends = t + E * kThreads >= i1;
+        if (warp == chosen) {
+            const Sum base = before + shfl(ahead, warp);
+            if (lane == drawn_lane(own, base + upto, draw)) {
+                Sum sum = base + lower;
+                int drawn = -1, last = -1;
+#pragma unroll
+                for (int k = 0; k < E; ++k) {
+                    sum = sum + Sum{w[k], 0.f};
+                    if (w[k] > 0) last = i + k;
+                    if (w[k] > 0 && drawn < 0 && sum > draw) drawn = i + k;
+                }
+                if (passes || ends) *out = drawn >= 0 ? drawn : last;
+                else s.last = last;
+            }
+        } else if (chosen < 0 && ends && threadIdx.x == 0) {
+            *out = s.last;
+        }
+        if (passes || ends) return;
+        before = before + shfl(warps, 31);
+        __syncthreads();
+    }
 }
 
 template <class T>
@@ -234,6 +298,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
     const int cluster = 1 << log2_cluster, log2_runs = log2_cluster + 4;
     static_assert(kWarps == 16, "a block of 16 runs");
     __shared__ Shared s;
+    // (the others have to be running before this block writes into their shared memory)
+    asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = cluster_rank(), b = blockIdx.x >> log2_cluster;
     const int first = __ldg(a.cu_ext + b), end = __ldg(a.cu_ext + b + 1);
@@ -247,42 +313,53 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
         }
         return;
     }
-    const int drafts = end - first - 1;
-    const float sample = __ldg(a.sample_u + b);
     if (warp == 0) {
+        const float sample = __ldg(a.sample_u + b);
         bool bad = false;
-        const int n = standing<T>(a, first, drafts, bad);
+        int token;
+        const int n = standing<T>(a, first, end - first - 1, token, bad);
         if (lane == 0) {
+            s.first = first;
+            s.drafts = end - first - 1;
             s.accepted = n;
-            s.drawn = INT32_MAX;
+            s.refused = token;
+            s.sample = sample;
             s.last = -1;
             if (bad && rank == 0) report(a.status, MSGL_DEVERR_TOKEN);
         }
     }
     __syncthreads();
-    const int taken = s.accepted, row = first + taken;
-    const bool refused = taken < drafts;
-    const T *p = static_cast<const T *>(a.target) + row * a.target_stride;
-    Row<T> r;
-    r.set(p, refused && a.draft ? static_cast<const T *>(a.draft) + row * a.draft_stride : nullptr,
-          refused && !a.draft ? __ldg(a.tokens + row + 1) : -1, a.vocab);
-    const int vectors = r.vectors();
-    const int length = ((vectors - 1) >> log2_runs) / 32 * 32 + 32;       // whole rounds of a warp
-    const int mine = rank * kWarps + warp;
-    for (bool second = false;; second = true) {
+    // What a request is about is looked up in shared memory where it is needed: kept in registers over the sums it was
+    // spilled, and the spilled registers came back out of L2, 700 cycles each.
+    auto row_of = [&](bool residual) {
+        const int taken = s.accepted, row = s.first + taken;
+        const bool refused = residual && taken < s.drafts;
+        Row<T> r;
+        r.set(static_cast<const T *>(a.target) + row * a.target_stride,
+              refused && a.draft ? static_cast<const T *>(a.draft) + row * a.draft_stride : nullptr,
+              refused && !a.draft ? s.refused : -1, a.vocab);
+        return r;
+    };
+    auto length_of = [&](int vectors) { return ((vectors - 1) >> log2_runs) / 32 * 32 + 32; };   // whole rounds of a warp
+    bool second = false;
+    for (;; second = true) {
+        const Row<T> r = row_of(!second);
+        const int vectors = r.vectors(), length = length_of(vectors), mine = rank * kWarps + warp;
         const int n0 = (int)min((int64_t)mine * length, (int64_t)vectors), n1 = min(n0 + length, vectors);
         const Sum sum = run_sum(r, n0, n1);
-        if (lane == 0) s.sums[warp] = sum;
-        __syncthreads();
-        Sum x{0.f, 0.f}, upto, lower;
-        if (warp == 0) {
-            if (lane < kWarps) x = s.sums[lane];
-            upto = warp_scan(x, lower);
-            if (lane == 31) s.total = upto;
+        // every block gets every run's sum
+        if (!second) cluster_wait();
+        if (lane < cluster) {
+            uint32_t at;
+            asm("mapa.shared::cluster.u32 %0, %1, %2;"
+                : "=r"(at)
+                : "r"((uint32_t)__cvta_generic_to_shared(&s.runs[mine])), "r"(lane));
+            asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(sum.hi), "f"(sum.lo) : "memory");
         }
         cluster_arrive();
         if (rank == 0 && !second) {
             // (written here, where the block waits anyway)
+            const int first = s.first, taken = s.accepted, drafts = s.drafts;
             for (int i = threadIdx.x; i <= drafts; i += kThreads)
                 if (i != taken) a.out_tokens[first + i] = i < taken ? __ldg(a.tokens + first + i + 1) : -1;
             if (threadIdx.x == kThreads - 1) {
@@ -291,81 +368,57 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
             }
         }
         cluster_wait();
-        // Every block goes through all blocks' sums in the same order and so comes to the same end; the one that
-        // the draw falls into goes on to its runs.  (One warp over all runs' sums at once, four a lane, was more
-        // code than it was worth: 7.2 against 6.8 us for 4 requests.  Rolled scans: 8.0.)
+        // every block goes through them in the same order and so comes to the same end: up to four neighbours a lane
         if (warp == 0) {
-            Sum y{0.f, 0.f}, ahead;
-            if (lane < cluster) {
-                uint32_t at;
-                asm("mapa.shared::cluster.u32 %0, %1, %2;"
-                    : "=r"(at)
-                    : "r"((uint32_t)__cvta_generic_to_shared(&s.total)), "r"(lane));
-                asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(y.hi), "=f"(y.lo) : "r"(at) : "memory");
+            const int log2_each = max(log2_runs - 5, 0), i0 = lane << log2_each;
+            Sum x[4], sum{0.f, 0.f}, lower;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                x[k] = Sum{0.f, 0.f};
+                if (k < 1 << log2_each && i0 + k < 1 << log2_runs) x[k] = s.runs[i0 + k];
+                if (k < 1 << log2_each) sum = loose(sum, x[k]);
             }
-            const Sum blocks = warp_scan(y, ahead), total = shfl(blocks, 31), draw = times(sample, total);
-            const bool bad = !(total.hi > 0 && total.hi <= 3.4e38f);
-            int run = -1;
-            if (!bad && drawn_lane(y, blocks, draw) == rank) {
-                const Sum base = shfl(ahead, rank);
-                run = drawn_lane(x, base + upto, draw);
-                if (lane == run) s.before = base + lower;
-            }
-            if (lane == 0) {
+            const Sum upto = warp_scan(sum, lower), total = shfl(upto, 31), draw = times(s.sample, total);
+            const int chosen = drawn_lane(sum, upto, draw);
+            if (lane == max(chosen, 0)) {
+                int run = -1;
+                bool passed = false;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const Sum with = lower + x[k];
+                    if (x[k].hi > 0 && !passed) {
+                        run = i0 + k;
+                        s.before = lower;
+                        passed = with > draw;
+                    }
+                    lower = with;
+                }
                 s.draw = draw;
                 s.run = run;
-                s.bad = bad;
+                s.bad = !(total.hi > 0 && total.hi <= 3.4e38f);
             }
         }
-        // (no block leaves, or sums anew, while another may still read its sums)
-        cluster_arrive();
         __syncthreads();
         // nothing left over (p nowhere above q): the target's own row
-        if (second || !s.bad || !refused) break;
+        if (second || !s.bad || s.accepted == s.drafts) break;
+        // (no block sums anew while another may still look at its sums)
+        cluster_arrive();
         cluster_wait();
-        r.set(p, nullptr, -1, a.vocab);
     }
+    int32_t *out = a.out_tokens + s.first + s.accepted;
     if (s.bad) {
         if (rank == 0 && threadIdx.x == 0) {
-            a.out_tokens[row] = -1;
+            *out = -1;
             report(a.status, MSGL_DEVERR_PROBS);
         }
-    } else if (s.run >= 0) {
-        // the token within the run: four a thread
-        constexpr int kEach = 4;
-        const int n0 = (rank * kWarps + s.run) * length, i1 = r.token(min(n0 + length, vectors));
-        Sum before = s.before;
-        for (int t = r.token(n0); t < i1; t += kEach * kThreads) {
-            const int i = t + kEach * (int)threadIdx.x;
-            float w[kEach];
-            Sum own{0.f, 0.f}, lower, ahead;
-#pragma unroll
-            for (int k = 0; k < kEach; ++k) w[k] = i + k < i1 ? r.at(i + k) : 0.f;
-#pragma unroll
-            for (int k = 0; k < kEach; ++k) own = own + Sum{w[k], 0.f};
-            const Sum upto = warp_scan(own, lower);
-            if (lane == 31) s.warp[warp] = upto;
-            __syncthreads();
-            const Sum warps = warp_scan(lane < kWarps ? s.warp[lane] : Sum{0.f, 0.f}, ahead);
-            Sum sum = (before + shfl(ahead, warp)) + lower;
-            before = before + shfl(warps, 31);
-            if (own.hi > 0) {
-                int drawn = INT32_MAX, last = -1;
-#pragma unroll
-                for (int k = 0; k < kEach; ++k) {
-                    sum = sum + Sum{w[k], 0.f};
-                    if (w[k] > 0) last = i + k;
-                    if (w[k] > 0 && drawn == INT32_MAX && sum > s.draw) drawn = i + k;
-                }
-                if (drawn != INT32_MAX) atomicMin(&s.drawn, drawn);
-                atomicMax(&s.last, last);
-            }
-            __syncthreads();
-            if (s.drawn != INT32_MAX) break;
-        }
-        if (threadIdx.x == 0) a.out_tokens[row] = s.drawn != INT32_MAX ? s.drawn : s.last;
+    } else if (s.run / kWarps == rank) {
+        const Row<T> r = row_of(!second);
+        const int vectors = r.vectors(), length = length_of(vectors), n0 = s.run * length;
+        const int i0 = max(r.token(n0), 0), i1 = min(r.token(min(n0 + length, vectors)), a.vocab);
+        if (i1 - i0 <= kThreads) draw_token<1>(r, s, i0, i1, out);
+        else if (i1 - i0 <= 2 * kThreads) draw_token<2>(r, s, i0, i1, out);
+        else draw_token<8>(r, s, i0, i1, out);
     }
-    cluster_wait();
 }
 
 }  // namespace
@@ -373,8 +426,9 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
 cudaError_t launch_verify_drafts(const VerifyArgs &a, cudaStream_t stream) {
     // As many blocks a request as all run at once, so that none begins its chain of lookups behind another's
     // row: two blocks an SM, in GPCs of 19 SMs on average, which hold 4 clusters of 8 blocks, 9 of 4 or 19 of 2;
-    // and at least 2048 tokens a block.  131072 tokens, us with 1, 2, 4, 8 blocks: 16 requests 33.6, 20.2, 13.5,
-    // 12.0; 64 (bf16) 24.2, 15.7, 14.7, 20.2; 128 36.6, 27.9, 31.2, 41.8; 37 (100003 tokens) 28.8, 18.7, 15.0, 18.0.
+    // and at least 2048 tokens a block.  131072 tokens, us with 1, 2, 4, 8 blocks: 16 requests 29.5, 17.4, 11.5, 9.4;
+    // 37 (100003 tokens) 25.0, 15.8, 13.5, 13.7; 64 (bf16) 22.4, 13.7, 12.8, 15.3; 128 32.2, 24.6, 27.4, 32.5; 300
+    // (32000 tokens) 16.2, 19.6, 27.9, 45.9.
     // Blocks of 256 threads, four an SM, are at most 3% ahead (small batches) and up to 18% behind.
     const int sms = sm_count(), n = a.num_reqs;
     int log2_cluster = n <= sms * 4 / 19 ? 3 : n <= sms * 9 / 19 ? 2 : n <= sms ? 1 : 0;
