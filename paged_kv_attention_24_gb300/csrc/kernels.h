@@ -157,7 +157,8 @@ struct PageMapArgs {
     int32_t *count_out;                   // [1]: free pages; compact: pages that move
     int32_t *table_out, *src, *dst, *used_out;   // compact
     int32_t out_stride;
-    uint32_t *used_bits, *stay_bits, *moves_before;   // in the workspace (set by the launchers)
+    uint32_t *used_bits, *stay_bits;      // in the workspace (set by the launchers): by words of 32 pages
+    uint2 *moves;                         // compact: which pages of a word move, and how many before them
     uint32_t *status;
 };
 size_t page_map_workspace_bytes(int32_t num_pages);

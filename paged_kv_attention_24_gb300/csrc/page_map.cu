@@ -8,15 +8,19 @@
 //
 // A bitmap of the pool, one bit a page, in the workspace: set from `held`, then every
 // table entry marks its page, then each block lists its share of the pages, its place in the
-// lists from a count of all bits before its own (the bitmap of a million pages is 128 KB,
-// which every block reads out of L2).  The kernels follow each other by programmatic dependent
+// lists from a count of all bits before its own, for which a cluster of 8 blocks goes over the
+// whole bitmap once (128 KB for a million pages, out of L2; each block by itself: compaction
+// 17.9 us in place of 16.2).  The kernels follow each other by programmatic dependent
 // launch; each waits for the one before, all of whose blocks did, before it touches
 // what that one wrote.
 //
 // Bound by scattered atomics and the lists' stores (half a million entries, 740 thousand pages:
-// free 14 us; 280 thousand and 550 thousand: compaction 18), which want many SMs: one cluster of 8
+// free 13.4 us; 280 thousand and 550 thousand: compaction 14.6; some 4 us of each for the atomics, 120 to
+// 130 a nanosecond, and 1 to 3 more or less by where the bitmap lies), which want many SMs: one cluster of 8
 // blocks with the bitmap in shared memory took 32 and 63 us (16 blocks 23 and 44: a shared-memory
-// atomic takes a cycle a lane).  Pools of up to 32 thousand pages under small tables are bound by latency and
+// atomic takes a cycle a lane).  A byte a page, written without atomics, is no faster to mark
+// (10.9 against 8.5 us for half a million random pages, with the clearing of the map) and eight times as much to
+// count.  Pools of up to 32 thousand pages under small tables are bound by latency and
 // launches, and such a cluster does them in one launch (small_pool_kernel).
 #include "kernels.h"
 
@@ -26,12 +30,20 @@ namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBatch = kThreads;                     // requests looked at together
-constexpr int kListThreads = 1024, kListWarps = kListThreads / 32;
+constexpr int kCluster = 8;                          // blocks that count together
 constexpr int kPerLane = 8;
 constexpr int kUnit = 32 * kPerLane;                 // table entries of one warp's turn
 
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 // x summed over the warp's lanes up to this one.
 __device__ __forceinline__ uint32_t warp_scan(uint32_t x) {
@@ -87,8 +99,10 @@ struct Unit {
 template <class R, class F>
 __device__ __forceinline__ void for_entries(const PageMapArgs &a, Batch &s, int blocks, bool tell, R ready, F f) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int first = blockIdx.x * kWarps + warp, warps = blocks * kWarps;
     const int chunks = max(1, (a.table_width + kUnit - 1) / kUnit);
+    // (the chunks of a row, of which the last are often empty, to different blocks: free 13.8 -> 13.4 us; rows of one
+    // chunk to warps that are neighbours, as their lengths are: 20000 of them 11.7 us, else 15.5)
+    const int first = chunks > 1 ? warp * blocks + blockIdx.x : blockIdx.x * kWarps + warp, warps = blocks * kWarps;
     Unit x;
     x.n = 0;
     const int64_t rounds = ((int64_t)a.num_reqs * chunks + warps - 1) / warps;
@@ -209,8 +223,7 @@ __device__ __forceinline__ void mark_unit(const PageMapArgs &a, const Unit &x, u
 
 __global__ void __launch_bounds__(kThreads) mark_kernel(const PageMapArgs a) {
     __shared__ Batch s;
-    let_next_start();
-    for_entries(a, s, gridDim.x, true, [] { wait_for_last(); }, [&](const Unit &x) { mark_unit(a, x, a.used_bits); });
+    for_entries(a, s, gridDim.x, true, [] { wait_for_last(); let_next_start(); }, [&](const Unit &x) { mark_unit(a, x, a.used_bits); });
 }
 
 // ----------------------------------------------------------------- the lists
@@ -228,27 +241,6 @@ __device__ __forceinline__ void block_sums(uint32_t (&x)[N], uint32_t (*part)[W]
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = __reduce_add_sync(0xffffffffu, lane < W ? part[i][lane] : 0);
-}
-
-// f(first word, four words of x, four of y) for all vectors of one or two bitmaps, by the whole block, as many of a
-// thread's loads together as registers allow: one round up to 786 (655) thousand pages (y: zeros where it is not given).
-template <bool kBoth, class F>
-__device__ __forceinline__ void for_words(const uint32_t *x, const uint32_t *y, int64_t words, F f) {
-    constexpr int kLoads = kBoth ? 5 : 6;
-    for (int64_t v0 = threadIdx.x; v0 < words / 4; v0 += kLoads * kListThreads) {
-        uint4 r[kLoads], s[kLoads];
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int64_t v = v0 + i * kListThreads;
-            s[i] = make_uint4(0, 0, 0, 0);
-            if (v >= words / 4) continue;
-            r[i] = __ldcg(reinterpret_cast<const uint4 *>(x) + v);
-            if (kBoth) s[i] = __ldcg(reinterpret_cast<const uint4 *>(y) + v);
-        }
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            if (v0 + i * kListThreads < words / 4) f(4 * (v0 + i * kListThreads), r[i], s[i]);
-    }
 }
 
 __device__ __forceinline__ uint32_t ones(const uint4 &x) { return __popc(x.x) + __popc(x.y) + __popc(x.z) + __popc(x.w); }
@@ -270,20 +262,65 @@ __device__ __forceinline__ void fill(int32_t *out, int64_t from, int64_t to, int
     for (int64_t i = me; i < quads; i += all) *reinterpret_cast<int4 *>(out + head + 4 * i) = make_int4(-1, -1, -1, -1);
 }
 
-// A block's share of the words.  It goes over them 1024 at a time: a thread looks at one, a scan says where its pages
-// go, and then each warp writes every 32nd word's.  (Every warp scanning for itself saves two barriers, but 32 warps
-// with the same scan keep the SM's issue slots busy: 6.7 against 5.7 us for the list of 740 thousand pages.)
+// A block's share of the words.  It goes over them a block of threads at a time: a thread looks at one, a scan says where
+// its pages go, and then each warp writes every 16th word's.  (Every warp scanning for itself saves two barriers, but
+// warps with the same scan keep the SM's issue slots busy: 6.7 against 5.7 us for the list of 740 thousand pages.)
 struct Share {
-    int64_t w0, w1, words;
+    int64_t w0, w1, words, first;    // first: where the cluster's shares begin
 };
-__device__ __forceinline__ Share share_of(const PageMapArgs &a) {
+__device__ __forceinline__ Share share_of(const PageMapArgs &a, int rank) {
     Share s;
     s.words = words_of(a.num_pages);
     const int64_t each = ((s.words + gridDim.x - 1) / gridDim.x + 31) / 32 * 32;
     s.w0 = min((int64_t)blockIdx.x * each, s.words);
     s.w1 = min(s.w0 + each, s.words);
+    s.first = min((int64_t)(blockIdx.x - rank) * each, s.words);
     return s;
 }
+
+// The part of one or two bitmaps that a block counts for its cluster: an eighth of the vectors.  The first kHold a
+// thread stay in its registers from count to count (all of them up to a million pages).
+template <bool kBoth>
+struct Slice {
+    static constexpr int kHold = 2;
+    const uint4 *x, *y;
+    int64_t v0, v1;
+    uint4 r[kHold], s[kHold];
+    __device__ __forceinline__ uint4 at(const uint4 *from, int64_t v) const {
+        return from && v < v1 ? __ldcg(from + v) : make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void load(const uint32_t *x_, const uint32_t *y_, int64_t words, int rank) {
+        x = reinterpret_cast<const uint4 *>(x_);
+        y = kBoth ? reinterpret_cast<const uint4 *>(y_) : nullptr;
+        const int64_t each = (words / 4 + kCluster - 1) / kCluster;
+        v0 = min(rank * each, words / 4) + threadIdx.x;
+        v1 = min((rank + 1) * each, words / 4);
+#pragma unroll
+        for (int i = 0; i < kHold; ++i) {
+            r[i] = at(x, v0 + i * kThreads);
+            if (kBoth) s[i] = at(y, v0 + i * kThreads);
+        }
+    }
+    // f(first word, four words of x, four of y)
+    template <class F>
+    __device__ __forceinline__ void each(bool both, F f) const {
+#pragma unroll
+        for (int i = 0; i < kHold; ++i)
+            if (v0 + i * kThreads < v1) f(4 * (v0 + i * kThreads), r[i], s[i]);
+        constexpr int kTogether = kBoth ? 2 : 4;
+        for (int64_t v = v0 + kHold * kThreads; v < v1; v += kTogether * kThreads) {
+            uint4 p[kTogether], q[kTogether];
+#pragma unroll
+            for (int i = 0; i < kTogether; ++i) {
+                p[i] = at(x, v + i * kThreads);
+                if (kBoth) q[i] = at(both ? y : nullptr, v + i * kThreads);
+            }
+#pragma unroll
+            for (int i = 0; i < kTogether; ++i)
+                if (v + i * kThreads < v1) f(4 * (v + i * kThreads), p[i], q[i]);
+        }
+    }
+};
 
 // x summed over the threads before this one of a block of W warps; all: over the whole block.
 template <int W>
@@ -297,33 +334,65 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t (&part)[W], 
     return __reduce_add_sync(0xffffffffu, lane < warp ? w : 0) + upto - x;
 }
 
-__global__ void __launch_bounds__(kListThreads) free_list_kernel(const PageMapArgs a) {
-    __shared__ uint32_t part[2][kListWarps], words[kListThreads], places[kListThreads];
-    const int warp = threadIdx.x >> 5;
-    const Share s = share_of(a);
+// Up to four numbers of every block of the cluster, in all of them.  The blocks are known to run (`started`) before
+// one writes into another's shared memory, and none is written to when it may have ended.
+struct Peers {
+    uint4 of[kCluster];
+    static __device__ __forceinline__ void started() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+    __device__ __forceinline__ void put(int rank, const uint4 &x) {
+        if (threadIdx.x >= kCluster) return;
+        uint32_t at;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;"
+            : "=r"(at)
+            : "r"((uint32_t)__cvta_generic_to_shared(of + rank)), "r"(threadIdx.x));
+        asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
+                     : "memory");
+    }
+};
+
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 2) free_list_kernel(const PageMapArgs a) {
+    __shared__ uint32_t part[3][kWarps], words[kThreads], places[kThreads];
+    __shared__ Peers peers;
+    Peers::started();
+    const int warp = threadIdx.x >> 5, rank = cluster_rank();
+    const Share s = share_of(a, rank);
     wait_for_last();
-    uint32_t n[2] = {0, 0};                                       // free pages before the share, and all
-    for_words<false>(a.used_bits, nullptr, s.words, [&](int64_t w, const uint4 &x, const uint4 &) {
+    auto load = [&](int64_t w0) { return w0 + threadIdx.x < s.w1 ? ~__ldcg(a.used_bits + w0 + threadIdx.x) : 0u; };
+    Slice<false> slice;
+    slice.load(a.used_bits, nullptr, s.words, rank);
+    uint32_t word = load(s.w0);
+    uint32_t n[3] = {0, 0, (uint32_t)__popc(word)};   // free pages: of the slice before the cluster's shares, of all of it; of the share
+    for (int64_t w0 = s.w0 + kThreads; w0 < s.w1; w0 += kThreads) n[2] += __popc(load(w0));
+    slice.each(false, [&](int64_t w, const uint4 &x, const uint4 &) {
         const uint32_t free = 128 - ones(x);
         n[1] += free;
-        if (w < s.w0) n[0] += free;
+        if (w < s.first) n[0] += free;
     });
-    uint32_t word = s.w0 + threadIdx.x < s.w1 ? ~__ldcg(a.used_bits + s.w0 + threadIdx.x) : 0;
-    block_sums<kListWarps>(n, part);
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.count_out[0] = (int32_t)n[1];
-    uint32_t place = n[0], all;
-    for (int64_t w0 = s.w0; w0 < s.w1; w0 += kListThreads) {
-        if (w0 > s.w0) word = w0 + threadIdx.x < s.w1 ? ~__ldcg(a.used_bits + w0 + threadIdx.x) : 0;
+    block_sums<kWarps>(n, part);
+    cluster_wait();
+    peers.put(rank, make_uint4(n[0], n[1], n[2], 0));
+    cluster_arrive();
+    cluster_wait();
+    uint32_t place = 0, total = 0, all;
+#pragma unroll
+    for (int k = 0; k < kCluster; ++k) {
+        const uint4 x = peers.of[k];
+        place += x.x + (k < rank ? x.z : 0);
+        total += x.y;
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.count_out[0] = (int32_t)total;
+    for (int64_t w0 = s.w0; w0 < s.w1; w0 += kThreads) {
+        if (w0 > s.w0) word = load(w0);
         __syncthreads();
-        const uint32_t before = block_scan<kListWarps>(__popc(word), part[0], all);
+        const uint32_t before = block_scan<kWarps>(__popc(word), part[0], all);
         words[threadIdx.x] = word;
         places[threadIdx.x] = place + before;
         __syncthreads();
-        const int mine = (int)min((int64_t)kListThreads, s.w1 - w0);
-        for (int i = warp; i < mine; i += kListWarps) write_bits(words[i], 32 * (w0 + i), places[i], a.pages_out, 0xffffffffu);
+        const int mine = (int)min((int64_t)kThreads, s.w1 - w0);
+        for (int i = warp; i < mine; i += kWarps) write_bits(words[i], 32 * (w0 + i), places[i], a.pages_out, 0xffffffffu);
         place += all;
     }
-    fill(a.pages_out, n[1], a.num_pages, kListThreads);
+    fill(a.pages_out, total, a.num_pages, kThreads);
 }
 
 // The pages of word w in front of page `used`.
@@ -333,90 +402,128 @@ __device__ __forceinline__ uint32_t below(uint32_t used, int64_t w) {
 }
 
 // The moves: the movable pages from page `used` on go to the free pages in front of it, both in order.  Leaves for
-// every word the number of moves before it.
-__global__ void __launch_bounds__(kListThreads) moves_kernel(const PageMapArgs a) {
-    __shared__ uint32_t part[3][kListWarps], used_words[kListThreads];
-    __shared__ uint4 words[kListThreads];
+// every word which of its pages move, and the number of moves before them.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 2) moves_kernel(const PageMapArgs a) {
+    __shared__ uint32_t part[5][kWarps], used_words[kThreads];
+    __shared__ uint4 words[kThreads];
+    __shared__ Peers peers[3];
+    Peers::started();
     let_next_start();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Share s = share_of(a);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = cluster_rank();
+    const Share s = share_of(a, rank);
     wait_for_last();
-    uint32_t n[1] = {0};
-    for_words<false>(a.used_bits, nullptr, s.words, [&](int64_t, const uint4 &x, const uint4 &) { n[0] += ones(x); });
-    block_sums<kListWarps>(n, part);
-    const uint32_t used = n[0] - (uint32_t)(32 * s.words - a.num_pages);
-    uint32_t m[3] = {0, 0, 0};                                    // moves before the share, holes before it, all moves
-    __syncthreads();
-    for_words<true>(a.used_bits, a.stay_bits, s.words, [&](int64_t w, const uint4 &x, const uint4 &y) {
-        if (32 * (w + 4) <= used) {
-            if (w < s.w0) m[1] += 128 - ones(x);
-            return;
-        }
-        const uint32_t u[4] = {x.x, x.y, x.z, x.w}, stays[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t front = below(used, w + i), moves = __popc(u[i] & ~stays[i] & ~front);
-            m[2] += moves;
-            if (w < s.w0) {
-                m[0] += moves;
-                m[1] += __popc(~u[i] & front);
-            }
-        }
-    });
     uint32_t u, stays;
     auto load = [&](int64_t w) {
         u = w < s.w1 ? __ldcg(a.used_bits + w) : 0xffffffffu;
         stays = w < s.w1 ? __ldcg(a.stay_bits + w) : 0xffffffffu;
     };
+    Slice<true> slice;
+    slice.load(a.used_bits, a.stay_bits, s.words, rank);
     load(s.w0 + threadIdx.x);
-    block_sums<kListWarps>(m, part);
+    uint32_t n[1] = {0};
+    slice.each(false, [&](int64_t, const uint4 &x, const uint4 &) { n[0] += ones(x); });
+    block_sums<kWarps>(n, part);
+    cluster_wait();
+    peers[0].put(rank, make_uint4(n[0], 0, 0, 0));
+    cluster_arrive();
+    cluster_wait();
+    uint32_t used = (uint32_t)a.num_pages - (uint32_t)(32 * s.words);
+#pragma unroll
+    for (int k = 0; k < kCluster; ++k) used += peers[0].of[k].x;
+    // moves of the slice before the cluster's shares, holes there, all its moves; moves and holes of the share
+    uint32_t m[5] = {0, 0, 0, 0, 0};
+    slice.each(true, [&](int64_t w, const uint4 &x, const uint4 &y) {
+        if (32 * (w + 4) <= used) {
+            if (w < s.first) m[1] += 128 - ones(x);
+            return;
+        }
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t front = below(used, w + i), moves = __popc(xs[i] & ~ys[i] & ~front);
+            m[2] += moves;
+            if (w < s.first) {
+                m[0] += moves;
+                m[1] += __popc(~xs[i] & front);
+            }
+        }
+    });
+    uint32_t front, moves, holes;
+    auto look = [&](int64_t w) {
+        front = below(used, w);
+        moves = u & ~stays & ~front;
+        holes = ~u & front;
+    };
+    for (int64_t w = s.w0 + threadIdx.x + kThreads; w - threadIdx.x < s.w1; w += kThreads) {   // (large pools)
+        const uint32_t u0 = u, stays0 = stays;
+        load(w);
+        look(w);
+        m[3] += __popc(moves);
+        m[4] += __popc(holes);
+        u = u0, stays = stays0;
+    }
+    look(s.w0 + threadIdx.x);
+    m[3] += __popc(moves);
+    m[4] += __popc(holes);
+    __syncthreads();
+    block_sums<kWarps>(m, part);
+    peers[1].put(rank, make_uint4(m[0], m[1], m[2], 0));
+    peers[2].put(rank, make_uint4(m[3], m[4], 0, 0));
+    cluster_arrive();
+    cluster_wait();
+    uint32_t from = 0, to = 0, total = 0, all_moves, all_holes;
+#pragma unroll
+    for (int k = 0; k < kCluster; ++k) {
+        const uint4 x = peers[1].of[k], y = peers[2].of[k];
+        from += x.x + (k < rank ? y.x : 0);
+        to += x.y + (k < rank ? y.y : 0);
+        total += x.z;
+    }
     if (blockIdx.x == 0 && threadIdx.x == 0) {
-        a.count_out[0] = (int32_t)m[2];
+        a.count_out[0] = (int32_t)total;
         a.used_out[0] = (int32_t)used;
     }
-    uint32_t from = m[0], to = m[1], all_moves, all_holes;
-    for (int64_t w0 = s.w0; w0 < s.w1; w0 += kListThreads) {
+    for (int64_t w0 = s.w0; w0 < s.w1; w0 += kThreads) {
         const int64_t w = w0 + threadIdx.x;
-        if (w0 > s.w0) load(w);
-        const uint32_t front = below(used, w), moves = u & ~stays & ~front, holes = ~u & front;
+        if (w0 > s.w0) {
+            load(w);
+            look(w);
+        }
         __syncthreads();
-        const uint32_t moved = from + block_scan<kListWarps>(__popc(moves), part[0], all_moves),
-                       filled = to + block_scan<kListWarps>(__popc(holes), part[1], all_holes);
-        if (w < s.w1) a.moves_before[w] = moved;
+        const uint32_t moved = from + block_scan<kWarps>(__popc(moves), part[0], all_moves),
+                       filled = to + block_scan<kWarps>(__popc(holes), part[1], all_holes);
+        if (w < s.w1) a.moves[w] = make_uint2(moves, moved);
         words[threadIdx.x] = make_uint4(moves, moved, holes, filled);
         used_words[threadIdx.x] = u;
         __syncthreads();
-        const int mine = (int)min((int64_t)kListThreads, s.w1 - w0);
-        for (int i = warp; i < mine; i += kListWarps) {
+        const int mine = (int)min((int64_t)kThreads, s.w1 - w0);
+        for (int i = warp; i < mine; i += kWarps) {
             const uint4 x = words[i];
             const int64_t page = 32 * (w0 + i) + lane;
-            write_bits(x.x, page - lane, x.y, a.src, m[2]);
-            write_bits(x.z, page - lane, x.w, a.dst, m[2]);
+            write_bits(x.x, page - lane, x.y, a.src, total);
+            write_bits(x.z, page - lane, x.w, a.dst, total);
             if (page < a.num_pages && !(x.x >> lane & 1)) a.pages_out[page] = used_words[i] >> lane & 1 ? (int32_t)page : -1;
         }
         from += all_moves;
         to += all_holes;
     }
-    fill(a.src, m[2], a.num_pages / 2, kListThreads);
-    fill(a.dst, m[2], a.num_pages / 2, kListThreads);
+    fill(a.src, total, a.num_pages / 2, kThreads);
+    fill(a.dst, total, a.num_pages / 2, kThreads);
 }
 
-// The new ids of a unit's pages: page `used` and those behind it that may move take the place of their number among
-// the moves (bits and numbers in global or in shared memory).
-__device__ __forceinline__ void rename_unit(const PageMapArgs &a, const Unit &x, int32_t used, const uint32_t *used_bits,
-                                            const uint32_t *stay_bits, const uint32_t *moves_before) {
-    // (an id that was given out here, in a row that is named twice, is in front of page `used` and stays)
+// The new ids of a unit's pages: one that moves takes the place of its number among the moves (by words of 32 pages: which
+// of them move, and the moves before them; in global or in shared memory).
+__device__ __forceinline__ void rename_unit(const PageMapArgs &a, const Unit &x, const uint2 *moves) {
+    // (an id that was given out here, in a row that is named twice, is of a page that does not move)
     int32_t to[kPerLane];                                      // the move's number, -1: none
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) {
         const int32_t id = x.has(k) ? x.id[k] : -1;
-        const bool may = id >= used && id >= 0 && id < a.num_pages;
-        const int w = may ? id >> 5 : 0;
-        const uint32_t bit = 1u << (id & 31);
+        const bool may = id >= 0 && id < a.num_pages;
         // (through L1: requests that share pages look up the same words)
-        const uint32_t moves = may ? used_bits[w] & ~stay_bits[w] : 0;
-        const uint32_t before = may ? moves_before[w] : 0;
-        to[k] = moves & bit ? (int32_t)(before + __popc(moves & (bit - 1) & ~below(used, w))) : -1;
+        const uint2 m = may ? moves[id >> 5] : make_uint2(0, 0);
+        const uint32_t bit = 1u << (id & 31);
+        to[k] = m.x & bit ? (int32_t)(m.y + __popc(m.x & (bit - 1))) : -1;
     }
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k)
@@ -437,34 +544,19 @@ __global__ void __launch_bounds__(kThreads) rename_kernel(const PageMapArgs a, i
             a.pages_out[__ldcg(a.src + i)] = __ldcg(a.dst + i);
         return;
     }
-    int32_t used = 0;
-    for_entries(
-        a, s, entry_blocks, false,
-        [&] {
-            wait_for_last();
-            used = __ldcg(a.used_out);
-        },
-        [&](const Unit &x) { rename_unit(a, x, used, a.used_bits, a.stay_bits, a.moves_before); });
+    for_entries(a, s, entry_blocks, false, [] { wait_for_last(); }, [&](const Unit &x) { rename_unit(a, x, a.moves); });
 }
 
 // --------------------------------------------------------------- small pools
 
 // All of it in one launch, for small pools and tables: a cluster of 8 blocks, each of which marks its share of the
 // entries in a bitmap in its own shared memory, joins all 8 (so that each knows every page), and lists and renames
-// its share.  Free pages of 64 requests in 15 thousand pages: 5.9 -> 4.9 us in a graph, launched one by one 8.3 ->
-// 6.4; compaction of 32 requests in 13 thousand: 9.2 -> 8.9 and 12.3 -> 10.3.  At 32 thousand pages the three or
-// four launches are level (free 6.9 to 7.4 against 5.4 to 6.9 in a graph, compaction 10.5 to 11.3 against 10.3 to 12.4),
-// at 60 thousand ahead (6.1 against 6.6, 11.3 against 13.1).
-constexpr int kCluster = 8, kSmallWords = 1024, kSmallUnits = 2 * kCluster * kWarps;
+// its share.  Free pages of 64 requests in 15 thousand pages: 6.8 -> 4.8 us in a graph, launched one by one 8.7 ->
+// 6.5; compaction of 32 requests in 13 thousand: 9.0 -> 7.9 and 12.3 -> 10.3.  At 32 thousand pages the three or
+// four launches are level in a graph (free 5.9 to 7.4 against 5.2 to 6.7, compaction 9.3 to 10.6 against 9.4 to 11.2), at
+// 60 thousand ahead (free 6.0 against 6.6).
+constexpr int kSmallWords = 1024, kSmallUnits = 2 * kCluster * kWarps;
 static_assert(kSmallWords == 2 * kThreads, "two words a thread");
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 // 8 bytes out of another block's shared memory.
 __device__ __forceinline__ uint2 ld_peer(const void *p, int rank) {
@@ -478,7 +570,8 @@ __device__ __forceinline__ uint2 ld_peer(const void *p, int rank) {
 template <bool kCompact>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) small_pool_kernel(const PageMapArgs a) {
     __shared__ __align__(16) uint32_t mine[kSmallWords], held[kSmallWords / kCluster], used[kSmallWords];
-    __shared__ __align__(16) uint32_t stays[kCompact ? kSmallWords : 4], places[kSmallWords], moved[kCompact ? kSmallWords : 4];
+    __shared__ uint32_t places[kSmallWords];
+    __shared__ uint2 moves[kCompact ? kSmallWords : 1];
     __shared__ uint32_t part[2][kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = cluster_rank(), t2 = 2 * threadIdx.x;
     const int words = (int)words_of(a.num_pages), share = (words / 2 + kCluster - 1) / kCluster * 2;
@@ -552,21 +645,20 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) sma
         uint32_t from = block_scan<kWarps>(go, part[0], all_go), place = block_scan<kWarps>(to, part[1], all_to);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const uint32_t front = below(total, t2 + i);
+            const uint32_t front = below(total, t2 + i), go = u[i] & ~st[i] & ~front;
             used[t2 + i] = u[i];
-            stays[t2 + i] = st[i];
-            moved[t2 + i] = from;
+            moves[t2 + i] = make_uint2(go, from);
             places[t2 + i] = place;
-            from += __popc(u[i] & ~st[i] & ~front);
+            from += __popc(go);
             place += __popc(~u[i] & front);
         }
         __syncthreads();
         for (int w = w0 + warp; w < w1; w += kWarps) {
-            const uint32_t front = below(total, w), go = used[w] & ~stays[w] & ~front;
+            const uint2 m = moves[w];
             const int page = 32 * w + lane;
-            write_bits(go, 32ll * w, moved[w], a.src, all_go);
-            write_bits(~used[w] & front, 32ll * w, places[w], a.dst, all_go);
-            if (page < a.num_pages && !(go >> lane & 1)) a.pages_out[page] = used[w] >> lane & 1 ? page : -1;
+            write_bits(m.x, 32ll * w, m.y, a.src, all_go);
+            write_bits(~used[w] & below(total, w), 32ll * w, places[w], a.dst, all_go);
+            if (page < a.num_pages && !(m.x >> lane & 1)) a.pages_out[page] = used[w] >> lane & 1 ? page : -1;
         }
         fill(a.src, all_go, a.num_pages / 2, kThreads);
         fill(a.dst, all_go, a.num_pages / 2, kThreads);
@@ -581,7 +673,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) sma
         for (uint32_t i = rank * kThreads + threadIdx.x; i < all_go; i += kCluster * kThreads)
             a.pages_out[__ldcg(a.src + i)] = __ldcg(a.dst + i);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) rename_unit(a, x[i], (int32_t)total, used, stays, moved);
+        for (int i = 0; i < 2; ++i) rename_unit(a, x[i], moves);
     }
 }
 
@@ -611,17 +703,22 @@ cudaError_t launch_marks(const PageMapArgs &a, int entry_blocks, cudaStream_t st
     return e == cudaSuccess ? launch_after(mark_kernel, entry_blocks, kThreads, stream, a) : e;
 }
 
-// A block for every kWarps units that full rows would have, at most two an SM.
+// A block for every kWarps units that full rows would have, at most two an SM.  An odd number, so that the chunks of a
+// long row do not all fall to the same blocks.
 int entry_blocks(const PageMapArgs &a) {
     const int64_t chunks = a.table_width > 0 ? (a.table_width + kUnit - 1) / kUnit : 1;
-    const int64_t want = ((int64_t)a.num_reqs * chunks + kWarps - 1) / kWarps, most = 2 * sm_count();
-    return (int)(want < 1 ? 1 : want < most ? want : most);
+    const int64_t want = ((int64_t)a.num_reqs * chunks + kWarps - 1) / kWarps, most = 2 * sm_count() - 1;
+    return (int)(want < most ? want : most) | 1;
 }
 
-// A block for every 32 words, at most one an SM.
+// A block for every 32 words, in whole clusters, at most 2 in a GPC (of 19 SMs on average): they start beside the blocks
+// that still mark, where twice as many wait for room (740 thousand pages: free 13.4 against 15.1 us, compaction 14.6
+// against 15.4).  Twice as many where a block would go over its share in several rounds (8 million pages: 15.7 against
+// 21.7 and 40 against 51).
 int list_blocks(const PageMapArgs &a) {
-    const int64_t want = (words_of(a.num_pages) + 31) / 32;
-    return (int)(want < 1 ? 1 : want < sm_count() ? want : sm_count());
+    const int64_t words = words_of(a.num_pages), want = (words + 32 * kCluster - 1) / (32 * kCluster);
+    const int64_t gpcs = (sm_count() + 18) / 19, most = (words > 2 * gpcs * kCluster * kThreads ? 4 : 2) * gpcs;
+    return kCluster * (int)(want < 1 ? 1 : want < most ? want : most);
 }
 
 // A thread for every four moves that there may be, at most a block an SM.
@@ -633,13 +730,13 @@ int move_blocks(const PageMapArgs &a) {
 }  // namespace
 
 size_t page_map_workspace_bytes(int32_t num_pages) {
-    return ((size_t)words_of(num_pages) * 4 * 3 + 255) / 256 * 256;
+    return ((size_t)words_of(num_pages) * 4 * 4 + 255) / 256 * 256;
 }
 
 static void set_workspace(PageMapArgs &a, void *workspace, bool compact) {
     a.used_bits = static_cast<uint32_t *>(workspace);
     a.stay_bits = compact ? a.used_bits + words_of(a.num_pages) : nullptr;
-    a.moves_before = compact ? a.stay_bits + words_of(a.num_pages) : nullptr;
+    a.moves = compact ? reinterpret_cast<uint2 *>(a.stay_bits + words_of(a.num_pages)) : nullptr;
 }
 
 cudaError_t launch_free_pages(PageMapArgs a, void *workspace, cudaStream_t stream) {
@@ -649,7 +746,7 @@ cudaError_t launch_free_pages(PageMapArgs a, void *workspace, cudaStream_t strea
     }
     set_workspace(a, workspace, false);
     cudaError_t e = launch_marks(a, entry_blocks(a), stream);
-    return e == cudaSuccess ? launch_after(free_list_kernel, list_blocks(a), kListThreads, stream, a) : e;
+    return e == cudaSuccess ? launch_after(free_list_kernel, list_blocks(a), kThreads, stream, a) : e;
 }
 
 cudaError_t launch_compact_pages(PageMapArgs a, void *workspace, cudaStream_t stream) {
@@ -660,7 +757,7 @@ cudaError_t launch_compact_pages(PageMapArgs a, void *workspace, cudaStream_t st
     set_workspace(a, workspace, true);
     const int blocks = entry_blocks(a);
     cudaError_t e = launch_marks(a, blocks, stream);
-    if (e == cudaSuccess) e = launch_after(moves_kernel, list_blocks(a), kListThreads, stream, a);
+    if (e == cudaSuccess) e = launch_after(moves_kernel, list_blocks(a), kThreads, stream, a);
     return e == cudaSuccess ? launch_after(rename_kernel, blocks + move_blocks(a), kThreads, stream, a, blocks) : e;
 }
 

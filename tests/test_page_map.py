@@ -201,6 +201,18 @@ def test_large_compaction():
     run_compact(table, None, lens, n, 1, some_held(rng, n, 0.05))
 
 
+@pytest.mark.parametrize("share", [0.0, 0.6])
+def test_a_pool_whose_shares_take_several_rounds(share):
+    n = 4600011
+    rng = np.random.default_rng(10)
+    table = rng.integers(0, n, (30, 9000)).astype(np.int32)
+    table[7, 0], table[8, 0] = n - 1, 0
+    lens = rng.integers(1, 9001, 30).tolist()
+    held = some_held(rng, n, share) if share else None
+    run_free(table, None, lens, n, 1, held)
+    run_compact(table, None, lens, n, 1, held)
+
+
 def test_a_compacted_pool_reads_as_before():
     ps, n = 16, 400
     table, rows, lens, rng = requests(20, ps, 300, n, 11, share=3)
