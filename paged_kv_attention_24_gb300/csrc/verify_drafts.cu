@@ -18,10 +18,11 @@
 // so that a row is read by many SMs; each warp sums a run of neighbouring tokens and
 // writes its sum into the shared memory of all the cluster's blocks, each of which
 // then finds the run in which the draw falls; only that one is read again (out of L2), by
-// the block that summed it.  128 requests over 131072 tokens of fp32: 24.3 us (the rows
-// alone 18 us at the copy rate; lookups in front, exchange and draw behind take the
-// rest); 4 over 50001 of bf16: 5.6 us.  With 64-bit sums: 72 and 14 us.  Sums sent by
-// st.async and waited for by one warp, in place of the cluster's barrier: 25.8 and 5.3.
+// the block that summed it, or, where runs are short, not even that one.  128 requests
+// over 131072 tokens of fp32: 24.3 us (the rows alone 18 us at the copy rate; lookups in
+// front, exchange and draw behind take the rest); 4 over 50001 of bf16: 5.0 us.  With
+// 64-bit sums: 72 and 14 us.  Sums sent by st.async and waited for by one warp, in place
+// of the cluster's barrier: 25.8 us, and 0.25 less for 4 requests.
 #include "kernels.h"
 
 namespace msgl {
@@ -80,18 +81,21 @@ __device__ __forceinline__ Sum shfl(const Sum &a, int lane) {
     return Sum{__shfl_sync(0xffffffffu, a.hi, lane), __shfl_sync(0xffffffffu, a.lo, lane)};
 }
 
-// Sums over the warp's lanes before this one (before) and up to this one (returned).
-__device__ __forceinline__ Sum warp_scan(Sum x, Sum &before) {
+// Sum over the warp's lanes up to this one.
+__device__ __forceinline__ Sum warp_scan(Sum x) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const Sum y{__shfl_up_sync(0xffffffffu, x.hi, o), __shfl_up_sync(0xffffffffu, x.lo, o)};
         if (lane >= o) x = loose(y, x);
     }
-    x = settled(x.hi, x.lo);
-    before = Sum{__shfl_up_sync(0xffffffffu, x.hi, 1), __shfl_up_sync(0xffffffffu, x.lo, 1)};
-    if (lane == 0) before = Sum{0.f, 0.f};
-    return x;
+    return settled(x.hi, x.lo);
+}
+
+// The sum up to the lane before, from the sums up to each lane.
+__device__ __forceinline__ Sum lane_before(const Sum &upto) {
+    const Sum x{__shfl_up_sync(0xffffffffu, upto.hi, 1), __shfl_up_sync(0xffffffffu, upto.lo, 1)};
+    return threadIdx.x & 31 ? x : Sum{0.f, 0.f};
 }
 
 // The first lane with any weight x at which the running sum `upto` passes the draw, else the last one with any; -1
@@ -182,10 +186,21 @@ struct Shared {
     bool bad;
 };
 
+// Four sums, and all lanes' of them, as one.
+__device__ __forceinline__ Sum warp_sum(const float (&hi)[4], const float (&lo)[4]) {
+    Sum sum = loose(loose(Sum{hi[0], lo[0]}, Sum{hi[1], lo[1]}), loose(Sum{hi[2], lo[2]}, Sum{hi[3], lo[3]}));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        sum = loose(sum, Sum{__shfl_xor_sync(0xffffffffu, sum.hi, o), __shfl_xor_sync(0xffffffffu, sum.lo, o)});
+    return settled(sum.hi, sum.lo);
+}
+
+constexpr int kUnroll = 4;           // vectors of a row that a lane has on the way
+
 // Sum of the weights of vectors [n0, n1).
 template <class T>
 __device__ __forceinline__ Sum run_sum(const Row<T> &r, int n0, int n1) {
-    constexpr int kN = Vec<T>::kN, kUnroll = 4;
+    constexpr int kN = Vec<T>::kN;
     const int lane = threadIdx.x & 31;
     // (four sums, so that one does not wait for the last; as two pairs, by the instructions that add two floats at once,
     // 39 us in place of 27 for 128 requests)
@@ -209,11 +224,86 @@ __device__ __forceinline__ Sum run_sum(const Row<T> &r, int n0, int n1) {
                     hi[k % 4] = s;
                 }
     }
-    Sum sum = loose(loose(Sum{hi[0], lo[0]}, Sum{hi[1], lo[1]}), loose(Sum{hi[2], lo[2]}, Sum{hi[3], lo[3]}));
+    return warp_sum(hi, lo);
+}
+
+// Vectors a lane of a short run: as many weights as a lane has registers for (four of fp32 are spilled).
+template <class T>
+constexpr int kShortRun = sizeof(T) == 4 ? 3 : 2;
+
+// The same of a short run, whose weights stay in w.
+template <class T>
+__device__ __forceinline__ Sum run_sum(const Row<T> &r, int n0, int n1, float (&w)[kShortRun<T>][Vec<T>::kN]) {
+    constexpr int kN = Vec<T>::kN, kUnroll = kShortRun<T>;
+    const int n = n0 + (threadIdx.x & 31);
+    float hi[4] = {}, lo[4] = {};
+    Vec<T> x[kUnroll], y[kUnroll];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        sum = loose(sum, Sum{__shfl_xor_sync(0xffffffffu, sum.hi, o), __shfl_xor_sync(0xffffffffu, sum.lo, o)});
-    return settled(sum.hi, sum.lo);
+    for (int u = 0; u < kUnroll; ++u)
+        if (n + 32 * u < n1) {
+            x[u] = r.target(n + 32 * u);
+            y[u] = r.draft(n + 32 * u);
+        }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+            w[u][k] = n + 32 * u < n1 ? r.at(n + 32 * u, k, x[u], y[u]) : 0.f;
+            const float s = hi[k % 4] + w[u][k];
+            lo[k % 4] += two_sum_error(hi[k % 4], w[u][k], s);
+            hi[k % 4] = s;
+        }
+    return warp_sum(hi, lo);
+}
+
+// The token (of the run's vectors, from n0 on) at which the running sum passes the draw; where rounding lets none pass, the
+// last one with any weight.  By the warp that has the run's weights.
+template <class T>
+__device__ __forceinline__ void draw_token(const Row<T> &r, int n0, const float (&w)[kShortRun<T>][Vec<T>::kN],
+                                           Sum before, const Sum &draw, int32_t *out) {
+    constexpr int kN = Vec<T>::kN, kUnroll = kShortRun<T>;
+    const int lane = threadIdx.x & 31;
+    Sum upto[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+        Sum own{w[u][0], 0.f};
+#pragma unroll
+        for (int k = 1; k < kN; ++k) own = loose(own, Sum{w[u][k], 0.f});
+        upto[u] = warp_scan(own);
+    }
+    float drawn[kN] = {};                                        // the lane's weights of the drawn round
+    Sum ahead{0.f, 0.f};
+    int round = -1, owner = 0;
+    bool passed = false;
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+        bool any = false;
+#pragma unroll
+        for (int k = 0; k < kN; ++k) any |= w[u][k] > 0;
+        const uint32_t heavy = __ballot_sync(0xffffffffu, any),
+                       over = __ballot_sync(0xffffffffu, any && before + upto[u] > draw);
+        if (heavy && !passed) {
+            passed = over;
+            round = u;
+            owner = over ? __ffs(over) - 1 : 31 - __clz(heavy);
+            ahead = before + lane_before(upto[u]);
+#pragma unroll
+            for (int k = 0; k < kN; ++k) drawn[k] = w[u][k];
+        }
+        before = before + shfl(upto[u], 31);
+    }
+    if (lane != owner || round < 0) return;
+    int token = -1;
+    passed = false;
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+        ahead = ahead + Sum{drawn[k], 0.f};
+        if (drawn[k] > 0 && !passed) {
+            token = r.token(n0 + lane + 32 * round) + k;
+            passed = ahead > draw;
+        }
+    }
+    *out = token;
 }
 
 // How many drafts stand: the first one that does not (its token in `refused`), or all.
@@ -258,15 +348,15 @@ __device__ __forceinline__ void draw_token(const Row<T> &r, Shared &s, int i0, i
     for (int t = i0;; t += E * kThreads) {
         const int i = t + E * (int)threadIdx.x;
         float w[E];
-        Sum own{0.f, 0.f}, lower, ahead;
+        Sum own{0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < E; ++k) w[k] = i + k < i1 ? r.at(i + k) : 0.f;
 #pragma unroll
         for (int k = 0; k < E; ++k) own = loose(own, Sum{w[k], 0.f});
-        const Sum upto = warp_scan(own, lower);
+        const Sum upto = warp_scan(own), lower = lane_before(upto);
         if (lane == 31) s.warp[warp] = upto;
         __syncthreads();
-        const Sum x = lane < kWarps ? s.warp[lane] : Sum{0.f, 0.f}, warps = warp_scan(x, ahead);
+        const Sum x = lane < kWarps ? s.warp[lane] : Sum{0.f, 0.f}, warps = warp_scan(x), ahead = lane_before(warps);
         // (where rounding lets no token pass, the last one with any weight counts)
         const int chosen = drawn_lane(x, before + warps, draw);
         const bool passes = __any_sync(0xffffffffu, x.hi > 0 && before + warps > draw), ends = t + E * kThreads >= i1;
@@ -293,7 +383,9 @@ __device__ __forceinline__ void draw_token(const Row<T> &r, Shared &s, int i0, i
     }
 }
 
-template <class T>
+// kShort: runs are short, and the drawn one's weights are still in its warp's registers (4 requests over 50001 tokens of
+// bf16: read again 5.5 us, else 5.0; one over 32000 of fp32 5.1 and 4.6; 300 over 8000 of bf16 8.2 and 7.5).
+template <class T, bool kShort>
 __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a, int log2_cluster) {
     const int cluster = 1 << log2_cluster, log2_runs = log2_cluster + 4;
     static_assert(kWarps == 16, "a block of 16 runs");
@@ -342,11 +434,14 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
     };
     auto length_of = [&](int vectors) { return ((vectors - 1) >> log2_runs) / 32 * 32 + 32; };   // whole rounds of a warp
     bool second = false;
+    float w[kShortRun<T>][Vec<T>::kN];
     for (;; second = true) {
         const Row<T> r = row_of(!second);
         const int vectors = r.vectors(), length = length_of(vectors), mine = rank * kWarps + warp;
         const int n0 = (int)min((int64_t)mine * length, (int64_t)vectors), n1 = min(n0 + length, vectors);
-        const Sum sum = run_sum(r, n0, n1);
+        Sum sum;
+        if constexpr (kShort) sum = run_sum(r, n0, n1, w);
+        else sum = run_sum(r, n0, n1);
         // every block gets every run's sum
         if (!second) cluster_wait();
         if (lane < cluster) {
@@ -371,15 +466,16 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
         // every block goes through them in the same order and so comes to the same end: up to four neighbours a lane
         if (warp == 0) {
             const int log2_each = max(log2_runs - 5, 0), i0 = lane << log2_each;
-            Sum x[4], sum{0.f, 0.f}, lower;
+            Sum x[4], sum{0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 x[k] = Sum{0.f, 0.f};
                 if (k < 1 << log2_each && i0 + k < 1 << log2_runs) x[k] = s.runs[i0 + k];
                 if (k < 1 << log2_each) sum = loose(sum, x[k]);
             }
-            const Sum upto = warp_scan(sum, lower), total = shfl(upto, 31), draw = times(s.sample, total);
+            const Sum upto = warp_scan(sum), total = shfl(upto, 31), draw = times(s.sample, total);
             const int chosen = drawn_lane(sum, upto, draw);
+            Sum lower = lane_before(upto);
             if (lane == max(chosen, 0)) {
                 int run = -1;
                 bool passed = false;
@@ -412,8 +508,13 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
             report(a.status, MSGL_DEVERR_PROBS);
         }
     } else if (s.run / kWarps == rank) {
+        if (kShort && warp != s.run % kWarps) return;
         const Row<T> r = row_of(!second);
         const int vectors = r.vectors(), length = length_of(vectors), n0 = s.run * length;
+        if constexpr (kShort) {
+            draw_token(r, n0, w, s.before, s.draw, out);
+            return;
+        }
         const int i0 = max(r.token(n0), 0), i1 = min(r.token(min(n0 + length, vectors)), a.vocab);
         if (i1 - i0 <= kThreads) draw_token<1>(r, s, i0, i1, out);
         else if (i1 - i0 <= 2 * kThreads) draw_token<2>(r, s, i0, i1, out);
@@ -443,8 +544,12 @@ cudaError_t launch_verify_drafts(const VerifyArgs &a, cudaStream_t stream) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return a.bf16 ? cudaLaunchKernelEx(&cfg, verify_kernel<__nv_bfloat16>, a, log2_cluster)
-                  : cudaLaunchKernelEx(&cfg, verify_kernel<float>, a, log2_cluster);
+    // (a row's shift may add a vector to it)
+    const int64_t per = a.bf16 ? 8 : 4, most = a.bf16 ? kShortRun<__nv_bfloat16> : kShortRun<float>;
+    const bool brief = (a.vocab + per - 1) / per + 1 <= (kWarps * 32 * most) << log2_cluster;
+    auto kernel = a.bf16 ? (brief ? verify_kernel<__nv_bfloat16, true> : verify_kernel<__nv_bfloat16, false>)
+                         : (brief ? verify_kernel<float, true> : verify_kernel<float, false>);
+    return cudaLaunchKernelEx(&cfg, kernel, a, log2_cluster);
 }
 
 }  // namespace msgl

@@ -64,6 +64,24 @@ def test_many_draws_of_a_flat_row():
     run(w)
 
 
+@pytest.mark.parametrize("dtype,requests,V", [(torch.float32, 5, 49148), (torch.bfloat16, 5, 65528),
+                                              (torch.float32, 170, 6140), (torch.bfloat16, 170, 8184)])
+def test_around_the_longest_rows_that_stay_in_registers(dtype, requests, V):
+    for n in (V - 5, V, V + 1, V + 13):
+        w = batch([i % 3 for i in range(requests)], n, dtype, seed=n)
+        w["su"][:4] = torch.tensor([0.0, 0.9999999, 1.0, 0.5])
+        run(w)
+        g, T = {k: v.cuda() for k, v in w.items()}, len(w["tokens"])
+        want = ref.verify(w["p"], w["q"], w["tokens"].tolist(), w["cu"].tolist(), w["au"].tolist(), w["su"].tolist(), None,
+                          [-1] * T)
+        for shift_p, shift_q in ((1, 3), (3, 3), (0, 7)):      # rows whose first vector is not whole
+            p, q = (torch.zeros(T * (n + 8) + 8, dtype=dtype, device="cuda")[s:s + T * (n + 8)].view(T, n + 8)[:, :n]
+                    for s in (shift_p, shift_q))
+            p.copy_(g["p"]), q.copy_(g["q"])
+            for a, b in zip(ops.verify_drafts(p, q, g["tokens"], g["cu"], g["au"], g["su"]), want):
+                assert a.tolist() == b.tolist(), (n, shift_p, shift_q)
+
+
 def test_strided_rows_and_odd_addresses():
     w = batch([2, 3, 0], 999, seed=4)
     g = {k: v.cuda() for k, v in w.items()}
