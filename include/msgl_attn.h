@@ -433,7 +433,8 @@ MSGL_API msgl_status msgl_rope_store_kv(const msgl_kv_pool *pool, const msgl_new
  *   out_tokens[first + i] = draft i for i < a, the new token at i = a, -1 behind it
  * kv_lens counts the tokens whose K/V of this step are kept: the cached_lens of the
  * next msgl_step_tables (the new token's K/V are stored by that step).
- * Weights are taken in 32 bits, sums in pairs of 32-bit numbers (about 46 bits).  What is not a number weighs nothing.
+ * Weights are taken in 32 bits, sums in pairs of 32-bit numbers (about 46 bits).  What is
+ * not a number weighs nothing.
  *
  *   target, draft  device fp32 or bf16 (both the same) [total_tokens, vocab], rows
  *                  stride elements apart; they need not sum to 1.  draft NULL: the

@@ -106,6 +106,14 @@ bool overlap(const Span &a, const Span &b) {
     if (a0 + ((a.rows - 1) * a.pitch + a.width) * size <= b0 || b0 + ((b.rows - 1) * b.pitch + b.width) * size <= a0)
         return false;
     if (b.rows > a.rows) return overlap(b, a);
+    if (a.pitch == b.pitch) {
+        // rows i of a and j of b meet where d - a.width < (i - j) pitch < d + b.width, d their bases' distance: the
+        // first such i - j says it for all (columns of one projection of 8000 tokens: the loop below takes 30 us)
+        const int64_t pitch = a.pitch * size, over = b0 - a0 - a.width * size;
+        int64_t steps = over >= 0 ? over / pitch + 1 : -((-over - 1) / pitch);
+        if (steps < 1 - b.rows) steps = 1 - b.rows;
+        return steps < a.rows && steps * pitch < b0 - a0 + b.width * size;
+    }
     // the last row of a that begins in front of the end of b's row r is the only one that can reach it
     for (int64_t r = 0; r < b.rows; ++r) {
         const int64_t from = b0 + r * b.pitch * size, to = from + b.width * size;

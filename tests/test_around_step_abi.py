@@ -92,6 +92,19 @@ def test_rope_store_refusals(lib):
     assert call(n_tokens=0, q=None, k=None, v=None, q_out=None, positions=None, out_loc=None) == 0
 
 
+@pytest.mark.parametrize("tokens", [1, 2, 500])
+def test_rope_store_refuses_columns_that_meet(lib, tokens):
+    """k and q_out columns of rows of 48 heads, a token's q_out sharing 16 bytes or more with the k of a token."""
+    row, k = 48 * 256, at(3) + 17 * 256
+    p, r = ops._Pool(at(0), at(1), 256, 16, 8, 128), ops._Rope(at(2), None, 64, 1, 0, 1.0)
+    for apart in {0, 1 - tokens, tokens - 1, tokens // 2, -(tokens // 2)}:
+        for shift in (16 - 16 * 256, -16, 0, 8 * 256 - 16):
+            n = ops._NewTokens(at(6), k, at(5), k + apart * row + shift, 16 * 128, row // 2, 8 * 128, row // 2, at(7), tokens,
+                               at(8), tokens, 16)
+            assert lib.msgl_rope_store_kv(ctypes.byref(p), ctypes.byref(n), ctypes.byref(r), None, None, 0.0, None, None) == INVALID
+            assert b"q_out overlaps k" in lib.msgl_last_error(), (apart, shift)
+
+
 def test_verify_drafts_refusals(lib):
     def call(batch=True, **over):
         d = ops._DraftBatch(at(0), at(1), 1000, 1000, 1000, 0, at(2), at(3), at(4), at(5), at(6), 3, 9, at(7), at(8), at(9))

@@ -110,6 +110,15 @@ def test_columns_of_one_projection(in_place):
         assert torch.all(wide[:, :2] == 7) and torch.all(wide[:, 18:] == 7)
 
 
+@pytest.mark.parametrize("T", [1, 2, 300])
+def test_output_between_the_inputs_columns(T):
+    q, k, v, pos, loc, pool = case(T, 16, 4, seed=T)
+    row = torch.cat([q, torch.zeros_like(q), k, v], 1)
+    out = ops.rope_store_kv(pool, row[:, :16], row[:, 32:36], row[:, 36:], pos[0], loc, ops.Rope(freqs(64)), q_out=row[:, 16:32])
+    check(q, k, v, pos, loc, pool, out, freqs(64))
+    assert torch.equal(row[:, :16], q) and torch.equal(row[:, 32:36], k) and torch.equal(row[:, 36:], v)
+
+
 def test_positions_out_of_a_larger_buffer():
     q, k, v, _, loc, pool = case(6, 8, 8, seed=7)
     buf = torch.randint(0, 900, (3, 50), dtype=torch.int32, device="cuda")
