@@ -17,23 +17,25 @@
 // of its heads where tokens are few, 4 heads a turn: 8 lanes hold a head, so that
 // both halves of every pair are in one lane, and a lane's part of the rotation
 // (the weights of the norm multiplied in) stays in its registers from head to head.
-// Heads come 6 turns ahead by cp.async into the lane's own places in shared memory, so
-// that no thread waits for another.  8256 tokens of 64/8 heads, normed: 55 us (6.1 TB/s of
-// the 338 MB; ncu: DRAM 66% busy, 28% of the warps), 4 tokens of 16/8 heads 2.4 us.  Slower:
+// Heads come 5 turns ahead by cp.async into the lane's own places in shared memory, so
+// that no thread waits for another.  8256 tokens of 64/8 heads, normed: 54.7 us (6.2 TB/s of
+// the 338 MB; ncu: DRAM 68% busy, 28% of the warps), 4 tokens of 16/8 heads 2.3 us.  Slower:
 // angles shared by a block through shared memory, cosines, sines and weights read
 // again for every head (370 instructions a turn in place of 200: 70 us); heads ahead in
-// registers, 2 to 5 turns (66 to 72 us); 4 turns ahead, or 6 or 7 blocks an SM (56 to 59).
+// registers, 2 to 5 turns (66 to 72 us); 4 turns ahead, or 24 or 28 warps an SM (56 to 59).  Blocks
+// of 128 threads and 6 turns ahead: 54.7 too, 64 tokens 3.2 in place of 3.0, 8192 of 8/8 heads 20.0
+// in place of 19.2.
 #include "kernels.h"
 
 namespace msgl {
 
 namespace {
 
-constexpr int kThreads = 128, kWarps = kThreads / 32;
+constexpr int kThreads = 64, kWarps = kThreads / 32;
 constexpr int kLanes = 8;                          // lanes of a head: two 16-byte chunks each
 constexpr int kHeads = 32 / kLanes;                // heads of a warp's turn
-constexpr int kAhead = 6;                          // turns whose heads are on their way
-constexpr int kBlocks = 5;                         // blocks an SM
+constexpr int kAhead = 5;                          // turns whose heads are on their way
+constexpr int kBlocks = 10;                         // blocks an SM
 
 // Two floats, for the instructions that take both at once.
 struct Two {
@@ -200,7 +202,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_store_kernel(const __g
                     float all = sum.lo() + sum.hi();
 #pragma unroll
                     for (int o = 1; o < kLanes; o <<= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-                    if (is_q ? a.q_norm : a.k_norm) scale = 1.f / sqrtf(all * (1.f / kHeadDim) + a.eps);
+                    // (rsqrtf is off by two units of the last place at most; a root and a division: 55.3 us)
+                    if (is_q ? a.q_norm : a.k_norm) scale = rsqrtf(all * (1.f / kHeadDim) + a.eps);
                 }
                 if (is_q || is_k) {
 #pragma unroll
@@ -233,10 +236,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_store_kernel(const __g
 
 cudaError_t launch_rope_store(const RopeStoreArgs &a, cudaStream_t stream) {
     const int turns = (a.hq + 2 * a.pool.hkv + kHeads - 1) / kHeads;
-    // As many warps as the GPU holds at once (5 blocks of 4 an SM): a token's heads in parts where tokens are
+    // As many warps as the GPU holds at once (10 blocks of 2 an SM): a token's heads in parts where tokens are
     // few, whole tokens where they are enough (64/8 heads, us with 1, 2, 4, 10, 20 parts: 64 tokens 11.0, 6.9, 5.2,
     // 4.1, 3.3; 256 tokens 11.4, 7.2, 5.7, 4.7, 6.0; 4096 tokens 33.7, 34.1, 39.6, 49.9, 71).
-    const int64_t fit = (int64_t)sm_count() * 5 * kWarps / a.n_tokens;
+    const int64_t fit = (int64_t)sm_count() * kBlocks * kWarps / a.n_tokens;
     const int parts = (int)(fit < 1 ? 1 : fit < turns ? fit : turns);
     const unsigned blocks = (unsigned)(((int64_t)a.n_tokens * parts + kWarps - 1) / kWarps);
     auto kernel = a.q_norm || a.k_norm ? (a.adjacent ? rope_store_kernel<true, true> : rope_store_kernel<false, true>)
