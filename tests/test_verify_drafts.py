@@ -149,6 +149,29 @@ def test_values_that_are_no_numbers(given):
     assert out.tokens[5] == -1 and out.accepted[4] == 0
 
 
+@pytest.mark.parametrize("requests", [1, 40, 160])              # clusters of 8, 4 and 1 blocks
+@pytest.mark.parametrize("dtype,V", [(torch.float32, 70001), (torch.bfloat16, 70001)])
+def test_the_edges_in_long_rows(dtype, V, requests):
+    """Rows too long for registers: borders between tokens, nothing left over, no weight, values that are no numbers."""
+    n = max(requests, 12)
+    w = batch([1] * 6 + [0] * (n - 6), 64, dtype, seed=n)
+    p, q = torch.zeros(len(w["tokens"]), V, dtype=dtype), torch.zeros(len(w["tokens"]), V, dtype=dtype)
+    w["p"], w["q"] = p, q
+    p[:, [5, 35000, 70000]] = torch.tensor([0.25, 0.25, 0.5], dtype=dtype)
+    w["au"][:] = 0.9999
+    w["tokens"][1:12:2] = 7                        # the first six requests' draft: p 0 and q 1
+    q[0:12:2, 7] = 1
+    q[2] = p[2]                                    # p nowhere above q: the target's own row
+    p[4, :], q[4, 5] = 0, 1                        # an empty row, left over or not
+    p[6, 40000] = float("inf")
+    p[8, 60000], q[8, 35000] = float("nan"), float("nan")
+    q[10, [5, 70000]] = 1                          # one token left over
+    w["su"][:12] = torch.tensor([0.0, 0.25, 0.9, 0.3, 0.1, 0.99, 0.0, 0.25, 0.4999999, 0.5, 1.0, float("nan")])
+    out = run(w, flags=ops.DEVERR_PROBS)
+    assert out.tokens[0:12:2].tolist() == [5, 35000, -1, -1, 5, 35000]
+    assert out.tokens[12:18].tolist() == [5, 35000, 35000, 70000, 70000, 70000]
+
+
 def test_bad_tokens():
     w = batch([3, 2], 400, seed=9, near=0.0)
     w["au"][:] = 0
