@@ -574,7 +574,8 @@ class Rope:
             raise ValueError("axes must have an entry in [0, 3] for each of inv_freq")
         # a fraction of a turn in 64 bits: whole turns of an integer position drop out of the product
         turns = [int(math.fmod(f / (2 * math.pi), 1.0) * 2.0 ** 64) % 2 ** 64 for f in freq]
-        self.turns = torch.tensor([t - 2 ** 64 if t >> 63 else t for t in turns], dtype=torch.int64, device=device or "cuda")
+        self.turns = torch.tensor([t - 2 ** 64 if t >> 63 else t for t in turns], dtype=torch.int64,
+                                  device="cuda" if device is None else device)
         self.axes, self.adjacent, self.factor = bytes(axes), bool(adjacent), float(factor)
 
 
