@@ -22,6 +22,7 @@
 // (10.9 against 8.5 us for half a million random pages, with the clearing of the map) and eight times as much to
 // count.  Pools of up to 32 thousand pages under small tables are bound by latency and
 // launches, and such a cluster does them in one launch (small_pool_kernel).
+#include "cluster.cuh"
 #include "kernels.h"
 
 namespace msgl {
@@ -36,14 +37,6 @@ constexpr int kUnit = 32 * kPerLane;                 // table entries of one war
 
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 // x summed over the warp's lanes up to this one.
 __device__ __forceinline__ uint32_t warp_scan(uint32_t x) {
@@ -334,18 +327,14 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t (&part)[W], 
     return __reduce_add_sync(0xffffffffu, lane < warp ? w : 0) + upto - x;
 }
 
-// Up to four numbers of every block of the cluster, in all of them.  The blocks are known to run (`started`) before
+// Up to four numbers of every block of the cluster, in all of them.  The blocks are known to run (cluster_started) before
 // one writes into another's shared memory, and none is written to when it may have ended.
 struct Peers {
     uint4 of[kCluster];
-    static __device__ __forceinline__ void started() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
     __device__ __forceinline__ void put(int rank, const uint4 &x) {
         if (threadIdx.x >= kCluster) return;
-        uint32_t at;
-        asm("mapa.shared::cluster.u32 %0, %1, %2;"
-            : "=r"(at)
-            : "r"((uint32_t)__cvta_generic_to_shared(of + rank)), "r"(threadIdx.x));
-        asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
+        asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(peer_address(of + rank, threadIdx.x)),
+                     "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
                      : "memory");
     }
 };
@@ -353,7 +342,7 @@ struct Peers {
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 2) free_list_kernel(const PageMapArgs a) {
     __shared__ uint32_t part[3][kWarps], words[kThreads], places[kThreads];
     __shared__ Peers peers;
-    Peers::started();
+    cluster_started();
     const int warp = threadIdx.x >> 5, rank = cluster_rank();
     const Share s = share_of(a, rank);
     wait_for_last();
@@ -407,7 +396,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 2) 
     __shared__ uint32_t part[5][kWarps], used_words[kThreads];
     __shared__ uint4 words[kThreads];
     __shared__ Peers peers[3];
-    Peers::started();
+    cluster_started();
     let_next_start();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = cluster_rank();
     const Share s = share_of(a, rank);
@@ -560,10 +549,8 @@ static_assert(kSmallWords == 2 * kThreads, "two words a thread");
 
 // 8 bytes out of another block's shared memory.
 __device__ __forceinline__ uint2 ld_peer(const void *p, int rank) {
-    uint32_t at;
     uint2 v;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(peer_address(p, rank)) : "memory");
     return v;
 }
 

@@ -23,6 +23,7 @@
 // front, exchange and draw behind take the rest); 4 over 50001 of bf16: 5.0 us.  With
 // 64-bit sums: 72 and 14 us.  Sums sent by st.async and waited for by one warp, in place
 // of the cluster's barrier: 25.8 us, and 0.25 less for 4 requests.
+#include "cluster.cuh"
 #include "kernels.h"
 
 namespace msgl {
@@ -30,15 +31,6 @@ namespace msgl {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 // hi + lo, |lo| at most half a unit of hi's last place.
 struct Sum {
@@ -391,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
     static_assert(kWarps == 16, "a block of 16 runs");
     __shared__ Shared s;
     // (the others have to be running before this block writes into their shared memory)
-    asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+    cluster_started();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = cluster_rank(), b = blockIdx.x >> log2_cluster;
     const int first = __ldg(a.cu_ext + b), end = __ldg(a.cu_ext + b + 1);
@@ -444,13 +436,10 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
         else sum = run_sum(r, n0, n1);
         // every block gets every run's sum
         if (!second) cluster_wait();
-        if (lane < cluster) {
-            uint32_t at;
-            asm("mapa.shared::cluster.u32 %0, %1, %2;"
-                : "=r"(at)
-                : "r"((uint32_t)__cvta_generic_to_shared(&s.runs[mine])), "r"(lane));
-            asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(sum.hi), "f"(sum.lo) : "memory");
-        }
+        if (lane < cluster)
+            asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(peer_address(&s.runs[mine], lane)), "f"(sum.hi),
+                         "f"(sum.lo)
+                         : "memory");
         cluster_arrive();
         if (rank == 0 && !second) {
             // (written here, where the block waits anyway)
