@@ -302,7 +302,7 @@ msgl_status msgl_check_copy_meta(int64_t num_slots, int32_t page_size, const int
             return bad(MSGL_ERR_INVALID_ARG, "pair %d: %d tokens are outside [0, page_size = %d]", i, tokens[i], page_size);
         if (!written.insert(dst[i]).second)
             return bad(MSGL_ERR_INVALID_ARG, "pair %d: page %d is an earlier pair's dst too", i, dst[i]);
-        read.insert(src[i]);
+        if (src[i] != dst[i]) read.insert(src[i]);   // (a page onto itself stays what it is)
     }
     for (int32_t i = 0; i < num_pairs; ++i)
         if (dst[i] >= 0 && read.count(dst[i]))

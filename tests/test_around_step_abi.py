@@ -273,6 +273,8 @@ def test_check_copy_meta():
     expect(INVALID, "pair 1: 17 tokens", ops.check_copy_meta, 160, 16, i32(0, 1), i32(5, 6), i32(1, 17))
     expect(INVALID, "pair 1: page 5 is an earlier", ops.check_copy_meta, 160, 16, i32(0, 1), i32(5, 5))
     expect(INVALID, "pair 0: page 1 is written and read", ops.check_copy_meta, 160, 16, i32(0, 1), i32(1, 5))
+    ops.check_copy_meta(160, 16, i32(5, 0), i32(5, 6))       # a page onto itself
+    expect(INVALID, "pair 0: page 5 is written and read", ops.check_copy_meta, 160, 16, i32(5, 5), i32(5, 6))
     with pytest.raises(ValueError):
         ops.check_copy_meta(160, 16, i32(0, 1), i32(1))
 

@@ -180,6 +180,11 @@ def test_long_lists_are_taken_in_groups():
     run_copy(p, src.tolist(), dst.tolist())
 
 
+def test_a_page_onto_itself_and_a_pool_named_twice():
+    p = pools(2, 20 * 16, 8, 16)
+    run_copy([p[0], p[1], p[0]], [5, 6], [5, 9])
+
+
 def test_bad_pairs_are_passed_over():
     p = pools(2, 20 * 16, 8, 16)
     run_copy(p, [1, 20, 3], [11, 12, 13], flags=ops.DEVERR_PAGE_RANGE)
