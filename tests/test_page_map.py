@@ -58,26 +58,28 @@ def test_free(ps, batch, longest, num_pages):
     run_free(table, rows, lens, num_pages, ps, some_held(rng, num_pages, 0.9), shift=5)
 
 
-def test_free_without_rows_and_with_shared_pages():
-    table, rows, lens, rng = requests(12, 4, 90, 700, 3, share=5)
-    run_free(table, rows, lens, 700, 4)
+@pytest.mark.parametrize("pages", [700, 40000])
+def test_free_without_rows_and_with_shared_pages(pages):
+    table, rows, lens, rng = requests(12, 4, 90, pages, 3, share=5)
+    run_free(table, rows, lens, pages, 4)
     lens3 = [0, 3, 8] + [4 * table.shape[1]] * 2              # (whole rows, whatever stands in them)
-    run_free(table, None, lens3, 700, 4, flags=ops.DEVERR_PAGE_RANGE if ref.names_no_page(table, None, lens3, 700, 4) else 0)
-    run_free(table, [rows[0], rows[0], -1], [lens[0], lens[0], 5], 700, 4)
+    run_free(table, None, lens3, pages, 4, flags=ops.DEVERR_PAGE_RANGE if ref.names_no_page(table, None, lens3, pages, 4) else 0)
+    run_free(table, [rows[0], rows[0], -1], [lens[0], lens[0], 5], pages, 4)
 
 
 @pytest.mark.parametrize("first", [0, 5, 31, 1000])
-def test_free_of_pages_in_a_row(first):
+@pytest.mark.parametrize("pages", [1500, 40000])
+def test_free_of_pages_in_a_row(pages, first):
     """Neighbouring pages share words of the bitmap: whole rows of them, broken runs, one page many times."""
     table = np.tile(np.arange(first, first + 300, dtype=np.int32), (40, 1))
     table[1::2] = table[1::2, ::-1]
     table[3, 10:200] = first + 7
     table[5, ::3] = -1
     lens = [300] * 40
-    run_free(table, None, lens, 1500, 1, flags=ops.DEVERR_PAGE_RANGE)
-    run_free(table[:3], None, [300, 299, 33], 1500, 1)
-    run_compact(table[:3], None, [300, 299, 33], 1500, 1)
-    run_compact(table, None, lens, 1500, 1, flags=ops.DEVERR_PAGE_RANGE)
+    run_free(table, None, lens, pages, 1, flags=ops.DEVERR_PAGE_RANGE)
+    run_free(table[:3], None, [300, 299, 33], pages, 1)
+    run_compact(table[:3], None, [300, 299, 33], pages, 1)
+    run_compact(table, None, lens, pages, 1, flags=ops.DEVERR_PAGE_RANGE)
 
 
 @pytest.mark.parametrize("batch", [70, 601])
@@ -102,20 +104,23 @@ def test_free_at_the_ends():
     run_free(empty, None, [], 0, 16)
     run_free(empty, None, [], 1, 16)
     run_free(np.zeros((2, 0), np.int32), None, [0, 0], 70, 1)
-    full = np.arange(320, dtype=np.int32).reshape(2, 160)
-    run_free(full, None, [160, 160], 320, 1)
-    run_free(full, None, [160, 159], 320, 1)
-    run_free(full, None, [0, 0], 320, 1, np.ones(320, np.uint8))
+    for n in (320, 40960):
+        full = np.arange(n, dtype=np.int32).reshape(2, n // 2)
+        run_free(full, None, [n // 2, n // 2], n, 1)
+        run_free(full, None, [n // 2, n // 2 - 1], n, 1)
+        run_free(full, None, [0, 0], n, 1, np.ones(n, np.uint8))
+    run_free(empty, None, [], 40000, 1)
 
 
-def test_free_of_what_is_wrong():
-    table, rows, lens, rng = requests(6, 8, 100, 300, 5)
-    ids = np.clip(table, 0, 299)
+@pytest.mark.parametrize("pages", [300, 40001])
+def test_free_of_what_is_wrong(pages):
+    table, rows, lens, rng = requests(6, 8, 100, pages, 5)
+    ids = np.clip(table, 0, pages - 1)
     for bad, flag in ((-1, ops.DEVERR_LENGTH), (8 * table.shape[1] + 1, ops.DEVERR_LENGTH), (2 ** 31 - 1, ops.DEVERR_LENGTH)):
-        run_free(ids, rows, [bad] + lens[1:], 300, 8, flags=flag)      # all that its row names is kept
-    run_free(ids, [table.shape[0], -2] + rows[2:], lens, 300, 8, flags=ops.DEVERR_ROW)
-    ids[rows[0], 0] = 300
-    run_free(ids, rows, [8] + lens[1:], 300, 8, flags=ops.DEVERR_PAGE_RANGE)
+        run_free(ids, rows, [bad] + lens[1:], pages, 8, flags=flag)      # all that its row names is kept
+    run_free(ids, [table.shape[0], -2] + rows[2:], lens, pages, 8, flags=ops.DEVERR_ROW)
+    ids[rows[0], 0] = pages
+    run_free(ids, rows, [8] + lens[1:], pages, 8, flags=ops.DEVERR_PAGE_RANGE)
 
 
 def test_free_of_millions_of_pages():
@@ -162,35 +167,46 @@ def test_compact(ps, batch, longest, num_pages, out):
     run_compact(table, rows, lens, num_pages, ps, some_held(rng, num_pages, 0.3), out=out)
 
 
-def test_compact_shared_pages_and_rows_named_twice():
-    table, rows, lens, rng = requests(12, 4, 90, 2000, 3, share=9)
-    got = run_compact(table, rows, lens, 2000, 4)
+@pytest.mark.parametrize("pages", [2000, 40000])
+def test_compact_shared_pages_and_rows_named_twice(pages):
+    table, rows, lens, rng = requests(12, 4, 90, pages, 3, share=9)
+    got = run_compact(table, rows, lens, pages, 4)
     again = got.page_table.cpu().numpy()
-    got = run_compact(again, rows, lens, 2000, 4)             # nothing is left to move
+    got = run_compact(again, rows, lens, pages, 4)             # nothing is left to move
     assert got.num_moves.item() == 0
-    run_compact(table, rows + rows[:5] + [-1], lens + lens[:5] + [7], 2000, 4)
-    run_compact(table, rows + rows[:5], lens + lens[:5], 2000, 4, out="new")
+    run_compact(table, rows + rows[:5] + [-1], lens + lens[:5] + [7], pages, 4)
+    run_compact(table, rows + rows[:5], lens + lens[:5], pages, 4, out="new")
+
+
+def test_compact_wide_rows_named_many_times():
+    """More units than warps: rows are read again after another warp has renamed them."""
+    table = np.random.default_rng(4).permutation(300000)[:2 * 60000].astype(np.int32).reshape(2, 60000)
+    run_compact(table, [0, 1] * 12, [60000, 59999, 60000, 31] * 6, 300000, 1)
 
 
 def test_compact_at_the_ends():
     empty = np.zeros((0, 0), np.int32)
     run_compact(empty, None, [], 0, 16)
     run_compact(empty, None, [], 5, 16)
-    full = np.random.default_rng(1).permutation(320).astype(np.int32).reshape(2, 160)
-    run_compact(full, None, [160, 160], 320, 1)
-    run_compact(full, None, [160, 1], 320, 1)
-    run_compact(full, None, [160, 20], 320, 1, np.ones(320, np.uint8))
-    run_compact(full, None, [160, 0], 320, 1, (np.arange(320) >= 300).astype(np.uint8))
+    run_compact(empty, None, [], 40000, 1)
+    for n in (320, 40960):
+        m = n // 2
+        full = np.random.default_rng(1).permutation(n).astype(np.int32).reshape(2, m)
+        run_compact(full, None, [m, m], n, 1)
+        run_compact(full, None, [m, 1], n, 1)
+        run_compact(full, None, [m, 20], n, 1, np.ones(n, np.uint8))
+        run_compact(full, None, [m, 0], n, 1, (np.arange(n) >= n - 20).astype(np.uint8))
 
 
-def test_compact_what_is_wrong():
-    table, rows, lens, rng = requests(6, 8, 100, 300, 5)
-    ids = np.clip(table, 0, 299)
-    run_compact(ids, rows, [-1] + lens[1:], 300, 8, flags=ops.DEVERR_LENGTH)
-    run_compact(ids, [table.shape[0]] + rows[1:], lens, 300, 8, flags=ops.DEVERR_ROW)
-    ids[rows[0], 0] = 300
+@pytest.mark.parametrize("pages", [300, 40001])
+def test_compact_what_is_wrong(pages):
+    table, rows, lens, rng = requests(6, 8, 100, pages, 5)
+    ids = np.clip(table, 0, pages - 1)
+    run_compact(ids, rows, [-1] + lens[1:], pages, 8, flags=ops.DEVERR_LENGTH)
+    run_compact(ids, [table.shape[0]] + rows[1:], lens, pages, 8, flags=ops.DEVERR_ROW)
+    ids[rows[0], 0] = pages
     ids[rows[0], 1] = -1
-    run_compact(ids, rows, [16] + lens[1:], 300, 8, flags=ops.DEVERR_PAGE_RANGE, out="new")
+    run_compact(ids, rows, [16] + lens[1:], pages, 8, flags=ops.DEVERR_PAGE_RANGE, out="new")
 
 
 def test_large_compaction():
@@ -231,27 +247,28 @@ def test_a_compacted_pool_reads_as_before():
     assert used[:c.num_used.item()].all() and not used[c.num_used.item():].any() and c.num_moves.item() > 0
 
 
-def test_graph_and_stream():
-    table, rows, lens, rng = requests(30, 4, 200, 4000, 13)
+@pytest.mark.parametrize("pages", [4000, 70000])                # one launch, several
+def test_graph_and_stream(pages):
+    table, rows, lens, rng = requests(30, 4, 200, pages, 13)
     t, r, n = i32(table, "cuda"), i32(rows, "cuda"), i32(lens, "cuda")
-    free = ops.FreePages(torch.zeros(4000, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda"))
+    free = ops.FreePages(torch.zeros(pages, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda"))
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
-    first = ops.free_pages(t, n, 16000, 4, r, stream=side)
+    first = ops.free_pages(t, n, 4 * pages, 4, r, stream=side)
     side.synchronize()
-    assert first.num_free.item() == 4000 - ref.held_by(table, rows, lens, 4000, 4).sum()
+    assert first.num_free.item() == pages - ref.held_by(table, rows, lens, pages, 4).sum()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        ops.free_pages(t, n, 16000, 4, r, out=free)
-        c = ops.compact_pages(t, n, 16000, 4, r)
-    for seed in (14, 15):
-        table, rows, lens, rng = requests(30, 4, 200, 4000, seed)
+        ops.free_pages(t, n, 4 * pages, 4, r, out=free)
+        c = ops.compact_pages(t, n, 4 * pages, 4, r)
+    for seed in range(14, 20):
+        table, rows, lens, rng = requests(30, 4, 200, pages, seed)
         t.copy_(i32(table)), r.copy_(i32(rows)), n.copy_(i32(lens))
         graph.replay()
-        want = np.nonzero(~ref.held_by(table, rows, lens, 4000, 4))[0].tolist()
-        assert free.pages.tolist() == want + [-1] * (4000 - len(want))
-        assert np.array_equal(t.cpu().numpy(), ref.compact(table, rows, lens, None, 4000, 4)[0])
-        assert c.num_used.item() == 4000 - len(want)
+        want = np.nonzero(~ref.held_by(table, rows, lens, pages, 4))[0].tolist()
+        assert free.pages.tolist() == want + [-1] * (pages - len(want))
+        assert np.array_equal(t.cpu().numpy(), ref.compact(table, rows, lens, None, pages, 4)[0])
+        assert c.num_used.item() == pages - len(want)
 
 
 def test_refusals():
