@@ -666,8 +666,9 @@ msgl_status msgl_rope_store_kv(const msgl_kv_pool *pool, const msgl_new_tokens *
                         flat(reinterpret_cast<const int32_t *>(rope->turns), 2 * rope->num_pairs, "rope->turns"),
                         {static_cast<const int32_t *>(pool->k_pool), pool->num_slots, kv_row / 2, kv_row / 2, "the K pool"},
                         {static_cast<const int32_t *>(pool->v_pool), pool->num_slots, kv_row / 2, kv_row / 2, "the V pool"}};
+    const bool in_place = n.q_out == n.q && n.out_stride == n.q_stride;
     for (const Span &in : ins) {
-        if (in.at == ins[0].at && n.q_out == n.q && n.out_stride == n.q_stride) continue;   // in place
+        if (&in == &ins[0] && in_place) continue;   // (q alone: k or v may begin where it does and be turned while they are read)
         if (overlap(out, in)) return fail(MSGL_ERR_INVALID_ARG, "q_out overlaps %s", in.name);
     }
     a.k_pool = static_cast<__nv_bfloat16 *>(pool->k_pool);

@@ -1,0 +1,42 @@
+"""Buffers that a call around the step may not be given twice (no GPU): every call below is refused by a host check before
+anything is launched."""
+import ctypes
+
+import pytest
+
+from paged_kv_attention_24_gb300 import ops
+
+INVALID = 1
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    from paged_kv_attention_24_gb300 import build
+    build.build()
+    return ops.load()
+
+
+def at(k):
+    """A device address that nothing else of a call overlaps."""
+    return (k + 1) << 24
+
+
+def rope(lib, q_norm=None, k_norm=None, pool=(at(0), at(1)), hq=8, **over):
+    """Four tokens of hq/8 heads, three axes; each buffer on its own but for what `over` says."""
+    p = ops._Pool(*pool, 256, 16, 8, 128)
+    n = ops._NewTokens(at(3), at(4), at(5), at(6), hq * 128, 8 * 128, 8 * 128, hq * 128, at(7), 4, at(8), 4, hq)
+    turns = over.pop("turns", at(2))
+    for k, v in over.items():
+        assert hasattr(n, k)
+        setattr(n, k, v)
+    r = ops._Rope(turns, None, 64, 3, 0, 1.0)
+    return lib.msgl_rope_store_kv(ctypes.byref(p), ctypes.byref(n), ctypes.byref(r), q_norm, k_norm, 1e-6, None, None)
+
+
+@pytest.mark.parametrize("name,over", [
+    ("k", dict(k=at(3))), ("v", dict(v=at(3))), ("positions", dict(positions=at(3))), ("out_loc", dict(out_loc=at(3))),
+    ("rope->turns", dict(turns=at(3))), ("q_norm", dict(q_norm=at(3))), ("k_norm", dict(k_norm=at(3))),
+    ("the K pool", dict(pool=(at(3), at(1)))), ("the V pool", dict(pool=(at(0), at(3))))])
+def test_rotation_in_place_spares_q_alone(lib, name, over):
+    assert rope(lib, q_out=at(3), **over) == INVALID
+    assert lib.msgl_last_error() == f"q_out overlaps {name}".encode()
