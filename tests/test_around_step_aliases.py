@@ -40,3 +40,23 @@ def rope(lib, q_norm=None, k_norm=None, pool=(at(0), at(1)), hq=8, **over):
 def test_rotation_in_place_spares_q_alone(lib, name, over):
     assert rope(lib, q_out=at(3), **over) == INVALID
     assert lib.msgl_last_error() == f"q_out overlaps {name}".encode()
+
+
+def verify(lib, **over):
+    d = ops._DraftBatch(at(0), at(1), 1000, 1000, 1000, 0, at(2), at(3), at(4), at(5), at(6), 3, 9, at(7), at(8), at(9))
+    for k, v in over.items():
+        assert hasattr(d, k)
+        setattr(d, k, v)
+    return lib.msgl_verify_drafts(ctypes.byref(d), None, None)
+
+
+@pytest.mark.parametrize("name", ["tokens", "cu_ext", "accept_u", "sample_u", "target", "draft"])
+def test_lengths_in_place_spare_the_cached_lengths_alone(lib, name):
+    assert verify(lib, kv_lens=at(6), **{name: at(6)}) == INVALID
+    assert lib.msgl_last_error() == f"kv_lens overlaps {name}".encode()
+
+
+@pytest.mark.parametrize("name", ["accepted", "out_tokens"])
+def test_no_other_output_lies_over_the_cached_lengths(lib, name):
+    assert verify(lib, kv_lens=at(6), **{name: at(6)}) == INVALID
+    assert verify(lib, **{name: at(6)}) == INVALID
