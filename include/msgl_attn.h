@@ -382,6 +382,8 @@ MSGL_API msgl_status msgl_step_tables(int64_t num_slots, int32_t page_size, int3
  *                be columns of one projection's output
  *   q_out        the same for the turned q; may be q itself (same stride), and may not
  *                otherwise overlap an input
+ *                (nor may the pools overlap an input, q_out or each other: k and v of one
+ *                token are stored while another's are read)
  *   positions    device int32, axis a of token t at a * axis_stride + t; any int32 value.
  *                axis_stride: at least n_tokens, or 0 (the same positions on every axis)
  *   out_loc      device int32 [n_tokens]: the token's pool slot.  -1: not a token (the

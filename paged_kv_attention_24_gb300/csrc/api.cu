@@ -663,14 +663,19 @@ msgl_status msgl_rope_store_kv(const msgl_kv_pool *pool, const msgl_new_tokens *
                         flat(static_cast<const int32_t *>(k_norm), msgl::kHeadDim / 2, "k_norm"),
                         {n.positions, one_axis ? 1 : rope->num_axes, n.n_tokens, one_axis ? n.n_tokens : n.axis_stride, "positions"},
                         flat(n.out_loc, n.n_tokens, "out_loc"),
-                        flat(reinterpret_cast<const int32_t *>(rope->turns), 2 * rope->num_pairs, "rope->turns"),
-                        {static_cast<const int32_t *>(pool->k_pool), pool->num_slots, kv_row / 2, kv_row / 2, "the K pool"},
-                        {static_cast<const int32_t *>(pool->v_pool), pool->num_slots, kv_row / 2, kv_row / 2, "the V pool"}};
+                        flat(reinterpret_cast<const int32_t *>(rope->turns), 2 * rope->num_pairs, "rope->turns")};
+    const int64_t pool_words = pool->num_slots * (kv_row / 2);
+    const Span pools[] = {flat(static_cast<const int32_t *>(pool->k_pool), pool_words, "the K pool"),
+                          flat(static_cast<const int32_t *>(pool->v_pool), pool_words, "the V pool")};
     const bool in_place = n.q_out == n.q && n.out_stride == n.q_stride;
     for (const Span &in : ins) {
         if (&in == &ins[0] && in_place) continue;   // (q alone: k or v may begin where it does and be turned while they are read)
         if (overlap(out, in)) return fail(MSGL_ERR_INVALID_ARG, "q_out overlaps %s", in.name);
     }
+    for (const Span &rows : pools)
+        if (overlap(out, rows)) return fail(MSGL_ERR_INVALID_ARG, "q_out overlaps %s", rows.name);
+    // (the pools are outputs too)
+    if ((s = check_overlaps(pools, 2, ins, 8))) return s;
     a.k_pool = static_cast<__nv_bfloat16 *>(pool->k_pool);
     a.v_pool = static_cast<__nv_bfloat16 *>(pool->v_pool);
     a.q = static_cast<const __nv_bfloat16 *>(n.q);

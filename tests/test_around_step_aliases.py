@@ -60,3 +60,20 @@ def test_lengths_in_place_spare_the_cached_lengths_alone(lib, name):
 def test_no_other_output_lies_over_the_cached_lengths(lib, name):
     assert verify(lib, kv_lens=at(6), **{name: at(6)}) == INVALID
     assert verify(lib, **{name: at(6)}) == INVALID
+
+
+@pytest.mark.parametrize("pool", ["K", "V"])
+@pytest.mark.parametrize("name", ["q", "k", "v", "positions", "out_loc", "rope->turns", "q_norm", "k_norm"])
+def test_no_input_of_the_rotary_store_lies_in_the_pools(lib, name, pool):
+    """(a token's rows are stored while another's are read)"""
+    first = at(0 if pool == "K" else 1)
+    for where in (first, first + 255 * 2048, first + 128 * 2048 - 2048):
+        kw = {"turns" if name == "rope->turns" else name: where}
+        assert rope(lib, **kw) == INVALID
+        assert lib.msgl_last_error() == f"the {pool} pool overlaps {name}".encode()
+
+
+def test_the_two_pools_of_the_rotary_store_are_two(lib):
+    for v in (at(0), at(0) + 255 * 2048, at(0) - 255 * 2048):
+        assert rope(lib, pool=(at(0), v)) == INVALID
+        assert lib.msgl_last_error() == b"the K pool overlaps the V pool"
