@@ -538,8 +538,9 @@ MSGL_API msgl_status msgl_copy_pages(const msgl_kv_pool *pools, int32_t num_pool
  * of its pages is given away; an id outside the pool (MSGL_DEVERR_PAGE_RANGE) is
  * skipped.  The outputs may overlap neither an input nor each other.
  *   workspace    device scratch of at least msgl_page_map_workspace_size() bytes, 256-byte
- *                aligned, fully rewritten by every call; two calls (or captured graphs)
- *                that may overlap need one each
+ *                aligned; what it held does not matter.  It may overlap neither an input nor
+ *                an output, and two calls (or captured graphs) that may run at once need
+ *                one each
  */
 MSGL_API size_t msgl_page_map_workspace_size(int64_t num_slots, int32_t page_size);
 

@@ -170,6 +170,11 @@ msgl_status check_map_workspace(const void *workspace, size_t bytes, int32_t num
     return MSGL_OK;
 }
 
+// The part of a page-map workspace that a call writes.
+Span map_span(void *workspace, int32_t num_pages) {
+    return flat(static_cast<const int32_t *>(workspace), (int64_t)(msgl::page_map_workspace_bytes(num_pages) / 4), "workspace");
+}
+
 // The arguments that msgl_free_pages and msgl_compact_pages share.
 msgl_status prepare_page_map(int64_t num_slots, int32_t page_size, const int32_t *req_table, int32_t num_rows,
                              int32_t table_stride, int32_t table_width, const int32_t *req_rows, const int32_t *lens,
@@ -872,10 +877,10 @@ msgl_status msgl_free_pages(int64_t num_slots, int32_t page_size, const int32_t 
     if (s) return s;
     if (!num_free || (a.num_pages > 0 && !pages))
         return fail(MSGL_ERR_INVALID_ARG, "pages and num_free must be non-NULL");
-    const Span outs[] = {flat(pages, a.num_pages, "pages"), flat(num_free, 1, "num_free")};
+    const Span outs[] = {flat(pages, a.num_pages, "pages"), flat(num_free, 1, "num_free"), map_span(workspace, a.num_pages)};
     const Span ins[] = {{req_table, num_rows, table_width, table_stride, "req_table"}, flat(req_rows, num_reqs, "req_rows"),
                         flat(lens, num_reqs, "lens"), bytes_span(held, a.num_pages, "held")};
-    if ((s = check_overlaps(outs, 2, ins, 4))) return s;
+    if ((s = check_overlaps(outs, 3, ins, 4))) return s;
     if ((s = check_map_workspace(workspace, workspace_bytes, a.num_pages))) return s;
     a.pages_out = pages;
     a.count_out = num_free;
@@ -904,11 +909,12 @@ msgl_status msgl_compact_pages(int64_t num_slots, int32_t page_size, const int32
     const Span outs[] = {flat(out->remap, a.num_pages, "out->remap"), flat(out->src, a.num_pages / 2, "out->src"),
                          flat(out->dst, a.num_pages / 2, "out->dst"), flat(out->num_moves, 1, "out->num_moves"),
                          flat(out->num_used, 1, "out->num_used"),
-                         {out->page_ids, num_rows, table_width, out->stride, "out->page_ids"}};
+                         {out->page_ids, num_rows, table_width, out->stride, "out->page_ids"},
+                         map_span(workspace, a.num_pages)};
     const Span ins[] = {flat(req_rows, num_reqs, "req_rows"), flat(lens, num_reqs, "lens"),
                         bytes_span(held, a.num_pages, "held"),
                         {in_place ? nullptr : req_table, num_rows, table_width, table_stride, "req_table"}};
-    if ((s = check_overlaps(outs, 6, ins, 4))) return s;
+    if ((s = check_overlaps(outs, 7, ins, 4))) return s;
     if ((s = check_map_workspace(workspace, workspace_bytes, a.num_pages))) return s;
     a.pages_out = out->remap;
     a.count_out = out->num_moves;

@@ -77,3 +77,35 @@ def test_the_two_pools_of_the_rotary_store_are_two(lib):
     for v in (at(0), at(0) + 255 * 2048, at(0) - 255 * 2048):
         assert rope(lib, pool=(at(0), v)) == INVALID
         assert lib.msgl_last_error() == b"the K pool overlaps the V pool"
+
+
+def page_map(lib, compact, ws=at(10), **over):
+    """16 pages, 4 rows of 8 columns, 2 requests."""
+    b = dict(req_table=at(0), req_rows=at(1), lens=at(2), held=at(3), pages=at(4), num_free=at(5), page_ids=at(4), remap=at(5),
+             src=at(6), dst=at(7), num_moves=at(8), num_used=at(9))
+    assert not set(over) - set(b)
+    b.update(over)
+    args = 256, 16, b["req_table"], 4, 8, 8, b["req_rows"], b["lens"], 2, b["held"]
+    tail = ws, lib.msgl_page_map_workspace_size(256, 16), None, None
+    if not compact:
+        return lib.msgl_free_pages(*args, b["pages"], b["num_free"], *tail)
+    out = ops._CompactOut(b["page_ids"], 8, b["remap"], b["src"], b["dst"], b["num_moves"], b["num_used"])
+    return lib.msgl_compact_pages(*args, ctypes.byref(out), *tail)
+
+
+IN = [("req_table", 128), ("req_rows", 8), ("lens", 8), ("held", 16)]
+FREE = [("pages", 64), ("num_free", 4)]
+COMPACT = [("page_ids", 128), ("remap", 64), ("src", 32), ("dst", 32), ("num_moves", 4), ("num_used", 4)]
+
+
+@pytest.mark.parametrize("compact,name,size", [(False, *x) for x in IN + FREE] + [(True, *x) for x in IN + COMPACT])
+def test_the_page_calls_workspace_is_scratch_of_its_own(lib, compact, name, size):
+    need = lib.msgl_page_map_workspace_size(256, 16)
+    for where in (at(10), at(10) + need - size, at(10) + 4 - size):
+        assert page_map(lib, compact, **{name: where}) == INVALID, where - at(10)
+        assert b"workspace" in lib.msgl_last_error() and name.encode() in lib.msgl_last_error()
+
+
+def test_the_table_in_place_is_not_the_workspace_either(lib):
+    assert page_map(lib, True, req_table=at(10), page_ids=at(10)) == INVALID
+    assert b"workspace" in lib.msgl_last_error()
