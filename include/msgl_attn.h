@@ -372,7 +372,7 @@ MSGL_API msgl_status msgl_step_tables(int64_t num_slots, int32_t page_size, int3
  * with x_j, y_j = dims j and j + num_pairs, or (adjacent) 2j and 2j + 1; dims from
  * 2 * num_pairs on stay as they are.  With q_norm / k_norm a head is first
  * replaced by x * w / sqrt(mean(x^2) + eps).  All of it is computed in 32 bits (the
- * angle modulo a turn exactly) and rounded to bf16 once; v is copied.
+ * angle modulo a turn in 64, then rounded) and rounded to bf16 once; v is copied.
  *
  *   turns        device uint64 [num_pairs]: f_j / (2 pi) * 2^64 modulo 2^64
  *   axes         host uint8 [num_pairs]: axis_j < num_axes, or NULL (all 0)

@@ -10,7 +10,8 @@
 // after an optional norm of the head, x * w / sqrt(mean(x^2) + eps).  The frequency
 // comes as a 64-bit fraction of a whole turn, so that the product with an integer
 // position modulo 2^64 is the angle modulo a turn with nothing lost, however far the
-// position; its upper 32 bits go through sincospif (an error of 2^-25 of the angle).
+// position; rounded to 32 bits (by 2^-24 of the angle at most, so that the slow pairs'
+// small angles keep their digits) it goes through sincospif.
 // Everything is in 32 bits up to the one rounding to bf16.
 //
 // Bound by HBM for many tokens, by latency for few.  A warp takes a token, or a part
@@ -163,9 +164,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_store_kernel(const __g
         const uint32_t bits = j % 32 < 16 ? a.axis_bits[2 * i] : a.axis_bits[2 * i + 1];
         const int axis = bits >> (2 * (j % 16)) & 3;
         const int64_t pos = __ldg(a.positions + axis * a.axis_stride + t);
-        const uint64_t turn = __ldg(a.turns + j) * (uint64_t)pos;
+        const int64_t turn = (int64_t)(__ldg(a.turns + j) * (uint64_t)pos);
         float s, c;
-        sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
+        sincospif((float)turn * 0x1p-63f, &s, &c);
         cosines[j] = c * a.factor;
         sines[j] = s * a.factor;
     }
