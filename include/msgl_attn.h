@@ -428,7 +428,7 @@ MSGL_API msgl_status msgl_rope_store_kv(const msgl_kv_pool *pool, const msgl_new
  * p and q rows first + i of target and draft.  With a the number of drafts in
  * front of the first one that does not stand, and r = first + a:
  *   w = max(p_r - q_r, 0) when a draft was refused, p_r when none was or when
- *       that is zero everywhere;
+ *       that has no positive finite sum (it is zero everywhere, or q_r no probabilities);
  *   the new token = the first v with w_0 + .. + w_v > sample_u[b] * sum(w)
  *       (the last one with w > 0 when there is none, as for sample_u >= 1)
  *   accepted[b] = a;  kv_lens[b] = cached_lens[b] + a + 1
