@@ -474,10 +474,12 @@ MSGL_API msgl_status msgl_verify_drafts(const msgl_draft_batch *batch, uint32_t 
  * both, so the child gets a page of its own for it:
  *   F = lens[i] / page_size, tail = lens[i] % page_size
  *   req_table[child][p] = req_table[parent][p]             for p < F
- *   tail > 0: req_table[child][F] = free_pages[k], k the number of earlier forks with a tail;
+ *   tail > 0: req_table[child][F] = free_pages[k], k the number of earlier forks with a tail
+ *             whose rows and length are in range (refused for something else or not);
  *             copy_src[i] = req_table[parent][F], copy_dst[i] = that page, copy_tokens[i] = tail
  *   else      copy_src[i] = copy_dst[i] = -1, copy_tokens[i] = 0
- *   pages_taken[0] = how many of free_pages are now in use
+ *   pages_taken[0] = the number of all such forks, at most num_free: free_pages from there
+ *             on are as free as before (so are those in front that a refused fork left)
  * The copies are the arguments of msgl_copy_pages.  Later columns of the child's row stay
  * as they are.  lens[i] counts tokens that the parent keeps: a page that it will write
  * again (under drafts that may yet be refused) is not to be shared.
@@ -488,8 +490,10 @@ MSGL_API msgl_status msgl_verify_drafts(const msgl_draft_batch *batch, uint32_t 
  * table_width (MSGL_DEVERR_LENGTH); one that free_pages does not reach
  * (MSGL_DEVERR_NO_PAGES); and one whose new page or partly filled page is
  * outside [0, num_slots / page_size) (MSGL_DEVERR_PAGE_RANGE).  A refused fork's
- * row is left as it was and nothing is copied for it; its place among the free
- * pages is kept.  The outputs may overlap neither an input nor each other.
+ * row is left as it was and nothing is copied for it.  Its place among the free
+ * pages stays unused, so that the others' places do not depend on it; a fork whose
+ * rows are outside the table or whose length cannot be has no place.  The outputs
+ * may overlap neither an input nor each other.
  */
 typedef struct msgl_fork_out {
     int32_t *copy_src, *copy_dst, *copy_tokens;   /* device int32 [num_forks] */

@@ -630,7 +630,7 @@ class Forked(NamedTuple):
     src: torch.Tensor          # [N]  page to copy, -1 where none is
     dst: torch.Tensor          # [N]
     tokens: torch.Tensor       # [N]  tokens on it
-    pages_taken: torch.Tensor  # [1]  how many of the free pages are now in use
+    pages_taken: torch.Tensor  # [1]  how many places among the free pages were given out (to refused forks too)
 
 
 def fork_requests(req_table: torch.Tensor, parent_rows: torch.Tensor, child_rows: torch.Tensor, lens: torch.Tensor,
