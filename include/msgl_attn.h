@@ -388,9 +388,11 @@ MSGL_API msgl_status msgl_step_tables(int64_t num_slots, int32_t page_size, int3
  *                axis_stride: at least n_tokens, or 0 (the same positions on every axis)
  *   out_loc      device int32 [n_tokens]: the token's pool slot.  -1: not a token (the
  *                padding of msgl_step_tables, and the tokens of a request that it
- *                refused): nothing is read or written for it, its row of q_out
- *                stays as it was.  Another slot out of range sets
- *                MSGL_DEVERR_SLOT_RANGE: q is turned, nothing stored.
+ *                refused): nothing is written for it, its row of q_out stays as it
+ *                was.  Its rows of q, k and v and its positions may be read, so they
+ *                have to be memory like the others'; what they hold does not matter.
+ *                Another slot out of range sets MSGL_DEVERR_SLOT_RANGE: q is turned,
+ *                nothing stored.
  *   q_norm, k_norm  device bf16 [head_dim] or NULL
  * Duplicate slots are undefined (one of the rows wins).
  */

@@ -588,7 +588,7 @@ def rope_store_kv(pool: KVPool, q: torch.Tensor, k: torch.Tensor, v: torch.Tenso
     q [T,Hq,D], k and v [T,Hkv,D] may be columns of one tensor (tokens any multiple of 8
     elements apart); ``q_out`` may be q itself.  ``positions`` int32 [T] or [axes, T].  ``q_norm`` and
     ``k_norm`` bf16 [D] norm each head first.  A token with out_loc -1 is none (padding): its row of
-    q_out is not written.
+    q_out is not written, whatever its other rows hold.
     """
     r = (_native or _binding()).rope_store_kv(pool.k, pool.v, pool.page_size, q, k, v, positions, out_loc, rope.turns,
                                               rope.axes, rope.adjacent, rope.factor, q_out, q_norm, k_norm, eps, status,

@@ -55,3 +55,18 @@ def test_many_turns(T, hq, hkv, norms, adjacent):
     assert ops.read_status(status) == 0
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("T", [1, 5])
+def test_what_padding_holds_does_not_matter(T, norm):
+    """A batch of padding alone: rows of infinities, the farthest positions, nothing written and nothing reported."""
+    q, kv = (torch.full((T, h, D), float("inf"), dtype=torch.bfloat16, device="cuda") for h in (16, 8))
+    pool = ops.KVPool(*[torch.full((T, 8, D), 9.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)], 1)
+    out, status = torch.full_like(q, 3.0), ops.new_status()
+    pos = torch.full((4, T), -2 ** 31, dtype=torch.int32, device="cuda")
+    w = torch.ones(D, dtype=torch.bfloat16, device="cuda") if norm else None
+    ops.rope_store_kv(pool, q, kv, kv, pos, torch.full((T,), -1, dtype=torch.int32, device="cuda"),
+                      ops.Rope([1e6 ** (-j / 64) for j in range(64)], [j % 4 for j in range(64)]), q_out=out, q_norm=w, k_norm=w,
+                      status=status)
+    assert (out == 3).all() and (pool.k == 9).all() and (pool.v == 9).all() and ops.read_status(status) == 0
