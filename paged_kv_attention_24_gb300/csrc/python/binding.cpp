@@ -617,11 +617,12 @@ PyObject *copy_pages(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int64_t N = src.numel();
         if (dst.numel() != N) refuse("%s must have an entry for each of src", "dst");
         const int32_t *tokens = entries(a[3], "tokens", N, dev), *count = entries(a[4], "count", 1, dev);
-        const Ref seq(PySequence_Fast(a[0], "pools must be a sequence of KVPool"));
-        const Py_ssize_t pools = PySequence_Fast_GET_SIZE(seq.p);
+        // (a tuple of the caller's pools: what looks up their attributes may be Python code that changes a list)
+        const Ref fast(PySequence_Fast(a[0], "pools must be a sequence of KVPool")), seq(PySequence_Tuple(fast.p));
+        const Py_ssize_t pools = PyTuple_GET_SIZE(seq.p);
         std::vector<msgl_kv_pool> c((size_t)pools);
         for (Py_ssize_t i = 0; i < pools; ++i) {
-            PyObject *pool = PySequence_Fast_GET_ITEM(seq.p, i);
+            PyObject *pool = PyTuple_GET_ITEM(seq.p, i);
             const Ref ko(PyObject_GetAttr(pool, names[0])), vo(PyObject_GetAttr(pool, names[1])),
                 po(PyObject_GetAttr(pool, names[2]));
             const at::Tensor &k = checked(ko.p, "k_pool", at::kBFloat16, dev), &v = checked(vo.p, "v_pool", at::kBFloat16, dev);
