@@ -118,8 +118,8 @@ typedef struct msgl_page_table {
  *   k, v     device bf16 [n_tokens, num_kv_heads, head_dim]
  *   out_loc  device int32 [n_tokens]; row t goes to slot out_loc[t]
  *   status   device uint32 or NULL
- * Pool rows not named in out_loc are untouched.  Duplicate slots in out_loc
- * are undefined (one of the rows wins).  An out-of-range slot sets
+ * Pool rows not named in out_loc are untouched.  Duplicate slots in out_loc are
+ * undefined (what ends there may be of either row, or of both).  An out-of-range slot sets
  * MSGL_DEVERR_SLOT_RANGE and that row is skipped.  The copy is bit-exact.
  */
 MSGL_API msgl_status msgl_store_kv(const msgl_kv_pool *pool, const void *k, const void *v,
@@ -394,7 +394,7 @@ MSGL_API msgl_status msgl_step_tables(int64_t num_slots, int32_t page_size, int3
  *                Another slot out of range sets MSGL_DEVERR_SLOT_RANGE: q is turned,
  *                nothing stored.
  *   q_norm, k_norm  device bf16 [head_dim] or NULL
- * Duplicate slots are undefined (one of the rows wins).
+ * Duplicate slots are undefined (what ends there may be of either row, or of both).
  */
 typedef struct msgl_rope {
     const uint64_t *turns;         /* device */
@@ -519,7 +519,7 @@ MSGL_API msgl_status msgl_fork_requests(int64_t num_slots, int32_t page_size, in
  *   count        device int32 [1] or NULL: only the first count[0] pairs
  * A page id outside the pool (MSGL_DEVERR_PAGE_RANGE) or a count of tokens out of
  * range (MSGL_DEVERR_LENGTH) skips the pair.  A page that is written and
- * is also another pair's src or dst is undefined (some order wins).
+ * is also another pair's src or dst is undefined (parts of either may end there).
  */
 MSGL_API msgl_status msgl_copy_pages(const msgl_kv_pool *pools, int32_t num_pools, const int32_t *src,
                                      const int32_t *dst, const int32_t *tokens, int32_t num_pairs,
@@ -536,7 +536,8 @@ MSGL_API msgl_status msgl_copy_pages(const msgl_kv_pool *pools, int32_t num_pool
  *   req_rows     device int32 [num_reqs] or NULL (row b); -1: no request (padding)
  *   lens         device int32 [num_reqs], at most 2^24 of them
  *   held         device uint8 [num_slots / page_size] or NULL: not 0 for a page that something
- *                else holds (a radix cache's pages, a request that waits)
+ *                else holds (a radix cache's pages, a request that waits).  The caller keeps
+ *                these: include/msgl_radix.h hands page ids out and does not list them
  *   pages        device int32 [num_slots / page_size] (output): the free pages' ids, -1 behind them
  *   num_free     device int32 [1] (output): how many there are
  * A row outside the table (MSGL_DEVERR_ROW) holds nothing; a request whose length is

@@ -15,7 +15,7 @@
 // what that one wrote.
 //
 // Bound by scattered atomics and the lists' stores (half a million entries, 740 thousand pages:
-// free 13.4 us; 280 thousand and 550 thousand: compaction 14.6; some 4 us of each for the atomics, 120 to
+// free 13.3 us; 280 thousand and 550 thousand: compaction 14.6 to 15.7; some 4 us of each for the atomics, 120 to
 // 130 a nanosecond, and 1 to 3 more or less by where the bitmap lies), which want many SMs: one cluster of 8
 // blocks with the bitmap in shared memory took 32 and 63 us (16 blocks 23 and 44: a shared-memory
 // atomic takes a cycle a lane).  A byte a page, written without atomics, is no faster to mark

@@ -6,7 +6,7 @@
 // new one and a copy of what is in it.
 //
 // Both are copies: of table rows (latency: rows, lengths, ids, stores; 4 forks of 63 pages
-// 2.1 us, 256 of up to 16384 4.7) and of pool rows (HBM: every byte read once and written once;
+// 2.3 us, 256 of up to 16384 4.8) and of pool rows (HBM: every byte read once and written once;
 // 1024 pages of 16 slots in 4 layers, 537 MB, in 80 us, 6.7 TB/s).
 #include <limits.h>
 

@@ -19,8 +19,8 @@
 // writes its sum into the shared memory of all the cluster's blocks, each of which
 // then finds the run in which the draw falls; only that one is read again (out of L2), by
 // the block that summed it, or, where runs are short, not even that one.  128 requests
-// over 131072 tokens of fp32: 24.3 us (the rows alone 18 us at the copy rate; lookups in
-// front, exchange and draw behind take the rest); 4 over 50001 of bf16: 5.0 us.  With
+// over 131072 tokens of fp32: 24.6 us (the rows alone 18 us at the copy rate; lookups in
+// front, exchange and draw behind take the rest); 4 over 50001 of bf16: 4.9 us.  With
 // 64-bit sums: 72 and 14 us.  Sums sent by st.async and waited for by one warp, in place
 // of the cluster's barrier: 25.8 us, and 0.25 less for 4 requests.
 #include "cluster.cuh"
